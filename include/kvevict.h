@@ -360,6 +360,121 @@ int kvevict_load_state(kvevict_t* h, const void* buf, size_t bytes, void* stream
 int kvevict_prefill_scores_noalloc(const uint16_t* keys, int32_t heads, int32_t S,
                                    int32_t head_dim, float* colsum, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the step: what makes a token's keys, and what reads the cache.
+ * The pages leave both to the model that owns the cache (page
+ * "veloxquant_mlx.quantizers.keyformer module", keyformer_get_kv hands keys and
+ * values to its attention); these are that model's two operators on this
+ * library's layouts. A decoding layer l calls, per token,
+ *     kvevict_qk_norm_rope   queries and keys of the token
+ *     kvevict_attend_cache   its attention over layer l's rows and itself
+ * and, once every layer has run, kvevict_step_kv inserts the token's keys and
+ * values and evicts.
+ *
+ * Both hold no state and allocate nothing on the device. They run on the
+ * device that is current, which must be the one the pointers belong to. Their
+ * descriptions are read before the call returns. Strides count elements; the
+ * last dimension is contiguous, pointers start on a 16-byte boundary and every
+ * stride is a multiple of 16 bytes. Calls may overlap on any streams and
+ * threads as long as none writes what another uses. */
+#define KVEVICT_DTYPE_FP16 0
+#define KVEVICT_DTYPE_BF16 1
+#define KVEVICT_DTYPE_FP32 2   /* inputs and weights of kvevict_qk_norm_rope only */
+
+typedef struct kvevict_qk {
+  int32_t in_dtype;       /* of q and k: FP16, BF16 or FP32 */
+  int32_t out_dtype;      /* of q_out and k_out: FP16 (the cache's) or BF16 */
+  int32_t weight_dtype;   /* of q_weight and k_weight: FP16, BF16 or FP32 */
+  int32_t batch, seq;     /* >= 0 */
+  int32_t n_heads;        /* query heads, >= 0 */
+  int32_t n_kv_heads;     /* key heads, >= 0 */
+  int32_t head_dim;       /* D, 64 or 128 */
+  float eps;              /* of the norm, >= 0 */
+  int32_t reserved;       /* 0 */
+  double rope_theta;      /* RoPE base, > 0; the cache's kvevict_config.rope_theta */
+  int64_t pos0;           /* position of token 0 where positions is null */
+  const void* q;          /* device [batch, seq, n_heads, D]; null if n_heads = 0 */
+  const void* k;          /* device [batch, seq, n_kv_heads, D]; null if n_kv_heads = 0 */
+  void* q_out;            /* device, the shapes of q and k */
+  void* k_out;
+  const void* q_weight;   /* device [D], or null: queries are rotated without a norm */
+  const void* k_weight;   /* device [D], or null */
+  const int32_t* positions; /* device int32 [batch, seq], contiguous, or null: pos0 + s */
+  int64_t q_stride[3];    /* between sequences, tokens and heads */
+  int64_t k_stride[3];
+  int64_t q_out_stride[3];
+  int64_t k_out_stride[3]; /* any order: [B, H, S, D] is what kvevict_prefill takes */
+} kvevict_qk;
+
+/* RMS norm of every query and key head, y = x * w / sqrt(mean(x^2) + eps), and
+ * the rotation of the pairs (i, i + D/2) by p * theta^(-2i/D), in fp32 with one
+ * rounding to out_dtype. q_out may be q itself, and k_out k, with the same type
+ * and strides; outputs overlap nothing else. Positions are any int32 (from
+ * pos0: any int64). One kernel launch. Errors: INVALID_ARG, CUDA. */
+int kvevict_qk_norm_rope(const kvevict_qk* args, void* stream);
+
+typedef struct kvevict_attention {
+  int32_t dtype;          /* FP16 or BF16: q, out and every key and value */
+  int32_t batch;          /* B, sequences with one query token each, >= 0 */
+  int32_t n_heads;        /* G query heads, a multiple of n_kv_heads */
+  int32_t n_kv_heads;     /* H >= 1 */
+  int32_t head_dim;       /* D, 64 or 128 */
+  int32_t n;              /* own rows a sequence has room for, >= 0 */
+  int32_t prefix;         /* shared rows P, >= 0; n + prefix < 2^30 */
+  int32_t reserved;       /* 0 */
+  float scale;            /* of the logits, > 0 and finite; 0 = 1/sqrt(D) */
+  int32_t reserved2;      /* 0 */
+  const void* q;          /* device [B, G, D] */
+  void* out;              /* device [B, G, D] */
+  float* lse;             /* device float [B, G], contiguous, or null */
+  const void* k;          /* device [B, H, n, D]; null if n = 0 */
+  const void* v;
+  const int32_t* lens;    /* device int32 [B]: sequence b has min(max(lens[b], 0), n) rows; null: n */
+  const void* k_new;      /* device [B, H, D], the token's own key and value, or both null */
+  const void* v_new;
+  const void* prefix_k;   /* device [H, P, D], the rows all sequences share; null if P = 0 */
+  const void* prefix_v;
+  const int32_t* prefix_lens; /* device int32 [B]: sequence b shares the first min(max(.., 0), P); null: P */
+  void* workspace;        /* device, kvevict_attend_workspace bytes, 16-byte aligned; null if that is 0 */
+  int64_t q_stride[2];    /* between sequences and heads */
+  int64_t out_stride[2];
+  int64_t k_stride[3];    /* between sequences, heads and rows */
+  int64_t v_stride[3];
+  int64_t k_new_stride[2];
+  int64_t v_new_stride[2];
+  int64_t prefix_k_stride[2]; /* between heads and rows */
+  int64_t prefix_v_stride[2];
+  uint64_t workspace_bytes;
+} kvevict_attention;
+
+/* Attention of one query token a sequence: with s_j = q . k_j * scale over the
+ * sequence's own rows, the token's own key (k_new) and the shared rows,
+ *   out = sum_j e^(s_j) v_j / sum_j e^(s_j),   lse = log sum_j e^(s_j).
+ * Query head i reads key head i / (G / H). A sequence with no rows at all gets
+ * out = 0 and lse = -inf. Rows past a length are not read, whatever they hold.
+ * The shared rows are read once for all sequences, not once for each; without
+ * own rows the call is the prefix's part of a longer attention (a prompt
+ * chunk's tokens given as sequences), and lse joins it with the rest. Logits,
+ * softmax and sums are fp32; out is rounded once. out and lse overlap no input.
+ * The workspace holds nothing between calls and needs no initial value; calls
+ * that may run at the same time (captured graphs too) need one each.
+ * Errors: INVALID_ARG, CUDA. */
+int kvevict_attend(const kvevict_attention* args, void* stream);
+
+/* Device bytes that a call of this description needs as workspace (the
+ * pointers need not be set). *bytes: host. Errors: INVALID_ARG, CUDA. */
+int kvevict_attend_workspace(const kvevict_attention* args, size_t* bytes);
+
+/* kvevict_attend with layer l's kept rows of a value-carrying handle as the own
+ * rows: keys and values as kvevict_read_state and kvevict_read_values give
+ * them, a compaction still pending included, without changing the handle. batch,
+ * n_kv_heads and head_dim are the handle's, dtype is FP16, and n, k, v and lens
+ * must be 0 and null (the row count is min(next_pos, budget_l) when the call is
+ * made: a captured call keeps it). q and k_new are rotated at position
+ * kvevict_next_pos. Errors: as kvevict_attend; INVALID_ARG (a key-only handle,
+ * another device current than the handle's, layer out of range). */
+int kvevict_attend_cache(const kvevict_t* h, int32_t l, const kvevict_attention* args, void* stream);
+
 /* Message of the last failure on the calling thread ("" if none). */
 const char* kvevict_last_error(void);
 

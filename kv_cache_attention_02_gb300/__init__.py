@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -22,6 +23,7 @@ LIB_PATH = os.path.join(_HERE, "libkvevict.so")
 OK, ERR_INVALID_ARG, ERR_BAD_STATE, ERR_CUDA, ERR_OOM, ERR_DEVICE_CHECK = 0, -1, -2, -3, -4, -5
 SCORE_CUMULATIVE, SCORE_CURRENT = 0, 1
 PREFILL_BULK, PREFILL_SEQUENTIAL = 0, 1
+DTYPE_FP16, DTYPE_BF16, DTYPE_FP32 = 0, 1, 2
 DECODE_AUTO, DECODE_STREAM, DECODE_RESIDENT = 0, 1, 2
 MAX_LAYERS = 256
 MAX_PREFILL = 16384
@@ -76,6 +78,10 @@ SIGNATURES = {
     "kvevict_load_state": (ctypes.c_int, [P, P, ctypes.c_size_t, P]),
     "kvevict_last_error": (ctypes.c_char_p, []),
     "kvevict_prefill_scores_noalloc": (ctypes.c_int, [P, i32, i32, i32, P, P]),
+    "kvevict_qk_norm_rope": (ctypes.c_int, [P, P]),
+    "kvevict_attend": (ctypes.c_int, [P, P]),
+    "kvevict_attend_workspace": (ctypes.c_int, [P, P]),
+    "kvevict_attend_cache": (ctypes.c_int, [P, i32, P, P]),
 }
 
 
@@ -121,6 +127,158 @@ def prefill_scores_noalloc(keys, colsum, stream=None):
     assert tuple(colsum.shape) == (heads, S)
     _check(lib().kvevict_prefill_scores_noalloc(_ptr(keys), heads, S, D, _ptr(colsum),
                                                 _stream(stream)))
+
+
+# ``kvevict_qk`` and ``kvevict_attention`` of include/kvevict.h, field by field.
+_QK = struct.Struct("=8i f i d q 7Q 12q")
+_ATTENTION = struct.Struct("=8i f i 12Q 18q Q")
+_NO2, _NO3 = (0, 0), (0, 0, 0)
+
+
+def _dtypes(allowed):
+    import torch
+    codes = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+    return {t: c for t, c in codes.items() if c in allowed}
+
+
+class _Tensors:
+    """Checks one call's tensors: shape, type, contiguous last dimension, the current device."""
+
+    def __init__(self):
+        import torch
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else None
+
+    def __call__(self, name, t, shape, dtype, contiguous=False):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_cuda or t.get_device() != self.device:
+            raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+        stride = t.stride()
+        if contiguous:
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        elif stride[-1] != 1 and shape[-1] != 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+        # a dimension of one row has no stride to speak of
+        return t.data_ptr(), tuple(0 if n == 1 else s for n, s in zip(shape[:-1], stride))
+
+
+def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None, eps=1e-6, positions=None, pos0=0,
+                 stream=None):
+    """RMS norm of every query and key head and the rotation to the token's position, in one pass.
+
+    q [B, S, G, D], k [B, S, H, D]: fp16, bf16 or fp32 (views of a fused projection are fine). q_out, k_out: their
+    shapes in fp16 or bf16, in any layout with a contiguous last dimension; ``prompt_keys[:, l].transpose(1, 2)``
+    writes layer l of what ``KVEvict.prefill`` takes, ``k_new[:, l, None]`` of what ``KVEvict.step`` takes. q_weight,
+    k_weight [D] or None (no norm). positions: int32 [B, S], else token s is at pos0 + s. Either of q and k may be
+    None with its output. Errors: ValueError, KVEvictError.
+    """
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q goes with q_out and k with k_out")
+    some, some_out = (q, q_out) if q is not None else (k, k_out)
+    if some.dim() != 4:
+        raise ValueError("q and k must have shape [batch, seq, heads, head_dim]")
+    B, S, _, D = some.shape
+    ins, outs = _dtypes((DTYPE_FP16, DTYPE_BF16, DTYPE_FP32)), _dtypes((DTYPE_FP16, DTYPE_BF16))
+    if some.dtype not in ins or some_out.dtype not in outs:
+        raise ValueError("q and k must be fp16, bf16 or fp32, q_out and k_out fp16 or bf16")
+    check = _Tensors()
+    ptrs, strides, heads = [], [], []
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            ptrs.append((0, 0))
+            strides.append((_NO3, _NO3))
+            heads.append(0)
+            continue
+        shape = (B, S, int(x.shape[2]) if x.dim() == 4 else -1, D)
+        (px, sx), (py, sy) = check(name, x, shape, some.dtype), check(name + "_out", y, shape, some_out.dtype)
+        ptrs.append((px, py))
+        strides.append((sx, sy))
+        heads.append(shape[2])
+    weights = [0, 0]
+    wt = q_weight if q_weight is not None else k_weight
+    if wt is not None and wt.dtype not in ins:
+        raise ValueError("q_weight and k_weight must be fp16, bf16 or fp32")
+    for i, (name, w) in enumerate((("q_weight", q_weight), ("k_weight", k_weight))):
+        if w is not None:
+            weights[i] = check(name, w, (D,), wt.dtype, contiguous=True)[0]
+    at = check("positions", positions, (B, S), _torch().int32, contiguous=True)[0] if positions is not None else 0
+    args = _QK.pack(ins[some.dtype], outs[some_out.dtype], ins[wt.dtype] if wt is not None else DTYPE_FP32, B, S,
+                    heads[0], heads[1], D, eps, 0, rope_theta, pos0, ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1],
+                    weights[0], weights[1], at, *strides[0][0], *strides[1][0], *strides[0][1], *strides[1][1])
+    _check(lib().kvevict_qk_norm_rope(args, _stream(stream)))
+
+
+def _attention_args(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, kv_heads=None):
+    """The ``kvevict_attention`` of a call as a bytearray, its workspace not set."""
+    if q.dim() != 3:
+        raise ValueError("q must have shape [batch, heads, head_dim]")
+    B, G, D = q.shape
+    kinds = _dtypes((DTYPE_FP16, DTYPE_BF16))
+    if q.dtype not in kinds:
+        raise ValueError("q must be fp16 or bf16")
+    for name, x, y in (("k and v", k, v), ("k_new and v_new", k_new, v_new), ("prefix_k and prefix_v", prefix_k, prefix_v)):
+        if (x is None) != (y is None):
+            raise ValueError(f"{name} go together")
+    if lens is not None and k is None or prefix_lens is not None and prefix_k is None:
+        raise ValueError("lens goes with k and prefix_lens with prefix_k")
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be > 0")
+    check, kind = _Tensors(), q.dtype
+    H, n, prefix = kv_heads, 0, 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("k must have shape [batch, kv_heads, rows, head_dim]")
+        H, n = int(k.shape[1]), int(k.shape[2])
+    if prefix_k is not None:
+        if prefix_k.dim() != 3:
+            raise ValueError("prefix_k must have shape [kv_heads, rows, head_dim]")
+        H, prefix = H or int(prefix_k.shape[0]), int(prefix_k.shape[1])
+    if H is None and k_new is not None:
+        H = int(k_new.shape[1]) if k_new.dim() == 3 else -1
+    if H is None:
+        raise ValueError("nothing to attend to: k, k_new or prefix_k must be given")
+    pq, sq = check("q", q, (B, G, D), kind)
+    po, so = check("out", out, (B, G, D), kind)
+    pk = pv = pkn = pvn = ppk = ppv = 0
+    sk = sv = _NO3
+    skn = svn = spk = spv = _NO2
+    if n:
+        (pk, sk), (pv, sv) = check("k", k, (B, H, n, D), kind), check("v", v, (B, H, n, D), kind)
+    if k_new is not None:
+        (pkn, skn), (pvn, svn) = check("k_new", k_new, (B, H, D), kind), check("v_new", v_new, (B, H, D), kind)
+    if prefix:
+        ppk, spk = check("prefix_k", prefix_k, (H, prefix, D), kind)
+        ppv, spv = check("prefix_v", prefix_v, (H, prefix, D), kind)
+    int32, f32_ = _torch().int32, _torch().float32
+    pl = check("lens", lens, (B,), int32, contiguous=True)[0] if lens is not None else 0
+    ppl = check("prefix_lens", prefix_lens, (B,), int32, contiguous=True)[0] if prefix_lens is not None else 0
+    pe = check("lse", lse, (B, G), f32_, contiguous=True)[0] if lse is not None else 0
+    return bytearray(_ATTENTION.pack(kinds[kind], B, G, H, D, n, prefix, 0, scale or 0.0, 0, pq, po, pe, pk, pv, pl, pkn,
+                                     pvn, ppk, ppv, ppl, 0, *sq, *so, *sk, *sv, *skn, *svn, *spk, *spv, 0))
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_k=None, prefix_v=None,
+           prefix_lens=None, lse=None, scale=None, stream=None):
+    """Attention of one query token a sequence over its own rows, the token's own key and shared rows.
+
+    q, out [B, G, D] fp16 or bf16, everything else of q's type; k, v [B, H, n, D] with lens int32 [B] or None (n);
+    k_new, v_new [B, H, D]; prefix_k, prefix_v [H, P, D], read once for the whole batch, with prefix_lens int32 [B] or
+    None (P). Query head i reads key head i // (G // H). lse: float32 [B, G] output or None. scale: 1/sqrt(D) unless
+    given. A sequence with no rows gets out 0 and lse -inf. Any layout with a contiguous last dimension and strides of
+    whole 16-byte pieces. Errors: ValueError, KVEvictError.
+    """
+    args = _attention_args(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale)
+    _check(lib().kvevict_attend((ctypes.c_char * len(args)).from_buffer(args), _stream(stream)))
 
 
 def _ptr(t) -> int:
@@ -212,6 +370,17 @@ class KVEvict:
         else:
             _check(lib().kvevict_decode(self._h, _ptr(keys), int(keys.shape[0]), _ptr(evicted),
                                         _stream(stream)))
+
+    def attend(self, l: int, q, out, *, k_new=None, v_new=None, prefix_k=None, prefix_v=None, prefix_lens=None, lse=None,
+               scale=None, stream=None):
+        """``attend`` with layer l's kept keys and values as the own rows (a value-carrying handle; fp16).
+
+        q, out [B, G, D]; k_new, v_new [B, H, D]: the token's own, before the step that inserts them. Rows are as
+        ``read_state`` and ``read_values`` give them; the handle is not changed. A captured call keeps the row count
+        of its capture.
+        """
+        args = _attention_args(q, out, None, None, None, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, self.H)
+        _check(lib().kvevict_attend_cache(self._h, l, (ctypes.c_char * len(args)).from_buffer(args), _stream(stream)))
 
     def run_host(self, prefill_keys, decode_keys, evicted=None, stream=None):
         """End to end from host memory (pinned tensors or numpy uint16 arrays)."""

@@ -1,0 +1,121 @@
+// attend_internal.cuh -- structures and helpers shared by the query/key norm
+// with rotation (qk_norm_rope.cu), the attention kernels (attend_rows.cu) and
+// their entry points (attend.cu, runtime.cu).
+#pragma once
+
+#include "kvevict.h"
+#include "kvevict_internal.cuh"
+
+#include <cuda_bf16.h>
+
+#include <string>
+
+namespace kvx {
+
+constexpr int kFp16 = KVEVICT_DTYPE_FP16;
+constexpr int kBf16 = KVEVICT_DTYPE_BF16;
+constexpr int kFp32 = KVEVICT_DTYPE_FP32;
+
+struct QkArgs {
+  const void* q;           // element strides between sequences, tokens and heads
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride[3], k_stride[3], qo_stride[3], ko_stride[3];
+  const void* q_weight;    // [D] or null: no norm
+  const void* k_weight;
+  int w_dtype;
+  float eps;
+  const int32_t* positions;  // [B, S] or null: pos0 + s
+  int64_t pos0;
+  int B, S, G, H;          // G query heads, H key heads
+  int parts, per_part;     // a token's heads go to `parts` warps, per_part heads each
+  uint64_t turn[64];       // theta^(-2i/D) / 2 pi, as a 64-bit fraction of a turn
+};
+
+struct AttendArgs {
+  const void* q;           // [B, G, D]: element strides between sequences and heads
+  void* out;
+  float* lse;              // [B, G] or null
+  const void* k;           // own rows [B, H, n, D]
+  const void* v;
+  const int32_t* lens;     // [B] or null: n rows each
+  const void* k_new;       // the token's own key and value [B, H, D], or null
+  const void* v_new;
+  const void* pk;          // shared rows [H, P, D]
+  const void* pv;
+  const int32_t* plens;    // [B] or null: P rows each
+  int64_t q_stride[2], out_stride[2], k_stride[3], v_stride[3], kn_stride[2], vn_stride[2], pk_stride[2],
+      pv_stride[2];
+  const int32_t* pend;     // cache rows with a compaction pending: [B, H] the evicted slot or -1, else null
+  const float* rope_c;     // [D/2], the shift by -1 (with pend)
+  const float* rope_s;
+  int B, G, H, n, P;
+  float scale2;            // scale * log2(e): logits in base-2 units
+};
+
+// What a launch needs to know of the current device, looked up once.
+struct DeviceInfo {
+  int sms = 0;
+};
+int device_info(DeviceInfo* out);   // KVEVICT_* code; sets the last error
+void set_last_error(const std::string& msg);
+
+cudaError_t launch_qk_norm_rope(QkArgs a, int D, int in_dtype, int out_dtype, int sms, cudaStream_t s);
+cudaError_t launch_attend_rows(const AttendArgs& a, int D, int dtype, int sms, cudaStream_t s);
+
+// Checks the caller's description and fills the kernel's; own rows come from
+// `rows` (a handle's layer) where that is not null.
+struct CacheRows {
+  const void* k;
+  const void* v;
+  int64_t stride[3];
+  int n;
+  const int32_t* pend;
+  const float* rope_c;
+  const float* rope_s;
+  int batch, n_kv_heads, head_dim;
+};
+int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s);
+
+// ---------------------------------------------------------------- device helpers
+// 16 bytes that no later access of this SM wants: past L1.
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ float2 unpack16(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack16<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace kvx

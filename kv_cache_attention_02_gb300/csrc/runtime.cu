@@ -4,6 +4,7 @@
 // method runs in the kernels of decode.cu and prefill.cu.
 #include "kvevict.h"
 #include "kvevict_internal.cuh"
+#include "attend_internal.cuh"
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -846,6 +847,35 @@ int kvevict_read_values(kvevict_t* h, int32_t b, int32_t l, int32_t head, uint16
   rc = check_error_word(h, s);
   if (n_kept) *n_kept = n;
   return rc;
+}
+
+int kvevict_attend_cache(const kvevict_t* h, int32_t l, const kvevict_attention* args, void* stream) {
+  KV_RANGE();
+  try {
+    if (!h) return fail(KVEVICT_ERR_INVALID_ARG, "null handle");
+    if (int rc = with_values(h)) return rc;
+    if (l < 0 || l >= h->L) return fail(KVEVICT_ERR_INVALID_ARG, "layer out of range");
+    int dev = 0;
+    KV_CUDA(cudaGetDevice(&dev));
+    if (dev != h->device) return fail(KVEVICT_ERR_INVALID_ARG, "the handle belongs to another device than the current one");
+    const LayerInfo& li = h->layers[l];
+    kvx::CacheRows r{};
+    r.k = h->K + li.row_base * h->D;
+    r.v = h->V + li.row_base * h->D;
+    r.stride[0] = (int64_t)h->H * li.cap * h->D;
+    r.stride[1] = (int64_t)li.cap * h->D;
+    r.stride[2] = h->D;
+    r.n = (int)std::min<int64_t>(h->next_pos, li.budget);
+    r.pend = h->pend + (int64_t)l * h->B * h->H;
+    r.rope_c = h->rope_c + (size_t)(h->D / 2);
+    r.rope_s = h->rope_s + (size_t)(h->D / 2);
+    r.batch = h->B;
+    r.n_kv_heads = h->H;
+    r.head_dim = h->D;
+    return kvx::attend_run(args, &r, (cudaStream_t)stream);
+  } catch (...) {
+    return KVEVICT_ERR_OOM;
+  }
 }
 
 int kvevict_check(kvevict_t* h, void* stream) {

@@ -1,0 +1,224 @@
+"""Attention over own rows, a shared prefix and the token's own key against its 64-bit form."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import attention_reference as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def kvx():
+    import kv_cache_attention_02_gb300 as k
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    k.lib()
+    return k
+
+
+def _make(B, N, H, D, n=0, P=0, new=False, dtype=F16, seed=0, spread=1.5):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def r(*shape, scale=1.0):
+        return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(dtype)
+    rows = {}
+    if n:
+        rows.update(k=r(B, H, n, D), v=r(B, H, n, D))
+    if new:
+        rows.update(k_new=r(B, H, D), v_new=r(B, H, D))
+    if P:
+        rows.update(prefix_k=r(H, P, D), prefix_v=r(H, P, D))
+    return r(B, N * H, D, scale=spread), rows
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 63, 200, 1025])
+def test_lengths(kvx, n, D, dtype):
+    q, rows = _make(2, 3, 2, D, n=n, new=n % 2 == 0, dtype=dtype, seed=n)
+    ref.check_attend(kvx, q, **rows)
+
+
+@pytest.mark.parametrize("N", [1, 2, 7, 8, 9, 16, 17, 32, 40])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("P", [0, 70])
+def test_head_groups(kvx, N, D, P):
+    q, rows = _make(2, N, 2, D, n=45, P=P, new=True, seed=N)
+    ref.check_attend(kvx, q, **rows)
+
+
+@pytest.mark.parametrize("B,H,n", [(1, 1, 5000), (1, 8, 3000), (40, 8, 130), (3, 1, 1), (300, 4, 33), (1, 1, 40000)])
+def test_splits(kvx, B, H, n):
+    q, rows = _make(B, 4, H, 128, n=n, seed=n)
+    ref.check_attend(kvx, q, **rows)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,N,P", [(1, 1, 1), (1, 4, 127), (5, 3, 128), (2, 4, 129), (32, 4, 1000), (40, 4, 257), (7, 40, 640),
+                                   (130, 2, 384), (64, 5, 2100), (3, 2, 9000), (700, 4, 300)])
+def test_prefix_alone(kvx, B, N, P, D, dtype):
+    q, rows = _make(B, N, 2, D, P=P, dtype=dtype, seed=P)
+    ref.check_attend(kvx, q, **rows)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("B,N,H,D,n,P,new", [(4, 3, 8, 128, 64, 333, True), (33, 4, 2, 128, 100, 2000, True),
+                                            (33, 4, 2, 64, 100, 2000, False), (70, 8, 1, 128, 17, 1500, True),
+                                            (16, 12, 2, 64, 0, 900, True), (300, 2, 1, 128, 9, 700, True)])
+def test_prefix_with_own_rows(kvx, B, N, H, D, n, P, new, dtype):
+    q, rows = _make(B, N, H, D, n=n, P=P, new=new, dtype=dtype, seed=P + n)
+    ref.check_attend(kvx, q, **rows)
+    lens = torch.randint(0, n + 1, (B,), dtype=torch.int32, device="cuda") if n else None
+    plens = torch.randint(0, P + 1, (B,), dtype=torch.int32, device="cuda")
+    plens[0], plens[-1] = 0, P
+    ref.check_attend(kvx, q, prefix_lens=plens, **({"lens": lens} if n else {}), **rows)
+
+
+@pytest.mark.parametrize("B,P", [(6, 0), (6, 90), (48, 700), (200, 513)])
+@pytest.mark.parametrize("new", [False, True])
+def test_empty_ragged_and_poisoned_rows(kvx, B, P, new):
+    """Lengths of zero, one and out of range; rows past a length hold NaN and infinities."""
+    n = 50
+    q, rows = _make(B, 4, 2, 128, n=n, P=P, new=new, seed=P)
+    lens = torch.tensor([0, 1, n, n + 9, -3, 17] * (B // 6 + 1), dtype=torch.int32, device="cuda")[:B]
+    extra = {}
+    if P:
+        extra["prefix_lens"] = torch.tensor([0, P, 1, -1, 0, P // 2] * (B // 6 + 1), dtype=torch.int32, device="cuda")[:B]
+    for b in range(B):
+        at = min(max(int(lens[b]), 0), n)
+        rows["k"][b, :, at:], rows["v"][b, :, at:] = float("nan"), float("inf")
+    out, lse = ref.check_attend(kvx, q, lens=lens, **extra, **rows)
+    if not new:
+        assert (out[0] == 0).all() and (lse[0] == -math.inf).all()
+
+
+def test_prefix_rows_past_every_length_are_not_used(kvx):
+    q, rows = _make(40, 4, 2, 128, P=600, seed=8)
+    plens = torch.full((40,), 301, dtype=torch.int32, device="cuda")
+    plens[3] = 0
+    rows["prefix_k"][:, 301:], rows["prefix_v"][:, 301:] = float("nan"), float("nan")
+    ref.check_attend(kvx, q, prefix_lens=plens, **rows)
+
+
+@pytest.mark.parametrize("P", [0, 300])
+@pytest.mark.parametrize("B", [3, 50])
+def test_strides(kvx, B, P):
+    """Rows between sequences ([B, n, H, D]), queries inside a fused projection, outputs inside a larger buffer."""
+    H, N, D, n = 2, 4, 128, 70
+    q, rows = _make(B, N, H, D, n=n, P=P, new=True, seed=11)
+    qkv = torch.cat([q, q, q], 1)
+    for name in ("k", "v"):
+        rows[name] = rows[name].transpose(1, 2).contiguous().transpose(1, 2)
+    if P:
+        for name in ("prefix_k", "prefix_v"):
+            rows[name] = torch.stack([rows[name].transpose(0, 1)] * 2, 1)[:, 1].transpose(0, 1)
+    big = torch.full((B + 1, 2 * N * H, D), 3.0, dtype=F16, device="cuda")
+    ref.check_attend(kvx, qkv[:, N * H:2 * N * H], out=big[:B, N * H:], **rows)
+    assert (big[:, :N * H] == 3).all() and (big[B] == 3).all()
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 3.0])
+@pytest.mark.parametrize("P", [0, 260])
+@pytest.mark.parametrize("B", [2, 40])
+def test_scales_and_large_logits(kvx, B, P, scale):
+    """From flat weights to one key that takes everything, the running maximum moving often and far."""
+    q, rows = _make(B, 4, 2, 64, n=150, P=P, seed=5)
+    rows["k"] *= torch.linspace(0.1, 4, 150, device="cuda").to(F16)[:, None]
+    if P:
+        rows["prefix_k"] *= torch.linspace(0.1, 4, P, device="cuda").to(F16)[:, None]
+    ref.check_attend(kvx, q, scale=scale, **rows)
+
+
+@pytest.mark.parametrize("B", [2, 40])
+def test_infinite_and_nan_rows_that_count(kvx, B):
+    """A NaN in a row that counts shows in its sequence alone; a key of -inf logits takes no weight."""
+    q, rows = _make(B, 2, 2, 64, n=40, P=200, seed=6)
+    want, wlse = ref.check_attend(kvx, q, **rows)
+    rows["v"][1, 0, 7] = float("nan")
+    out, lse = torch.empty_like(q), torch.empty_like(wlse)
+    kvx.attend(q, out, lse=lse, **rows)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[1, :2]).all() and torch.equal(out[1, 2:], want[1, 2:]) and torch.equal(lse, wlse)
+    assert torch.equal(out[0], want[0]) and torch.equal(out[2:], want[2:])
+    rows["k"][1, 0, 7] = float("nan")
+    kvx.attend(q, out, lse=lse, **rows)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[1, :2]).all() and torch.isnan(lse[1, :2]).all() and torch.equal(lse[0], wlse[0])
+
+
+def test_offsets_past_32_bits(kvx):
+    """Strides whose products pass 2^31 elements: the second sequence and the last rows of a long buffer."""
+    H, N, D, n = 2, 4, 128, 40
+    far = 2 ** 31 + 1024                       # elements between sequences
+    if torch.cuda.mem_get_info()[0] < 24 * 2 ** 30:
+        pytest.skip("needs 24 GB")
+    base = [torch.zeros(far + 2 ** 20, dtype=F16, device="cuda") for _ in range(2)]
+    q, rows = _make(2, N, H, D, n=n, seed=9)
+    for name, x in zip(("k", "v"), base):
+        view = x.as_strided((2, H, n, D), (far, n * D, D, 1))
+        view.copy_(rows[name])
+        rows[name] = view
+    ref.check_attend(kvx, q, **rows)
+    step = 2 ** 25 + 128                       # elements between rows: row 63 is past 2^31
+    q, rows = _make(40, N, 1, D, P=64, seed=10)
+    for name, x in zip(("prefix_k", "prefix_v"), base):
+        view = x.as_strided((1, 64, D), (0, step, 1))
+        view.copy_(rows[name])
+        rows[name] = view
+    ref.check_attend(kvx, q, **rows)
+
+
+@pytest.mark.parametrize("B,n,P", [(2, 300, 0), (2, 30, 100), (40, 30, 1000), (150, 0, 1000)])
+def test_repeat_streams_and_graphs(kvx, B, n, P):
+    """The same bits call after call, on another stream, and from two captured graphs that replay together."""
+    q, rows = _make(B, 4, 2, 128, n=n, P=P, seed=12)
+    want, wlse = ref.check_attend(kvx, q, **rows)
+    side = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(q) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, o in zip(side, outs):
+            o.zero_()
+        torch.cuda.synchronize()
+        for s, o in zip(side, outs):
+            kvx.attend(q, o, stream=s, **rows)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, o in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            kvx.attend(q, o, **rows)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for s, g in zip(side, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+    q.neg_()
+    other = torch.empty_like(q)
+    kvx.attend(q, other, **rows)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], other) and not torch.equal(other, want)
+
+
+@pytest.mark.parametrize("B", [3, 60])
+def test_parts_join_by_lse(kvx, B):
+    """Prefix and own rows in two calls, joined by their log sums, are the one call."""
+    q, rows = _make(B, 4, 2, 128, n=80, P=500, seed=13)
+    out, lse = ref.check_attend(kvx, q, **rows)
+    a, la = ref.check_attend(kvx, q, k=rows["k"], v=rows["v"])
+    b, lb = ref.check_attend(kvx, q, prefix_k=rows["prefix_k"], prefix_v=rows["prefix_v"])
+    total = torch.logaddexp(la, lb)
+    joined = a * (la - total).exp()[..., None] + b * (lb - total).exp()[..., None]
+    # three roundings to fp16 (both parts and the whole) and the weights' half steps in the prefix part
+    assert (joined - out).abs().max() <= 4 * 2.0 ** -11 * max(a.abs().max(), b.abs().max(), 1.0)
+    torch.testing.assert_close(total, lse, rtol=1e-6, atol=1e-5)
