@@ -259,7 +259,8 @@ int kvevict_check(kvevict_t* h, void* stream);
  * never issues the query-tile copy of its first work item, with the same
  * outcome: a
  * handle then reports DEVICE_CHECK, the allocation-free call writes NaN
- * scores. Nothing faults or hangs. One-shot. Errors: none. */
+ * scores. A launch of kvevict_attend's prefix kernel that comes first takes the
+ * hook instead (its first key tile), and writes NaN. Nothing faults or hangs. One-shot. Errors: none. */
 int kvevict_test_stall_next_step(kvevict_t* h);
 
 /* Position the next decode key will occupy (= tokens absorbed so far): the
@@ -456,14 +457,21 @@ typedef struct kvevict_attention {
  * own rows the call is the prefix's part of a longer attention (a prompt
  * chunk's tokens given as sequences), and lse joins it with the rest. Logits,
  * softmax and sums are fp32; out is rounded once. out and lse overlap no input.
+ * Where prefix_lens differ, a shared value that is NaN or infinite may show in
+ * sequences that do not share its row (their weight of it is 0); rows past the
+ * longest length are not looked at. Waits in the prefix's kernel are bounded
+ * (4 s); one that runs out leaves NaN in out and lse, and on a handle sets its
+ * error word (kvevict_check).
  * The workspace holds nothing between calls and needs no initial value; calls
  * that may run at the same time (captured graphs too) need one each.
  * Errors: INVALID_ARG, CUDA. */
 int kvevict_attend(const kvevict_attention* args, void* stream);
 
-/* Device bytes that a call of this description needs as workspace (the
- * pointers need not be set). *bytes: host. Errors: INVALID_ARG, CUDA. */
-int kvevict_attend_workspace(const kvevict_attention* args, size_t* bytes);
+/* Device bytes that a call of this description needs as workspace, on the
+ * current device; of the pointers only k_new counts. with_cache: 1 for
+ * kvevict_attend_cache, 0 for kvevict_attend. *bytes: host. Errors:
+ * INVALID_ARG, CUDA. */
+int kvevict_attend_workspace(const kvevict_attention* args, int32_t with_cache, size_t* bytes);
 
 /* kvevict_attend with layer l's kept rows of a value-carrying handle as the own
  * rows: keys and values as kvevict_read_state and kvevict_read_values give

@@ -80,7 +80,7 @@ SIGNATURES = {
     "kvevict_prefill_scores_noalloc": (ctypes.c_int, [P, i32, i32, i32, P, P]),
     "kvevict_qk_norm_rope": (ctypes.c_int, [P, P]),
     "kvevict_attend": (ctypes.c_int, [P, P]),
-    "kvevict_attend_workspace": (ctypes.c_int, [P, P]),
+    "kvevict_attend_workspace": (ctypes.c_int, [P, i32, P]),
     "kvevict_attend_cache": (ctypes.c_int, [P, i32, P, P]),
 }
 
@@ -132,37 +132,62 @@ def prefill_scores_noalloc(keys, colsum, stream=None):
 # ``kvevict_qk`` and ``kvevict_attention`` of include/kvevict.h, field by field.
 _QK = struct.Struct("=8i f i d q 7Q 12q")
 _ATTENTION = struct.Struct("=8i f i 12Q 18q Q")
+_WORKSPACE_AT, _WORKSPACE_BYTES_AT = 40 + 11 * 8, 40 + 12 * 8 + 18 * 8   # offsets in kvevict_attention
 _NO2, _NO3 = (0, 0), (0, 0, 0)
 
 
-def _dtypes(allowed):
+def _torch():
+    """torch, with its types' codes (imported on first use: the library itself does not need it)."""
+    global _IN, _OUT, _loaded
+    if _loaded is not None:
+        return _loaded
     import torch
-    codes = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
-    return {t: c for t, c in codes.items() if c in allowed}
+    _loaded = torch
+    _IN = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+    _OUT = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
+    return torch
 
 
-class _Tensors:
-    """Checks one call's tensors: shape, type, contiguous last dimension, the current device."""
+_IN, _OUT, _loaded = {}, {}, None
 
-    def __init__(self):
-        import torch
-        self.device = torch.cuda.current_device() if torch.cuda.is_available() else None
 
-    def __call__(self, name, t, shape, dtype, contiguous=False):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_cuda or t.get_device() != self.device:
-            raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
-        stride = t.stride()
-        if contiguous:
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-        elif stride[-1] != 1 and shape[-1] != 1:
-            raise ValueError(f"the last dimension of {name} must be contiguous")
-        # a dimension of one row has no stride to speak of
-        return t.data_ptr(), tuple(0 if n == 1 else s for n, s in zip(shape[:-1], stride))
+def _wrong(name, t, shape, dtype, device):
+    if t.shape != shape:
+        return ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.dtype is not dtype:
+        return ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    return ValueError(f"{name} must be on the current CUDA device, got {t.device}" if not t.is_cuda or t.get_device() != device
+                      else f"{name} must be contiguous" if t.stride()[-1] == 1 or t.shape[-1] == 1
+                      else f"the last dimension of {name} must be contiguous")
+
+
+def _strided(name, t, shape, dtype, device):
+    """Pointer and strides of one call's tensor, after the checks; a dimension of one row has no stride to speak of."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise _wrong(name, t, shape, dtype, device)
+    stride = t.stride()
+    if stride[-1] != 1 and shape[-1] != 1:
+        raise _wrong(name, t, shape, dtype, device)
+    return t.data_ptr(), [0 if n == 1 else s for n, s in zip(shape, stride)][:-1]
+
+
+def _dense(name, t, shape, dtype, device):
+    """Pointer of a contiguous tensor, after the checks; null for None."""
+    if t is None:
+        return 0
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise _wrong(name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _place(torch, t, stream):
+    """The current device and the stream of a call whose first tensor is t."""
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
+    device = torch.cuda.current_device()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, _stream(stream)
 
 
 def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None, eps=1e-6, positions=None, pos0=0,
@@ -175,96 +200,109 @@ def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None
     k_weight [D] or None (no norm). positions: int32 [B, S], else token s is at pos0 + s. Either of q and k may be
     None with its output. Errors: ValueError, KVEvictError.
     """
+    torch = _torch()
     if q is None and k is None:
         raise ValueError("q or k must be given")
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q goes with q_out and k with k_out")
     some, some_out = (q, q_out) if q is not None else (k, k_out)
-    if some.dim() != 4:
+    if some.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must have shape [batch, seq, heads, head_dim]")
     B, S, _, D = some.shape
-    ins, outs = _dtypes((DTYPE_FP16, DTYPE_BF16, DTYPE_FP32)), _dtypes((DTYPE_FP16, DTYPE_BF16))
-    if some.dtype not in ins or some_out.dtype not in outs:
+    kind, kind_out = some.dtype, some_out.dtype
+    if kind not in _IN or kind_out not in _OUT:
         raise ValueError("q and k must be fp16, bf16 or fp32, q_out and k_out fp16 or bf16")
-    check = _Tensors()
-    ptrs, strides, heads = [], [], []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            ptrs.append((0, 0))
-            strides.append((_NO3, _NO3))
-            heads.append(0)
-            continue
-        shape = (B, S, int(x.shape[2]) if x.dim() == 4 else -1, D)
-        (px, sx), (py, sy) = check(name, x, shape, some.dtype), check(name + "_out", y, shape, some_out.dtype)
-        ptrs.append((px, py))
-        strides.append((sx, sy))
-        heads.append(shape[2])
-    weights = [0, 0]
-    wt = q_weight if q_weight is not None else k_weight
-    if wt is not None and wt.dtype not in ins:
+    device, s = _place(torch, some, stream)
+    G = H = pq = pqo = pk = pko = 0
+    sq = sqo = sk = sko = _NO3
+    if q is not None:
+        G = q.shape[2]
+        pq, sq = _strided("q", q, (B, S, G, D), kind, device)
+        pqo, sqo = _strided("q_out", q_out, (B, S, G, D), kind_out, device)
+    if k is not None:
+        H = k.shape[2]
+        pk, sk = _strided("k", k, (B, S, H, D), kind, device)
+        pko, sko = _strided("k_out", k_out, (B, S, H, D), kind_out, device)
+    wt = None if q_weight is None and k_weight is None else (q_weight if q_weight is not None else k_weight).dtype
+    if wt is not None and wt not in _IN:
         raise ValueError("q_weight and k_weight must be fp16, bf16 or fp32")
-    for i, (name, w) in enumerate((("q_weight", q_weight), ("k_weight", k_weight))):
-        if w is not None:
-            weights[i] = check(name, w, (D,), wt.dtype, contiguous=True)[0]
-    at = check("positions", positions, (B, S), _torch().int32, contiguous=True)[0] if positions is not None else 0
-    args = _QK.pack(ins[some.dtype], outs[some_out.dtype], ins[wt.dtype] if wt is not None else DTYPE_FP32, B, S,
-                    heads[0], heads[1], D, eps, 0, rope_theta, pos0, ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1],
-                    weights[0], weights[1], at, *strides[0][0], *strides[1][0], *strides[0][1], *strides[1][1])
-    _check(lib().kvevict_qk_norm_rope(args, _stream(stream)))
+    args = _QK.pack(_IN[kind], _OUT[kind_out], _IN[wt] if wt is not None else DTYPE_FP32, B, S, G, H, D, eps, 0, rope_theta,
+                    pos0, pq, pk, pqo, pko, _dense("q_weight", q_weight, (D,), wt, device),
+                    _dense("k_weight", k_weight, (D,), wt, device),
+                    _dense("positions", positions, (B, S), torch.int32, device), *sq, *sk, *sqo, *sko)
+    rc = lib().kvevict_qk_norm_rope(args, s)
+    if rc:
+        _check(rc)
 
 
-def _attention_args(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, kv_heads=None):
-    """The ``kvevict_attention`` of a call as a bytearray, its workspace not set."""
+def _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream, kv_heads):
+    """The ``kvevict_attention`` of a call and its stream."""
+    torch = _torch()
     if q.dim() != 3:
         raise ValueError("q must have shape [batch, heads, head_dim]")
     B, G, D = q.shape
-    kinds = _dtypes((DTYPE_FP16, DTYPE_BF16))
-    if q.dtype not in kinds:
+    kind = q.dtype
+    if kind not in _OUT:
         raise ValueError("q must be fp16 or bf16")
-    for name, x, y in (("k and v", k, v), ("k_new and v_new", k_new, v_new), ("prefix_k and prefix_v", prefix_k, prefix_v)):
-        if (x is None) != (y is None):
-            raise ValueError(f"{name} go together")
+    if (k is None) != (v is None) or (k_new is None) != (v_new is None) or (prefix_k is None) != (prefix_v is None):
+        raise ValueError("k and v, k_new and v_new, prefix_k and prefix_v go together")
     if lens is not None and k is None or prefix_lens is not None and prefix_k is None:
         raise ValueError("lens goes with k and prefix_lens with prefix_k")
     if scale is not None and not scale > 0:
         raise ValueError("scale must be > 0")
-    check, kind = _Tensors(), q.dtype
     H, n, prefix = kv_heads, 0, 0
     if k is not None:
         if k.dim() != 4:
             raise ValueError("k must have shape [batch, kv_heads, rows, head_dim]")
-        H, n = int(k.shape[1]), int(k.shape[2])
+        _, H, n, _ = k.shape
     if prefix_k is not None:
         if prefix_k.dim() != 3:
             raise ValueError("prefix_k must have shape [kv_heads, rows, head_dim]")
-        H, prefix = H or int(prefix_k.shape[0]), int(prefix_k.shape[1])
-    if H is None and k_new is not None:
-        H = int(k_new.shape[1]) if k_new.dim() == 3 else -1
+        prefix = prefix_k.shape[1]
+        if H is None:
+            H = prefix_k.shape[0]
     if H is None:
-        raise ValueError("nothing to attend to: k, k_new or prefix_k must be given")
-    pq, sq = check("q", q, (B, G, D), kind)
-    po, so = check("out", out, (B, G, D), kind)
+        if k_new is None:
+            raise ValueError("nothing to attend to: k, k_new or prefix_k must be given")
+        if k_new.dim() != 3:
+            raise ValueError("k_new must have shape [batch, kv_heads, head_dim]")
+        H = k_new.shape[1]
+    device, s = _place(torch, q, stream)
     pk = pv = pkn = pvn = ppk = ppv = 0
     sk = sv = _NO3
     skn = svn = spk = spv = _NO2
+    pq, sq = _strided("q", q, (B, G, D), kind, device)
+    po, so = _strided("out", out, (B, G, D), kind, device)
     if n:
-        (pk, sk), (pv, sv) = check("k", k, (B, H, n, D), kind), check("v", v, (B, H, n, D), kind)
+        pk, sk = _strided("k", k, (B, H, n, D), kind, device)
+        pv, sv = _strided("v", v, (B, H, n, D), kind, device)
     if k_new is not None:
-        (pkn, skn), (pvn, svn) = check("k_new", k_new, (B, H, D), kind), check("v_new", v_new, (B, H, D), kind)
+        pkn, skn = _strided("k_new", k_new, (B, H, D), kind, device)
+        pvn, svn = _strided("v_new", v_new, (B, H, D), kind, device)
     if prefix:
-        ppk, spk = check("prefix_k", prefix_k, (H, prefix, D), kind)
-        ppv, spv = check("prefix_v", prefix_v, (H, prefix, D), kind)
-    int32, f32_ = _torch().int32, _torch().float32
-    pl = check("lens", lens, (B,), int32, contiguous=True)[0] if lens is not None else 0
-    ppl = check("prefix_lens", prefix_lens, (B,), int32, contiguous=True)[0] if prefix_lens is not None else 0
-    pe = check("lse", lse, (B, G), f32_, contiguous=True)[0] if lse is not None else 0
-    return bytearray(_ATTENTION.pack(kinds[kind], B, G, H, D, n, prefix, 0, scale or 0.0, 0, pq, po, pe, pk, pv, pl, pkn,
-                                     pvn, ppk, ppv, ppl, 0, *sq, *so, *sk, *sv, *skn, *svn, *spk, *spv, 0))
+        ppk, spk = _strided("prefix_k", prefix_k, (H, prefix, D), kind, device)
+        ppv, spv = _strided("prefix_v", prefix_v, (H, prefix, D), kind, device)
+    return _ATTENTION.pack(
+        _OUT[kind], B, G, H, D, n, prefix, 0, scale or 0.0, 0, pq, po, _dense("lse", lse, (B, G), torch.float32, device), pk, pv,
+        _dense("lens", lens, (B,), torch.int32, device), pkn, pvn, ppk, ppv,
+        _dense("prefix_lens", prefix_lens, (B,), torch.int32, device), 0, *sq, *so, *sk, *sv, *skn, *svn, *spk, *spv, 0), s
 
 
-def _torch():
-    import torch
-    return torch
+def _with_workspace(args, cache, device, stream):
+    """The same call with the workspace it needs, taken from torch's allocator for its stream, and that tensor."""
+    torch, need = _torch(), ctypes.c_size_t(0)
+    _check(lib().kvevict_attend_workspace(args, cache, ctypes.addressof(need)))
+    if need.value == 0:
+        return args, None
+    if stream == torch._C._cuda_getCurrentRawStream(device):
+        space = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream or 0)):
+            space = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    filled = bytearray(args)
+    struct.pack_into("=Q", filled, _WORKSPACE_AT, space.data_ptr())
+    struct.pack_into("=Q", filled, _WORKSPACE_BYTES_AT, need.value)
+    return bytes(filled), space
 
 
 def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_k=None, prefix_v=None,
@@ -277,8 +315,12 @@ def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_
     given. A sequence with no rows gets out 0 and lse -inf. Any layout with a contiguous last dimension and strides of
     whole 16-byte pieces. Errors: ValueError, KVEvictError.
     """
-    args = _attention_args(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale)
-    _check(lib().kvevict_attend((ctypes.c_char * len(args)).from_buffer(args), _stream(stream)))
+    args, s = _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream, None)
+    if prefix_k is not None:
+        args, space = _with_workspace(args, 0, q.get_device(), s)
+    rc = lib().kvevict_attend(args, s)
+    if rc:
+        _check(rc)
 
 
 def _ptr(t) -> int:
@@ -379,8 +421,11 @@ class KVEvict:
         ``read_state`` and ``read_values`` give them; the handle is not changed. A captured call keeps the row count
         of its capture.
         """
-        args = _attention_args(q, out, None, None, None, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, self.H)
-        _check(lib().kvevict_attend_cache(self._h, l, (ctypes.c_char * len(args)).from_buffer(args), _stream(stream)))
+        args, s = _attention(q, out, None, None, None, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream,
+                             self.H)
+        if prefix_k is not None:
+            args, space = _with_workspace(args, 1, q.get_device(), s)
+        _check(lib().kvevict_attend_cache(self._h, l, args, s))
 
     def run_host(self, prefill_keys, decode_keys, evicted=None, stream=None):
         """End to end from host memory (pinned tensors or numpy uint16 arrays)."""

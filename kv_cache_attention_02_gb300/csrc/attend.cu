@@ -209,7 +209,28 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
   a.P = d->prefix;
   const double scale = d->scale > 0.f ? (double)d->scale : 1.0 / std::sqrt((double)d->head_dim);
   a.scale2 = (float)(scale * 1.4426950408889634);
-  return cuda_result(launch_attend_rows(a, d->head_dim, d->dtype, dev.sms, s), "launch");
+  PrefixArgs p{};
+  p.plan = prefix_plan(a.B, a.G, a.H, d->head_dim, a.P, rows || a.n > 0 || a.k_new, dev.sms);
+  if (p.plan.ctas) {
+    if (d->workspace_bytes < p.plan.bytes(d->head_dim) || !d->workspace || !aligned(d->workspace))
+      return invalid("workspace must be 16-byte aligned and hold kvevict_attend_workspace bytes");
+    p.a = a;
+    p.part_o = static_cast<float*>(d->workspace);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(d->workspace) + p.plan.o_bytes(d->head_dim));
+    p.err = rows ? rows->err : nullptr;
+    p.stall = take_scorer_stall() ? 1 : 0;
+    const cudaError_t e = launch_attend_prefix(p, d->head_dim, d->dtype, s);
+    if (e == cudaSuccess) {
+      if (p.plan.final) return KVEVICT_OK;
+      a.P = 0;             // joined from its parts
+      a.plens = nullptr;
+    } else if (e == cudaErrorNotSupported) {
+      p.plan.ctas = 0;     // strides that TMA cannot take: the row kernel reads the prefix itself
+    } else {
+      return cuda_result(e, "launch");
+    }
+  }
+  return cuda_result(launch_attend_rows(a, p.parts(), d->head_dim, d->dtype, dev.sms, s), "launch");
 }
 
 }  // namespace kvx
@@ -239,11 +260,17 @@ extern "C" int kvevict_attend(const kvevict_attention* args, void* stream) {
   return entry(__func__, [&] { return kvx::attend_run(args, nullptr, (cudaStream_t)stream); });
 }
 
-extern "C" int kvevict_attend_workspace(const kvevict_attention* args, size_t* bytes) {
+extern "C" int kvevict_attend_workspace(const kvevict_attention* args, int32_t with_cache, size_t* bytes) {
   return entry(__func__, [&] {
     if (!bytes) return kvx::invalid("bytes must not be null");
     if (int rc = kvx::attend_check(args)) return rc;
     *bytes = 0;
+    if (args->batch == 0 || args->prefix == 0) return KVEVICT_OK;
+    kvx::DeviceInfo dev;
+    if (int rc = kvx::device_info(&dev)) return rc;
+    const bool own = with_cache || args->n > 0 || args->k_new;
+    *bytes = kvx::prefix_plan(args->batch, args->n_heads, args->n_kv_heads, args->head_dim, args->prefix, own, dev.sms)
+                 .bytes(args->head_dim);
     return KVEVICT_OK;
   });
 }

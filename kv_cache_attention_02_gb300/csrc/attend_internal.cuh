@@ -54,6 +54,44 @@ struct AttendArgs {
   float scale2;            // scale * log2(e): logits in base-2 units
 };
 
+// How the prefix kernel's work is cut: (key head, query block, 128-key tile)
+// triples in that order, one contiguous range per CTA. ctas = 0: not used.
+struct PrefixPlan {
+  int ctas, pair, blocks, block_rows, nkt, units, final;   // units = H * blocks; final: no own rows to join
+  __host__ __device__ int64_t total() const { return (int64_t)units * nkt; }
+  __host__ __device__ int64_t start(int c) const { return c * total() / ctas; }
+  __host__ __device__ int cta_of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total()); }
+  // Workspace slot of the part of block u that CTA c computed. Where whole
+  // blocks go straight to the output, a CTA leaves at most two parts: one that
+  // begins inside a block and one that begins with it.
+  __host__ __device__ int64_t slot(int u, int c, bool from_start) const { return final ? 2 * c + from_start : u + c; }
+  int64_t slots() const { return final ? 2 * (int64_t)ctas : (int64_t)units + ctas; }
+  size_t o_bytes(int D) const;
+  size_t bytes(int D) const;
+  bool shared_blocks() const;   // whether any block is cut
+};
+PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int sms);
+
+// The parts of the prefix's attention in the workspace: per slot O as
+// [D/4][block_rows] float4 and (m, l) as [block_rows] float2, base-2 units.
+struct PrefixParts {
+  PrefixPlan plan;
+  const float* o;
+  const float2* ml;
+};
+
+struct PrefixArgs {
+  AttendArgs a;
+  PrefixPlan plan;
+  float* part_o;
+  float2* part_ml;
+  int* err;                // error word for bounded waits, or null
+  int stall;               // test hook: CTA 0's first tile is never issued
+  bool k_row_first, v_row_first;
+  __host__ __device__ PrefixParts parts() const { return PrefixParts{plan, part_o, part_ml}; }
+};
+cudaError_t launch_attend_prefix(const PrefixArgs& p, int D, int dtype, cudaStream_t s);   // NotSupported: no tensor map
+
 // What a launch needs to know of the current device, looked up once.
 struct DeviceInfo {
   int sms = 0;
@@ -62,7 +100,8 @@ int device_info(DeviceInfo* out);   // KVEVICT_* code; sets the last error
 void set_last_error(const std::string& msg);
 
 cudaError_t launch_qk_norm_rope(QkArgs a, int D, int in_dtype, int out_dtype, int sms, cudaStream_t s);
-cudaError_t launch_attend_rows(const AttendArgs& a, int D, int dtype, int sms, cudaStream_t s);
+// parts.plan.ctas > 0: joins the prefix's parts too (a.P is 0 then).
+cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, int D, int dtype, int sms, cudaStream_t s);
 
 // Checks the caller's description and fills the kernel's; own rows come from
 // `rows` (a handle's layer) where that is not null.
@@ -75,6 +114,7 @@ struct CacheRows {
   const float* rope_c;
   const float* rope_s;
   int batch, n_kv_heads, head_dim;
+  int* err;                // the handle's error word
 };
 int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s);
 
@@ -116,6 +156,37 @@ __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Adds the prefix's parts of query row r (b * N + j) of key head h, columns
+// 4 d4 .. + 3, to the sums (m, l, o), in the CTAs' order. A part with l = 0 has
+// no rows; a NaN l passes on.
+template <int D>
+__device__ __forceinline__ void join_parts(const PrefixParts& p, int h, int64_t r, int d4, float& m, float& l, float4& o) {
+  const int R = p.plan.block_rows;
+  const int blk = (int)(r / R), rr = (int)(r - (int64_t)blk * R), u = h * p.plan.blocks + blk;
+  const int c0 = p.plan.cta_of((int64_t)u * p.plan.nkt), c1 = p.plan.cta_of((int64_t)(u + 1) * p.plan.nkt - 1);
+  float mm = m;
+  for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, p.ml[p.plan.slot(u, c, c == c0) * R + rr].x);
+  const float f = m == mm ? 1.f : ex2_approx(m - mm);
+  l *= f;
+  o.x *= f;
+  o.y *= f;
+  o.z *= f;
+  o.w *= f;
+  for (int c = c0; c <= c1; ++c) {
+    const int64_t slot = p.plan.slot(u, c, c == c0);
+    const float2 ml = p.ml[slot * R + rr];
+    if (ml.y == 0.f) continue;
+    const float g = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
+    const float4 v = reinterpret_cast<const float4*>(p.o)[slot * (R * (D / 4)) + (int64_t)d4 * R + rr];
+    l = fmaf(g, ml.y, l);
+    o.x = fmaf(g, v.x, o.x);
+    o.y = fmaf(g, v.y, o.y);
+    o.z = fmaf(g, v.z, o.z);
+    o.w = fmaf(g, v.w, o.w);
+  }
+  m = mm;
 }
 
 }  // namespace kvx

@@ -1,0 +1,669 @@
+// attend_prefix.cu -- attention of many query rows over rows that all
+// sequences share, on the 5th-generation tensor cores: the prefix's part of
+// kvevict_attend, its keys and values read once for the whole batch.
+//
+// For one key head the queries of all sequences and of its N = G / H query
+// heads are the rows of one matrix Q [B*N, D], row b*N + j:
+//   S = Q K^T * scale,  P = e^(S - m),  O = P V,  l = sum P,
+// with the running maximum m and sum l of each row in fp32. P is rounded to
+// the inputs' 16-bit type for the second product and l is summed before that
+// rounding, so the roundings average out; with few rows (see PAIR) it goes in
+// as the sum of two 16-bit parts, as in attend_rows.cu. m follows the true
+// maximum only when it would be exceeded by more than 2^8, which P and l carry
+// without loss: most tiles then need no rescaling of O.
+//
+// Work: the (key head, block of query rows, 128-key tile) triples, in that
+// order, are cut into one contiguous range per CTA (one CTA an SM, which holds
+// all of the tensor memory), whatever the sizes: a block's tiles may end in one
+// CTA and begin in another. A range's piece of a block leaves its unnormalised
+// O, m and l in the workspace, where the join (attend_rows.cu or the kernel
+// below) finds them in a fixed order; a block that is one CTA's alone is written
+// out directly where nothing else has to join it.
+//
+// Two streams of 128 query rows share a CTA, each with its own accumulators S
+// and O (four times 128 TMEM columns), so that one stream's softmax runs while
+// the tensor cores work for the other:
+//   TILES  (more than 128 query rows a key head) the streams are two row blocks
+//          and both use every key and value tile;
+//   PAIR   (at most 128 rows, bound by memory) both are the same rows, and the
+//          streams take even and odd tiles.
+// Roles in a 384-thread CTA:
+//   warp 0      one thread issues TMA loads of key and value tiles (128 rows,
+//               128-byte swizzle) into one ring, in the order they are used;
+//   warp 1      issues tcgen05.mma: S = Q K^T from shared memory, then O += P V
+//               with P from TMEM and V as it lies in memory (its rows are the
+//               contraction: an MN-major operand);
+//   warps 4..11 two softmax warpgroups, one per stream, a query row a thread:
+//               tcgen05.ld S, mask, maximum, exp2, sum, P back into S's columns.
+// A stream's tcgen05.commit after S also covers the P V before it, so a thread
+// that has seen S may rescale O without another wait.
+// Every mbarrier wait is bounded; on expiry the CTA leaves NaN in its rows.
+#include "attend_internal.cuh"
+#include "tcgen05.cuh"
+
+namespace kvx {
+namespace {
+
+constexpr int kT = 128;                // query rows of a stream, keys of a tile
+constexpr int kPxThreads = 384;
+constexpr int kPxTmem = 512;
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLazy = 8.f;           // log2 of how far a weight may exceed 1
+
+template <int D>
+struct PxGeo {
+  static constexpr int KH = D / 64;              // 128-byte halves of a row
+  static constexpr int HALFB = kT * 128;         // one half tile, 16 KB
+  static constexpr int TILEB = KH * HALFB;
+  static constexpr int STAGES = 160 * 1024 / TILEB;
+  static constexpr int Q = 0, RING = 2 * TILEB, BARS = RING + STAGES * TILEB;
+  static constexpr int ML = TILEB;   // PAIR: the streams' maxima and sums, where TILES has its second query block
+  static constexpr int SMEM = BARS + (2 * STAGES + 8) * 8 + 16 + 1024;   // slack to align to 1024 bytes
+};
+
+// Instruction descriptors, kind::f16, f32 accumulator, M = 128: bits 7 and 10
+// the inputs' type (1: bf16), 16 B is MN-major, 17.. N / 8, 24.. M / 16.
+template <typename T>
+__host__ __device__ constexpr uint32_t px_idesc(int n, bool b_mn_major) {
+  return (1u << 4) | (std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10)) | (b_mn_major ? 1u << 16 : 0u) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kT >> 4) << 24);
+}
+
+// MN-major operand, 128-byte swizzle: 64 consecutive columns are 128 bytes,
+// 8 rows of the contraction 1024 bytes apart (stride byte offset), the next 64
+// columns one half tile on (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t half_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(half_bytes >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One CTA's walk over its range of (block, tile) pairs, the same in every role.
+struct Walk {
+  int64_t x, end;
+  int nkt;
+  __device__ __forceinline__ Walk(const PrefixArgs& p, int cta)
+      : x(p.plan.start(cta)), end(p.plan.start(cta + 1)), nkt(p.plan.nkt) {}
+  // Next segment: tiles k0 .. k1 - 1 of block u; false at the end.
+  __device__ __forceinline__ bool next(int& u, int& k0, int& k1) {
+    if (x >= end) return false;
+    u = (int)(x / nkt);
+    k0 = (int)(x - (int64_t)u * nkt);
+    k1 = (int)min((int64_t)nkt, k0 + (end - x));
+    x += k1 - k0;
+    return true;
+  }
+};
+
+// Rows of the prefix that some query row of block u has (warp-collective).
+__device__ __forceinline__ int block_limit(const PrefixArgs& p, int u) {
+  if (!p.a.plens) return p.a.P;
+  const int N = p.a.G / p.a.H;
+  const int64_t r0 = (int64_t)(u % p.plan.blocks) * p.plan.block_rows;
+  const int b0 = (int)(r0 / N);
+  const int b1 = (int)min((int64_t)p.a.B - 1, (r0 + p.plan.block_rows - 1) / N);
+  int lim = 0;
+  for (int b = b0 + (int)(threadIdx.x & 31); b <= b1; b += 32) lim = max(lim, p.a.plens[b]);
+  return min((int)__reduce_max_sync(~0u, lim), p.a.P);
+}
+
+template <typename T, int D, bool PAIR>
+__global__ void __launch_bounds__(kPxThreads, 1)
+    attend_prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                         const __grid_constant__ PrefixArgs p) {
+  using Gm = PxGeo<D>;
+  constexpr int NS = Gm::STAGES;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* smem = smem_raw + (base - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Gm::BARS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Gm::BARS + (2 * NS + 8) * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto full = [&](int s) { return smem_addr(&bars[s]); };
+  auto empty = [&](int s) { return smem_addr(&bars[NS + s]); };
+  auto s_full = [&](int w) { return smem_addr(&bars[2 * NS + w]); };
+  auto p_full = [&](int w) { return smem_addr(&bars[2 * NS + 2 + w]); };
+  auto o_done = [&](int w) { return smem_addr(&bars[2 * NS + 4 + w]); };
+  const uint32_t q_full = smem_addr(&bars[2 * NS + 6]);
+  const uint32_t drain = smem_addr(&bars[2 * NS + 7]);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const AttendArgs& a = p.a;
+  const int N = a.G / a.H;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(s_full(w), 1);
+      mbar_init(p_full(w), 4);
+      mbar_init(o_done(w), 1);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(drain, 1);               // abort path only
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kPxTmem);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // TMEM columns: O of stream w at 128 w, S (and P over it) at 256 + 128 w
+  auto tm_o = [&](int w) { return tmem + (uint32_t)(kT * w); };
+  auto tm_s = [&](int w) { return tmem + (uint32_t)(2 * kT + kT * w); };
+
+  Walk walk(p, blockIdx.x);
+  int u, k0, k1;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    int64_t issued = 0;
+    bool ok = true;
+    while (ok && walk.next(u, k0, k1)) {
+      const int n = min(k1, (block_limit(p, u) + kT - 1) / kT) - k0;
+      const int h = u / p.plan.blocks;
+      if (lane == 0) {
+        auto load = [&](const CUtensorMap* map, bool row_first, int kt) {
+          const int s = (int)(issued % NS);
+          if (issued >= NS && !wait_or_abort(empty(s), (uint32_t)((issued / NS - 1) & 1), abort_flag, p.err)) return false;
+          if (!(p.stall && blockIdx.x == 0 && issued == 0)) {   // test hook: CTA 0's first tile never comes
+            mbar_expect_tx(full(s), Gm::TILEB);
+            const int row = (k0 + kt) * kT;
+            for (int kh = 0; kh < Gm::KH; ++kh)
+              tma_load_3d(base + Gm::RING + s * Gm::TILEB + kh * Gm::HALFB, map, kh * 64, row_first ? row : h,
+                          row_first ? h : row, full(s));
+          }
+          ++issued;
+          return true;
+        };
+        for (int i = 0; i < n && ok; ++i) {
+          if (i == 0) {
+            ok = load(&kmap, p.k_row_first, 0);
+            if (PAIR && ok && n > 1) ok = load(&kmap, p.k_row_first, 1);
+          }
+          ok = ok && load(&vmap, p.v_row_first, i);
+          const int nk = PAIR ? i + 2 : i + 1;
+          if (ok && nk < n) ok = load(&kmap, p.k_row_first, nk);
+        }
+      }
+      ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+    }
+    if (lane == 0 && *abort_flag)      // let copies in flight land before the CTA leaves
+      for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
+        (void)mbar_wait_bounded(full((int)(i % NS)), (uint32_t)((i / NS) & 1), 10000000ull);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    constexpr uint32_t kIdS = px_idesc<T>(kT, false), kIdO = px_idesc<T>(D, true);
+    int64_t used = 0;
+    uint32_t np[2] = {0, 0};           // weights tiles consumed, per stream
+    int seg = 0;                       // segments that have tiles
+    bool ok = true;
+    while (ok && walk.next(u, k0, k1)) {
+      const int limit = block_limit(p, u);
+      const int n = min(k1, (limit + kT - 1) / kT) - k0;
+      if (n <= 0) continue;
+      ok = __all_sync(~0u, wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag, p.err));
+      ++seg;
+      if (!ok) break;
+      tc_fence_after();
+      auto tile = [&]() -> int {       // the next ring stage, once its tile is there; -1 on abort
+        const int s = (int)(used % NS);
+        const bool here = wait_or_abort(full(s), (uint32_t)((used / NS) & 1), abort_flag, p.err);
+        ++used;
+        return __all_sync(~0u, here) ? s : -1;
+      };
+      auto mma_s = [&](int w, int s) {
+        if (lane == 0) {
+          const uint32_t qa = base + Gm::Q + (PAIR ? 0 : w) * Gm::TILEB, kb = base + Gm::RING + s * Gm::TILEB;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (uint32_t)((kk >> 2) * Gm::HALFB + (kk & 3) * 32);
+            tc_mma_ss(tm_s(w), sw128_desc(qa + off), sw128_desc(kb + off), kIdS, kk > 0);
+          }
+          tc_commit(s_full(w));
+        }
+      };
+      auto release = [&](int s) {
+        if (lane == 0) tc_commit(empty(s));
+      };
+      // O_w += P_w V: P of keys 0..63 in S's columns 0..31, of keys 64..127 in
+      // 64..95, the second parts (PAIR) 32 columns on
+      auto mma_o = [&](int w, int s, bool first) {
+        if (!__all_sync(~0u, wait_or_abort(p_full(w), np[w] & 1, abort_flag, p.err))) return false;
+        ++np[w];
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t vb = base + Gm::RING + s * Gm::TILEB;
+#pragma unroll
+          for (int part = 0; part < (PAIR ? 2 : 1); ++part)
+#pragma unroll
+            for (int kk = 0; kk < kT / 16; ++kk)
+              tc_mma_ts(tm_o(w), tm_s(w) + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8 + 32 * part),
+                        sw128_mn_desc(vb + kk * 2048, Gm::HALFB), kIdO, !(first && kk == 0 && part == 0));
+        }
+        return true;
+      };
+      // A value tile that reaches past the block's rows: what lies there may be
+      // anything, and 0 * NaN would spoil the sums, so it becomes zeros.
+      auto clean = [&](int s, int kt) {
+        const int from = limit - kt * kT;
+        if (from >= kT || limit == a.P) return;      // TMA has filled rows past P with zeros
+        for (int x = lane; x < (kT - from) * (D / 8); x += 32) {
+          const int row = from + x / (D / 8), c = x % (D / 8);
+          *reinterpret_cast<uint4*>(smem + Gm::RING + s * Gm::TILEB + (c >> 3) * Gm::HALFB + row * 128 + (c & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      };
+      int s;
+      if (PAIR) {
+        for (int i = 0; i < min(n, 2) && ok; ++i) {
+          ok = (s = tile()) >= 0;
+          if (ok) mma_s(i, s), release(s);
+        }
+        for (int i = 0; i < n && ok; ++i) {
+          const int w = i & 1;
+          if (!(ok = (s = tile()) >= 0)) break;
+          clean(s, k0 + i);
+          if (!(ok = mma_o(w, s, i < 2))) break;
+          release(s);
+          if (i + 2 >= n && lane == 0) tc_commit(o_done(w));
+          if (i + 2 < n) {
+            if (!(ok = (s = tile()) >= 0)) break;
+            mma_s(w, s);
+            release(s);
+          }
+        }
+      } else {
+        ok = (s = tile()) >= 0;
+        if (ok) mma_s(0, s), mma_s(1, s), release(s);
+        for (int i = 0; i < n && ok; ++i) {
+          const bool more = i + 1 < n;
+          int sk = 0;
+          if (!(ok = (s = tile()) >= 0)) break;
+          clean(s, k0 + i);
+          if (!(ok = mma_o(0, s, i == 0))) break;
+          if (more) {
+            if (!(ok = (sk = tile()) >= 0)) break;
+            mma_s(0, sk);
+          } else if (lane == 0) {
+            tc_commit(o_done(0));
+          }
+          if (!(ok = mma_o(1, s, i == 0))) break;
+          release(s);
+          if (more) {
+            mma_s(1, sk);
+            release(sk);
+          } else if (lane == 0) {
+            tc_commit(o_done(1));
+          }
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax warpgroups
+    const int w = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;          // query row of the stream = TMEM lane
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t ns = 0, no = 0;                         // logits tiles and finished outputs seen
+    while (walk.next(u, k0, k1)) {
+      const int limit = block_limit(p, u);
+      const int n = max(0, min(k1, (limit + kT - 1) / kT) - k0);
+      const int h = u / p.plan.blocks;
+      const int64_t r = (int64_t)(u % p.plan.blocks) * p.plan.block_rows + (PAIR ? 0 : w * kT) + row;
+      const bool valid = r < (int64_t)a.B * N;
+      const int b = valid ? (int)(r / N) : 0, head = h * N + (valid ? (int)(r - (int64_t)b * N) : 0);
+      const int rows = valid && a.plens ? max(0, min(a.plens[b], a.P)) : a.P;
+      if (n > 0) {
+        // the queries into shared memory as TMA would swizzle them; PAIR: each
+        // warpgroup brings half of every row
+        const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0] + (int64_t)head * a.q_stride[1];
+        unsigned char* dst = smem + Gm::Q + (PAIR ? 0 : w) * Gm::TILEB + row * 128;
+        constexpr int CH = PAIR ? D / 16 : D / 8;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int c = (PAIR ? w * CH : 0) + i;
+          const uint4 v = valid ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * Gm::HALFB + (((c ^ row) & 7) << 4)) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      float m = kNegInf, l = 0.f;
+      bool ok = true, begun = false;
+      const uint32_t ts = tm_s(w) + lanes, to = tm_o(w) + lanes;
+      for (int i = PAIR ? w : 0; i < n; i += PAIR ? 2 : 1) {
+        ok = __all_sync(~0u, wait_or_abort(s_full(w), ns & 1, abort_flag, p.err));
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        const int left = rows - (k0 + i) * kT;       // columns from here on are masked
+        const bool whole = __all_sync(~0u, left >= kT);
+        float m8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m8[e] = kNegInf;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          float v[64];
+          tmem_ld64(ts + 64 * c, v);
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) v[e] = 64 * c + e < left ? v[e] : kNegInf;
+          }
+#pragma unroll
+          for (int e = 0; e < 64; ++e) m8[e & 7] = fmaxf(m8[e & 7], v[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m8[e] = fmaxf(m8[e], m8[e + 4]);
+        const float mx = fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])) * a.scale2;
+        const bool up = mx > m + kLazy;
+        if (__any_sync(~0u, up)) {
+          const float nm = up ? mx : m, f = nm == m ? 1.f : ex2(m - nm);
+          m = nm;
+          l *= f;
+          if (begun) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float v[32];
+              uint32_t o[32];
+              tmem_ld32(to + 32 * c, v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(v[e] * f);
+              tmem_st32(to + 32 * c, o);
+            }
+          }
+        }
+        begun = true;
+        const float nb = m == kNegInf ? 0.f : -m;    // nothing so far: every weight 2^-inf = 0
+        const float2 sc2 = make_float2(a.scale2, a.scale2), nb2 = make_float2(nb, nb);
+        float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          float v[64];
+          tmem_ld64(ts + 64 * c, v);
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) v[e] = 64 * c + e < left ? v[e] : kNegInf;
+          }
+          uint32_t hi[32], lo[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float2 t0 = ffma2(make_float2(v[e], v[e + 1]), sc2, nb2);
+            const float2 t1 = ffma2(make_float2(v[e + 2], v[e + 3]), sc2, nb2);
+            const float2 p0 = make_float2(ex2(t0.x), ex2(t0.y)), p1 = make_float2(ex2(t1.x), ex2(t1.y));
+            l0 = fadd2(l0, p0);
+            l1 = fadd2(l1, p1);
+            hi[e / 2] = pack16<T>(p0.x, p0.y);
+            hi[e / 2 + 1] = pack16<T>(p1.x, p1.y);
+            if (PAIR) {
+              const float2 b0 = unpack16<T>(hi[e / 2]), b1 = unpack16<T>(hi[e / 2 + 1]);
+              lo[e / 2] = pack16<T>(p0.x - b0.x, p0.y - b0.y);
+              lo[e / 2 + 1] = pack16<T>(p1.x - b1.x, p1.y - b1.y);
+            }
+          }
+          tmem_st32(ts + 64 * c, hi);
+          if (PAIR) tmem_st32(ts + 64 * c + 32, lo);
+        }
+        l += (l0.x + l0.y) + (l1.x + l1.y);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(w));
+      }
+      if (begun && ok) {
+        ok = __all_sync(~0u, wait_or_abort(o_done(w), no & 1, abort_flag, p.err));
+        ++no;
+        tc_fence_after();
+      }
+      if (!ok) l = __int_as_float(0x7FFFFFFF);       // NaN: this row's result is lost
+      float f0 = 1.f, f1 = 0.f;
+      if (PAIR) {
+        // the two streams' maxima and sums meet in shared memory, their O in the
+        // registers of whichever warpgroup writes the columns: a warp of either
+        // reaches the same TMEM lanes
+        float2* ml = reinterpret_cast<float2*>(smem + Gm::ML);
+        ml[w * kT + row] = make_float2(m, l);
+        tc_fence_before();
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        tc_fence_after();
+        const float2 x = ml[row], y = ml[kT + row];
+        m = fmaxf(x.x, y.x);
+        f0 = x.x == m ? 1.f : ex2(x.x - m);
+        f1 = y.x == m ? 1.f : ex2(y.x - m);
+        l = x.y * f0 + y.y * f1;
+      }
+      auto columns = [&](int c, float* v) {          // O's columns 32 c .. + 31 of this row
+        const uint32_t at = tmem + lanes + 32 * c;
+        if (n == 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        } else if (!PAIR) {
+          tmem_ld32(at + kT * w, v);
+        } else {
+          tmem_ld32(at, v);
+          if (n > 1) {
+            float y[32];
+            tmem_ld32(at + kT, y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(y[e], f1, v[e] * f0);
+          }
+        }
+      };
+      constexpr int CC = PAIR ? D / 64 : D / 32;
+      // a block of this CTA alone goes to the output, any other to the workspace
+      if (p.plan.final && k0 == 0 && k1 == p.plan.nkt) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)head * a.out_stride[1];
+#pragma unroll 1
+        for (int i = 0; i < CC; ++i) {
+          const int c = (PAIR ? w * CC : 0) + i;
+          float v[32];
+          columns(c, v);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[x] = pack16<T>(v[e + 2 * x] * inv, v[e + 2 * x + 1] * inv);
+            if (valid) *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        if (valid && a.lse && !(PAIR && w))
+          a.lse[(int64_t)b * a.G + head] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+      } else {
+        const int64_t slot = p.plan.slot(u, blockIdx.x, k0 == 0);
+        const int R = p.plan.block_rows, rr = (PAIR ? 0 : w * kT) + row;
+        float4* o = reinterpret_cast<float4*>(p.part_o) + slot * (R * (D / 4)) + rr;
+#pragma unroll 1
+        for (int i = 0; i < CC; ++i) {
+          const int c = (PAIR ? w * CC : 0) + i;
+          float v[32];
+          columns(c, v);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) o[(int64_t)(8 * c + e / 4) * R] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+        if (!(PAIR && w)) p.part_ml[slot * R + rr] = make_float2(m, l);
+      }
+      tc_fence_before();
+      // both warpgroups are through with this block's queries and accumulators
+      uint32_t stop;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.u32 p, %1, 0;\n\t"
+          "bar.red.or.pred q, 3, 256, p;\n\t"
+          "selp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(stop)
+          : "r"((uint32_t)(!ok || *abort_flag))
+          : "memory");
+      if (stop) {
+        // the blocks this CTA will not come to: NaN as well
+        while (walk.next(u, k0, k1)) {
+          const int rr = (PAIR ? 0 : w * kT) + row;
+          const int64_t r2 = (int64_t)(u % p.plan.blocks) * p.plan.block_rows + rr;
+          if (!(p.plan.final && k0 == 0 && k1 == p.plan.nkt)) {
+            p.part_ml[p.plan.slot(u, blockIdx.x, k0 == 0) * p.plan.block_rows + rr] =
+                make_float2(0.f, __int_as_float(0x7FFFFFFF));
+          } else if (r2 < (int64_t)a.B * N) {
+            const int b2 = (int)(r2 / N), h2 = (u / p.plan.blocks) * N + (int)(r2 - (int64_t)b2 * N);
+            T* dst = static_cast<T*>(a.out) + b2 * a.out_stride[0] + (int64_t)h2 * a.out_stride[1];
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+            if (a.lse) a.lse[(int64_t)b2 * a.G + h2] = __int_as_float(0x7FFFFFFF);
+          }
+        }
+        break;
+      }
+    }
+  }
+
+  // -------------------------------------------------------------------- teardown
+  __syncthreads();
+  if (*abort_flag && tid == 32) {
+    // let any MMA still in flight finish before the accumulators are freed
+    tc_commit(drain);
+    (void)mbar_wait_bounded(drain, 0, 10000000ull);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kPxTmem);
+  }
+}
+
+// Joins the parts of blocks that several CTAs share, where the prefix is all
+// there is. One grid column per boundary between CTAs; the first boundary
+// inside a block takes it, in gridDim.y shares of its elements.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ PrefixArgs p) {
+  const PrefixPlan& pl = p.plan;
+  const AttendArgs& a = p.a;
+  const int64_t x = pl.start(blockIdx.x + 1);
+  const int u = (int)(x / pl.nkt);
+  const int64_t u0 = (int64_t)u * pl.nkt;
+  if (x == u0 || pl.start(blockIdx.x) > u0) return;
+  const int N = a.G / a.H, R = pl.block_rows, h = u / pl.blocks;
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < R * (D / 4); i += gridDim.y * 256) {
+    const int rr = i % R, d4 = i / R;
+    const int64_t r = (int64_t)(u % pl.blocks) * R + rr;
+    if (r >= (int64_t)a.B * N) continue;
+    float m = kNegInf, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    join_parts<D>(p.parts(), h, r, d4, m, l, o);
+    const int b = (int)(r / N), head = h * N + (int)(r - (int64_t)b * N);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)head * a.out_stride[1] + 4 * d4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * inv, o.y * inv), pack16<T>(o.z * inv, o.w * inv));
+    if (d4 == 0 && a.lse) a.lse[(int64_t)b * a.G + head] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+template <typename T, int D, bool PAIR>
+cudaError_t launch_px(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefixArgs& p, cudaStream_t s) {
+  auto kernel = attend_prefix_kernel<T, D, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PxGeo<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  kernel<<<p.plan.ctas, kPxThreads, PxGeo<D>::SMEM, s>>>(kmap, vmap, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !p.plan.final || !p.plan.shared_blocks()) return e;
+  attend_join_kernel<T, D><<<dim3(p.plan.ctas - 1, p.plan.block_rows / 16), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Shared rows [H, P, D] as a 3-D tensor, the dimension of the smaller stride
+// first (a dimension of one has no stride of its own); boxes of 64 elements
+// (128 bytes) x 128 rows; rows past P read as zeros.
+bool encode_rows(CUtensorMap* map, const void* base, const int64_t* stride, int H, int P, int D, int dtype,
+                 bool* row_first) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  int64_t hs = stride[0], rs = stride[1];
+  if (P == 1) rs = D;
+  if (H == 1) hs = (int64_t)P * rs;
+  if (hs < D || rs < D) return false;      // broadcast or overlapping rows
+  *row_first = rs <= hs;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)(*row_first ? P : H), (cuuint64_t)(*row_first ? H : P)};
+  const cuuint64_t strides[2] = {(cuuint64_t)(*row_first ? rs : hs) * 2, (cuuint64_t)(*row_first ? hs : rs) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(*row_first ? kT : 1), (cuuint32_t)(*row_first ? 1 : kT)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int sms) {
+  PrefixPlan pl{};
+  const int64_t rows = (int64_t)B * (G / H);
+  if (B < 2 || rows < 16 || P < 256) return pl;   // ctas = 0: the row kernel reads the prefix itself
+  pl.pair = rows <= kT;
+  pl.block_rows = pl.pair ? kT : 2 * kT;
+  pl.blocks = (int)((rows + pl.block_rows - 1) / pl.block_rows);
+  pl.nkt = (P + kT - 1) / kT;
+  pl.units = H * pl.blocks;
+  pl.final = !own;
+  const int64_t total = pl.total();
+  pl.ctas = (int)std::min<int64_t>(sms, pl.pair ? (total + 1) / 2 : total);
+  return pl;
+}
+
+size_t PrefixPlan::o_bytes(int D) const { return (size_t)slots() * block_rows * D * 4; }
+size_t PrefixPlan::bytes(int D) const { return ctas ? o_bytes(D) + (size_t)slots() * block_rows * 8 : 0; }
+bool PrefixPlan::shared_blocks() const {
+  for (int c = 1; c < ctas; ++c)
+    if (start(c) % nkt) return true;
+  return false;
+}
+
+cudaError_t launch_attend_prefix(const PrefixArgs& args, int D, int dtype, cudaStream_t s) {
+  PrefixArgs p = args;
+  CUtensorMap kmap, vmap;
+  if (!encode_rows(&kmap, p.a.pk, p.a.pk_stride, p.a.H, p.a.P, D, dtype, &p.k_row_first) ||
+      !encode_rows(&vmap, p.a.pv, p.a.pv_stride, p.a.H, p.a.P, D, dtype, &p.v_row_first))
+    return cudaErrorNotSupported;
+  if (dtype == kBf16) {
+    if (D == 64)
+      return p.plan.pair ? launch_px<__nv_bfloat16, 64, true>(kmap, vmap, p, s)
+                         : launch_px<__nv_bfloat16, 64, false>(kmap, vmap, p, s);
+    return p.plan.pair ? launch_px<__nv_bfloat16, 128, true>(kmap, vmap, p, s)
+                       : launch_px<__nv_bfloat16, 128, false>(kmap, vmap, p, s);
+  }
+  if (D == 64)
+    return p.plan.pair ? launch_px<__half, 64, true>(kmap, vmap, p, s) : launch_px<__half, 64, false>(kmap, vmap, p, s);
+  return p.plan.pair ? launch_px<__half, 128, true>(kmap, vmap, p, s) : launch_px<__half, 128, false>(kmap, vmap, p, s);
+}
+
+}  // namespace kvx

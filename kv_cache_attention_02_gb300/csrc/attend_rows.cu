@@ -125,7 +125,8 @@ __device__ __forceinline__ void rotate_back(uint4& lo, uint4& hi, const float* r
 
 // QT: groups of 8 query heads (1 or 2).
 template <typename T, int D, int QT, bool PEND>
-__global__ void __launch_bounds__(kThreads) attend_rows_kernel(const AttendArgs a, const int qchunks) {
+__global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_constant__ AttendArgs a,
+                                                                  const __grid_constant__ PrefixParts parts, const int qchunks) {
   using R = Rows<T, D>;
   constexpr int KC = R::KC, VH = R::VH, QN = 8 * QT;
   __shared__ __align__(16) float part_o[kWarps][QN][D];
@@ -371,6 +372,7 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const AttendArgs 
       o.w = fmaf(f, v.w, o.w);
       ll = fmaf(f, *cluster.map_shared_rank(&cta_ml[q][1], r), ll);
     }
+    if (parts.plan.ctas) join_parts<D>(parts, h, (int64_t)b * N + q0 + q, d / 4, mm, ll, o);
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const int gq = h * N + q0 + q;
     T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)gq * a.out_stride[1] + d;
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const AttendArgs 
 }
 
 template <typename T, int D, int QT, bool PEND>
-cudaError_t launch_one(const AttendArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_one(const AttendArgs& a, const PrefixParts& parts, int sms, cudaStream_t s) {
   const int N = a.G / a.H;
   const int qchunks = (N + 8 * QT - 1) / (8 * QT);
   const int64_t units = (int64_t)a.B * a.H * qchunks;
@@ -407,22 +409,22 @@ cudaError_t launch_one(const AttendArgs& a, int sms, cudaStream_t s) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, qchunks);
+  return cudaLaunchKernelEx(&cfg, kernel, a, parts, qchunks);
 }
 
 template <typename T, int D, bool PEND>
-cudaError_t launch_q(const AttendArgs& a, int sms, cudaStream_t s) {
-  return a.G / a.H <= 8 ? launch_one<T, D, 1, PEND>(a, sms, s) : launch_one<T, D, 2, PEND>(a, sms, s);
+cudaError_t launch_q(const AttendArgs& a, const PrefixParts& parts, int sms, cudaStream_t s) {
+  return a.G / a.H <= 8 ? launch_one<T, D, 1, PEND>(a, parts, sms, s) : launch_one<T, D, 2, PEND>(a, parts, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_rows(const AttendArgs& a, int D, int dtype, int sms, cudaStream_t s) {
+cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, int D, int dtype, int sms, cudaStream_t s) {
   if (a.pend)   // a handle's rows are fp16
-    return D == 64 ? launch_q<__half, 64, true>(a, sms, s) : launch_q<__half, 128, true>(a, sms, s);
+    return D == 64 ? launch_q<__half, 64, true>(a, parts, sms, s) : launch_q<__half, 128, true>(a, parts, sms, s);
   if (dtype == kBf16)
-    return D == 64 ? launch_q<__nv_bfloat16, 64, false>(a, sms, s) : launch_q<__nv_bfloat16, 128, false>(a, sms, s);
-  return D == 64 ? launch_q<__half, 64, false>(a, sms, s) : launch_q<__half, 128, false>(a, sms, s);
+    return D == 64 ? launch_q<__nv_bfloat16, 64, false>(a, parts, sms, s) : launch_q<__nv_bfloat16, 128, false>(a, parts, sms, s);
+  return D == 64 ? launch_q<__half, 64, false>(a, parts, sms, s) : launch_q<__half, 128, false>(a, parts, sms, s);
 }
 
 }  // namespace kvx

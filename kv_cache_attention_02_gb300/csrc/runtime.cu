@@ -872,6 +872,7 @@ int kvevict_attend_cache(const kvevict_t* h, int32_t l, const kvevict_attention*
     r.batch = h->B;
     r.n_kv_heads = h->H;
     r.head_dim = h->D;
+    r.err = h->err;
     return kvx::attend_run(args, &r, (cudaStream_t)stream);
   } catch (...) {
     return KVEVICT_ERR_OOM;

@@ -77,10 +77,10 @@ def test_attend_null_and_empty(kvx):
     assert lib.kvevict_attend(None, None) == kvx.ERR_INVALID_ARG
     assert lib.kvevict_attend(_attention(kvx, batch=0, q=0, out=0, k=0, v=0), None) == kvx.OK
     assert lib.kvevict_attend_cache(None, 0, _attention(kvx), None) == kvx.ERR_INVALID_ARG
-    assert lib.kvevict_attend_workspace(_attention(kvx), None) == kvx.ERR_INVALID_ARG
+    assert lib.kvevict_attend_workspace(_attention(kvx), 0, None) == kvx.ERR_INVALID_ARG
     n = ctypes.c_size_t(1)
-    assert lib.kvevict_attend_workspace(None, ctypes.addressof(n)) == kvx.ERR_INVALID_ARG
-    assert lib.kvevict_attend_workspace(_attention(kvx, head_dim=32), ctypes.addressof(n)) == kvx.ERR_INVALID_ARG
+    assert lib.kvevict_attend_workspace(None, 0, ctypes.addressof(n)) == kvx.ERR_INVALID_ARG
+    assert lib.kvevict_attend_workspace(_attention(kvx, head_dim=32), 0, ctypes.addressof(n)) == kvx.ERR_INVALID_ARG
 
 
 def test_tensors_are_checked(kvx):
