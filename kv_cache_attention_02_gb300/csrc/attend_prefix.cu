@@ -58,7 +58,7 @@ struct PxGeo {
   static constexpr int STAGES = 160 * 1024 / TILEB;
   static constexpr int Q = 0, RING = 2 * TILEB, BARS = RING + STAGES * TILEB;
   static constexpr int ML = TILEB;   // PAIR: the streams' maxima and sums, where TILES has its second query block
-  static constexpr int SMEM = BARS + (2 * STAGES + 8) * 8 + 16 + 1024;   // slack to align to 1024 bytes
+  static constexpr int SMEM = BARS + (2 * STAGES + 12) * 8 + 16 + 1024;   // slack to align to 1024 bytes
 };
 
 // Instruction descriptors, kind::f16, f32 accumulator, M = 128: bits 7 and 10
@@ -93,6 +93,20 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+// All 128 columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
+  uint32_t r[128];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int e = 0; e < 128; ++e) v[e] = __uint_as_float(r[e]);
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -103,7 +117,39 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
+// 16 consecutive columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One thread of the warp, always the same, chosen in a way that tells the
+// compiler that the warp stays uniform: descriptors then live in uniform
+// registers. With `lane == 0` instead, moving them there bound the rate at which
+// MMAs were issued (388 against 322 us for the MMAs of 4096 x 32 query rows on
+// 8192 keys alone).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 // One CTA's walk over its range of (block, tile) pairs, the same in every role.
 struct Walk {
@@ -145,12 +191,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (base - raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Gm::BARS);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Gm::BARS + (2 * NS + 8) * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Gm::BARS + (2 * NS + 12) * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full = [&](int s) { return smem_addr(&bars[s]); };
   auto empty = [&](int s) { return smem_addr(&bars[NS + s]); };
   auto s_full = [&](int w) { return smem_addr(&bars[2 * NS + w]); };
-  auto p_full = [&](int w) { return smem_addr(&bars[2 * NS + 2 + w]); };
+  auto p_full = [&](int w, int c) { return smem_addr(&bars[2 * NS + 8 + 2 * w + c]); };   // halves of 64 keys
   auto o_done = [&](int w) { return smem_addr(&bars[2 * NS + 4 + w]); };
   const uint32_t q_full = smem_addr(&bars[2 * NS + 6]);
   const uint32_t drain = smem_addr(&bars[2 * NS + 7]);
@@ -166,7 +212,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full(w), 1);
-      mbar_init(p_full(w), 4);
+      mbar_init(p_full(w, 0), 4);
+      mbar_init(p_full(w, 1), 4);
       mbar_init(o_done(w), 1);
     }
     mbar_init(q_full, 8);
@@ -185,26 +232,31 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 
   Walk walk(p, blockIdx.x);
   int u, k0, k1;
-
+  // The launch's 384 x 168 registers, shared out anew: 4 warps of 120 and 8 of
+  // 192 a thread, so that a softmax thread holds a row's 128 logits.
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    int64_t issued = 0;
-    bool ok = true;
+    int s = 0, held = 0;               // next stage, stages in flight (at most NS)
+    uint32_t phase = 0;
+    bool ok = true, stall = p.stall && blockIdx.x == 0;   // test hook: CTA 0's first tile never comes
     while (ok && walk.next(u, k0, k1)) {
       const int n = min(k1, (block_limit(p, u) + kT - 1) / kT) - k0;
       const int h = u / p.plan.blocks;
       if (lane == 0) {
         auto load = [&](const CUtensorMap* map, bool row_first, int kt) {
-          const int s = (int)(issued % NS);
-          if (issued >= NS && !wait_or_abort(empty(s), (uint32_t)((issued / NS - 1) & 1), abort_flag, p.err)) return false;
-          if (!(p.stall && blockIdx.x == 0 && issued == 0)) {   // test hook: CTA 0's first tile never comes
+          if (held == NS && !wait_or_abort(empty(s), phase ^ 1, abort_flag, p.err)) return false;
+          if (!stall) {
             mbar_expect_tx(full(s), Gm::TILEB);
             const int row = (k0 + kt) * kT;
             for (int kh = 0; kh < Gm::KH; ++kh)
               tma_load_3d(base + Gm::RING + s * Gm::TILEB + kh * Gm::HALFB, map, kh * 64, row_first ? row : h,
                           row_first ? h : row, full(s));
           }
-          ++issued;
+          stall = false;
+          held = min(held + 1, NS);
+          if (++s == NS) s = 0, phase ^= 1;
           return true;
         };
         for (int i = 0; i < n && ok; ++i) {
@@ -220,12 +272,19 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       ok = __shfl_sync(~0u, (int)ok, 0) != 0;
     }
     if (lane == 0 && *abort_flag)      // let copies in flight land before the CTA leaves
-      for (int64_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
-        (void)mbar_wait_bounded(full((int)(i % NS)), (uint32_t)((i / NS) & 1), 10000000ull);
+      for (int i = 0; i < held; ++i) {
+        if (--s < 0) s = NS - 1, phase ^= 1;
+        (void)mbar_wait_bounded(full(s), phase, 10000000ull);
+      }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t kIdS = px_idesc<T>(kT, false), kIdO = px_idesc<T>(D, true);
-    int64_t used = 0;
+    // descriptors of the first query block and ring stage; an offset adds to the
+    // address field, in 16-byte units
+    const uint64_t qd = sw128_desc(base + Gm::Q), kd = sw128_desc(base + Gm::RING);
+    const uint64_t vd = sw128_mn_desc(base + Gm::RING, Gm::HALFB);
+    int next = 0;                      // ring stage and its phase
+    uint32_t phase = 0;
     uint32_t np[2] = {0, 0};           // weights tiles consumed, per stream
     int seg = 0;                       // segments that have tiles
     bool ok = true;
@@ -238,40 +297,43 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (!ok) break;
       tc_fence_after();
       auto tile = [&]() -> int {       // the next ring stage, once its tile is there; -1 on abort
-        const int s = (int)(used % NS);
-        const bool here = wait_or_abort(full(s), (uint32_t)((used / NS) & 1), abort_flag, p.err);
-        ++used;
+        const int s = next;
+        const bool here = wait_or_abort(full(s), phase, abort_flag, p.err);
+        if (++next == NS) next = 0, phase ^= 1;
         return __all_sync(~0u, here) ? s : -1;
       };
       auto mma_s = [&](int w, int s) {
-        if (lane == 0) {
-          const uint32_t qa = base + Gm::Q + (PAIR ? 0 : w) * Gm::TILEB, kb = base + Gm::RING + s * Gm::TILEB;
+        if (elect_one()) {
+          const uint64_t qa = qd + (uint64_t)((PAIR ? 0 : w) * (Gm::TILEB >> 4)), kb = kd + (uint64_t)(s * (Gm::TILEB >> 4));
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (uint32_t)((kk >> 2) * Gm::HALFB + (kk & 3) * 32);
-            tc_mma_ss(tm_s(w), sw128_desc(qa + off), sw128_desc(kb + off), kIdS, kk > 0);
+            const uint64_t off = (uint64_t)(((kk >> 2) * Gm::HALFB + (kk & 3) * 32) >> 4);
+            tc_mma_ss(tm_s(w), qa + off, kb + off, kIdS, kk > 0);
           }
           tc_commit(s_full(w));
         }
       };
       auto release = [&](int s) {
-        if (lane == 0) tc_commit(empty(s));
+        if (elect_one()) tc_commit(empty(s));
       };
       // O_w += P_w V: P of keys 0..63 in S's columns 0..31, of keys 64..127 in
       // 64..95, the second parts (PAIR) 32 columns on
       auto mma_o = [&](int w, int s, bool first) {
-        if (!__all_sync(~0u, wait_or_abort(p_full(w), np[w] & 1, abort_flag, p.err))) return false;
-        ++np[w];
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t vb = base + Gm::RING + s * Gm::TILEB;
+        const uint64_t vb = vd + (uint64_t)(s * (Gm::TILEB >> 4));
 #pragma unroll
-          for (int part = 0; part < (PAIR ? 2 : 1); ++part)
+        for (int c = 0; c < 2; ++c) {
+          if (!__all_sync(~0u, wait_or_abort(p_full(w, c), np[w] & 1, abort_flag, p.err))) return false;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kT / 16; ++kk)
-              tc_mma_ts(tm_o(w), tm_s(w) + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8 + 32 * part),
-                        sw128_mn_desc(vb + kk * 2048, Gm::HALFB), kIdO, !(first && kk == 0 && part == 0));
+            for (int part = 0; part < (PAIR ? 2 : 1); ++part)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_ts(tm_o(w), tm_s(w) + (uint32_t)(c * 64 + kk * 8 + 32 * part),
+                          vb + (uint64_t)((4 * c + kk) * (2048 >> 4)), kIdO, !(first && c + kk + part == 0));
+          }
         }
+        ++np[w];
         return true;
       };
       // A value tile that reaches past the block's rows: what lies there may be
@@ -299,7 +361,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           clean(s, k0 + i);
           if (!(ok = mma_o(w, s, i < 2))) break;
           release(s);
-          if (i + 2 >= n && lane == 0) tc_commit(o_done(w));
+          if (i + 2 >= n && elect_one()) tc_commit(o_done(w));
           if (i + 2 < n) {
             if (!(ok = (s = tile()) >= 0)) break;
             mma_s(w, s);
@@ -318,7 +380,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           if (more) {
             if (!(ok = (sk = tile()) >= 0)) break;
             mma_s(0, sk);
-          } else if (lane == 0) {
+          } else if (elect_one()) {
             tc_commit(o_done(0));
           }
           if (!(ok = mma_o(1, s, i == 0))) break;
@@ -326,14 +388,16 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           if (more) {
             mma_s(1, sk);
             release(sk);
-          } else if (lane == 0) {
+          } else if (elect_one()) {
             tc_commit(o_done(1));
           }
         }
       }
     }
-  } else if (warp >= 4) {
+  }
+  } else {
     // ---------------------------------------------------------------- softmax warpgroups
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int w = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;          // query row of the stream = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -372,23 +436,19 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         tc_fence_after();
         const int left = rows - (k0 + i) * kT;       // columns from here on are masked
         const bool whole = __all_sync(~0u, left >= kT);
-        float m8[8];
+        float v[kT];
+        tmem_ld128(ts, v);
+        if (!whole) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = kNegInf;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          float v[64];
-          tmem_ld64(ts + 64 * c, v);
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e) v[e] = 64 * c + e < left ? v[e] : kNegInf;
-          }
-#pragma unroll
-          for (int e = 0; e < 64; ++e) m8[e & 7] = fmaxf(m8[e & 7], v[e]);
+          for (int e = 0; e < kT; ++e) v[e] = e < left ? v[e] : kNegInf;
         }
+        float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) m8[e] = fmaxf(m8[e], m8[e + 4]);
-        const float mx = fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])) * a.scale2;
+        for (int e = 4; e < kT; e += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            m4[x] = e + 4 < kT ? fmaxf(m4[x], fmaxf(v[e + x], v[e + 4 + x])) : fmaxf(m4[x], v[e + x]);
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale2;
         const bool up = mx > m + kLazy;
         if (__any_sync(~0u, up)) {
           const float nm = up ? mx : m, f = nm == m ? 1.f : ex2(m - nm);
@@ -396,52 +456,51 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           l *= f;
           if (begun) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float v[32];
-              uint32_t o[32];
-              tmem_ld32(to + 32 * c, v);
+            for (int c = 0; c < D / 16; ++c) {
+              float x[16];
+              uint32_t o[16];
+              tmem_ld16(to + 16 * c, x);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(v[e] * f);
-              tmem_st32(to + 32 * c, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(x[e] * f);
+              tmem_st16(to + 16 * c, o);
             }
           }
         }
         begun = true;
         const float nb = m == kNegInf ? 0.f : -m;    // nothing so far: every weight 2^-inf = 0
         const float2 sc2 = make_float2(a.scale2, a.scale2), nb2 = make_float2(nb, nb);
-        float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
-#pragma unroll 1
+        float2 l4[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) l4[x] = make_float2(0.f, 0.f);
+        // 64 keys at a time: the tensor cores start on the first half's weights
+        // while the second half's are computed
+#pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float v[64];
-          tmem_ld64(ts + 64 * c, v);
-          if (!whole) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) v[e] = 64 * c + e < left ? v[e] : kNegInf;
-          }
-          uint32_t hi[32], lo[32];
+          for (int g = 0; g < 2; ++g) {
+            uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float2 t0 = ffma2(make_float2(v[e], v[e + 1]), sc2, nb2);
-            const float2 t1 = ffma2(make_float2(v[e + 2], v[e + 3]), sc2, nb2);
-            const float2 p0 = make_float2(ex2(t0.x), ex2(t0.y)), p1 = make_float2(ex2(t1.x), ex2(t1.y));
-            l0 = fadd2(l0, p0);
-            l1 = fadd2(l1, p1);
-            hi[e / 2] = pack16<T>(p0.x, p0.y);
-            hi[e / 2 + 1] = pack16<T>(p1.x, p1.y);
-            if (PAIR) {
-              const float2 b0 = unpack16<T>(hi[e / 2]), b1 = unpack16<T>(hi[e / 2 + 1]);
-              lo[e / 2] = pack16<T>(p0.x - b0.x, p0.y - b0.y);
-              lo[e / 2 + 1] = pack16<T>(p1.x - b1.x, p1.y - b1.y);
+            for (int e = 0; e < 32; e += 2) {
+              const int k = 64 * c + 32 * g + e;
+              const float2 t = ffma2(make_float2(v[k], v[k + 1]), sc2, nb2);
+              const float2 pp = make_float2(ex2(t.x), ex2(t.y));
+              l4[(e >> 1) & 3] = fadd2(l4[(e >> 1) & 3], pp);
+              hi[e / 2] = pack16<T>(pp.x, pp.y);
+              if (PAIR) {
+                const float2 back = unpack16<T>(hi[e / 2]);
+                lo[e / 2] = pack16<T>(pp.x - back.x, pp.y - back.y);
+              }
             }
+            tmem_st16(ts + 64 * c + 16 * g, hi);
+            if (PAIR) tmem_st16(ts + 64 * c + 32 + 16 * g, lo);
           }
-          tmem_st32(ts + 64 * c, hi);
-          if (PAIR) tmem_st32(ts + 64 * c + 32, lo);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(w, c));
         }
-        l += (l0.x + l0.y) + (l1.x + l1.y);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(w));
+        l4[0] = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
+        l += l4[0].x + l4[0].y;
       }
       if (begun && ok) {
         ok = __all_sync(~0u, wait_or_abort(o_done(w), no & 1, abort_flag, p.err));
@@ -592,6 +651,14 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 template <typename T, int D, bool PAIR>
 cudaError_t launch_px(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefixArgs& p, cudaStream_t s) {
   auto kernel = attend_prefix_kernel<T, D, PAIR>;
+  // The kernel's redistribution of registers needs the 168 a thread that its
+  // launch bound gives it: checked, as it would wait forever with fewer.
+  static const cudaError_t regs = [&] {
+    cudaFuncAttributes f;
+    const cudaError_t r = cudaFuncGetAttributes(&f, kernel);
+    return r != cudaSuccess ? r : f.numRegs == 168 ? cudaSuccess : cudaErrorLaunchOutOfResources;
+  }();
+  if (regs != cudaSuccess) return regs;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PxGeo<D>::SMEM);
   if (e != cudaSuccess) return e;
   kernel<<<p.plan.ctas, kPxThreads, PxGeo<D>::SMEM, s>>>(kmap, vmap, p);
