@@ -158,35 +158,4 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// Adds the prefix's parts of query row r (b * N + j) of key head h, columns
-// 4 d4 .. + 3, to the sums (m, l, o), in the CTAs' order. A part with l = 0 has
-// no rows; a NaN l passes on.
-template <int D>
-__device__ __forceinline__ void join_parts(const PrefixParts& p, int h, int64_t r, int d4, float& m, float& l, float4& o) {
-  const int R = p.plan.block_rows;
-  const int blk = (int)(r / R), rr = (int)(r - (int64_t)blk * R), u = h * p.plan.blocks + blk;
-  const int c0 = p.plan.cta_of((int64_t)u * p.plan.nkt), c1 = p.plan.cta_of((int64_t)(u + 1) * p.plan.nkt - 1);
-  float mm = m;
-  for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, p.ml[p.plan.slot(u, c, c == c0) * R + rr].x);
-  const float f = m == mm ? 1.f : ex2_approx(m - mm);
-  l *= f;
-  o.x *= f;
-  o.y *= f;
-  o.z *= f;
-  o.w *= f;
-  for (int c = c0; c <= c1; ++c) {
-    const int64_t slot = p.plan.slot(u, c, c == c0);
-    const float2 ml = p.ml[slot * R + rr];
-    if (ml.y == 0.f) continue;
-    const float g = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
-    const float4 v = reinterpret_cast<const float4*>(p.o)[slot * (R * (D / 4)) + (int64_t)d4 * R + rr];
-    l = fmaf(g, ml.y, l);
-    o.x = fmaf(g, v.x, o.x);
-    o.y = fmaf(g, v.y, o.y);
-    o.z = fmaf(g, v.z, o.z);
-    o.w = fmaf(g, v.w, o.w);
-  }
-  m = mm;
-}
-
 }  // namespace kvx

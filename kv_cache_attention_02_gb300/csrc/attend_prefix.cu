@@ -41,6 +41,8 @@
 #include "attend_internal.cuh"
 #include "tcgen05.cuh"
 
+#include <algorithm>
+
 namespace kvx {
 namespace {
 
@@ -107,16 +109,6 @@ __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
   for (int e = 0; e < 128; ++e) v[e] = __uint_as_float(r[e]);
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
 // 16 consecutive columns of this thread's lane, waited for.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
   uint32_t r[16];
@@ -435,10 +427,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         ++ns;
         tc_fence_after();
         const int left = rows - (k0 + i) * kT;       // columns from here on are masked
-        const bool whole = __all_sync(~0u, left >= kT);
+        const bool none = left <= 0;
+        // a length ends inside this tile, or rows that no sequence has begin in it
+        const bool partial = __any_sync(~0u, !none && left < kT) || limit - (k0 + i) * kT < kT;
         float v[kT];
         tmem_ld128(ts, v);
-        if (!whole) {
+        if (partial) {
 #pragma unroll
           for (int e = 0; e < kT; ++e) v[e] = e < left ? v[e] : kNegInf;
         }
@@ -448,7 +442,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             m4[x] = e + 4 < kT ? fmaxf(m4[x], fmaxf(v[e + x], v[e + 4 + x])) : fmaxf(m4[x], v[e + x]);
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale2;
+        const float mx = none ? kNegInf : fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale2;
         const bool up = mx > m + kLazy;
         if (__any_sync(~0u, up)) {
           const float nm = up ? mx : m, f = nm == m ? 1.f : ex2(m - nm);
@@ -467,7 +461,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           }
         }
         begun = true;
-        const float nb = m == kNegInf ? 0.f : -m;    // nothing so far: every weight 2^-inf = 0
+        // a row past its length: every weight 2^-inf = 0 (and so are masked ones,
+        // with a row that has had nothing so far)
+        const float nb = none ? kNegInf : m == kNegInf ? 0.f : -m;
         const float2 sc2 = make_float2(a.scale2, a.scale2), nb2 = make_float2(nb, nb);
         float2 l4[4];
 #pragma unroll
@@ -622,30 +618,78 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 }
 
 // Joins the parts of blocks that several CTAs share, where the prefix is all
-// there is. One grid column per boundary between CTAs; the first boundary
-// inside a block takes it, in gridDim.y shares of its elements.
+// there is: grid (block, 32 rows of it, 32 columns), or, with more blocks than
+// CTAs, (boundary between CTAs, ..), where the first boundary inside a block
+// takes it. A lane is a row, and the eight warps
+// take every eighth part, so that all of a block's loads are under way at once.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ PrefixArgs p) {
   const PrefixPlan& pl = p.plan;
   const AttendArgs& a = p.a;
-  const int64_t x = pl.start(blockIdx.x + 1);
-  const int u = (int)(x / pl.nkt);
-  const int64_t u0 = (int64_t)u * pl.nkt;
-  if (x == u0 || pl.start(blockIdx.x) > u0) return;
-  const int N = a.G / a.H, R = pl.block_rows, h = u / pl.blocks;
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < R * (D / 4); i += gridDim.y * 256) {
-    const int rr = i % R, d4 = i / R;
-    const int64_t r = (int64_t)(u % pl.blocks) * R + rr;
-    if (r >= (int64_t)a.B * N) continue;
-    float m = kNegInf, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    join_parts<D>(p.parts(), h, r, d4, m, l, o);
-    const int b = (int)(r / N), head = h * N + (int)(r - (int64_t)b * N);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)head * a.out_stride[1] + 4 * d4;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * inv, o.y * inv), pack16<T>(o.z * inv, o.w * inv));
-    if (d4 == 0 && a.lse) a.lse[(int64_t)b * a.G + head] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+  int u = blockIdx.x;
+  if (pl.units >= pl.ctas) {
+    const int64_t x = pl.start(blockIdx.x + 1);
+    u = (int)(x / pl.nkt);
+    if (x == (int64_t)u * pl.nkt || pl.start(blockIdx.x) > (int64_t)u * pl.nkt) return;
   }
+  const int64_t u0 = (int64_t)u * pl.nkt;
+  __shared__ float2 ml_s[8][32];
+  __shared__ float4 o_s[8][8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int N = a.G / a.H, R = pl.block_rows, h = u / pl.blocks;
+  const int rr = blockIdx.y * 32 + lane, d4 = blockIdx.z * 8;
+  const int c0 = pl.cta_of(u0), c1 = pl.cta_of(u0 + pl.nkt - 1);
+  if (c0 == c1) return;                      // one CTA's alone: written out by it
+  float m = kNegInf, l = 0.f;
+  float4 o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0 + warp; c <= c1; c += 8) {
+    const int64_t slot = pl.slot(u, c, c == c0);
+    const float2 ml = p.part_ml[slot * R + rr];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + slot * (R * (D / 4)) + (int64_t)d4 * R + rr;
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = src[i * R];
+    if (ml.y == 0.f) continue;               // no rows, no O; a NaN sum passes on
+    const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2(m - nm), g = ml.x == nm ? 1.f : ex2(ml.x - nm);
+    m = nm;
+    l = l * f + ml.y * g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o[i].x = o[i].x * f + v[i].x * g;
+      o[i].y = o[i].y * f + v[i].y * g;
+      o[i].z = o[i].z * f + v[i].z * g;
+      o[i].w = o[i].w * f + v[i].w * g;
+    }
+  }
+  ml_s[warp][lane] = make_float2(m, l);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o_s[warp][i][lane] = o[i];
+  __syncthreads();
+  const int64_t r = (int64_t)(u % pl.blocks) * R + rr;
+  if (r >= (int64_t)a.B * N) return;
+  m = kNegInf;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, ml_s[w][lane].x);
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float2 ml = ml_s[w][lane];
+    const float g = ml.x == m ? 1.f : ex2(ml.x - m);
+    const float4 v = o_s[w][warp][lane];
+    l = fmaf(ml.y, g, l);
+    y.x = fmaf(v.x, g, y.x);
+    y.y = fmaf(v.y, g, y.y);
+    y.z = fmaf(v.z, g, y.z);
+    y.w = fmaf(v.w, g, y.w);
+  }
+  const int b = (int)(r / N), head = h * N + (int)(r - (int64_t)b * N);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)head * a.out_stride[1] + 4 * (d4 + warp);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(y.x * inv, y.y * inv), pack16<T>(y.z * inv, y.w * inv));
+  if (d4 + warp == 0 && a.lse) a.lse[(int64_t)b * a.G + head] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <typename T, int D, bool PAIR>
@@ -664,7 +708,7 @@ cudaError_t launch_px(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pr
   kernel<<<p.plan.ctas, kPxThreads, PxGeo<D>::SMEM, s>>>(kmap, vmap, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.plan.final || !p.plan.shared_blocks()) return e;
-  attend_join_kernel<T, D><<<dim3(p.plan.ctas - 1, p.plan.block_rows / 16), 256, 0, s>>>(p);
+  attend_join_kernel<T, D><<<dim3(std::min(p.plan.units, p.plan.ctas - 1), p.plan.block_rows / 32, D / 32), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 

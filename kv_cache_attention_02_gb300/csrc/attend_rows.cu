@@ -312,6 +312,62 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
     if (more) R::load_v(vr, cur, g, c);
   }
 
+  // ---------------------------------------------------------------- the prefix's parts
+  // Each part (a range of shared rows that one CTA of attend_prefix.cu took) joins
+  // one warp's sums as if it were another tile; the query rows b * N + q0 + q may
+  // lie in two blocks.
+  if (parts.plan.ctas) {
+    const int RB = parts.plan.block_rows;
+    const int64_t r0 = (int64_t)b * N + q0;
+    for (int64_t blk = r0 / RB; blk <= (r0 + nq - 1) / RB; ++blk) {
+      const int u = h * parts.plan.blocks + (int)blk, off = (int)(r0 - blk * RB);   // query q is row off + q
+      const int c0 = parts.plan.cta_of((int64_t)u * parts.plan.nkt);
+      const int c1 = parts.plan.cta_of((int64_t)(u + 1) * parts.plan.nkt - 1);
+      auto inside = [&](int q) { return q < nq && off + q >= 0 && off + q < RB; };
+      for (int pc = c0 + rank * kWarps + warp; pc <= c1; pc += stride) {
+        const int64_t slot = parts.plan.slot(u, pc, pc == c0);
+        const float2* ml = parts.ml + slot * RB;
+        const float4* po = reinterpret_cast<const float4*>(parts.o) + slot * (RB * (D / 4));
+#pragma unroll
+        for (int i = 0; i < QT; ++i) {
+          float4 v[2][VH][2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int q = 2 * c + k + 8 * i;
+            const bool in = inside(q);
+#pragma unroll
+            for (int x = 0; x < VH; ++x)
+#pragma unroll
+              for (int w = 0; w < 2; ++w)
+                v[k][x][w] = in ? po[(16 * x + 2 * g + w) * RB + off + q] : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          const int q = g + 8 * i;
+          float2 part = inside(q) ? ml[off + q] : make_float2(kNegInf, 0.f);
+          const float nm = fmaxf(m[i], part.x);
+          const float f = m[i] == nm ? 1.f : ex2_approx(m[i] - nm);
+          // a part without rows has left no O; a NaN sum passes on
+          const float fp = part.y == 0.f ? 0.f : part.x == nm ? 1.f : ex2_approx(part.x - nm);
+          m[i] = nm;
+          l[i] = l[i] * f + (c == 0 && fp != 0.f ? part.y * fp : 0.f);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float fa = __shfl_sync(~0u, f, 8 * c + 4 * k), fb = __shfl_sync(~0u, fp, 8 * c + 4 * k);
+#pragma unroll
+            for (int x = 0; x < VH; ++x)
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const float4 y = fb != 0.f ? v[k][x][w] : make_float4(0.f, 0.f, 0.f, 0.f);
+                acc[x][2 * w][i][k] = acc[x][2 * w][i][k] * fa + y.x * fb;
+                acc[x][2 * w][i][k + 2] = acc[x][2 * w][i][k + 2] * fa + y.y * fb;
+                acc[x][2 * w + 1][i][k] = acc[x][2 * w + 1][i][k] * fa + y.z * fb;
+                acc[x][2 * w + 1][i][k + 2] = acc[x][2 * w + 1][i][k + 2] * fa + y.w * fb;
+              }
+          }
+        }
+      }
+    }
+  }
+
   // ---------------------------------------------------------------- join the warps
 #pragma unroll
   for (int i = 0; i < QT; ++i) {
@@ -372,7 +428,6 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
       o.w = fmaf(f, v.w, o.w);
       ll = fmaf(f, *cluster.map_shared_rank(&cta_ml[q][1], r), ll);
     }
-    if (parts.plan.ctas) join_parts<D>(parts, h, (int64_t)b * N + q0 + q, d / 4, mm, ll, o);
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const int gq = h * N + q0 + q;
     T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)gq * a.out_stride[1] + d;
@@ -387,7 +442,7 @@ cudaError_t launch_one(const AttendArgs& a, const PrefixParts& parts, int sms, c
   const int N = a.G / a.H;
   const int qchunks = (N + 8 * QT - 1) / (8 * QT);
   const int64_t units = (int64_t)a.B * a.H * qchunks;
-  const int64_t tiles = ((int64_t)a.P + 15) / 16 + ((int64_t)a.n + 15) / 16 + 1;
+  const int64_t tiles = ((int64_t)a.P + 15) / 16 + ((int64_t)a.n + 15) / 16 + 1 + parts.plan.ctas / a.H;
   // Split a unit's rows over a cluster until the GPU has about 16 warps an SM
   // or a warp has one tile.
   int C = 1;
