@@ -468,7 +468,8 @@ typedef struct kvevict_attention {
 int kvevict_attend(const kvevict_attention* args, void* stream);
 
 /* Device bytes that a call of this description needs as workspace, on the
- * current device; of the pointers only k_new counts. with_cache: 1 for
+ * current device; of the pointers only k_new counts (whether it is null).
+ * with_cache: 1 for
  * kvevict_attend_cache, 0 for kvevict_attend. *bytes: host. Errors:
  * INVALID_ARG, CUDA. */
 int kvevict_attend_workspace(const kvevict_attention* args, int32_t with_cache, size_t* bytes);

@@ -316,8 +316,7 @@ def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_
     whole 16-byte pieces. Errors: ValueError, KVEvictError.
     """
     args, s = _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream, None)
-    if prefix_k is not None:
-        args, space = _with_workspace(args, 0, q.get_device(), s)
+    args, space = _with_workspace(args, 0, q.get_device(), s)
     rc = lib().kvevict_attend(args, s)
     if rc:
         _check(rc)
@@ -423,8 +422,7 @@ class KVEvict:
         """
         args, s = _attention(q, out, None, None, None, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream,
                              self.H)
-        if prefix_k is not None:
-            args, space = _with_workspace(args, 1, q.get_device(), s)
+        args, space = _with_workspace(args, 1, q.get_device(), s)
         _check(lib().kvevict_attend_cache(self._h, l, args, s))
 
     def run_host(self, prefill_keys, decode_keys, evicted=None, stream=None):

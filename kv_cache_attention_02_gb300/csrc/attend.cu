@@ -139,6 +139,14 @@ int attend_check(const kvevict_attention* d) {
   return KVEVICT_OK;
 }
 
+// The prefix kernel's plan; not used (the row kernel reads the shared rows
+// itself) where TMA cannot describe the rows.
+PrefixPlan plan_prefix(const kvevict_attention* d, bool own, int sms) {
+  const bool fit = d->prefix > 0 && prefix_strides_fit(d->prefix_k_stride, d->n_kv_heads, d->prefix, d->head_dim) &&
+                   prefix_strides_fit(d->prefix_v_stride, d->n_kv_heads, d->prefix, d->head_dim);
+  return fit ? prefix_plan(d->batch, d->n_heads, d->n_kv_heads, d->head_dim, d->prefix, own, sms) : PrefixPlan{};
+}
+
 }  // namespace
 
 int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s) {
@@ -209,28 +217,33 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
   a.P = d->prefix;
   const double scale = d->scale > 0.f ? (double)d->scale : 1.0 / std::sqrt((double)d->head_dim);
   a.scale2 = (float)(scale * 1.4426950408889634);
+  const int D = d->head_dim;
   PrefixArgs p{};
-  p.plan = prefix_plan(a.B, a.G, a.H, d->head_dim, a.P, rows || a.n > 0 || a.k_new, dev.sms);
+  p.plan = plan_prefix(d, rows || a.n > 0 || a.k_new, dev.sms);
+  const bool alone = p.plan.ctas && p.plan.final;      // the prefix is all there is
+  RowsPlan rp{};
+  if (!alone)
+    rp = rows_plan(a.B, a.G, a.H, D, a.n, p.plan.ctas ? 0 : a.P, a.k_new, rows != nullptr, p.plan.ctas > 0, dev.sms);
+  const size_t need = p.plan.bytes(D) + rp.bytes(D);
+  if (need && (d->workspace_bytes < need || !d->workspace || !aligned(d->workspace)))
+    return invalid("workspace must be 16-byte aligned and hold kvevict_attend_workspace bytes");
+  char* space = static_cast<char*>(d->workspace);
   if (p.plan.ctas) {
-    if (d->workspace_bytes < p.plan.bytes(d->head_dim) || !d->workspace || !aligned(d->workspace))
-      return invalid("workspace must be 16-byte aligned and hold kvevict_attend_workspace bytes");
     p.a = a;
-    p.part_o = static_cast<float*>(d->workspace);
-    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(d->workspace) + p.plan.o_bytes(d->head_dim));
+    p.part_o = reinterpret_cast<float*>(space);
+    p.part_ml = reinterpret_cast<float2*>(space + p.plan.o_bytes(D));
     p.err = rows ? rows->err : nullptr;
     p.stall = take_scorer_stall() ? 1 : 0;
-    const cudaError_t e = launch_attend_prefix(p, d->head_dim, d->dtype, s);
-    if (e == cudaSuccess) {
-      if (p.plan.final) return KVEVICT_OK;
-      a.P = 0;             // joined from its parts
-      a.plens = nullptr;
-    } else if (e == cudaErrorNotSupported) {
-      p.plan.ctas = 0;     // strides that TMA cannot take: the row kernel reads the prefix itself
-    } else {
-      return cuda_result(e, "launch");
-    }
+    const cudaError_t e = launch_attend_prefix(p, D, d->dtype, s);
+    if (e != cudaSuccess) return cuda_result(e, "launch");
+    if (alone) return KVEVICT_OK;
+    space += p.plan.bytes(D);
+    a.P = 0;               // joined from its parts
+    a.plens = nullptr;
   }
-  return cuda_result(launch_attend_rows(a, p.parts(), d->head_dim, d->dtype, dev.sms, s), "launch");
+  rp.part_o = reinterpret_cast<float*>(space);
+  rp.part_ml = reinterpret_cast<float2*>(space + rp.o_bytes(D));
+  return cuda_result(launch_attend_rows(a, p.parts(), rp, D, d->dtype, dev.sms, s), "launch");
 }
 
 }  // namespace kvx
@@ -265,12 +278,18 @@ extern "C" int kvevict_attend_workspace(const kvevict_attention* args, int32_t w
     if (!bytes) return kvx::invalid("bytes must not be null");
     if (int rc = kvx::attend_check(args)) return rc;
     *bytes = 0;
-    if (args->batch == 0 || args->prefix == 0) return KVEVICT_OK;
+    if (args->batch == 0) return KVEVICT_OK;
     kvx::DeviceInfo dev;
     if (int rc = kvx::device_info(&dev)) return rc;
+    const int B = args->batch, G = args->n_heads, H = args->n_kv_heads, D = args->head_dim;
     const bool own = with_cache || args->n > 0 || args->k_new;
-    *bytes = kvx::prefix_plan(args->batch, args->n_heads, args->n_kv_heads, args->head_dim, args->prefix, own, dev.sms)
-                 .bytes(args->head_dim);
+    const kvx::PrefixPlan pp = kvx::plan_prefix(args, own, dev.sms);
+    *bytes = pp.bytes(D);
+    if (pp.ctas && !own) return KVEVICT_OK;
+    // a handle's rows are not in the description: as many as there can be
+    const int n = with_cache ? 1 << 29 : args->n;
+    *bytes += kvx::rows_plan(B, G, H, D, n, pp.ctas ? 0 : args->prefix, args->k_new != nullptr, with_cache != 0,
+                             pp.ctas > 0, dev.sms).bytes(D);
     return KVEVICT_OK;
   });
 }

@@ -70,6 +70,7 @@ struct PrefixPlan {
   size_t bytes(int D) const;
   bool shared_blocks() const;   // whether any block is cut
 };
+bool prefix_strides_fit(const int64_t* stride, int H, int P, int D);
 PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int sms);
 
 // The parts of the prefix's attention in the workspace: per slot O as
@@ -90,7 +91,7 @@ struct PrefixArgs {
   bool k_row_first, v_row_first;
   __host__ __device__ PrefixParts parts() const { return PrefixParts{plan, part_o, part_ml}; }
 };
-cudaError_t launch_attend_prefix(const PrefixArgs& p, int D, int dtype, cudaStream_t s);   // NotSupported: no tensor map
+cudaError_t launch_attend_prefix(const PrefixArgs& p, int D, int dtype, cudaStream_t s);
 
 // What a launch needs to know of the current device, looked up once.
 struct DeviceInfo {
@@ -100,8 +101,23 @@ int device_info(DeviceInfo* out);   // KVEVICT_* code; sets the last error
 void set_last_error(const std::string& msg);
 
 cudaError_t launch_qk_norm_rope(QkArgs a, int D, int in_dtype, int out_dtype, int sms, cudaStream_t s);
+
+// How the row kernel's work is cut: with ctas > 0 all units' tiles in a row, one
+// contiguous range per CTA; otherwise a cluster per unit.
+struct RowsPlan {
+  int ctas, qchunks, qn, final;   // a unit: qn query heads of a key head, qchunks units; final: no prefix parts to join
+  int64_t units;
+  float* part_o;                  // [slot][qn][D]
+  float2* part_ml;                // [slot][qn] maximum (base 2) and sum
+  __host__ __device__ int64_t slot(int64_t u, int c, bool from_start) const { return final ? 2 * c + from_start : u + c; }
+  int64_t slots() const { return final ? 2 * (int64_t)ctas : units + ctas; }
+  size_t o_bytes(int D) const;
+  size_t bytes(int D) const;
+};
+RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool pend, bool prefix_parts, int sms);
 // parts.plan.ctas > 0: joins the prefix's parts too (a.P is 0 then).
-cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, int D, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int D, int dtype,
+                               int sms, cudaStream_t s);
 
 // Checks the caller's description and fills the kernel's; own rows come from
 // `rows` (a handle's layer) where that is not null.

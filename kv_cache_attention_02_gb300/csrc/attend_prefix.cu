@@ -712,17 +712,20 @@ cudaError_t launch_px(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pr
   return cudaGetLastError();
 }
 
+// Strides between heads and rows, where a dimension of one has none of its own.
+void row_strides(const int64_t* stride, int H, int P, int D, int64_t* hs, int64_t* rs) {
+  *rs = P == 1 ? D : stride[1];
+  *hs = H == 1 ? (int64_t)P * *rs : stride[0];
+}
+
 // Shared rows [H, P, D] as a 3-D tensor, the dimension of the smaller stride
-// first (a dimension of one has no stride of its own); boxes of 64 elements
-// (128 bytes) x 128 rows; rows past P read as zeros.
+// first; boxes of 64 elements (128 bytes) x 128 rows; rows past P read as zeros.
 bool encode_rows(CUtensorMap* map, const void* base, const int64_t* stride, int H, int P, int D, int dtype,
                  bool* row_first) {
   auto enc = encode_fn();
   if (!enc) return false;
-  int64_t hs = stride[0], rs = stride[1];
-  if (P == 1) rs = D;
-  if (H == 1) hs = (int64_t)P * rs;
-  if (hs < D || rs < D) return false;      // broadcast or overlapping rows
+  int64_t hs, rs;
+  row_strides(stride, H, P, D, &hs, &rs);
   *row_first = rs <= hs;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)(*row_first ? P : H), (cuuint64_t)(*row_first ? H : P)};
   const cuuint64_t strides[2] = {(cuuint64_t)(*row_first ? rs : hs) * 2, (cuuint64_t)(*row_first ? hs : rs) * 2};
@@ -735,6 +738,13 @@ bool encode_rows(CUtensorMap* map, const void* base, const int64_t* stride, int 
 }
 
 }  // namespace
+
+// What TMA can describe: rows that are apart, strides below 2^40 bytes.
+bool prefix_strides_fit(const int64_t* stride, int H, int P, int D) {
+  int64_t hs, rs;
+  row_strides(stride, H, P, D, &hs, &rs);
+  return hs >= D && rs >= D && hs < ((int64_t)1 << 39) && rs < ((int64_t)1 << 39);
+}
 
 PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int sms) {
   PrefixPlan pl{};
@@ -764,7 +774,7 @@ cudaError_t launch_attend_prefix(const PrefixArgs& args, int D, int dtype, cudaS
   CUtensorMap kmap, vmap;
   if (!encode_rows(&kmap, p.a.pk, p.a.pk_stride, p.a.H, p.a.P, D, dtype, &p.k_row_first) ||
       !encode_rows(&vmap, p.a.pv, p.a.pv_stride, p.a.H, p.a.P, D, dtype, &p.v_row_first))
-    return cudaErrorNotSupported;
+    return cudaErrorInvalidValue;
   if (dtype == kBf16) {
     if (D == 64)
       return p.plan.pair ? launch_px<__nv_bfloat16, 64, true>(kmap, vmap, p, s)

@@ -28,10 +28,15 @@
 // room for the second instruction here, and the output keeps the accuracy of
 // its own rounding.
 //
-// A (sequence, key head, up to 16 query heads) is split over a cluster of CTAs
-// when there are too few of them to fill the GPU; the parts are joined through
-// distributed shared memory, in a fixed order, with no second launch and no
-// workspace.
+// Work: a unit is a sequence's key head with up to 16 of its query heads.
+//   Few tiles (a latency, mostly): one cluster of CTAs a unit, its tiles dealt to
+//     the cluster's warps, the sums joined through distributed shared memory; one
+//     launch, no workspace.
+//   Many (STREAM): all units' tiles in a row are cut into one contiguous range per
+//     resident CTA, so that no SM waits for another whatever the lengths are. A
+//     unit that is one CTA's alone is written out by it, a cut one leaves its
+//     parts in the workspace for a second, small kernel, which joins them in a
+//     fixed order, with the shared prefix's parts if there are any.
 #include "attend_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -44,6 +49,13 @@ namespace cg = cooperative_groups;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kStreamTiles = 4;        // a stream from this many tiles a warp on
+
+constexpr int stream_ctas_per_sm(int D) { return D == 64 ? 4 : 2; }
+int rows_qt(int N) { return N <= 8 ? 1 : 2; }
+int64_t rows_tiles(int n, int P, bool has_new, bool pend) {   // of a unit, at most
+  return ((int64_t)P + 15) / 16 + ((int64_t)n + pend + 15) / 16 + has_new;
+}
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -123,36 +135,160 @@ __device__ __forceinline__ void rotate_back(uint4& lo, uint4& hi, const float* r
   hi = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// QT: groups of 8 query heads (1 or 2).
-template <typename T, int D, int QT, bool PEND>
-__global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_constant__ AttendArgs a,
-                                                                  const __grid_constant__ PrefixParts parts, const int qchunks) {
+// Columns d .. d + 3 of query head gq from its sums, and the head's log sum.
+template <typename T>
+__device__ __forceinline__ void write_out(const AttendArgs& a, int b, int gq, int d, float m, float l, float4 o) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)gq * a.out_stride[1] + d;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * inv, o.y * inv), pack16<T>(o.z * inv, o.w * inv));
+  if (d == 0 && a.lse) a.lse[(int64_t)b * a.G + gq] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// Rows of sequence b: shared (np) and own (n), and the tiles of 16 they make.
+struct SeqRows {
+  int np, n, tp, to;
+  __device__ __forceinline__ SeqRows(const AttendArgs& a, int b) {
+    np = a.plens ? max(0, min(a.plens[b], a.P)) : a.P;
+    n = a.lens ? max(0, min(a.lens[b], a.n)) : a.n;
+    tp = (np + 15) >> 4;
+    to = (n + (a.pend ? 1 : 0) + 15) >> 4;   // an evicted row may still be in place
+  }
+  // of a unit; in a stream every unit has at least one
+  __device__ __forceinline__ int tiles(const AttendArgs& a) const { return tp + to + (a.k_new ? 1 : 0); }
+};
+__device__ __forceinline__ int stream_tiles(const AttendArgs& a, int b) { return max(1, SeqRows(a, b).tiles(a)); }
+
+// Where sequences lie in the row of all units' tiles (warp-collective): the
+// total, and the first tile of the sequence that `find` returns.
+struct Stream {
+  int64_t total, base;
+  int upb;                                    // units of a sequence
+  bool even;                                  // all sequences have as many tiles
+  __device__ __forceinline__ Stream(const AttendArgs& a, int qchunks) : total(0), base(0), upb(a.H * qchunks) {
+    even = !a.lens && !a.plens;
+    if (even) {
+      total = (int64_t)a.B * upb * stream_tiles(a, 0);
+      return;
+    }
+    const int lane = threadIdx.x & 31;
+    int64_t sum = 0;
+    for (int b = lane; b < a.B; b += 32) sum += stream_tiles(a, b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    total = sum * upb;
+  }
+  // The sequence that tile x belongs to (x < total).
+  __device__ __forceinline__ int find(const AttendArgs& a, int64_t x) {
+    if (even) {
+      const int64_t per = (int64_t)upb * stream_tiles(a, 0);
+      const int b = (int)(x / per);
+      base = b * per;
+      return b;
+    }
+    return scan(a, [&](int, int64_t end) { return end * upb > x; });
+  }
+  // Sets base for sequence b.
+  __device__ __forceinline__ void seek(const AttendArgs& a, int b) {
+    if (even)
+      base = (int64_t)b * upb * stream_tiles(a, 0);
+    else
+      (void)scan(a, [&](int s, int64_t) { return s == b; });
+  }
+  __device__ __forceinline__ int64_t start(int c, int ctas) const { return c * total / ctas; }
+  __device__ __forceinline__ int cta_of(int64_t x, int ctas) const { return (int)(((x + 1) * ctas - 1) / total); }
+
+ private:
+  template <typename F>
+  __device__ __forceinline__ int scan(const AttendArgs& a, F&& hit) {
+    const int lane = threadIdx.x & 31;
+    int64_t run = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int64_t own = b0 + lane < a.B ? stream_tiles(a, b0 + lane) : 0;
+      int64_t incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t found = __ballot_sync(~0u, b0 + lane < a.B && hit(b0 + lane, run + incl));
+      if (found) {
+        const int f = __ffs(found) - 1;
+        base = (run + __shfl_sync(~0u, incl - own, f)) * upb;
+        return b0 + f;
+      }
+      run += __shfl_sync(~0u, incl, 31);
+    }
+    return a.B;   // not reached
+  }
+};
+
+// QT: groups of 8 query heads (1 or 2). STREAM: two CTAs an SM at D = 128, four
+// at 64 (the registers of a warp's 16 rows, its sums and its queries).
+template <typename T, int D, int QT, bool PEND, bool STREAM>
+__global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
+    attend_rows_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ PrefixParts parts,
+                       const __grid_constant__ RowsPlan plan) {
   using R = Rows<T, D>;
   constexpr int KC = R::KC, VH = R::VH, QN = 8 * QT;
   __shared__ __align__(16) float part_o[kWarps][QN][D];
   __shared__ float part_ml[kWarps][QN][2];
-  __shared__ __align__(16) float cta_o[QN][D];
+  __shared__ __align__(16) float cta_o[STREAM ? 1 : QN][D];
   __shared__ float cta_ml[QN][2];
 
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int C = STREAM ? 1 : (int)cluster.num_blocks(), rank = STREAM ? 0 : (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int N = a.G / a.H;
-  const int unit = (int)(blockIdx.x / (unsigned)C);
-  const int qc = unit % qchunks, bh = unit / qchunks;
-  const int b = bh / a.H, h = bh - b * a.H;
-  const int q0 = qc * QN, nq = min(QN, N - q0);   // query heads h*N + q0 .. + nq - 1
+  const int N = a.G / a.H, qchunks = plan.qchunks;
 
-  // rows of each source, in tiles of 16: shared, own, the token's own
-  const int np = a.plens ? max(0, min(a.plens[b], a.P)) : a.P;
-  int n = a.lens ? max(0, min(a.lens[b], a.n)) : a.n;
+  int b, ub;                                      // sequence, unit of it
+  int64_t at = 0, end = 0, base = 0;              // STREAM: next tile, the range's end, the sequence's first tile
+  int upb = 0;
+  if (STREAM) {
+    Stream st(a, qchunks);
+    at = st.start(blockIdx.x, plan.ctas);
+    end = st.start(blockIdx.x + 1, plan.ctas);
+    if (at >= end) return;
+    b = st.find(a, at);
+    base = st.base;
+    upb = st.upb;
+    ub = 0;
+  } else {
+    const int unit = (int)(blockIdx.x / (unsigned)C);
+    b = unit / (a.H * qchunks);
+    ub = unit - b * a.H * qchunks;
+  }
+
+  while (true) {                                  // STREAM: the range's segments, each of one unit
+  const SeqRows seq(a, b);
+  int first = 0, total = seq.tiles(a);
+  bool whole = true;
+  int64_t slot = 0;
+  int next_b = b;
+  if (STREAM) {
+    if (at >= end) break;
+    total = max(1, total);
+    const int tb = total;
+    const int64_t rem = at - base;
+    ub = (int)(rem / tb);
+    first = (int)(rem - (int64_t)ub * tb);
+    total = (int)min((int64_t)tb, first + (end - at));
+    at += total - first;
+    whole = plan.final && first == 0 && total == tb;
+    slot = plan.slot((int64_t)b * upb + ub, blockIdx.x, first == 0);
+    if (at == base + (int64_t)upb * tb) {
+      base = at;
+      next_b = b + 1;
+    }
+  }
+  const int qc = ub % qchunks, h = ub / qchunks, bh = b * a.H + h;
+  const int q0 = qc * QN, nq = min(QN, N - q0);   // query heads h*N + q0 .. + nq - 1
+  const int np = seq.np, tp = seq.tp, to = seq.to;
+  int n = seq.n;
   int e = -1;                                     // the evicted row still in place
   if (PEND) {
     e = a.pend[bh];
     if (e >= 0) n += 1;
   }
-  const int tp = (np + 15) >> 4, to = (n + 15) >> 4;
-  const int total = tp + to + (a.k_new ? 1 : 0);
   auto tile_at = [&](int t) {
     Tile<T> x;
     x.moved = 16;
@@ -170,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
       x.k = static_cast<const T*>(a.k) + b * a.k_stride[0] + h * a.k_stride[1] + (int64_t)r0 * x.ks;
       x.v = static_cast<const T*>(a.v) + b * a.v_stride[0] + h * a.v_stride[1] + (int64_t)r0 * x.vs;
       const int left = n - r0;
-      x.live = left >= 16 ? 0xFFFFu : (1u << left) - 1u;
+      x.live = left >= 16 ? 0xFFFFu : left > 0 ? (1u << left) - 1u : 0u;
       if (PEND && e >= 0) {
         if (e >= r0 && e < r0 + 16) x.live &= ~(1u << (e - r0));
         x.moved = max(0, min(16, e - r0 + 1));
@@ -179,13 +315,13 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
       x.ks = x.vs = 0;
       x.k = static_cast<const T*>(a.k_new) + b * a.kn_stride[0] + h * a.kn_stride[1];
       x.v = static_cast<const T*>(a.v_new) + b * a.vn_stride[0] + h * a.vn_stride[1];
-      x.live = 1u;
+      x.live = a.k_new ? 1u : 0u;            // (a unit without any rows has one tile of none)
     }
     return x;
   };
 
   const int stride = C * kWarps;
-  int t = rank * kWarps + warp;
+  int t = first + rank * kWarps + warp;
   uint4 kr[2][KC], vr[VH][4];
   Tile<T> cur{};
   if (t < total) {
@@ -316,7 +452,7 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
   // Each part (a range of shared rows that one CTA of attend_prefix.cu took) joins
   // one warp's sums as if it were another tile; the query rows b * N + q0 + q may
   // lie in two blocks.
-  if (parts.plan.ctas) {
+  if (!STREAM && parts.plan.ctas) {
     const int RB = parts.plan.block_rows;
     const int64_t r0 = (int64_t)b * N + q0;
     for (int64_t blk = r0 / RB; blk <= (r0 + nq - 1) / RB; ++blk) {
@@ -405,11 +541,24 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
       o.w = fmaf(f, v.w, o.w);
       ll = fmaf(f, part_ml[w][q][1], ll);
     }
-    *reinterpret_cast<float4*>(&cta_o[q][d]) = o;
-    if (d == 0) {
-      cta_ml[q][0] = mm;
-      cta_ml[q][1] = ll;
+    if (!STREAM) {
+      *reinterpret_cast<float4*>(&cta_o[STREAM ? 0 : q][d]) = o;
+      if (d == 0) {
+        cta_ml[q][0] = mm;
+        cta_ml[q][1] = ll;
+      }
+    } else if (whole) {
+      write_out<T>(a, b, h * N + q0 + q, d, mm, ll, o);
+    } else {
+      reinterpret_cast<float4*>(plan.part_o)[(slot * QN + q) * D4 + d / 4] = o;
+      if (d == 0) plan.part_ml[slot * QN + q] = make_float2(mm, ll);
     }
+  }
+  if (STREAM) {
+    __syncthreads();                              // the next segment's sums go where these were
+    b = next_b;
+    if (b >= a.B) break;
+    continue;
   }
   // ---------------------------------------------------------------- join the cluster
   cluster.sync();
@@ -428,27 +577,95 @@ __global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_cons
       o.w = fmaf(f, v.w, o.w);
       ll = fmaf(f, *cluster.map_shared_rank(&cta_ml[q][1], r), ll);
     }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    const int gq = h * N + q0 + q;
-    T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)gq * a.out_stride[1] + d;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * inv, o.y * inv), pack16<T>(o.z * inv, o.w * inv));
-    if (d == 0 && a.lse) a.lse[(int64_t)b * a.G + gq] = ll == 0.f ? kNegInf : (mm + log2f(ll)) * 0.69314718055994531f;
+    write_out<T>(a, b, h * N + q0 + q, d, mm, ll, o);
   }
   cluster.sync();   // no CTA leaves while another reads its shared memory
+  break;
+  }
+}
+
+// Joins the parts of a stream's cut units, and the prefix's: one block a query
+// head, a lane for four columns, the parts dealt to the warps.
+template <typename T, int D, int QT>
+__global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_constant__ AttendArgs a,
+                                                               const __grid_constant__ PrefixParts parts,
+                                                               const __grid_constant__ RowsPlan plan) {
+  constexpr int D4 = D / 4, QN = 8 * QT;
+  __shared__ float2 ml_s[8];
+  __shared__ float4 o_s[8][D4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int N = a.G / a.H, b = (int)(blockIdx.x / (unsigned)a.G), gq = (int)(blockIdx.x - (unsigned)b * a.G);
+  const int h = gq / N, j = gq - h * N, qc = j / QN, q = j - qc * QN;
+  Stream st(a, plan.qchunks);
+  st.seek(a, b);
+  const int ub = h * plan.qchunks + qc, tb = stream_tiles(a, b);
+  const int64_t x = st.base + (int64_t)ub * tb, u = (int64_t)b * st.upb + ub;
+  const int c0 = st.cta_of(x, plan.ctas), c1 = st.cta_of(x + tb - 1, plan.ctas);
+  if (plan.final && c0 == c1) return;             // written out by that CTA
+  const int nr = c1 - c0 + 1;
+  int np = 0, p0 = 0, pu = 0, prow = 0;
+  if (parts.plan.ctas) {
+    const int64_t r = (int64_t)b * N + j;
+    const int blk = (int)(r / parts.plan.block_rows);
+    prow = (int)(r - (int64_t)blk * parts.plan.block_rows);
+    pu = h * parts.plan.blocks + blk;
+    p0 = parts.plan.cta_of((int64_t)pu * parts.plan.nkt);
+    np = parts.plan.cta_of((int64_t)(pu + 1) * parts.plan.nkt - 1) - p0 + 1;
+  }
+  float m = kNegInf, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = warp; i < nr + np; i += 8) {
+    float2 ml;
+    const float4* src;
+    if (i < nr) {
+      const int64_t slot = plan.slot(u, c0 + i, i == 0) * QN + q;
+      ml = plan.part_ml[slot];
+      src = reinterpret_cast<const float4*>(plan.part_o) + slot * D4 + lane;
+    } else {
+      const int64_t slot = parts.plan.slot(pu, p0 + i - nr, i == nr) * parts.plan.block_rows;
+      ml = parts.ml[slot + prow];
+      src = reinterpret_cast<const float4*>(parts.o) + slot * D4 + (int64_t)lane * parts.plan.block_rows + prow;
+    }
+    // a part without rows has left no O; a NaN sum passes on
+    const float4 v = ml.y != 0.f && lane < D4 ? *src : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2_approx(m - nm), w = ml.x == nm ? 1.f : ex2_approx(ml.x - nm);
+    m = nm;
+    l = l * f + (ml.y != 0.f ? ml.y * w : 0.f);
+    o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
+  }
+  if (lane == 0) ml_s[warp] = make_float2(m, l);
+  if (lane < D4) o_s[warp][lane] = o;
+  __syncthreads();
+  if (warp != 0 || lane >= D4) return;
+  for (int w = 1; w < 8; ++w) {
+    const float2 ml = ml_s[w];
+    const float4 v = o_s[w][lane];
+    const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2_approx(m - nm), y = ml.x == nm ? 1.f : ex2_approx(ml.x - nm);
+    m = nm;
+    l = l * f + ml.y * y;
+    o = make_float4(o.x * f + v.x * y, o.y * f + v.y * y, o.z * f + v.z * y, o.w * f + v.w * y);
+  }
+  write_out<T>(a, b, gq, 4 * lane, m, l, o);
 }
 
 template <typename T, int D, int QT, bool PEND>
-cudaError_t launch_one(const AttendArgs& a, const PrefixParts& parts, int sms, cudaStream_t s) {
-  const int N = a.G / a.H;
-  const int qchunks = (N + 8 * QT - 1) / (8 * QT);
-  const int64_t units = (int64_t)a.B * a.H * qchunks;
-  const int64_t tiles = ((int64_t)a.P + 15) / 16 + ((int64_t)a.n + 15) / 16 + 1 + parts.plan.ctas / a.H;
-  // Split a unit's rows over a cluster until the GPU has about 16 warps an SM
+cudaError_t launch_one(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int sms, cudaStream_t s) {
+  if (plan.ctas) {
+    attend_rows_kernel<T, D, QT, PEND, true><<<plan.ctas, kThreads, 0, s>>>(a, parts, plan);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    attend_rows_join_kernel<T, D, QT><<<(unsigned)((int64_t)a.B * a.G), 256, 0, s>>>(a, parts, plan);
+    return cudaGetLastError();
+  }
+  const int64_t units = (int64_t)a.B * a.H * plan.qchunks;
+  const int64_t tiles = rows_tiles(a.n, a.P, a.k_new, a.pend) + parts.plan.ctas / a.H;
+  // Split a unit's tiles over a cluster until the GPU has about 12 warps an SM
   // or a warp has one tile.
   int C = 1;
   while (C < 16 && units * C * kWarps < (int64_t)sms * 12 && (int64_t)C * kWarps < tiles) C *= 2;
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  auto kernel = attend_rows_kernel<T, D, QT, PEND>;
+  auto kernel = attend_rows_kernel<T, D, QT, PEND, false>;
   if (C > 8) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
@@ -464,22 +681,38 @@ cudaError_t launch_one(const AttendArgs& a, const PrefixParts& parts, int sms, c
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, parts, qchunks);
+  return cudaLaunchKernelEx(&cfg, kernel, a, parts, plan);
 }
 
 template <typename T, int D, bool PEND>
-cudaError_t launch_q(const AttendArgs& a, const PrefixParts& parts, int sms, cudaStream_t s) {
-  return a.G / a.H <= 8 ? launch_one<T, D, 1, PEND>(a, parts, sms, s) : launch_one<T, D, 2, PEND>(a, parts, sms, s);
+cudaError_t launch_q(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int sms, cudaStream_t s) {
+  return rows_qt(a.G / a.H) == 1 ? launch_one<T, D, 1, PEND>(a, parts, plan, sms, s)
+                                 : launch_one<T, D, 2, PEND>(a, parts, plan, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, int D, int dtype, int sms, cudaStream_t s) {
+RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool pend, bool prefix_parts, int sms) {
+  RowsPlan pl{};
+  const int qt = rows_qt(G / H);
+  pl.qn = 8 * qt;
+  pl.qchunks = (G / H + pl.qn - 1) / pl.qn;
+  pl.units = (int64_t)B * H * pl.qchunks;
+  pl.final = !prefix_parts;
+  const int64_t ctas = (int64_t)sms * stream_ctas_per_sm(D), total = pl.units * rows_tiles(n, P, has_new, pend);
+  if (total >= ctas * kWarps * kStreamTiles && (int64_t)B * G <= 0x7FFFFFFF) pl.ctas = (int)ctas;
+  return pl;
+}
+
+size_t RowsPlan::o_bytes(int D) const { return (size_t)slots() * qn * D * 4; }
+size_t RowsPlan::bytes(int D) const { return ctas ? o_bytes(D) + (size_t)slots() * qn * 8 : 0; }
+
+cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int D, int dtype, int sms, cudaStream_t s) {
   if (a.pend)   // a handle's rows are fp16
-    return D == 64 ? launch_q<__half, 64, true>(a, parts, sms, s) : launch_q<__half, 128, true>(a, parts, sms, s);
+    return D == 64 ? launch_q<__half, 64, true>(a, parts, plan, sms, s) : launch_q<__half, 128, true>(a, parts, plan, sms, s);
   if (dtype == kBf16)
-    return D == 64 ? launch_q<__nv_bfloat16, 64, false>(a, parts, sms, s) : launch_q<__nv_bfloat16, 128, false>(a, parts, sms, s);
-  return D == 64 ? launch_q<__half, 64, false>(a, parts, sms, s) : launch_q<__half, 128, false>(a, parts, sms, s);
+    return D == 64 ? launch_q<__nv_bfloat16, 64, false>(a, parts, plan, sms, s) : launch_q<__nv_bfloat16, 128, false>(a, parts, plan, sms, s);
+  return D == 64 ? launch_q<__half, 64, false>(a, parts, plan, sms, s) : launch_q<__half, 128, false>(a, parts, plan, sms, s);
 }
 
 }  // namespace kvx

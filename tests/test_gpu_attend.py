@@ -56,6 +56,44 @@ def test_splits(kvx, B, H, n):
     ref.check_attend(kvx, q, **rows)
 
 
+@pytest.mark.parametrize("B,N,H,D,n,dtype", [(40, 4, 8, 128, 401, F16), (9, 3, 4, 128, 3001, BF16), (3, 12, 2, 128, 17000, F16),
+                                            (1, 40, 1, 64, 60001, BF16), (600, 1, 4, 64, 90, F16), (1500, 2, 4, 128, 3, F16),
+                                            (5, 16, 8, 64, 5000, F16)])
+@pytest.mark.parametrize("new", [False, True])
+def test_many_tiles(kvx, B, N, H, D, n, dtype, new):
+    """Work cut into ranges that begin and end inside a unit; even lengths, then ragged ones with empty sequences."""
+    q, rows = _make(B, N, H, D, n=n, new=new, dtype=dtype, seed=n)
+    ref.check_attend(kvx, q, **rows)
+    lens = torch.randint(0, n + 1, (B,), dtype=torch.int32, device="cuda")
+    lens[B // 2:B // 2 + 40] = 0
+    lens[0] = n
+    ref.check_attend(kvx, q, lens=lens, **rows)
+
+
+@pytest.mark.parametrize("B,N,H,D,n,P", [(40, 4, 8, 128, 401, 700), (200, 3, 4, 64, 400, 300), (30, 20, 8, 128, 350, 1000),
+                                        (1, 4, 2, 128, 30000, 20000)])
+def test_many_tiles_with_prefix(kvx, B, N, H, D, n, P):
+    q, rows = _make(B, N, H, D, n=n, P=P, new=True, seed=P)
+    ref.check_attend(kvx, q, **rows)
+    lens = torch.randint(0, n + 1, (B,), dtype=torch.int32, device="cuda")
+    plens = torch.randint(0, P + 1, (B,), dtype=torch.int32, device="cuda")
+    lens[B // 3:B // 2], plens[B // 4:B // 2] = 0, 0
+    ref.check_attend(kvx, q, lens=lens, prefix_lens=plens, **rows)
+
+
+def test_prefix_strides_of_all_kinds(kvx):
+    """Padded rows, heads inside rows, and a prefix that is the same for all heads (which TMA cannot describe)."""
+    q, rows = _make(40, 4, 3, 128, P=300, seed=14)
+    k, v = rows["prefix_k"], rows["prefix_v"]
+    padded = torch.zeros(3, 309, 136, dtype=F16, device="cuda")
+    padded[:, :300, :128] = k
+    inside = torch.zeros(300, 3, 136, dtype=F16, device="cuda")
+    inside[:, :, :128] = v.transpose(0, 1)
+    ref.check_attend(kvx, q, prefix_k=padded[:, :300, :128], prefix_v=inside[:, :, :128].transpose(0, 1))
+    same = [x[:1].expand(3, -1, -1) for x in (k, v)]
+    ref.check_attend(kvx, q, prefix_k=same[0], prefix_v=same[1])
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("B,N,P", [(1, 1, 1), (1, 4, 127), (5, 3, 128), (2, 4, 129), (32, 4, 1000), (40, 4, 257), (7, 40, 640),
@@ -172,7 +210,7 @@ def test_offsets_past_32_bits(kvx):
     ref.check_attend(kvx, q, **rows)
 
 
-@pytest.mark.parametrize("B,n,P", [(2, 300, 0), (2, 30, 100), (40, 30, 1000), (150, 0, 1000)])
+@pytest.mark.parametrize("B,n,P", [(2, 300, 0), (2, 30, 100), (40, 30, 1000), (150, 0, 1000), (40, 2100, 0), (40, 2100, 600)])
 def test_repeat_streams_and_graphs(kvx, B, n, P):
     """The same bits call after call, on another stream, and from two captured graphs that replay together."""
     q, rows = _make(B, 4, 2, 128, n=n, P=P, seed=12)
@@ -222,3 +260,21 @@ def test_parts_join_by_lse(kvx, B):
     # three roundings to fp16 (both parts and the whole) and the weights' half steps in the prefix part
     assert (joined - out).abs().max() <= 4 * 2.0 ** -11 * max(a.abs().max(), b.abs().max(), 1.0)
     torch.testing.assert_close(total, lse, rtol=1e-6, atol=1e-5)
+
+
+def test_bounded_wait_leaves_nan(kvx):
+    """A wait that runs out cannot reach the return code: NaN in every output instead, and the next call is unaffected.
+    The library's test hook leaves one copy unissued; nothing faults or hangs."""
+    import time
+    q, rows = _make(40, 4, 1, 128, P=300, seed=15)      # one block on one CTA or two: all of it depends on the first tile
+    want, wlse = ref.check_attend(kvx, q, **rows)
+    out, lse = torch.zeros_like(q), torch.zeros_like(wlse)
+    assert kvx.lib().kvevict_test_stall_next_step(None) == kvx.OK
+    t0 = time.time()
+    kvx.attend(q, out, lse=lse, **rows)
+    torch.cuda.synchronize()
+    assert 0.5 < time.time() - t0 < 10.0
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    kvx.attend(q, out, lse=lse, **rows)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
