@@ -134,7 +134,33 @@ struct CacheRows {
 };
 int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s);
 
+// A launch in clusters of `cluster` CTAs; overlap: it may begin before the kernel
+// launched before it on the stream has ended (that one calls launch_dependents,
+// this one wait_for_primary before it uses its results).
+template <typename... K, typename... A>
+cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, size_t smem, int cluster, bool overlap,
+                         cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = overlap ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------- device helpers
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 16 bytes that no later access of this SM wants: past L1.
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   uint4 r;

@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   const AttendArgs& a = p.a;
   const int N = a.G / a.H;
 
+  launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(full(s), 1);
@@ -627,10 +628,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const PrefixPlan& pl = p.plan;
   const AttendArgs& a = p.a;
   int u = blockIdx.x;
+  bool mine = true;
   if (pl.units >= pl.ctas) {
     const int64_t x = pl.start(blockIdx.x + 1);
     u = (int)(x / pl.nkt);
-    if (x == (int64_t)u * pl.nkt || pl.start(blockIdx.x) > (int64_t)u * pl.nkt) return;
+    mine = x != (int64_t)u * pl.nkt && pl.start(blockIdx.x) <= (int64_t)u * pl.nkt;
   }
   const int64_t u0 = (int64_t)u * pl.nkt;
   __shared__ float2 ml_s[8][32];
@@ -639,11 +641,13 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int N = a.G / a.H, R = pl.block_rows, h = u / pl.blocks;
   const int rr = blockIdx.y * 32 + lane, d4 = blockIdx.z * 8;
   const int c0 = pl.cta_of(u0), c1 = pl.cta_of(u0 + pl.nkt - 1);
-  if (c0 == c1) return;                      // one CTA's alone: written out by it
+  wait_for_primary();                        // in every block: this kernel ends after the one before it
+  if (!mine || c0 == c1) return;             // one CTA's alone: written out by it
   float m = kNegInf, l = 0.f;
   float4 o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
   for (int c = c0 + warp; c <= c1; c += 8) {
     const int64_t slot = pl.slot(u, c, c == c0);
     const float2 ml = p.part_ml[slot * R + rr];
@@ -651,7 +655,6 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     float4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = src[i * R];
-    if (ml.y == 0.f) continue;               // no rows, no O; a NaN sum passes on
     const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2(m - nm), g = ml.x == nm ? 1.f : ex2(ml.x - nm);
     m = nm;
     l = l * f + ml.y * g;
@@ -708,8 +711,8 @@ cudaError_t launch_px(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pr
   kernel<<<p.plan.ctas, kPxThreads, PxGeo<D>::SMEM, s>>>(kmap, vmap, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.plan.final || !p.plan.shared_blocks()) return e;
-  attend_join_kernel<T, D><<<dim3(std::min(p.plan.units, p.plan.ctas - 1), p.plan.block_rows / 32, D / 32), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  const dim3 grid(std::min(p.plan.units, p.plan.ctas - 1), p.plan.block_rows / 32, D / 32);
+  return launch_after(attend_join_kernel<T, D>, grid, 256, 0, 1, true, s, p);
 }
 
 // Strides between heads and rows, where a dimension of one has none of its own.

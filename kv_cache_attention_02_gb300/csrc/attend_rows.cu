@@ -49,12 +49,14 @@ namespace cg = cooperative_groups;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr int kStreamTiles = 4;        // a stream from this many tiles a warp on
+constexpr int kStreamTiles = 4;        // a stream from this many tiles of 16 rows a warp on
 
-constexpr int stream_ctas_per_sm(int D) { return D == 64 ? 4 : 2; }
+constexpr int stream_ctas_per_sm(int D) { return D == 64 ? 3 : 2; }
 int rows_qt(int N) { return N <= 8 ? 1 : 2; }
-int64_t rows_tiles(int n, int P, bool has_new, bool pend) {   // of a unit, at most
-  return ((int64_t)P + 15) / 16 + ((int64_t)n + pend + 15) / 16 + has_new;
+// Rows a warp takes at a time: 32 where a stream's registers hold them.
+constexpr int tile_rows(int qt, bool stream) { return stream && qt == 1 ? 32 : 16; }
+int64_t rows_tiles(int rows, int n, int P, bool has_new, bool pend) {   // of a unit, at most
+  return ((int64_t)P + rows - 1) / rows + ((int64_t)n + pend + rows - 1) / rows + has_new;
 }
 
 template <typename T>
@@ -79,24 +81,24 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// 16 consecutive rows of one source; row r is there if bit r of `live` is set.
+// 16 KG consecutive rows of one source; row r is there if bit r of `live` is set.
 template <typename T>
 struct Tile {
   const T* k;
   const T* v;
   int64_t ks, vs;
   uint32_t live;
-  int moved;    // rows from here on await the re-rotation by -1 (16: none)
+  int moved;    // rows from here on await the re-rotation by -1 (32: none)
 };
 
-template <typename T, int D>
+template <typename T, int D, int KG>
 struct Rows {
   static constexpr int KC = D / 32;   // 16-byte pieces of a key row in one lane
   static constexpr int VH = D / 64;   // 64-wide column groups of a value row
 
-  __device__ __forceinline__ static void load_k(uint4 (&kr)[2][KC], const Tile<T>& t, int g, int c) {
+  __device__ __forceinline__ static void load_k(uint4 (&kr)[2 * KG][KC], const Tile<T>& t, int g, int c) {
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
+    for (int nt = 0; nt < 2 * KG; ++nt) {
       const int r = g + 8 * nt;
       const T* p = t.k + (int64_t)r * t.ks + 8 * c;
       const bool on = (t.live >> r) & 1u;
@@ -104,9 +106,9 @@ struct Rows {
       for (int i = 0; i < KC; ++i) kr[nt][i] = on ? ld_stream16(p + 32 * i) : make_uint4(0, 0, 0, 0);
     }
   }
-  __device__ __forceinline__ static void load_v(uint4 (&vr)[VH][4], const Tile<T>& t, int g, int c) {
+  __device__ __forceinline__ static void load_v(uint4 (&vr)[VH][4 * KG], const Tile<T>& t, int g, int c) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4 * KG; ++j) {
       const int r = 2 * c + (j & 1) + 8 * (j >> 1);
       const T* p = t.v + (int64_t)r * t.vs + 8 * g;
       const bool on = (t.live >> r) & 1u;
@@ -115,6 +117,17 @@ struct Rows {
     }
   }
 };
+
+// Starts a tile towards L2 (rows that lie together only). Used for a range's
+// second tile, whose loads the registers cannot yet take; for every tile it
+// costs more than it hides (7 ragged sequences of up to 65521 rows: 138 us so,
+// 150 us prefetching throughout, 139 us not at all).
+template <typename T, int D>
+__device__ __forceinline__ void prefetch_tile(const Tile<T>& t, int lane) {
+  const int rows = 32 - __clz(t.live);           // up to the last one that is there
+  if (t.ks == D && t.vs == D && lane < 2 && rows)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lane ? t.v : t.k), "r"(rows * D * 2) : "memory");
+}
 
 // A cache key whose compaction is pending: rotated by -1 position, every
 // product and sum rounded to fp32, then to fp16, as the step kernel and the
@@ -144,22 +157,27 @@ __device__ __forceinline__ void write_out(const AttendArgs& a, int b, int gq, in
   if (d == 0 && a.lse) a.lse[(int64_t)b * a.G + gq] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-// Rows of sequence b: shared (np) and own (n), and the tiles of 16 they make.
+// Rows of sequence b: shared (np) and own (n), and the tiles of TR that they make.
+template <int TR>
 struct SeqRows {
   int np, n, tp, to;
   __device__ __forceinline__ SeqRows(const AttendArgs& a, int b) {
     np = a.plens ? max(0, min(a.plens[b], a.P)) : a.P;
     n = a.lens ? max(0, min(a.lens[b], a.n)) : a.n;
-    tp = (np + 15) >> 4;
-    to = (n + (a.pend ? 1 : 0) + 15) >> 4;   // an evicted row may still be in place
+    tp = (np + TR - 1) / TR;
+    to = (n + (a.pend ? 1 : 0) + TR - 1) / TR;   // an evicted row may still be in place
   }
   // of a unit; in a stream every unit has at least one
   __device__ __forceinline__ int tiles(const AttendArgs& a) const { return tp + to + (a.k_new ? 1 : 0); }
 };
-__device__ __forceinline__ int stream_tiles(const AttendArgs& a, int b) { return max(1, SeqRows(a, b).tiles(a)); }
+template <int TR>
+__device__ __forceinline__ int stream_tiles(const AttendArgs& a, int b) {
+  return max(1, SeqRows<TR>(a, b).tiles(a));
+}
 
 // Where sequences lie in the row of all units' tiles (warp-collective): the
 // total, and the first tile of the sequence that `find` returns.
+template <int TR>
 struct Stream {
   int64_t total, base;
   int upb;                                    // units of a sequence
@@ -167,12 +185,12 @@ struct Stream {
   __device__ __forceinline__ Stream(const AttendArgs& a, int qchunks) : total(0), base(0), upb(a.H * qchunks) {
     even = !a.lens && !a.plens;
     if (even) {
-      total = (int64_t)a.B * upb * stream_tiles(a, 0);
+      total = (int64_t)a.B * upb * stream_tiles<TR>(a, 0);
       return;
     }
     const int lane = threadIdx.x & 31;
     int64_t sum = 0;
-    for (int b = lane; b < a.B; b += 32) sum += stream_tiles(a, b);
+    for (int b = lane; b < a.B; b += 32) sum += stream_tiles<TR>(a, b);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     total = sum * upb;
@@ -180,7 +198,7 @@ struct Stream {
   // The sequence that tile x belongs to (x < total).
   __device__ __forceinline__ int find(const AttendArgs& a, int64_t x) {
     if (even) {
-      const int64_t per = (int64_t)upb * stream_tiles(a, 0);
+      const int64_t per = (int64_t)upb * stream_tiles<TR>(a, 0);
       const int b = (int)(x / per);
       base = b * per;
       return b;
@@ -190,7 +208,7 @@ struct Stream {
   // Sets base for sequence b.
   __device__ __forceinline__ void seek(const AttendArgs& a, int b) {
     if (even)
-      base = (int64_t)b * upb * stream_tiles(a, 0);
+      base = (int64_t)b * upb * stream_tiles<TR>(a, 0);
     else
       (void)scan(a, [&](int s, int64_t) { return s == b; });
   }
@@ -203,7 +221,7 @@ struct Stream {
     const int lane = threadIdx.x & 31;
     int64_t run = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int64_t own = b0 + lane < a.B ? stream_tiles(a, b0 + lane) : 0;
+      const int64_t own = b0 + lane < a.B ? stream_tiles<TR>(a, b0 + lane) : 0;
       int64_t incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -222,13 +240,14 @@ struct Stream {
   }
 };
 
-// QT: groups of 8 query heads (1 or 2). STREAM: two CTAs an SM at D = 128, four
-// at 64 (the registers of a warp's 16 rows, its sums and its queries).
+// QT: groups of 8 query heads (1 or 2). STREAM: two CTAs an SM at D = 128, three
+// at 64 (the registers of a warp's tile, its sums and its queries).
 template <typename T, int D, int QT, bool PEND, bool STREAM>
 __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
     attend_rows_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ PrefixParts parts,
                        const __grid_constant__ RowsPlan plan) {
-  using R = Rows<T, D>;
+  constexpr int TR = tile_rows(QT, STREAM), KG = TR / 16;
+  using R = Rows<T, D, KG>;
   constexpr int KC = R::KC, VH = R::VH, QN = 8 * QT;
   __shared__ __align__(16) float part_o[kWarps][QN][D];
   __shared__ float part_ml[kWarps][QN][2];
@@ -240,14 +259,18 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int N = a.G / a.H, qchunks = plan.qchunks;
 
+  launch_dependents();
   int b, ub;                                      // sequence, unit of it
   int64_t at = 0, end = 0, base = 0;              // STREAM: next tile, the range's end, the sequence's first tile
   int upb = 0;
   if (STREAM) {
-    Stream st(a, qchunks);
+    Stream<TR> st(a, qchunks);
     at = st.start(blockIdx.x, plan.ctas);
     end = st.start(blockIdx.x + 1, plan.ctas);
-    if (at >= end) return;
+    if (at >= end) {
+      wait_for_primary();
+      return;
+    }
     b = st.find(a, at);
     base = st.base;
     upb = st.upb;
@@ -259,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   }
 
   while (true) {                                  // STREAM: the range's segments, each of one unit
-  const SeqRows seq(a, b);
+  const SeqRows<TR> seq(a, b);
   int first = 0, total = seq.tiles(a);
   bool whole = true;
   int64_t slot = 0;
@@ -291,25 +314,25 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   }
   auto tile_at = [&](int t) {
     Tile<T> x;
-    x.moved = 16;
+    x.moved = 32;
     if (t < tp) {
       x.ks = a.pk_stride[1];
       x.vs = a.pv_stride[1];
-      x.k = static_cast<const T*>(a.pk) + h * a.pk_stride[0] + (int64_t)t * 16 * x.ks;
-      x.v = static_cast<const T*>(a.pv) + h * a.pv_stride[0] + (int64_t)t * 16 * x.vs;
-      const int left = np - t * 16;
-      x.live = left >= 16 ? 0xFFFFu : (1u << left) - 1u;
+      x.k = static_cast<const T*>(a.pk) + h * a.pk_stride[0] + (int64_t)t * TR * x.ks;
+      x.v = static_cast<const T*>(a.pv) + h * a.pv_stride[0] + (int64_t)t * TR * x.vs;
+      const int left = np - t * TR;
+      x.live = left >= TR ? ~0u >> (32 - TR) : (1u << left) - 1u;
     } else if (t < tp + to) {
-      const int r0 = (t - tp) * 16;
+      const int r0 = (t - tp) * TR;
       x.ks = a.k_stride[2];
       x.vs = a.v_stride[2];
       x.k = static_cast<const T*>(a.k) + b * a.k_stride[0] + h * a.k_stride[1] + (int64_t)r0 * x.ks;
       x.v = static_cast<const T*>(a.v) + b * a.v_stride[0] + h * a.v_stride[1] + (int64_t)r0 * x.vs;
       const int left = n - r0;
-      x.live = left >= 16 ? 0xFFFFu : left > 0 ? (1u << left) - 1u : 0u;
+      x.live = left >= TR ? ~0u >> (32 - TR) : left > 0 ? (1u << left) - 1u : 0u;
       if (PEND && e >= 0) {
-        if (e >= r0 && e < r0 + 16) x.live &= ~(1u << (e - r0));
-        x.moved = max(0, min(16, e - r0 + 1));
+        if (e >= r0 && e < r0 + TR) x.live &= ~(1u << (e - r0));
+        x.moved = max(0, min(32, e - r0 + 1));
       }
     } else {
       x.ks = x.vs = 0;
@@ -322,12 +345,13 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
 
   const int stride = C * kWarps;
   int t = first + rank * kWarps + warp;
-  uint4 kr[2][KC], vr[VH][4];
+  uint4 kr[2 * KG][KC], vr[VH][4 * KG];
   Tile<T> cur{};
   if (t < total) {
     cur = tile_at(t);
     R::load_k(kr, cur, g, c);
     R::load_v(vr, cur, g, c);
+    if (t + stride < total) prefetch_tile<T, D>(tile_at(t + stride), lane);
   }
   // queries: row g of each group of 8, in the keys' order
   uint4 qr[QT][KC];
@@ -350,27 +374,29 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   for (int x = 0; x < VH * 4 * QT * 4; ++x) (&acc[0][0][0][0])[x] = 0.f;
 
   while (t < total) {
-    if (PEND && cur.moved < 16) {
+    if (PEND && cur.moved < TR) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < 2 * KG; ++nt)
         if (g + 8 * nt >= cur.moved) {
 #pragma unroll
           for (int i = 0; i < KC / 2; ++i)
             rotate_back(kr[nt][i], kr[nt][i + KC / 2], a.rope_c + 32 * i + 8 * c, a.rope_s + 32 * i + 8 * c);
         }
     }
-    float s[2][4];
+    float s[2 * KG][4];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
+    for (int nt = 0; nt < 2 * KG; ++nt)
 #pragma unroll
       for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
+    // (the groups of eight keys are independent: one's sum hides the other's)
 #pragma unroll
-      for (int i = 0; i < KC; ++i)
+    for (int i = 0; i < KC; ++i)
 #pragma unroll
-        for (int w = 0; w < 4; w += 2)
+      for (int w = 0; w < 4; w += 2)
+#pragma unroll
+        for (int nt = 0; nt < 2 * KG; ++nt)
           mma16816<T>(s[nt], word(qr[0][i], w), QT > 1 ? word(qr[QT - 1][i], w) : 0u, word(qr[0][i], w + 1),
                       QT > 1 ? word(qr[QT - 1][i], w + 1) : 0u, word(kr[nt][i], w), word(kr[nt][i], w + 1));
-    }
     const uint32_t live = cur.live;
     t += stride;
     const bool more = t < total;
@@ -380,14 +406,14 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
     }
 
     // weights of this lane's rows 2c, 2c + 1, 2c + 8, 2c + 9 for query g (and g + 8)
-    uint32_t hi[QT][2], lo[QT][2];
+    uint32_t hi[QT][2 * KG], lo[QT][2 * KG];
     float grow[QT];
     bool up = false;
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
       float tm = kNegInf;
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < 2 * KG; ++nt)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float& v = s[nt][2 * i + x];
@@ -424,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
     for (int i = 0; i < QT; ++i) {
       const float base = m[i] == kNegInf ? 0.f : m[i];   // nothing so far: every weight 2^-inf = 0
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
+      for (int nt = 0; nt < 2 * KG; ++nt) {
         const float p0 = ex2_approx(s[nt][2 * i] - base), p1 = ex2_approx(s[nt][2 * i + 1] - base);
         l[i] += p0 + p1;
         hi[i][nt] = pack16<T>(p0, p1);
@@ -433,18 +459,21 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
       }
     }
 #pragma unroll
-    for (int x = 0; x < VH; ++x)
+    for (int k = 0; k < KG; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w0 = word(vr[x][0], j), w1 = word(vr[x][1], j), w2 = word(vr[x][2], j), w3 = word(vr[x][3], j);
-        const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-        const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+      for (int x = 0; x < VH; ++x)
 #pragma unroll
-        for (int i = 0; i < QT; ++i) {
-          mma16816<T>(acc[x][j][i], a0, a1, a2, a3, hi[i][0], hi[i][1]);
-          mma16816<T>(acc[x][j][i], a0, a1, a2, a3, lo[i][0], lo[i][1]);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w0 = word(vr[x][4 * k], j), w1 = word(vr[x][4 * k + 1], j);
+          const uint32_t w2 = word(vr[x][4 * k + 2], j), w3 = word(vr[x][4 * k + 3], j);
+          const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+          const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+          for (int i = 0; i < QT; ++i) {
+            mma16816<T>(acc[x][j][i], a0, a1, a2, a3, hi[i][2 * k], hi[i][2 * k + 1]);
+            mma16816<T>(acc[x][j][i], a0, a1, a2, a3, lo[i][2 * k], lo[i][2 * k + 1]);
+          }
         }
-      }
     if (more) R::load_v(vr, cur, g, c);
   }
 
@@ -453,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   // one warp's sums as if it were another tile; the query rows b * N + q0 + q may
   // lie in two blocks.
   if (!STREAM && parts.plan.ctas) {
+    wait_for_primary();
     const int RB = parts.plan.block_rows;
     const int64_t r0 = (int64_t)b * N + q0;
     for (int64_t blk = r0 / RB; blk <= (r0 + nq - 1) / RB; ++blk) {
@@ -582,6 +612,9 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   cluster.sync();   // no CTA leaves while another reads its shared memory
   break;
   }
+  // the join that follows waits for this kernel alone: it ends after the
+  // prefix's, beside whose last CTAs it may have run
+  if (STREAM) wait_for_primary();
 }
 
 // Joins the parts of a stream's cut units, and the prefix's: one block a query
@@ -596,11 +629,13 @@ __global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int N = a.G / a.H, b = (int)(blockIdx.x / (unsigned)a.G), gq = (int)(blockIdx.x - (unsigned)b * a.G);
   const int h = gq / N, j = gq - h * N, qc = j / QN, q = j - qc * QN;
-  Stream st(a, plan.qchunks);
+  constexpr int TR = tile_rows(QT, true);
+  Stream<TR> st(a, plan.qchunks);
   st.seek(a, b);
-  const int ub = h * plan.qchunks + qc, tb = stream_tiles(a, b);
+  const int ub = h * plan.qchunks + qc, tb = stream_tiles<TR>(a, b);
   const int64_t x = st.base + (int64_t)ub * tb, u = (int64_t)b * st.upb + ub;
   const int c0 = st.cta_of(x, plan.ctas), c1 = st.cta_of(x + tb - 1, plan.ctas);
+  wait_for_primary();                             // in every block: this kernel ends after the one before it
   if (plan.final && c0 == c1) return;             // written out by that CTA
   const int nr = c1 - c0 + 1;
   int np = 0, p0 = 0, pu = 0, prow = 0;
@@ -614,25 +649,38 @@ __global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_cons
   }
   float m = kNegInf, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = warp; i < nr + np; i += 8) {
-    float2 ml;
-    const float4* src;
-    if (i < nr) {
-      const int64_t slot = plan.slot(u, c0 + i, i == 0) * QN + q;
-      ml = plan.part_ml[slot];
-      src = reinterpret_cast<const float4*>(plan.part_o) + slot * D4 + lane;
-    } else {
-      const int64_t slot = parts.plan.slot(pu, p0 + i - nr, i == nr) * parts.plan.block_rows;
-      ml = parts.ml[slot + prow];
-      src = reinterpret_cast<const float4*>(parts.o) + slot * D4 + (int64_t)lane * parts.plan.block_rows + prow;
+  for (int i0 = warp; i0 < nr + np; i0 += 32) {    // four parts' loads under way at once
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + 8 * k;
+      ml[k] = make_float2(kNegInf, 0.f);
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < nr) {
+        const int64_t slot = plan.slot(u, c0 + i, i == 0) * QN + q;
+        ml[k] = plan.part_ml[slot];
+        if (lane < D4) v[k] = reinterpret_cast<const float4*>(plan.part_o)[slot * D4 + lane];
+      } else if (i < nr + np) {
+        const int64_t slot = parts.plan.slot(pu, p0 + i - nr, i == nr) * parts.plan.block_rows;
+        ml[k] = parts.ml[slot + prow];
+        if (lane < D4)
+          v[k] = reinterpret_cast<const float4*>(parts.o)[slot * D4 + (int64_t)lane * parts.plan.block_rows + prow];
+      }
     }
-    // a part without rows has left no O; a NaN sum passes on
-    const float4 v = ml.y != 0.f && lane < D4 ? *src : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2_approx(m - nm), w = ml.x == nm ? 1.f : ex2_approx(ml.x - nm);
+    float nm = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) nm = fmaxf(nm, ml[k].x);
+    const float f = m == nm ? 1.f : ex2_approx(m - nm);
     m = nm;
-    l = l * f + (ml.y != 0.f ? ml.y * w : 0.f);
-    o = make_float4(o.x * f + v.x * w, o.y * f + v.y * w, o.z * f + v.z * w, o.w * f + v.w * w);
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = ml[k].x == nm ? 1.f : ex2_approx(ml[k].x - nm);
+      l = fmaf(ml[k].y, w, l);
+      o = make_float4(fmaf(v[k].x, w, o.x), fmaf(v[k].y, w, o.y), fmaf(v[k].z, w, o.z), fmaf(v[k].w, w, o.w));
+    }
   }
   if (lane == 0) ml_s[warp] = make_float2(m, l);
   if (lane < D4) o_s[warp][lane] = o;
@@ -652,36 +700,23 @@ __global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_cons
 template <typename T, int D, int QT, bool PEND>
 cudaError_t launch_one(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int sms, cudaStream_t s) {
   if (plan.ctas) {
-    attend_rows_kernel<T, D, QT, PEND, true><<<plan.ctas, kThreads, 0, s>>>(a, parts, plan);
-    const cudaError_t e = cudaGetLastError();
+    // either may begin while the kernel before it ends (the first one only where
+    // that is the prefix's of this call)
+    const cudaError_t e = launch_after(attend_rows_kernel<T, D, QT, PEND, true>, plan.ctas, kThreads, 0, 1,
+                                       parts.plan.ctas > 0, s, a, parts, plan);
     if (e != cudaSuccess) return e;
-    attend_rows_join_kernel<T, D, QT><<<(unsigned)((int64_t)a.B * a.G), 256, 0, s>>>(a, parts, plan);
-    return cudaGetLastError();
+    return launch_after(attend_rows_join_kernel<T, D, QT>, dim3((unsigned)((int64_t)a.B * a.G)), 256, 0, 1, true, s, a,
+                        parts, plan);
   }
   const int64_t units = (int64_t)a.B * a.H * plan.qchunks;
-  const int64_t tiles = rows_tiles(a.n, a.P, a.k_new, a.pend) + parts.plan.ctas / a.H;
+  const int64_t tiles = rows_tiles(tile_rows(QT, false), a.n, a.P, a.k_new, a.pend) + parts.plan.ctas / a.H;
   // Split a unit's tiles over a cluster until the GPU has about 12 warps an SM
   // or a warp has one tile.
   int C = 1;
-  while (C < 16 && units * C * kWarps < (int64_t)sms * 12 && (int64_t)C * kWarps < tiles) C *= 2;
+  while (C < 8 && units * C * kWarps < (int64_t)sms * 12 && (int64_t)C * kWarps < tiles) C *= 2;
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  auto kernel = attend_rows_kernel<T, D, QT, PEND, false>;
-  if (C > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(units * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = C;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, parts, plan);
+  return launch_after(attend_rows_kernel<T, D, QT, PEND, false>, dim3((unsigned)(units * C)), kThreads, 0, C,
+                      parts.plan.ctas > 0, s, a, parts, plan);
 }
 
 template <typename T, int D, bool PEND>
@@ -699,7 +734,7 @@ RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool 
   pl.qchunks = (G / H + pl.qn - 1) / pl.qn;
   pl.units = (int64_t)B * H * pl.qchunks;
   pl.final = !prefix_parts;
-  const int64_t ctas = (int64_t)sms * stream_ctas_per_sm(D), total = pl.units * rows_tiles(n, P, has_new, pend);
+  const int64_t ctas = (int64_t)sms * stream_ctas_per_sm(D), total = pl.units * rows_tiles(16, n, P, has_new, pend);
   if (total >= ctas * kWarps * kStreamTiles && (int64_t)B * G <= 0x7FFFFFFF) pl.ctas = (int)ctas;
   return pl;
 }

@@ -159,6 +159,25 @@ def test_strides(kvx, B, P):
     assert (big[:, :N * H] == 3).all() and (big[B] == 3).all()
 
 
+@pytest.mark.parametrize("which", ["k", "v", "k_new", "v_new", "prefix_k", "prefix_v", "row"])
+@pytest.mark.parametrize("B,n", [(3, 70), (60, 400)])
+def test_buffers_at_16_bytes(kvx, B, n, which):
+    """Buffers and strides that are multiples of 16 bytes but not of 32."""
+    q, rows = _make(B, 4, 2, 128, n=n, P=100, new=True, seed=3)
+    for name in ([which] if which != "row" else ["k", "v"]):
+        x = rows[name]
+        pad = torch.zeros(*x.shape[:-1], 136, dtype=F16, device="cuda")
+        if which == "row":
+            pad[..., :128] = x
+            rows[name] = pad[..., :128]
+        else:
+            flat = torch.zeros(x.numel() + 8, dtype=F16, device="cuda")
+            flat[8:] = x.reshape(-1)
+            rows[name] = flat[8:].view(x.shape)
+            assert rows[name].data_ptr() % 32 == 16
+    ref.check_attend(kvx, q, **rows)
+
+
 @pytest.mark.parametrize("scale", [1e-3, 0.5, 3.0])
 @pytest.mark.parametrize("P", [0, 260])
 @pytest.mark.parametrize("B", [2, 40])
