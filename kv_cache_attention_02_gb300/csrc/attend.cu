@@ -141,10 +141,13 @@ int attend_check(const kvevict_attention* d) {
 
 // The prefix kernel's plan; not used (the row kernel reads the shared rows
 // itself) where TMA cannot describe the rows.
-PrefixPlan plan_prefix(const kvevict_attention* d, bool own, int sms) {
+PrefixPlan plan_prefix(const kvevict_attention* d, bool own, int64_t rows, int sms) {
   const bool fit = d->prefix > 0 && prefix_strides_fit(d->prefix_k_stride, d->n_kv_heads, d->prefix, d->head_dim) &&
                    prefix_strides_fit(d->prefix_v_stride, d->n_kv_heads, d->prefix, d->head_dim);
-  return fit ? prefix_plan(d->batch, d->n_heads, d->n_kv_heads, d->head_dim, d->prefix, own, sms) : PrefixPlan{};
+  return fit
+             ? prefix_plan(d->batch, d->n_heads, d->n_kv_heads, d->prefix, own,
+                           rows * d->batch * d->n_kv_heads, sms)
+             : PrefixPlan{};
 }
 
 }  // namespace
@@ -219,7 +222,8 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
   a.scale2 = (float)(scale * 1.4426950408889634);
   const int D = d->head_dim;
   PrefixArgs p{};
-  p.plan = plan_prefix(d, rows || a.n > 0 || a.k_new, dev.sms);
+  const int own = a.n + (a.k_new ? 1 : 0);             // rows of a sequence, at most
+  p.plan = plan_prefix(d, rows || own, own, dev.sms);
   const bool alone = p.plan.ctas && p.plan.final;      // the prefix is all there is
   RowsPlan rp{};
   if (!alone)
@@ -283,7 +287,7 @@ extern "C" int kvevict_attend_workspace(const kvevict_attention* args, int32_t w
     if (int rc = kvx::device_info(&dev)) return rc;
     const int B = args->batch, G = args->n_heads, H = args->n_kv_heads, D = args->head_dim;
     const bool own = with_cache || args->n > 0 || args->k_new;
-    const kvx::PrefixPlan pp = kvx::plan_prefix(args, own, dev.sms);
+    const kvx::PrefixPlan pp = kvx::plan_prefix(args, own, 0, dev.sms);
     *bytes = pp.bytes(D);
     if (pp.ctas && !own) return KVEVICT_OK;
     // a handle's rows are not in the description: as many as there can be

@@ -54,24 +54,37 @@ struct AttendArgs {
   float scale2;            // scale * log2(e): logits in base-2 units
 };
 
-// How the prefix kernel's work is cut: (key head, query block, 128-key tile)
-// triples in that order, one contiguous range per CTA. ctas = 0: not used.
+// How the prefix kernel's work, the (key head, query block, 128-key tile)
+// triples in that order, is cut into one contiguous range per CTA: evenly, or
+// (split) each block alone into as many ranges, where that uses nearly as many
+// CTAs: a range that begins a second block pays for its start twice. ctas = 0:
+// not used.
 struct PrefixPlan {
-  int ctas, pair, blocks, block_rows, nkt, units, final;   // units = H * blocks; final: no own rows to join
+  int ctas, split, pair, blocks, block_rows, nkt, units, final;   // units = H * blocks; final: no own rows to join
+  int64_t slots;                // parts that the workspace has room for
   __host__ __device__ int64_t total() const { return (int64_t)units * nkt; }
-  __host__ __device__ int64_t start(int c) const { return c * total() / ctas; }
-  __host__ __device__ int cta_of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total()); }
+  __host__ __device__ int64_t start(int c) const {
+    if (!split) return c * total() / ctas;
+    const int u = c / split;
+    return (int64_t)u * nkt + (int64_t)(c - u * split) * nkt / split;
+  }
+  __host__ __device__ int cta_of(int64_t x) const {
+    if (!split) return (int)(((x + 1) * ctas - 1) / total());
+    const int u = (int)(x / nkt);
+    return u * split + (int)(((x - (int64_t)u * nkt + 1) * split - 1) / nkt);
+  }
   // Workspace slot of the part of block u that CTA c computed. Where whole
   // blocks go straight to the output, a CTA leaves at most two parts: one that
   // begins inside a block and one that begins with it.
   __host__ __device__ int64_t slot(int u, int c, bool from_start) const { return final ? 2 * c + from_start : u + c; }
-  int64_t slots() const { return final ? 2 * (int64_t)ctas : (int64_t)units + ctas; }
   size_t o_bytes(int D) const;
   size_t bytes(int D) const;
   bool shared_blocks() const;   // whether any block is cut
 };
 bool prefix_strides_fit(const int64_t* stride, int H, int P, int D);
-PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int sms);
+// own_rows: rows of all sequences and key heads that the row kernel reads beside
+// it (the workspace does not depend on their number); own: whether there are any.
+PrefixPlan prefix_plan(int B, int G, int H, int P, bool own, int64_t own_rows, int sms);
 
 // The parts of the prefix's attention in the workspace: per slot O as
 // [D/4][block_rows] float4 and (m, l) as [block_rows] float2, base-2 units.

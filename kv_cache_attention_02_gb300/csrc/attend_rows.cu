@@ -49,7 +49,9 @@ namespace cg = cooperative_groups;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr int kStreamTiles = 4;        // a stream from this many tiles of 16 rows a warp on
+// A stream from this many tiles of 16 rows a warp on; beside a prefix from fewer,
+// as a cluster that has its sums would wait for the prefix's parts.
+constexpr int kStreamTiles = 8, kBesideTiles = 1;
 
 constexpr int stream_ctas_per_sm(int D) { return D == 64 ? 3 : 2; }
 int rows_qt(int N) { return N <= 8 ? 1 : 2; }
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
     at = st.start(blockIdx.x, plan.ctas);
     end = st.start(blockIdx.x + 1, plan.ctas);
     if (at >= end) {
-      wait_for_primary();
+      if ((int)blockIdx.x == plan.ctas - 1) wait_for_primary();
       return;
     }
     b = st.find(a, at);
@@ -612,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   cluster.sync();   // no CTA leaves while another reads its shared memory
   break;
   }
-  // the join that follows waits for this kernel alone: it ends after the
-  // prefix's, beside whose last CTAs it may have run
-  if (STREAM) wait_for_primary();
+  // The join that follows waits for this kernel alone, so its last CTA ends after
+  // the prefix's kernel, beside which the others may have come and gone.
+  if (STREAM && (int)blockIdx.x == plan.ctas - 1) wait_for_primary();
 }
 
 // Joins the parts of a stream's cut units, and the prefix's: one block a query
@@ -735,7 +737,7 @@ RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool 
   pl.units = (int64_t)B * H * pl.qchunks;
   pl.final = !prefix_parts;
   const int64_t ctas = (int64_t)sms * stream_ctas_per_sm(D), total = pl.units * rows_tiles(16, n, P, has_new, pend);
-  if (total >= ctas * kWarps * kStreamTiles && (int64_t)B * G <= 0x7FFFFFFF) pl.ctas = (int)ctas;
+  if (total >= ctas * kWarps * (prefix_parts ? kBesideTiles : kStreamTiles) && (int64_t)B * G <= 0x7FFFFFFF) pl.ctas = (int)ctas;
   return pl;
 }
 
