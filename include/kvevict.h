@@ -375,8 +375,8 @@ int kvevict_prefill_scores_noalloc(const uint16_t* keys, int32_t heads, int32_t 
  * Both hold no state and allocate nothing on the device. They run on the
  * device that is current, which must be the one the pointers belong to. Their
  * descriptions are read before the call returns. Strides count elements; the
- * last dimension is contiguous, pointers start on a 16-byte boundary and every
- * stride is a multiple of 16 bytes. Calls may overlap on any streams and
+ * last dimension is contiguous, pointers start on a 16-byte boundary and the
+ * stride of every dimension of more than one entry is a multiple of 16 bytes. Calls may overlap on any streams and
  * threads as long as none writes what another uses. */
 #define KVEVICT_DTYPE_FP16 0
 #define KVEVICT_DTYPE_BF16 1

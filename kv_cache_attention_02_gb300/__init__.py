@@ -133,7 +133,7 @@ def prefill_scores_noalloc(keys, colsum, stream=None):
 _QK = struct.Struct("=8i f i d q 7Q 12q")
 _ATTENTION = struct.Struct("=8i f i 12Q 18q Q")
 _WORKSPACE_AT, _WORKSPACE_BYTES_AT = 40 + 11 * 8, 40 + 12 * 8 + 18 * 8   # offsets in kvevict_attention
-_NO2, _NO3 = (0, 0), (0, 0, 0)
+_NO3, _NO4 = (0, 0, 0), (0, 0, 0, 0)     # strides of tensors that are not there
 
 
 def _torch():
@@ -157,18 +157,16 @@ def _wrong(name, t, shape, dtype, device):
     if t.dtype is not dtype:
         return ValueError(f"{name} must be {dtype}, got {t.dtype}")
     return ValueError(f"{name} must be on the current CUDA device, got {t.device}" if not t.is_cuda or t.get_device() != device
-                      else f"{name} must be contiguous" if t.stride()[-1] == 1 or t.shape[-1] == 1
+                      else f"{name} must be contiguous" if t.stride()[-1] == 1
                       else f"the last dimension of {name} must be contiguous")
 
 
 def _strided(name, t, shape, dtype, device):
-    """Pointer and strides of one call's tensor, after the checks; a dimension of one row has no stride to speak of."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
-        raise _wrong(name, t, shape, dtype, device)
+    """Pointer and strides of one call's tensor, after the checks."""
     stride = t.stride()
-    if stride[-1] != 1 and shape[-1] != 1:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or stride[-1] != 1:
         raise _wrong(name, t, shape, dtype, device)
-    return t.data_ptr(), [0 if n == 1 else s for n, s in zip(shape, stride)][:-1]
+    return t.data_ptr(), stride
 
 
 def _dense(name, t, shape, dtype, device):
@@ -214,7 +212,7 @@ def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None
         raise ValueError("q and k must be fp16, bf16 or fp32, q_out and k_out fp16 or bf16")
     device, s = _place(torch, some, stream)
     G = H = pq = pqo = pk = pko = 0
-    sq = sqo = sk = sko = _NO3
+    sq = sqo = sk = sko = _NO4
     if q is not None:
         G = q.shape[2]
         pq, sq = _strided("q", q, (B, S, G, D), kind, device)
@@ -229,7 +227,7 @@ def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None
     args = _QK.pack(_IN[kind], _OUT[kind_out], _IN[wt] if wt is not None else DTYPE_FP32, B, S, G, H, D, eps, 0, rope_theta,
                     pos0, pq, pk, pqo, pko, _dense("q_weight", q_weight, (D,), wt, device),
                     _dense("k_weight", k_weight, (D,), wt, device),
-                    _dense("positions", positions, (B, S), torch.int32, device), *sq, *sk, *sqo, *sko)
+                    _dense("positions", positions, (B, S), torch.int32, device), *sq[:3], *sk[:3], *sqo[:3], *sko[:3])
     rc = lib().kvevict_qk_norm_rope(args, s)
     if rc:
         _check(rc)
@@ -269,8 +267,8 @@ def _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens
         H = k_new.shape[1]
     device, s = _place(torch, q, stream)
     pk = pv = pkn = pvn = ppk = ppv = 0
-    sk = sv = _NO3
-    skn = svn = spk = spv = _NO2
+    sk = sv = _NO4
+    skn = svn = spk = spv = _NO3
     pq, sq = _strided("q", q, (B, G, D), kind, device)
     po, so = _strided("out", out, (B, G, D), kind, device)
     if n:
@@ -285,7 +283,9 @@ def _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens
     return _ATTENTION.pack(
         _OUT[kind], B, G, H, D, n, prefix, 0, scale or 0.0, 0, pq, po, _dense("lse", lse, (B, G), torch.float32, device), pk, pv,
         _dense("lens", lens, (B,), torch.int32, device), pkn, pvn, ppk, ppv,
-        _dense("prefix_lens", prefix_lens, (B,), torch.int32, device), 0, *sq, *so, *sk, *sv, *skn, *svn, *spk, *spv, 0), s
+        _dense("prefix_lens", prefix_lens, (B,), torch.int32, device), 0,
+        sq[0], sq[1], so[0], so[1], sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], skn[0], skn[1], svn[0], svn[1], spk[0], spk[1],
+        spv[0], spv[1], 0), s
 
 
 def _with_workspace(args, cache, device, stream):

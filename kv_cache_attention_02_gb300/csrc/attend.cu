@@ -27,10 +27,11 @@ int cuda_result(cudaError_t e, const char* what) {
 
 bool aligned(const void* p, unsigned to = 16) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// Whole 16-byte pieces between the entries of every dimension that has several.
 template <int K>
-bool strides16(const int64_t (&s)[K], int elem) {
+bool strides16(const int64_t (&s)[K], const int32_t (&extent)[K], int elem) {
   for (int i = 0; i < K; ++i)
-    if ((s[i] * elem) & 15) return false;
+    if (extent[i] > 1 && ((s[i] * elem) & 15)) return false;
   return true;
 }
 
@@ -72,11 +73,12 @@ int qk_run(const kvevict_qk* d, cudaStream_t s) {
   if (d->n_heads > 0 && (!d->q || !d->q_out)) return invalid("q and q_out must not be null");
   if (d->n_kv_heads > 0 && (!d->k || !d->k_out)) return invalid("k and k_out must not be null");
   const int ie = d->in_dtype == kFp32 ? 4 : 2;
-  if (d->n_heads > 0 && (!aligned(d->q) || !aligned(d->q_out) || !strides16(d->q_stride, ie) ||
-                         !strides16(d->q_out_stride, 2)))
+  const int32_t qx[3] = {d->batch, d->seq, d->n_heads}, kx[3] = {d->batch, d->seq, d->n_kv_heads};
+  if (d->n_heads > 0 && (!aligned(d->q) || !aligned(d->q_out) || !strides16(d->q_stride, qx, ie) ||
+                         !strides16(d->q_out_stride, qx, 2)))
     return invalid("q and q_out must be 16-byte aligned, with strides of multiples of 16 bytes");
-  if (d->n_kv_heads > 0 && (!aligned(d->k) || !aligned(d->k_out) || !strides16(d->k_stride, ie) ||
-                            !strides16(d->k_out_stride, 2)))
+  if (d->n_kv_heads > 0 && (!aligned(d->k) || !aligned(d->k_out) || !strides16(d->k_stride, kx, ie) ||
+                            !strides16(d->k_out_stride, kx, 2)))
     return invalid("k and k_out must be 16-byte aligned, with strides of multiples of 16 bytes");
   const unsigned we = d->weight_dtype == kFp32 ? 4 : 2;
   if (!aligned(d->q_weight, we) || !aligned(d->k_weight, we) || !aligned(d->positions, 4))
@@ -165,15 +167,17 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
   if (d->n > 0 && (!d->k || !d->v)) return invalid("k and v must not be null with n > 0");
   if (d->prefix > 0 && (!d->prefix_k || !d->prefix_v)) return invalid("prefix_k and prefix_v must not be null with prefix > 0");
   if (!d->k_new != !d->v_new) return invalid("k_new and v_new must be given together");
-  if (!aligned(d->q) || !aligned(d->out) || !strides16(d->q_stride, 2) || !strides16(d->out_stride, 2))
+  const int32_t qx[2] = {d->batch, d->n_heads}, kx[3] = {d->batch, d->n_kv_heads, d->n};
+  const int32_t nx[2] = {d->batch, d->n_kv_heads}, px[2] = {d->n_kv_heads, d->prefix};
+  if (!aligned(d->q) || !aligned(d->out) || !strides16(d->q_stride, qx, 2) || !strides16(d->out_stride, qx, 2))
     return invalid("q and out must be 16-byte aligned, with strides of multiples of 16 bytes");
-  if (d->n > 0 && (!aligned(d->k) || !aligned(d->v) || !strides16(d->k_stride, 2) || !strides16(d->v_stride, 2)))
+  if (d->n > 0 && (!aligned(d->k) || !aligned(d->v) || !strides16(d->k_stride, kx, 2) || !strides16(d->v_stride, kx, 2)))
     return invalid("k and v must be 16-byte aligned, with strides of multiples of 16 bytes");
-  if (d->k_new && (!aligned(d->k_new) || !aligned(d->v_new) || !strides16(d->k_new_stride, 2) ||
-                   !strides16(d->v_new_stride, 2)))
+  if (d->k_new && (!aligned(d->k_new) || !aligned(d->v_new) || !strides16(d->k_new_stride, nx, 2) ||
+                   !strides16(d->v_new_stride, nx, 2)))
     return invalid("k_new and v_new must be 16-byte aligned, with strides of multiples of 16 bytes");
-  if (d->prefix > 0 && (!aligned(d->prefix_k) || !aligned(d->prefix_v) || !strides16(d->prefix_k_stride, 2) ||
-                        !strides16(d->prefix_v_stride, 2)))
+  if (d->prefix > 0 && (!aligned(d->prefix_k) || !aligned(d->prefix_v) || !strides16(d->prefix_k_stride, px, 2) ||
+                        !strides16(d->prefix_v_stride, px, 2)))
     return invalid("prefix_k and prefix_v must be 16-byte aligned, with strides of multiples of 16 bytes");
   if (!aligned(d->lse, 4) || !aligned(d->lens, 4) || !aligned(d->prefix_lens, 4))
     return invalid("lse, lens and prefix_lens must be 4-byte aligned");

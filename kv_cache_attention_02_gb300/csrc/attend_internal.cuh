@@ -30,6 +30,7 @@ struct QkArgs {
   int64_t pos0;
   int B, S, G, H;          // G query heads, H key heads
   int parts, per_part;     // a token's heads go to `parts` warps, per_part heads each
+  int runs;                // sequences whose tokens of one position go to one warp
   uint64_t turn[64];       // theta^(-2i/D) / 2 pi, as a 64-bit fraction of a turn
 };
 
@@ -159,14 +160,17 @@ cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int threads, size_t sm
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = overlap ? 2 : 1;
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = cluster;
+    at[cfg.numAttrs].val.clusterDim.y = 1;
+    at[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  if (overlap) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -25,6 +25,7 @@ namespace kvx {
 namespace {
 
 constexpr int kQkThreads = 256;
+constexpr int kQkCtas = 3;     // CTAs an SM
 
 template <typename T>
 struct Chunk8;   // 8 consecutive elements
@@ -77,11 +78,13 @@ __device__ __forceinline__ float weight_at(const void* w, int dtype, int i) {
   return __half2float(static_cast<const __half*>(w)[i]);
 }
 
-template <typename TI, typename TO, int D>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkArgs a) {
+// RUNS: several sequences a unit (a loop more; 3% of the call with 40 heads).
+template <typename TI, typename TO, int D, bool RUNS>
+__global__ void __launch_bounds__(kQkThreads, kQkCtas) qk_norm_rope_kernel(const QkArgs a) {
   constexpr int LPH = D / 16;            // lanes of a head
   constexpr int HPW = 32 / LPH;          // heads a warp takes at a time
   constexpr int APL = 8 / HPW;           // angles a lane computes
+  constexpr int kAhead = sizeof(TI) == 4 ? 1 : 2;   // groups of heads whose loads are under way (32 bytes a lane each in fp32)
   __shared__ float w_s[2][D];
   __shared__ uint64_t turn_s[D / 2];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -94,29 +97,50 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkArgs a
   __syncthreads();
 
   const int heads = a.G + a.H;
-  const int64_t units = (int64_t)a.B * a.S * a.parts;
+  // a unit: `runs` sequences' tokens of one position (one token where the caller
+  // gives positions), per_part of their heads
+  const int64_t chunks = (a.B + a.runs - 1) / a.runs, units = a.S * chunks * a.parts;
   const int64_t step = (int64_t)gridDim.x * (kQkThreads / 32);
   for (int64_t u = (int64_t)blockIdx.x * (kQkThreads / 32) + (tid >> 5); u < units; u += step) {
-    const int64_t token = u / a.parts;
-    const int part = (int)(u - token * a.parts);
-    const int64_t b = token / a.S, s = token - b * a.S;
-    const int h_end = min(heads, (part + 1) * a.per_part);
-    const TI* qb = static_cast<const TI*>(a.q) + b * a.q_stride[0] + s * a.q_stride[1];
-    const TI* kb = static_cast<const TI*>(a.k) + b * a.k_stride[0] + s * a.k_stride[1];
-    TO* qo = static_cast<TO*>(a.q_out) + b * a.qo_stride[0] + s * a.qo_stride[1];
-    TO* ko = static_cast<TO*>(a.k_out) + b * a.ko_stride[0] + s * a.ko_stride[1];
-    auto src = [&](int h) {
-      return (h < a.G ? qb + (int64_t)h * a.q_stride[2] : kb + (int64_t)(h - a.G) * a.k_stride[2]) + 8 * c;
+    const int64_t rest = u / a.parts;
+    const int part = (int)(u - rest * a.parts);
+    const int64_t chunk = rest / a.S, s = rest - chunk * a.S;
+    const int b0 = (int)chunk * (RUNS ? a.runs : 1), b_end = RUNS ? min(a.B, b0 + a.runs) : b0 + 1;
+    const int h0 = part * a.per_part + sub, h_end = min(heads, (part + 1) * a.per_part);
+    const TI* const qs = static_cast<const TI*>(a.q) + b0 * a.q_stride[0] + s * a.q_stride[1] + 8 * c;
+    const TI* const ks = static_cast<const TI*>(a.k) + b0 * a.k_stride[0] + s * a.k_stride[1] + 8 * c;
+    TO* const qd = static_cast<TO*>(a.q_out) + b0 * a.qo_stride[0] + s * a.qo_stride[1] + 8 * c;
+    TO* const kd = static_cast<TO*>(a.k_out) + b0 * a.ko_stride[0] + s * a.ko_stride[1] + 8 * c;
+    auto src = [&](int b, int h) {
+      const TI* p = h < a.G ? qs + (int64_t)h * a.q_stride[2] : ks + (int64_t)(h - a.G) * a.k_stride[2];
+      return RUNS ? p + (b - b0) * (h < a.G ? a.q_stride[0] : a.k_stride[0]) : p;
     };
-    int h = part * a.per_part + sub;
-    Chunk8<TI> lo{}, hi{};
-    if (h < h_end) {
-      const TI* p = src(h);
-      lo.load(p);
-      hi.load(p + D / 2);
+    // kAhead groups of heads under way: the loads of one ahead of the others' arithmetic
+    Chunk8<TI> lo[kAhead], hi[kAhead];
+    int fb = b0, fh = h0;                // the next to load
+    auto next = [&](int& b, int& h) {
+      h += HPW;
+      if (RUNS && h - sub >= h_end) {
+        h = h0;
+        ++b;
+      }
+    };
+    auto fetch = [&](int k) {
+      if ((!RUNS || fb < b_end) && fh < h_end) {
+        const TI* p = src(fb, fh);
+        lo[k].load(p);
+        hi[k].load(p + D / 2);
+      }
+      next(fb, fh);
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      lo[k] = {};
+      hi[k] = {};
+      fetch(k);
     }
-    // the token's angles: lane (c, sub) computes pairs 8c + sub*APL .. + APL - 1
-    const int64_t pos = a.positions ? (int64_t)a.positions[token] : a.pos0 + s;
+    // the position's angles: lane (c, sub) computes pairs 8c + sub*APL .. + APL - 1
+    const int64_t pos = a.positions ? (int64_t)a.positions[(int64_t)b0 * a.S + s] : a.pos0 + s;
     float cs[8], sn[8];
     {
       float mc[APL], ms[APL];
@@ -131,60 +155,67 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkArgs a
         sn[i] = __shfl_sync(~0u, ms[i % APL], (i / APL) * LPH + c);
       }
     }
-    for (int h0 = part * a.per_part; h0 < h_end; h0 += HPW) {
-      float x[8], y[8];
-      lo.get(x);
-      hi.get(y);
-      const bool live = h < h_end;
-      const int hn = h + HPW;
-      if (hn < h_end) {                    // the next heads' loads, ahead of this pass's arithmetic
-        const TI* p = src(hn);
-        lo.load(p);
-        hi.load(p + D / 2);
-      }
-      const int kind = h < a.G ? 0 : 1;
-      float ss = 0.f;
+    int b = b0, h = h0;
+    auto done = [&] { return RUNS ? b >= b_end : h - sub >= h_end; };
+    while (!done()) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+      for (int k = 0; k < kAhead; ++k) {
+        if (done()) break;
+        float x[8], y[8];
+        lo[k].get(x);
+        hi[k].get(y);
+        const bool live = h < h_end;
+        fetch(k);
+        const int kind = h < a.G ? 0 : 1;
+        float ss = 0.f;
 #pragma unroll
-      for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
-      if (kind ? a.k_weight != nullptr : a.q_weight != nullptr) {
-        const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = x[i] * r * w_s[kind][8 * c + i];
-          y[i] = y[i] * r * w_s[kind][D / 2 + 8 * c + i];
+        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
+        if (kind ? a.k_weight != nullptr : a.q_weight != nullptr) {
+          const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = x[i] * r * w_s[kind][8 * c + i];
+            y[i] = y[i] * r * w_s[kind][D / 2 + 8 * c + i];
+          }
         }
-      }
-      if (live) {
-        uint32_t ol[4], oh[4];
+        if (live) {
+          uint32_t ol[4], oh[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 2 * i;
-          ol[i] = pack16<TO>(x[e] * cs[e] - y[e] * sn[e], x[e + 1] * cs[e + 1] - y[e + 1] * sn[e + 1]);
-          oh[i] = pack16<TO>(x[e] * sn[e] + y[e] * cs[e], x[e + 1] * sn[e + 1] + y[e + 1] * cs[e + 1]);
+          for (int i = 0; i < 4; ++i) {
+            const int e = 2 * i;
+            ol[i] = pack16<TO>(x[e] * cs[e] - y[e] * sn[e], x[e + 1] * cs[e + 1] - y[e + 1] * sn[e + 1]);
+            oh[i] = pack16<TO>(x[e] * sn[e] + y[e] * cs[e], x[e + 1] * sn[e + 1] + y[e + 1] * cs[e + 1]);
+          }
+          TO* d = kind ? kd + (int64_t)(h - a.G) * a.ko_stride[2] : qd + (int64_t)h * a.qo_stride[2];
+          if (RUNS) d += (b - b0) * (kind ? a.ko_stride[0] : a.qo_stride[0]);
+          *reinterpret_cast<uint4*>(d) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+          *reinterpret_cast<uint4*>(d + D / 2) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
         }
-        TO* d = (kind ? ko + (int64_t)(h - a.G) * a.ko_stride[2] : qo + (int64_t)h * a.qo_stride[2]) + 8 * c;
-        *reinterpret_cast<uint4*>(d) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-        *reinterpret_cast<uint4*>(d + D / 2) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+        next(b, h);
       }
-      h = hn;
     }
   }
 }
 
-template <typename TI, typename TO>
+template <typename TI, typename TO, bool RUNS>
 cudaError_t launch_d(const QkArgs& a, int D, unsigned grid, cudaStream_t s) {
   if (D == 64)
-    qk_norm_rope_kernel<TI, TO, 64><<<grid, kQkThreads, 0, s>>>(a);
+    qk_norm_rope_kernel<TI, TO, 64, RUNS><<<grid, kQkThreads, 0, s>>>(a);
   else
-    qk_norm_rope_kernel<TI, TO, 128><<<grid, kQkThreads, 0, s>>>(a);
+    qk_norm_rope_kernel<TI, TO, 128, RUNS><<<grid, kQkThreads, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_r(const QkArgs& a, int D, unsigned grid, cudaStream_t s) {
+  return a.runs > 1 ? launch_d<TI, TO, true>(a, D, grid, s) : launch_d<TI, TO, false>(a, D, grid, s);
 }
 
 template <typename TI>
 cudaError_t launch_o(const QkArgs& a, int D, int out_dtype, unsigned grid, cudaStream_t s) {
-  return out_dtype == kBf16 ? launch_d<TI, __nv_bfloat16>(a, D, grid, s) : launch_d<TI, __half>(a, D, grid, s);
+  return out_dtype == kBf16 ? launch_r<TI, __nv_bfloat16>(a, D, grid, s) : launch_r<TI, __half>(a, D, grid, s);
 }
 
 }  // namespace
@@ -193,15 +224,20 @@ cudaError_t launch_qk_norm_rope(QkArgs a, int D, int in_dtype, int out_dtype, in
   const int hpw = 512 / D;   // heads a warp takes at a time
   const int64_t tokens = (int64_t)a.B * a.S;
   const int heads = a.G + a.H;
-  // With few tokens a token's heads are spread over warps (the call is one
-  // latency); with many, one warp takes all of a token's heads and computes
-  // its angles once.
-  const bool spread = tokens < (int64_t)sms * 32;
-  a.per_part = spread ? hpw : heads;
+  // Units for every resident warp twice over: a token's heads are spread over
+  // warps while there are fewer tokens. With few heads several sequences' tokens
+  // of one position go to one warp, which computes their angles once (where
+  // positions are pos0 + s): 64 x 4096 tokens of 4 + 4 heads, D = 64, 148 -> 102
+  // us; with 40 heads the angles cost nothing, and this order of the rows 4%.
+  const int groups = (heads + hpw - 1) / hpw;
+  const int64_t goal = (int64_t)2 * sms * kQkCtas * (kQkThreads / 32);
+  const int parts = (int)std::min<int64_t>((goal + tokens - 1) / tokens, groups);
+  a.per_part = (groups + parts - 1) / parts * hpw;
   a.parts = (heads + a.per_part - 1) / a.per_part;
-  const int64_t units = tokens * a.parts;
+  a.runs = a.positions ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({tokens / goal, 8 / groups, a.B}));
+  const int64_t units = (int64_t)a.S * ((a.B + a.runs - 1) / a.runs) * a.parts;
   const int64_t blocks = (units + kQkThreads / 32 - 1) / (kQkThreads / 32);
-  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * 8);
+  const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sms * kQkCtas);
   if (in_dtype == kFp32) return launch_o<float>(a, D, out_dtype, grid, s);
   if (in_dtype == kBf16) return launch_o<__nv_bfloat16>(a, D, out_dtype, grid, s);
   return launch_o<__half>(a, D, out_dtype, grid, s);

@@ -30,7 +30,7 @@ def _qk(kvx, **kw):
     (dict(head_dim=96), "head_dim"), (dict(eps=-1.0), "eps"), (dict(eps=float("nan")), "eps"),
     (dict(rope_theta=0.0), "rope_theta"), (dict(rope_theta=float("inf")), "rope_theta"), (dict(reserved=1), "reserved"),
     (dict(q=0), "null"), (dict(k_out=0), "null"), (dict(q=A + 8), "aligned"), (dict(k_out=A + 2), "aligned"),
-    (dict(q_stride=(64, 64, 60)), "16 bytes"), (dict(k_out_stride=(4, 64, 64)), "16 bytes"),
+    (dict(q_stride=(64, 64, 60)), "16 bytes"), (dict(batch=2, k_out_stride=(4, 64, 64)), "16 bytes"),
     (dict(q_weight=A + 1), "aligned"), (dict(positions=A + 2), "aligned"),
 ])
 def test_qk_refusals(kvx, kw, frag):
@@ -64,7 +64,7 @@ def _attention(kvx, **kw):
     (dict(k=0), "null"), (dict(v=0), "null"), (dict(prefix_v=0), "null"), (dict(k_new=0), "together"),
     (dict(v_new=0), "together"), (dict(q=A + 2), "aligned"), (dict(v=A + 8), "aligned"), (dict(k_new=A + 4), "aligned"),
     (dict(prefix_k=A + 2), "aligned"), (dict(out_stride=(64, 4)), "16 bytes"), (dict(k_stride=(64, 64, 68)), "16 bytes"),
-    (dict(v_new_stride=(4, 64)), "16 bytes"), (dict(prefix_v_stride=(64, 1)), "16 bytes"), (dict(lens=A + 1), "4-byte"),
+    (dict(batch=2, v_new_stride=(4, 64)), "16 bytes"), (dict(prefix_v_stride=(64, 1)), "16 bytes"), (dict(lens=A + 1), "4-byte"),
     (dict(lse=A + 2), "4-byte"),
 ])
 def test_attend_refusals(kvx, kw, frag):
