@@ -147,7 +147,7 @@ PrefixPlan plan_prefix(const kvevict_attention* d, bool own, int64_t rows, int s
   const bool fit = d->prefix > 0 && prefix_strides_fit(d->prefix_k_stride, d->n_kv_heads, d->prefix, d->head_dim) &&
                    prefix_strides_fit(d->prefix_v_stride, d->n_kv_heads, d->prefix, d->head_dim);
   return fit
-             ? prefix_plan(d->batch, d->n_heads, d->n_kv_heads, d->prefix, own,
+             ? prefix_plan(d->batch, d->n_heads, d->n_kv_heads, d->head_dim, d->prefix, own,
                            rows * d->batch * d->n_kv_heads, sms)
              : PrefixPlan{};
 }

@@ -85,7 +85,7 @@ struct PrefixPlan {
 bool prefix_strides_fit(const int64_t* stride, int H, int P, int D);
 // own_rows: rows of all sequences and key heads that the row kernel reads beside
 // it (the workspace does not depend on their number); own: whether there are any.
-PrefixPlan prefix_plan(int B, int G, int H, int P, bool own, int64_t own_rows, int sms);
+PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int64_t own_rows, int sms);
 
 // The parts of the prefix's attention in the workspace: per slot O as
 // [D/4][block_rows] float4 and (m, l) as [block_rows] float2, base-2 units.

@@ -231,6 +231,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
+    if (lane < 2)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &vmap : &kmap)) : "memory");
     int s = 0, held = 0;               // next stage, stages in flight (at most NS)
     uint32_t phase = 0;
     bool ok = true, stall = p.stall && blockIdx.x == 0;   // test hook: CTA 0's first tile never comes
@@ -749,10 +751,16 @@ bool prefix_strides_fit(const int64_t* stride, int H, int P, int D) {
   return hs >= D && rs >= D && hs < ((int64_t)1 << 39) && rs < ((int64_t)1 << 39);
 }
 
-PrefixPlan prefix_plan(int B, int G, int H, int P, bool own, int64_t own_rows, int sms) {
+PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int64_t own_rows, int sms) {
   PrefixPlan pl{};
   const int64_t rows = (int64_t)B * (G / H);
-  if (B < 2 || rows < 16 || P < 256) return pl;   // ctas = 0: the row kernel reads the prefix itself
+  // The row kernel reads the prefix once for every sequence (and 16 query heads),
+  // from L2 after the first: faster while that is little, as this kernel and its
+  // join take 11 us at least. 32 query heads on 8 of 128, no own rows, this | that:
+  // 8 x 2048 shared rows (67 MB) 12 | 13 us, 16 x 2048 12 | 21, 4 x 2048 12 | 10; beside
+  // 256 own rows 16 x 2048 (134 MB) 16 | 22, 8 x 2048 16 | 14.
+  const int64_t visits = (int64_t)B * ((G / H + 15) / 16);
+  if (visits < 2 || visits * H * P * D * 4 < (own ? 96 : 64) * 1000000ll) return pl;   // ctas = 0
   pl.pair = rows <= kT;
   pl.block_rows = pl.pair ? kT : 2 * kT;
   pl.blocks = (int)((rows + pl.block_rows - 1) / pl.block_rows);
@@ -765,7 +773,9 @@ PrefixPlan prefix_plan(int B, int G, int H, int P, bool own, int64_t own_rows, i
   // together (32 sequences on 16384 shared + 512 own rows: 35 us against
   // 44 us one after the other).
   const int64_t share = own_rows > 0 ? sms * total / (total + own_rows / kT) : sms;
-  const int64_t most = std::max<int64_t>(1, std::min(share, pl.pair ? (total + 1) / 2 : total));
+  // (not so few that a CTA has more than 16 tiles, or two blocks, beside little)
+  const int64_t least = std::max<int64_t>(pl.units, total / 16);
+  const int64_t most = std::min<int64_t>({std::max(share, least), sms, pl.pair ? (total + 1) / 2 : total});
   pl.ctas = (int)most;
   if (pl.units <= most) {
     const int split = (int)std::min<int64_t>(most / pl.units, pl.nkt);

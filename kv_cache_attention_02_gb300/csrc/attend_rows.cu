@@ -52,11 +52,22 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // A stream from this many tiles of 16 rows a warp on; beside a prefix from fewer,
 // as a cluster that has its sums would wait for the prefix's parts.
 constexpr int kStreamTiles = 8, kBesideTiles = 1;
+// A stream too where a cluster's warps would have this many tiles each: few, long
+// units that a cluster cannot spread over the GPU.
+constexpr int kClusterTiles = 8;
 
 constexpr int stream_ctas_per_sm(int D) { return D == 64 ? 3 : 2; }
 int rows_qt(int N) { return N <= 8 ? 1 : 2; }
 // Rows a warp takes at a time: 32 where a stream's registers hold them.
 constexpr int tile_rows(int qt, bool stream) { return stream && qt == 1 ? 32 : 16; }
+// CTAs of a unit's cluster: its tiles are split while all CTAs are resident
+// together (two an SM: a second wave costs the call's latency again, 8 sequences of
+// 512 rows 7.9 us against 11) and a warp has more than one tile.
+int cluster_ctas(int64_t units, int64_t tiles, int sms) {
+  int C = 1;
+  while (C < 8 && units * C <= sms && (int64_t)C * kWarps < tiles) C *= 2;
+  return C;
+}
 int64_t rows_tiles(int rows, int n, int P, bool has_new, bool pend) {   // of a unit, at most
   return ((int64_t)P + rows - 1) / rows + ((int64_t)n + pend + rows - 1) / rows + has_new;
 }
@@ -182,20 +193,21 @@ __device__ __forceinline__ int stream_tiles(const AttendArgs& a, int b) {
 template <int TR>
 struct Stream {
   int64_t total, base;
+  int ctas;                                   // that have work: never more than there are tiles
   int upb;                                    // units of a sequence
   bool even;                                  // all sequences have as many tiles
-  __device__ __forceinline__ Stream(const AttendArgs& a, int qchunks) : total(0), base(0), upb(a.H * qchunks) {
+  __device__ __forceinline__ Stream(const AttendArgs& a, const RowsPlan& plan) : base(0), upb(a.H * plan.qchunks) {
     even = !a.lens && !a.plens;
-    if (even) {
-      total = (int64_t)a.B * upb * stream_tiles<TR>(a, 0);
-      return;
-    }
-    const int lane = threadIdx.x & 31;
     int64_t sum = 0;
-    for (int b = lane; b < a.B; b += 32) sum += stream_tiles<TR>(a, b);
+    if (even) {
+      sum = (int64_t)a.B * stream_tiles<TR>(a, 0);
+    } else {
+      for (int b = threadIdx.x & 31; b < a.B; b += 32) sum += stream_tiles<TR>(a, b);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    }
     total = sum * upb;
+    ctas = (int)min((int64_t)plan.ctas, total);
   }
   // The sequence that tile x belongs to (x < total).
   __device__ __forceinline__ int find(const AttendArgs& a, int64_t x) {
@@ -214,8 +226,8 @@ struct Stream {
     else
       (void)scan(a, [&](int s, int64_t) { return s == b; });
   }
-  __device__ __forceinline__ int64_t start(int c, int ctas) const { return c * total / ctas; }
-  __device__ __forceinline__ int cta_of(int64_t x, int ctas) const { return (int)(((x + 1) * ctas - 1) / total); }
+  __device__ __forceinline__ int64_t start(int c) const { return c * total / ctas; }
+  __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
 
  private:
   template <typename F>
@@ -266,13 +278,13 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   int64_t at = 0, end = 0, base = 0;              // STREAM: next tile, the range's end, the sequence's first tile
   int upb = 0;
   if (STREAM) {
-    Stream<TR> st(a, qchunks);
-    at = st.start(blockIdx.x, plan.ctas);
-    end = st.start(blockIdx.x + 1, plan.ctas);
-    if (at >= end) {
+    Stream<TR> st(a, plan);
+    if ((int)blockIdx.x >= st.ctas) {
       if ((int)blockIdx.x == plan.ctas - 1) wait_for_primary();
       return;
     }
+    at = st.start(blockIdx.x);
+    end = st.start(blockIdx.x + 1);
     b = st.find(a, at);
     base = st.base;
     upb = st.upb;
@@ -632,11 +644,11 @@ __global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_cons
   const int N = a.G / a.H, b = (int)(blockIdx.x / (unsigned)a.G), gq = (int)(blockIdx.x - (unsigned)b * a.G);
   const int h = gq / N, j = gq - h * N, qc = j / QN, q = j - qc * QN;
   constexpr int TR = tile_rows(QT, true);
-  Stream<TR> st(a, plan.qchunks);
+  Stream<TR> st(a, plan);
   st.seek(a, b);
   const int ub = h * plan.qchunks + qc, tb = stream_tiles<TR>(a, b);
   const int64_t x = st.base + (int64_t)ub * tb, u = (int64_t)b * st.upb + ub;
-  const int c0 = st.cta_of(x, plan.ctas), c1 = st.cta_of(x + tb - 1, plan.ctas);
+  const int c0 = st.cta_of(x), c1 = st.cta_of(x + tb - 1);
   wait_for_primary();                             // in every block: this kernel ends after the one before it
   if (plan.final && c0 == c1) return;             // written out by that CTA
   const int nr = c1 - c0 + 1;
@@ -712,10 +724,7 @@ cudaError_t launch_one(const AttendArgs& a, const PrefixParts& parts, const Rows
   }
   const int64_t units = (int64_t)a.B * a.H * plan.qchunks;
   const int64_t tiles = rows_tiles(tile_rows(QT, false), a.n, a.P, a.k_new, a.pend) + parts.plan.ctas / a.H;
-  // Split a unit's tiles over a cluster until the GPU has about 12 warps an SM
-  // or a warp has one tile.
-  int C = 1;
-  while (C < 8 && units * C * kWarps < (int64_t)sms * 12 && (int64_t)C * kWarps < tiles) C *= 2;
+  const int C = cluster_ctas(units, tiles, sms);
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_after(attend_rows_kernel<T, D, QT, PEND, false>, dim3((unsigned)(units * C)), kThreads, 0, C,
                       parts.plan.ctas > 0, s, a, parts, plan);
@@ -736,8 +745,11 @@ RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool 
   pl.qchunks = (G / H + pl.qn - 1) / pl.qn;
   pl.units = (int64_t)B * H * pl.qchunks;
   pl.final = !prefix_parts;
-  const int64_t ctas = (int64_t)sms * stream_ctas_per_sm(D), total = pl.units * rows_tiles(16, n, P, has_new, pend);
-  if (total >= ctas * kWarps * (prefix_parts ? kBesideTiles : kStreamTiles) && (int64_t)B * G <= 0x7FFFFFFF) pl.ctas = (int)ctas;
+  const int64_t ctas = (int64_t)sms * stream_ctas_per_sm(D), tiles = rows_tiles(16, n, P, has_new, pend);
+  const int64_t total = pl.units * tiles;
+  if ((int64_t)B * G <= 0x7FFFFFFF && (total >= ctas * kWarps * (prefix_parts ? kBesideTiles : kStreamTiles) ||
+                                       tiles >= (int64_t)cluster_ctas(pl.units, tiles, sms) * kWarps * kClusterTiles))
+    pl.ctas = (int)std::min<int64_t>(ctas, (total + kWarps - 1) / kWarps);
   return pl;
 }
 

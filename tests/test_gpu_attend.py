@@ -70,6 +70,16 @@ def test_many_tiles(kvx, B, N, H, D, n, dtype, new):
     ref.check_attend(kvx, q, lens=lens, **rows)
 
 
+@pytest.mark.parametrize("B,N,H,D,n", [(40, 4, 8, 128, 401), (2, 40, 2, 128, 11000), (1500, 2, 4, 64, 90)])
+@pytest.mark.parametrize("top", [0, 1, 40, 300])
+def test_room_for_many_tiles_but_few_rows(kvx, B, N, H, D, n, top):
+    """Room that would be cut into a range per CTA, lengths that make fewer tiles than there are CTAs."""
+    q, rows = _make(B, N, H, D, n=n, new=top == 40, seed=n)
+    lens = torch.randint(0, top + 1, (B,), dtype=torch.int32, device="cuda").clamp(max=n)
+    lens[3:] = lens[3:] // 40
+    ref.check_attend(kvx, q, lens=lens, **rows)
+
+
 @pytest.mark.parametrize("B,N,H,D,n,P", [(40, 4, 8, 128, 401, 700), (200, 3, 4, 64, 400, 300), (30, 20, 8, 128, 350, 1000),
                                         (1, 4, 2, 128, 30000, 20000)])
 def test_many_tiles_with_prefix(kvx, B, N, H, D, n, P):
@@ -83,13 +93,13 @@ def test_many_tiles_with_prefix(kvx, B, N, H, D, n, P):
 
 def test_prefix_strides_of_all_kinds(kvx):
     """Padded rows, heads inside rows, and a prefix that is the same for all heads (which TMA cannot describe)."""
-    q, rows = _make(40, 4, 3, 128, P=300, seed=14)
+    q, rows = _make(60, 4, 3, 128, P=900, seed=14)
     k, v = rows["prefix_k"], rows["prefix_v"]
-    padded = torch.zeros(3, 309, 136, dtype=F16, device="cuda")
-    padded[:, :300, :128] = k
-    inside = torch.zeros(300, 3, 136, dtype=F16, device="cuda")
+    padded = torch.zeros(3, 909, 136, dtype=F16, device="cuda")
+    padded[:, :900, :128] = k
+    inside = torch.zeros(900, 3, 136, dtype=F16, device="cuda")
     inside[:, :, :128] = v.transpose(0, 1)
-    ref.check_attend(kvx, q, prefix_k=padded[:, :300, :128], prefix_v=inside[:, :, :128].transpose(0, 1))
+    ref.check_attend(kvx, q, prefix_k=padded[:, :900, :128], prefix_v=inside[:, :, :128].transpose(0, 1))
     same = [x[:1].expand(3, -1, -1) for x in (k, v)]
     ref.check_attend(kvx, q, prefix_k=same[0], prefix_v=same[1])
 
@@ -101,6 +111,59 @@ def test_prefix_strides_of_all_kinds(kvx):
 def test_prefix_alone(kvx, B, N, P, D, dtype):
     q, rows = _make(B, N, 2, D, P=P, dtype=dtype, seed=P)
     ref.check_attend(kvx, q, **rows)
+
+
+# Enough rows for the tensor-core kernel, which reads them once: up to 128 query rows a key head (both of its streams on
+# the same rows) and more (a row block each), blocks cut over CTAs and whole, tiles that end inside, odd head groups.
+SHARED = [(128, 1, 8, 128, 130), (100, 1, 4, 64, 1300), (32, 4, 8, 128, 1100), (2, 40, 2, 128, 11000), (3, 12, 2, 64, 45000),
+          (33, 4, 8, 128, 500), (70, 8, 2, 128, 1000), (130, 2, 4, 64, 1000), (300, 5, 2, 64, 901), (512, 4, 8, 128, 129),
+          (700, 3, 2, 128, 257), (17, 40, 3, 64, 5000), (43, 3, 8, 128, 8191)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("B,N,H,D,P", SHARED)
+def test_large_prefix(kvx, B, N, H, D, P, dtype):
+    q, rows = _make(B, N, H, D, P=P, dtype=dtype, seed=P)
+    ref.check_attend(kvx, q, **rows)
+
+
+@pytest.mark.parametrize("B,N,H,D,P", SHARED)
+@pytest.mark.parametrize("n", [0, 5, 90])
+def test_large_prefix_with_own_rows(kvx, B, N, H, D, P, n):
+    """Beside few own rows (or the token's own alone) and beside more; then unequal lengths of both, none among them, and
+    shared rows that no sequence has left as NaN."""
+    dtype = BF16 if P % 2 else F16
+    q, rows = _make(B, N, H, D, n=n, P=P, new=n != 5, dtype=dtype, seed=P + n)
+    ref.check_attend(kvx, q, **rows)
+    gen = torch.Generator().manual_seed(P)
+    plens = torch.randint(0, P - 60, (B,), dtype=torch.int32, generator=gen).cuda()
+    plens[B // 3:B // 2] = 0
+    extra = {"prefix_lens": plens}
+    top = int(plens.max())
+    rows["prefix_k"][:, top:], rows["prefix_v"][:, top:] = float("nan"), float("nan")
+    if n:
+        extra["lens"] = torch.randint(0, n + 1, (B,), dtype=torch.int32, generator=gen).cuda()
+        extra["lens"][B // 4:B // 2 + 1] = 0
+    ref.check_attend(kvx, q, **extra, **rows)
+
+
+@pytest.mark.parametrize("B,N,H,D,P", SHARED[::3])
+def test_large_prefix_alone_with_unequal_lengths(kvx, B, N, H, D, P):
+    q, rows = _make(B, N, H, D, P=P, seed=P + 1)
+    plens = torch.randint(0, P + 1, (B,), dtype=torch.int32, device="cuda")
+    plens[0], plens[B // 2:] = P, 0
+    out, lse = ref.check_attend(kvx, q, prefix_lens=plens, **rows)
+    assert (out[B // 2:] == 0).all() and (lse[B // 2:] == -math.inf).all()
+    out, lse = ref.check_attend(kvx, q, prefix_lens=torch.zeros_like(plens), **rows)
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 3.0])
+@pytest.mark.parametrize("B,N,H,D,P", [(32, 4, 8, 128, 1100), (300, 5, 2, 64, 901)])
+def test_large_prefix_and_large_logits(kvx, B, N, H, D, P, scale):
+    q, rows = _make(B, N, H, D, P=P, seed=5)
+    rows["prefix_k"] *= torch.linspace(0.1, 4, P, device="cuda").to(F16)[:, None]
+    ref.check_attend(kvx, q, scale=scale, **rows)
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -135,8 +198,8 @@ def test_empty_ragged_and_poisoned_rows(kvx, B, P, new):
 
 
 def test_prefix_rows_past_every_length_are_not_used(kvx):
-    q, rows = _make(40, 4, 2, 128, P=600, seed=8)
-    plens = torch.full((40,), 301, dtype=torch.int32, device="cuda")
+    q, rows = _make(140, 4, 2, 128, P=600, seed=8)
+    plens = torch.full((140,), 301, dtype=torch.int32, device="cuda")
     plens[3] = 0
     rows["prefix_k"][:, 301:], rows["prefix_v"][:, 301:] = float("nan"), float("nan")
     ref.check_attend(kvx, q, prefix_lens=plens, **rows)
@@ -221,7 +284,7 @@ def test_offsets_past_32_bits(kvx):
         rows[name] = view
     ref.check_attend(kvx, q, **rows)
     step = 2 ** 25 + 128                       # elements between rows: row 63 is past 2^31
-    q, rows = _make(40, N, 1, D, P=64, seed=10)
+    q, rows = _make(2500, N, 1, D, P=64, seed=10)
     for name, x in zip(("prefix_k", "prefix_v"), base):
         view = x.as_strided((1, 64, D), (0, step, 1))
         view.copy_(rows[name])
@@ -229,7 +292,7 @@ def test_offsets_past_32_bits(kvx):
     ref.check_attend(kvx, q, **rows)
 
 
-@pytest.mark.parametrize("B,n,P", [(2, 300, 0), (2, 30, 100), (40, 30, 1000), (150, 0, 1000), (40, 2100, 0), (40, 2100, 600)])
+@pytest.mark.parametrize("B,n,P", [(2, 300, 0), (2, 30, 100), (40, 30, 3000), (150, 0, 1000), (40, 2100, 0), (150, 900, 900)])
 def test_repeat_streams_and_graphs(kvx, B, n, P):
     """The same bits call after call, on another stream, and from two captured graphs that replay together."""
     q, rows = _make(B, 4, 2, 128, n=n, P=P, seed=12)
@@ -267,10 +330,10 @@ def test_repeat_streams_and_graphs(kvx, B, n, P):
     assert torch.equal(outs[0], other) and not torch.equal(other, want)
 
 
-@pytest.mark.parametrize("B", [3, 60])
-def test_parts_join_by_lse(kvx, B):
+@pytest.mark.parametrize("B,P", [(3, 500), (120, 900)])
+def test_parts_join_by_lse(kvx, B, P):
     """Prefix and own rows in two calls, joined by their log sums, are the one call."""
-    q, rows = _make(B, 4, 2, 128, n=80, P=500, seed=13)
+    q, rows = _make(B, 4, 2, 128, n=80, P=P, seed=13)
     out, lse = ref.check_attend(kvx, q, **rows)
     a, la = ref.check_attend(kvx, q, k=rows["k"], v=rows["v"])
     b, lb = ref.check_attend(kvx, q, prefix_k=rows["prefix_k"], prefix_v=rows["prefix_v"])
@@ -285,7 +348,7 @@ def test_bounded_wait_leaves_nan(kvx):
     """A wait that runs out cannot reach the return code: NaN in every output instead, and the next call is unaffected.
     The library's test hook leaves one copy unissued; nothing faults or hangs."""
     import time
-    q, rows = _make(40, 4, 1, 128, P=300, seed=15)      # one block on one CTA or two: all of it depends on the first tile
+    q, rows = _make(250, 1, 1, 128, P=600, seed=15)     # one block of rows: all of it depends on the first tile
     want, wlse = ref.check_attend(kvx, q, **rows)
     out, lse = torch.zeros_like(q), torch.zeros_like(wlse)
     assert kvx.lib().kvevict_test_stall_next_step(None) == kvx.OK
