@@ -38,6 +38,15 @@
 // A stream's tcgen05.commit after S also covers the P V before it, so a thread
 // that has seen S may rescale O without another wait.
 // Every mbarrier wait is bounded; on expiry the CTA leaves NaN in its rows.
+//
+// Measured on GB300: 4096 x 32 query rows on 8192 keys, D = 128, bf16, 365-410 us
+// by the box, 1.34-1.51 PFLOP/s (0.72-0.81 of the measured matrix rate, 62% of the
+// tensor pipe's cycles); its MMAs with no softmax between them take 327 us, without
+// waits 309. 32 sequences on 65536 rows 50 us for the kernel, 5.4 TB/s; a call's start,
+// one tile and its end are 9.7 us of that (2.5 launch and set-up, 5 the chain of one
+// tile, 2 the parts), which is most of a short prefix's time. Tried and slower: three
+// logits buffers at D = 64 with one general issue loop (53 against 47 us), a
+// suspended or a longer plain poll of the barriers (524, 542 against 505).
 #include "attend_internal.cuh"
 #include "tcgen05.cuh"
 
@@ -228,168 +237,168 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   // The launch's 384 x 168 registers, shared out anew: 4 warps of 120 and 8 of
   // 192 a thread, so that a softmax thread holds a row's 128 logits.
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
-    if (lane < 2)
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &vmap : &kmap)) : "memory");
-    int s = 0, held = 0;               // next stage, stages in flight (at most NS)
-    uint32_t phase = 0;
-    bool ok = true, stall = p.stall && blockIdx.x == 0;   // test hook: CTA 0's first tile never comes
-    while (ok && walk.next(u, k0, k1)) {
-      const int n = min(k1, (block_limit(p, u) + kT - 1) / kT) - k0;
-      const int h = u / p.plan.blocks;
-      if (lane == 0) {
-        auto load = [&](const CUtensorMap* map, bool row_first, int kt) {
-          if (held == NS && !wait_or_abort(empty(s), phase ^ 1, abort_flag, p.err)) return false;
-          if (!stall) {
-            mbar_expect_tx(full(s), Gm::TILEB);
-            const int row = (k0 + kt) * kT;
-            for (int kh = 0; kh < Gm::KH; ++kh)
-              tma_load_3d(base + Gm::RING + s * Gm::TILEB + kh * Gm::HALFB, map, kh * 64, row_first ? row : h,
-                          row_first ? h : row, full(s));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &vmap : &kmap)) : "memory");
+      int s = 0, held = 0;               // next stage, stages in flight (at most NS)
+      uint32_t phase = 0;
+      bool ok = true, stall = p.stall && blockIdx.x == 0;   // test hook: CTA 0's first tile never comes
+      while (ok && walk.next(u, k0, k1)) {
+        const int n = min(k1, (block_limit(p, u) + kT - 1) / kT) - k0;
+        const int h = u / p.plan.blocks;
+        if (lane == 0) {
+          auto load = [&](const CUtensorMap* map, bool row_first, int kt) {
+            if (held == NS && !wait_or_abort(empty(s), phase ^ 1, abort_flag, p.err)) return false;
+            if (!stall) {
+              mbar_expect_tx(full(s), Gm::TILEB);
+              const int row = (k0 + kt) * kT;
+              for (int kh = 0; kh < Gm::KH; ++kh)
+                tma_load_3d(base + Gm::RING + s * Gm::TILEB + kh * Gm::HALFB, map, kh * 64, row_first ? row : h,
+                            row_first ? h : row, full(s));
+            }
+            stall = false;
+            held = min(held + 1, NS);
+            if (++s == NS) s = 0, phase ^= 1;
+            return true;
+          };
+          for (int i = 0; i < n && ok; ++i) {
+            if (i == 0) {
+              ok = load(&kmap, p.k_row_first, 0);
+              if (PAIR && ok && n > 1) ok = load(&kmap, p.k_row_first, 1);
+            }
+            ok = ok && load(&vmap, p.v_row_first, i);
+            const int nk = PAIR ? i + 2 : i + 1;
+            if (ok && nk < n) ok = load(&kmap, p.k_row_first, nk);
           }
-          stall = false;
-          held = min(held + 1, NS);
-          if (++s == NS) s = 0, phase ^= 1;
+        }
+        ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+      }
+      if (lane == 0 && *abort_flag)      // let copies in flight land before the CTA leaves
+        for (int i = 0; i < held; ++i) {
+          if (--s < 0) s = NS - 1, phase ^= 1;
+          (void)mbar_wait_bounded(full(s), phase, 10000000ull);
+        }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t kIdS = px_idesc<T>(kT, false), kIdO = px_idesc<T>(D, true);
+      // descriptors of the first query block and ring stage; an offset adds to the
+      // address field, in 16-byte units
+      const uint64_t qd = sw128_desc(base + Gm::Q), kd = sw128_desc(base + Gm::RING);
+      const uint64_t vd = sw128_mn_desc(base + Gm::RING, Gm::HALFB);
+      int next = 0;                      // ring stage and its phase
+      uint32_t phase = 0;
+      uint32_t np[2] = {0, 0};           // weights tiles consumed, per stream
+      int seg = 0;                       // segments that have tiles
+      bool ok = true;
+      while (ok && walk.next(u, k0, k1)) {
+        const int limit = block_limit(p, u);
+        const int n = min(k1, (limit + kT - 1) / kT) - k0;
+        if (n <= 0) continue;
+        ok = __all_sync(~0u, wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag, p.err));
+        ++seg;
+        if (!ok) break;
+        tc_fence_after();
+        auto tile = [&]() -> int {       // the next ring stage, once its tile is there; -1 on abort
+          const int s = next;
+          const bool here = wait_or_abort(full(s), phase, abort_flag, p.err);
+          if (++next == NS) next = 0, phase ^= 1;
+          return __all_sync(~0u, here) ? s : -1;
+        };
+        auto mma_s = [&](int w, int s) {
+          if (elect_one()) {
+            const uint64_t qa = qd + (uint64_t)((PAIR ? 0 : w) * (Gm::TILEB >> 4)), kb = kd + (uint64_t)(s * (Gm::TILEB >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)(((kk >> 2) * Gm::HALFB + (kk & 3) * 32) >> 4);
+              tc_mma_ss(tm_s(w), qa + off, kb + off, kIdS, kk > 0);
+            }
+            tc_commit(s_full(w));
+          }
+        };
+        auto release = [&](int s) {
+          if (elect_one()) tc_commit(empty(s));
+        };
+        // O_w += P_w V: P of keys 0..63 in S's columns 0..31, of keys 64..127 in
+        // 64..95, the second parts (PAIR) 32 columns on
+        auto mma_o = [&](int w, int s, bool first) {
+          const uint64_t vb = vd + (uint64_t)(s * (Gm::TILEB >> 4));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (!__all_sync(~0u, wait_or_abort(p_full(w, c), np[w] & 1, abort_flag, p.err))) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int part = 0; part < (PAIR ? 2 : 1); ++part)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_ts(tm_o(w), tm_s(w) + (uint32_t)(c * 64 + kk * 8 + 32 * part),
+                            vb + (uint64_t)((4 * c + kk) * (2048 >> 4)), kIdO, !(first && c + kk + part == 0));
+            }
+          }
+          ++np[w];
           return true;
         };
-        for (int i = 0; i < n && ok; ++i) {
-          if (i == 0) {
-            ok = load(&kmap, p.k_row_first, 0);
-            if (PAIR && ok && n > 1) ok = load(&kmap, p.k_row_first, 1);
+        // A value tile that reaches past the block's rows: what lies there may be
+        // anything, and 0 * NaN would spoil the sums, so it becomes zeros.
+        auto clean = [&](int s, int kt) {
+          const int from = limit - kt * kT;
+          if (from >= kT || limit == a.P) return;      // TMA has filled rows past P with zeros
+          for (int x = lane; x < (kT - from) * (D / 8); x += 32) {
+            const int row = from + x / (D / 8), c = x % (D / 8);
+            *reinterpret_cast<uint4*>(smem + Gm::RING + s * Gm::TILEB + (c >> 3) * Gm::HALFB + row * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
           }
-          ok = ok && load(&vmap, p.v_row_first, i);
-          const int nk = PAIR ? i + 2 : i + 1;
-          if (ok && nk < n) ok = load(&kmap, p.k_row_first, nk);
-        }
-      }
-      ok = __shfl_sync(~0u, (int)ok, 0) != 0;
-    }
-    if (lane == 0 && *abort_flag)      // let copies in flight land before the CTA leaves
-      for (int i = 0; i < held; ++i) {
-        if (--s < 0) s = NS - 1, phase ^= 1;
-        (void)mbar_wait_bounded(full(s), phase, 10000000ull);
-      }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    constexpr uint32_t kIdS = px_idesc<T>(kT, false), kIdO = px_idesc<T>(D, true);
-    // descriptors of the first query block and ring stage; an offset adds to the
-    // address field, in 16-byte units
-    const uint64_t qd = sw128_desc(base + Gm::Q), kd = sw128_desc(base + Gm::RING);
-    const uint64_t vd = sw128_mn_desc(base + Gm::RING, Gm::HALFB);
-    int next = 0;                      // ring stage and its phase
-    uint32_t phase = 0;
-    uint32_t np[2] = {0, 0};           // weights tiles consumed, per stream
-    int seg = 0;                       // segments that have tiles
-    bool ok = true;
-    while (ok && walk.next(u, k0, k1)) {
-      const int limit = block_limit(p, u);
-      const int n = min(k1, (limit + kT - 1) / kT) - k0;
-      if (n <= 0) continue;
-      ok = __all_sync(~0u, wait_or_abort(q_full, (uint32_t)(seg & 1), abort_flag, p.err));
-      ++seg;
-      if (!ok) break;
-      tc_fence_after();
-      auto tile = [&]() -> int {       // the next ring stage, once its tile is there; -1 on abort
-        const int s = next;
-        const bool here = wait_or_abort(full(s), phase, abort_flag, p.err);
-        if (++next == NS) next = 0, phase ^= 1;
-        return __all_sync(~0u, here) ? s : -1;
-      };
-      auto mma_s = [&](int w, int s) {
-        if (elect_one()) {
-          const uint64_t qa = qd + (uint64_t)((PAIR ? 0 : w) * (Gm::TILEB >> 4)), kb = kd + (uint64_t)(s * (Gm::TILEB >> 4));
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (uint64_t)(((kk >> 2) * Gm::HALFB + (kk & 3) * 32) >> 4);
-            tc_mma_ss(tm_s(w), qa + off, kb + off, kIdS, kk > 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        };
+        int s;
+        if (PAIR) {
+          for (int i = 0; i < min(n, 2) && ok; ++i) {
+            ok = (s = tile()) >= 0;
+            if (ok) mma_s(i, s), release(s);
           }
-          tc_commit(s_full(w));
-        }
-      };
-      auto release = [&](int s) {
-        if (elect_one()) tc_commit(empty(s));
-      };
-      // O_w += P_w V: P of keys 0..63 in S's columns 0..31, of keys 64..127 in
-      // 64..95, the second parts (PAIR) 32 columns on
-      auto mma_o = [&](int w, int s, bool first) {
-        const uint64_t vb = vd + (uint64_t)(s * (Gm::TILEB >> 4));
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (!__all_sync(~0u, wait_or_abort(p_full(w, c), np[w] & 1, abort_flag, p.err))) return false;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int part = 0; part < (PAIR ? 2 : 1); ++part)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_ts(tm_o(w), tm_s(w) + (uint32_t)(c * 64 + kk * 8 + 32 * part),
-                          vb + (uint64_t)((4 * c + kk) * (2048 >> 4)), kIdO, !(first && c + kk + part == 0));
-          }
-        }
-        ++np[w];
-        return true;
-      };
-      // A value tile that reaches past the block's rows: what lies there may be
-      // anything, and 0 * NaN would spoil the sums, so it becomes zeros.
-      auto clean = [&](int s, int kt) {
-        const int from = limit - kt * kT;
-        if (from >= kT || limit == a.P) return;      // TMA has filled rows past P with zeros
-        for (int x = lane; x < (kT - from) * (D / 8); x += 32) {
-          const int row = from + x / (D / 8), c = x % (D / 8);
-          *reinterpret_cast<uint4*>(smem + Gm::RING + s * Gm::TILEB + (c >> 3) * Gm::HALFB + row * 128 + (c & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-      };
-      int s;
-      if (PAIR) {
-        for (int i = 0; i < min(n, 2) && ok; ++i) {
-          ok = (s = tile()) >= 0;
-          if (ok) mma_s(i, s), release(s);
-        }
-        for (int i = 0; i < n && ok; ++i) {
-          const int w = i & 1;
-          if (!(ok = (s = tile()) >= 0)) break;
-          clean(s, k0 + i);
-          if (!(ok = mma_o(w, s, i < 2))) break;
-          release(s);
-          if (i + 2 >= n && elect_one()) tc_commit(o_done(w));
-          if (i + 2 < n) {
+          for (int i = 0; i < n && ok; ++i) {
+            const int w = i & 1;
             if (!(ok = (s = tile()) >= 0)) break;
-            mma_s(w, s);
+            clean(s, k0 + i);
+            if (!(ok = mma_o(w, s, i < 2))) break;
             release(s);
+            if (i + 2 >= n && elect_one()) tc_commit(o_done(w));
+            if (i + 2 < n) {
+              if (!(ok = (s = tile()) >= 0)) break;
+              mma_s(w, s);
+              release(s);
+            }
           }
-        }
-      } else {
-        ok = (s = tile()) >= 0;
-        if (ok) mma_s(0, s), mma_s(1, s), release(s);
-        for (int i = 0; i < n && ok; ++i) {
-          const bool more = i + 1 < n;
-          int sk = 0;
-          if (!(ok = (s = tile()) >= 0)) break;
-          clean(s, k0 + i);
-          if (!(ok = mma_o(0, s, i == 0))) break;
-          if (more) {
-            if (!(ok = (sk = tile()) >= 0)) break;
-            mma_s(0, sk);
-          } else if (elect_one()) {
-            tc_commit(o_done(0));
-          }
-          if (!(ok = mma_o(1, s, i == 0))) break;
-          release(s);
-          if (more) {
-            mma_s(1, sk);
-            release(sk);
-          } else if (elect_one()) {
-            tc_commit(o_done(1));
+        } else {
+          ok = (s = tile()) >= 0;
+          if (ok) mma_s(0, s), mma_s(1, s), release(s);
+          for (int i = 0; i < n && ok; ++i) {
+            const bool more = i + 1 < n;
+            int sk = 0;
+            if (!(ok = (s = tile()) >= 0)) break;
+            clean(s, k0 + i);
+            if (!(ok = mma_o(0, s, i == 0))) break;
+            if (more) {
+              if (!(ok = (sk = tile()) >= 0)) break;
+              mma_s(0, sk);
+            } else if (elect_one()) {
+              tc_commit(o_done(0));
+            }
+            if (!(ok = mma_o(1, s, i == 0))) break;
+            release(s);
+            if (more) {
+              mma_s(1, sk);
+              release(sk);
+            } else if (elect_one()) {
+              tc_commit(o_done(1));
+            }
           }
         }
       }
     }
-  }
   } else {
     // ---------------------------------------------------------------- softmax warpgroups
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");

@@ -18,10 +18,11 @@
 //     share a register, so the lane that holds both keys' pieces interleaves
 //     them with one byte permute each; the weights are the logits' accumulator
 //     registers as they are.
-// A warp takes 16 rows at a time. Its key registers are refilled as soon as the
-// logits are out of them, its value registers as soon as the sums are, so one
-// of the two is always in flight. Running maximum, sum and output stay in fp32
-// registers; the maximum is looked at again only when some lane exceeds it.
+// A warp takes 16 rows at a time, 32 in a stream with up to 8 query heads. Its key
+// registers are refilled as soon as the logits are out of them, its value registers
+// as soon as the sums are, so one of the two is always in flight. Running maximum,
+// sum and output stay in fp32 registers; the maximum is looked at again only when
+// some lane exceeds it.
 //
 // The weights go into the second product as a sum of two 16-bit parts
 // (p = hi + lo), 22 bits in all for fp16 and 16 for bf16: the matrix pipe has
@@ -37,6 +38,15 @@
 //     unit that is one CTA's alone is written out by it, a cut one leaves its
 //     parts in the workspace for a second, small kernel, which joins them in a
 //     fixed order, with the shared prefix's parts if there are any.
+//
+// Measured on GB300 (D = 128, 32 query heads on 8, fp16): 32 sequences of 2048 rows
+// 45-46 us, 5.8-6.0 TB/s of rows (0.87 of the measured copy rate); 7 unequal ones of
+// up to 65521 rows 139 us, 6.0 TB/s; one of 512 rows 5 us, all latency. Tried and
+// slower: the tiles through shared memory by cp.async, two more in flight (63 against
+// 50 us), 32-byte loads (53 against 50), more and smaller ranges (54-59), L2
+// prefetches throughout (150 against 139 on the unequal lengths). Bound by loads
+// in flight a warp's registers hold: 16 KB of them, 8 warps an SM, the
+// latencies of start, join and unequal SMs on top (SMs are busy 84% of the time).
 #include "attend_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -296,335 +306,335 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   }
 
   while (true) {                                  // STREAM: the range's segments, each of one unit
-  const SeqRows<TR> seq(a, b);
-  int first = 0, total = seq.tiles(a);
-  bool whole = true;
-  int64_t slot = 0;
-  int next_b = b;
-  if (STREAM) {
-    if (at >= end) break;
-    total = max(1, total);
-    const int tb = total;
-    const int64_t rem = at - base;
-    ub = (int)(rem / tb);
-    first = (int)(rem - (int64_t)ub * tb);
-    total = (int)min((int64_t)tb, first + (end - at));
-    at += total - first;
-    whole = plan.final && first == 0 && total == tb;
-    slot = plan.slot((int64_t)b * upb + ub, blockIdx.x, first == 0);
-    if (at == base + (int64_t)upb * tb) {
-      base = at;
-      next_b = b + 1;
-    }
-  }
-  const int qc = ub % qchunks, h = ub / qchunks, bh = b * a.H + h;
-  const int q0 = qc * QN, nq = min(QN, N - q0);   // query heads h*N + q0 .. + nq - 1
-  const int np = seq.np, tp = seq.tp, to = seq.to;
-  int n = seq.n;
-  int e = -1;                                     // the evicted row still in place
-  if (PEND) {
-    e = a.pend[bh];
-    if (e >= 0) n += 1;
-  }
-  auto tile_at = [&](int t) {
-    Tile<T> x;
-    x.moved = 32;
-    if (t < tp) {
-      x.ks = a.pk_stride[1];
-      x.vs = a.pv_stride[1];
-      x.k = static_cast<const T*>(a.pk) + h * a.pk_stride[0] + (int64_t)t * TR * x.ks;
-      x.v = static_cast<const T*>(a.pv) + h * a.pv_stride[0] + (int64_t)t * TR * x.vs;
-      const int left = np - t * TR;
-      x.live = left >= TR ? ~0u >> (32 - TR) : (1u << left) - 1u;
-    } else if (t < tp + to) {
-      const int r0 = (t - tp) * TR;
-      x.ks = a.k_stride[2];
-      x.vs = a.v_stride[2];
-      x.k = static_cast<const T*>(a.k) + b * a.k_stride[0] + h * a.k_stride[1] + (int64_t)r0 * x.ks;
-      x.v = static_cast<const T*>(a.v) + b * a.v_stride[0] + h * a.v_stride[1] + (int64_t)r0 * x.vs;
-      const int left = n - r0;
-      x.live = left >= TR ? ~0u >> (32 - TR) : left > 0 ? (1u << left) - 1u : 0u;
-      if (PEND && e >= 0) {
-        if (e >= r0 && e < r0 + TR) x.live &= ~(1u << (e - r0));
-        x.moved = max(0, min(32, e - r0 + 1));
+    const SeqRows<TR> seq(a, b);
+    int first = 0, total = seq.tiles(a);
+    bool whole = true;
+    int64_t slot = 0;
+    int next_b = b;
+    if (STREAM) {
+      if (at >= end) break;
+      total = max(1, total);
+      const int tb = total;
+      const int64_t rem = at - base;
+      ub = (int)(rem / tb);
+      first = (int)(rem - (int64_t)ub * tb);
+      total = (int)min((int64_t)tb, first + (end - at));
+      at += total - first;
+      whole = plan.final && first == 0 && total == tb;
+      slot = plan.slot((int64_t)b * upb + ub, blockIdx.x, first == 0);
+      if (at == base + (int64_t)upb * tb) {
+        base = at;
+        next_b = b + 1;
       }
-    } else {
-      x.ks = x.vs = 0;
-      x.k = static_cast<const T*>(a.k_new) + b * a.kn_stride[0] + h * a.kn_stride[1];
-      x.v = static_cast<const T*>(a.v_new) + b * a.vn_stride[0] + h * a.vn_stride[1];
-      x.live = a.k_new ? 1u : 0u;            // (a unit without any rows has one tile of none)
     }
-    return x;
-  };
-
-  const int stride = C * kWarps;
-  int t = first + rank * kWarps + warp;
-  uint4 kr[2 * KG][KC], vr[VH][4 * KG];
-  Tile<T> cur{};
-  if (t < total) {
-    cur = tile_at(t);
-    R::load_k(kr, cur, g, c);
-    R::load_v(vr, cur, g, c);
-    if (t + stride < total) prefetch_tile<T, D>(tile_at(t + stride), lane);
-  }
-  // queries: row g of each group of 8, in the keys' order
-  uint4 qr[QT][KC];
-#pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    const int q = q0 + g + 8 * i;
-    const T* p = static_cast<const T*>(a.q) + b * a.q_stride[0] + (int64_t)(h * N + q) * a.q_stride[1] + 8 * c;
-#pragma unroll
-    for (int j = 0; j < KC; ++j)
-      qr[i][j] = q < N ? *reinterpret_cast<const uint4*>(p + 32 * j) : make_uint4(0, 0, 0, 0);
-  }
-
-  float m[QT], l[QT], acc[VH][4][QT][4];
-#pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    m[i] = kNegInf;
-    l[i] = 0.f;
-  }
-#pragma unroll
-  for (int x = 0; x < VH * 4 * QT * 4; ++x) (&acc[0][0][0][0])[x] = 0.f;
-
-  while (t < total) {
-    if (PEND && cur.moved < TR) {
-#pragma unroll
-      for (int nt = 0; nt < 2 * KG; ++nt)
-        if (g + 8 * nt >= cur.moved) {
-#pragma unroll
-          for (int i = 0; i < KC / 2; ++i)
-            rotate_back(kr[nt][i], kr[nt][i + KC / 2], a.rope_c + 32 * i + 8 * c, a.rope_s + 32 * i + 8 * c);
+    const int qc = ub % qchunks, h = ub / qchunks, bh = b * a.H + h;
+    const int q0 = qc * QN, nq = min(QN, N - q0);   // query heads h*N + q0 .. + nq - 1
+    const int np = seq.np, tp = seq.tp, to = seq.to;
+    int n = seq.n;
+    int e = -1;                                     // the evicted row still in place
+    if (PEND) {
+      e = a.pend[bh];
+      if (e >= 0) n += 1;
+    }
+    auto tile_at = [&](int t) {
+      Tile<T> x;
+      x.moved = 32;
+      if (t < tp) {
+        x.ks = a.pk_stride[1];
+        x.vs = a.pv_stride[1];
+        x.k = static_cast<const T*>(a.pk) + h * a.pk_stride[0] + (int64_t)t * TR * x.ks;
+        x.v = static_cast<const T*>(a.pv) + h * a.pv_stride[0] + (int64_t)t * TR * x.vs;
+        const int left = np - t * TR;
+        x.live = left >= TR ? ~0u >> (32 - TR) : (1u << left) - 1u;
+      } else if (t < tp + to) {
+        const int r0 = (t - tp) * TR;
+        x.ks = a.k_stride[2];
+        x.vs = a.v_stride[2];
+        x.k = static_cast<const T*>(a.k) + b * a.k_stride[0] + h * a.k_stride[1] + (int64_t)r0 * x.ks;
+        x.v = static_cast<const T*>(a.v) + b * a.v_stride[0] + h * a.v_stride[1] + (int64_t)r0 * x.vs;
+        const int left = n - r0;
+        x.live = left >= TR ? ~0u >> (32 - TR) : left > 0 ? (1u << left) - 1u : 0u;
+        if (PEND && e >= 0) {
+          if (e >= r0 && e < r0 + TR) x.live &= ~(1u << (e - r0));
+          x.moved = max(0, min(32, e - r0 + 1));
         }
-    }
-    float s[2 * KG][4];
-#pragma unroll
-    for (int nt = 0; nt < 2 * KG; ++nt)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
-    // (the groups of eight keys are independent: one's sum hides the other's)
-#pragma unroll
-    for (int i = 0; i < KC; ++i)
-#pragma unroll
-      for (int w = 0; w < 4; w += 2)
-#pragma unroll
-        for (int nt = 0; nt < 2 * KG; ++nt)
-          mma16816<T>(s[nt], word(qr[0][i], w), QT > 1 ? word(qr[QT - 1][i], w) : 0u, word(qr[0][i], w + 1),
-                      QT > 1 ? word(qr[QT - 1][i], w + 1) : 0u, word(kr[nt][i], w), word(kr[nt][i], w + 1));
-    const uint32_t live = cur.live;
-    t += stride;
-    const bool more = t < total;
-    if (more) {
+      } else {
+        x.ks = x.vs = 0;
+        x.k = static_cast<const T*>(a.k_new) + b * a.kn_stride[0] + h * a.kn_stride[1];
+        x.v = static_cast<const T*>(a.v_new) + b * a.vn_stride[0] + h * a.vn_stride[1];
+        x.live = a.k_new ? 1u : 0u;            // (a unit without any rows has one tile of none)
+      }
+      return x;
+    };
+
+    const int stride = C * kWarps;
+    int t = first + rank * kWarps + warp;
+    uint4 kr[2 * KG][KC], vr[VH][4 * KG];
+    Tile<T> cur{};
+    if (t < total) {
       cur = tile_at(t);
       R::load_k(kr, cur, g, c);
+      R::load_v(vr, cur, g, c);
+      if (t + stride < total) prefetch_tile<T, D>(tile_at(t + stride), lane);
     }
-
-    // weights of this lane's rows 2c, 2c + 1, 2c + 8, 2c + 9 for query g (and g + 8)
-    uint32_t hi[QT][2 * KG], lo[QT][2 * KG];
-    float grow[QT];
-    bool up = false;
+    // queries: row g of each group of 8, in the keys' order
+    uint4 qr[QT][KC];
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
-      float tm = kNegInf;
+      const int q = q0 + g + 8 * i;
+      const T* p = static_cast<const T*>(a.q) + b * a.q_stride[0] + (int64_t)(h * N + q) * a.q_stride[1] + 8 * c;
+#pragma unroll
+      for (int j = 0; j < KC; ++j)
+        qr[i][j] = q < N ? *reinterpret_cast<const uint4*>(p + 32 * j) : make_uint4(0, 0, 0, 0);
+    }
+
+    float m[QT], l[QT], acc[VH][4][QT][4];
+#pragma unroll
+    for (int i = 0; i < QT; ++i) {
+      m[i] = kNegInf;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < VH * 4 * QT * 4; ++x) (&acc[0][0][0][0])[x] = 0.f;
+
+    while (t < total) {
+      if (PEND && cur.moved < TR) {
+#pragma unroll
+        for (int nt = 0; nt < 2 * KG; ++nt)
+          if (g + 8 * nt >= cur.moved) {
+#pragma unroll
+            for (int i = 0; i < KC / 2; ++i)
+              rotate_back(kr[nt][i], kr[nt][i + KC / 2], a.rope_c + 32 * i + 8 * c, a.rope_s + 32 * i + 8 * c);
+          }
+      }
+      float s[2 * KG][4];
 #pragma unroll
       for (int nt = 0; nt < 2 * KG; ++nt)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float& v = s[nt][2 * i + x];
-          v = ((live >> (8 * nt + 2 * c + x)) & 1u) ? v * a.scale2 : kNegInf;
-          tm = fmaxf(tm, v);
-        }
-      grow[i] = tm;
-      up |= tm > m[i];
-    }
-    if (__any_sync(~0u, up)) {
+        for (int x = 0; x < 4; ++x) s[nt][x] = 0.f;
+      // (the groups of eight keys are independent: one's sum hides the other's)
+#pragma unroll
+      for (int i = 0; i < KC; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; w += 2)
+#pragma unroll
+          for (int nt = 0; nt < 2 * KG; ++nt)
+            mma16816<T>(s[nt], word(qr[0][i], w), QT > 1 ? word(qr[QT - 1][i], w) : 0u, word(qr[0][i], w + 1),
+                        QT > 1 ? word(qr[QT - 1][i], w + 1) : 0u, word(kr[nt][i], w), word(kr[nt][i], w + 1));
+      const uint32_t live = cur.live;
+      t += stride;
+      const bool more = t < total;
+      if (more) {
+        cur = tile_at(t);
+        R::load_k(kr, cur, g, c);
+      }
+
+      // weights of this lane's rows 2c, 2c + 1, 2c + 8, 2c + 9 for query g (and g + 8)
+      uint32_t hi[QT][2 * KG], lo[QT][2 * KG];
+      float grow[QT];
+      bool up = false;
 #pragma unroll
       for (int i = 0; i < QT; ++i) {
-        float tm = grow[i];
-        tm = fmaxf(tm, __shfl_xor_sync(~0u, tm, 1));
-        tm = fmaxf(tm, __shfl_xor_sync(~0u, tm, 2));
-        const float nm = fmaxf(m[i], tm);
-        const float f = nm == m[i] ? 1.f : ex2_approx(m[i] - nm);   // first rows: 2^-inf = 0
-        m[i] = nm;
-        l[i] *= f;
-        // the accumulators' columns are queries 2c and 2c + 1
-        const float f0 = __shfl_sync(~0u, f, 8 * c), f1 = __shfl_sync(~0u, f, 8 * c + 4);
+        float tm = kNegInf;
+#pragma unroll
+        for (int nt = 0; nt < 2 * KG; ++nt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float& v = s[nt][2 * i + x];
+            v = ((live >> (8 * nt + 2 * c + x)) & 1u) ? v * a.scale2 : kNegInf;
+            tm = fmaxf(tm, v);
+          }
+        grow[i] = tm;
+        up |= tm > m[i];
+      }
+      if (__any_sync(~0u, up)) {
+#pragma unroll
+        for (int i = 0; i < QT; ++i) {
+          float tm = grow[i];
+          tm = fmaxf(tm, __shfl_xor_sync(~0u, tm, 1));
+          tm = fmaxf(tm, __shfl_xor_sync(~0u, tm, 2));
+          const float nm = fmaxf(m[i], tm);
+          const float f = nm == m[i] ? 1.f : ex2_approx(m[i] - nm);   // first rows: 2^-inf = 0
+          m[i] = nm;
+          l[i] *= f;
+          // the accumulators' columns are queries 2c and 2c + 1
+          const float f0 = __shfl_sync(~0u, f, 8 * c), f1 = __shfl_sync(~0u, f, 8 * c + 4);
+#pragma unroll
+          for (int x = 0; x < VH; ++x)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[x][j][i][0] *= f0;
+              acc[x][j][i][1] *= f1;
+              acc[x][j][i][2] *= f0;
+              acc[x][j][i][3] *= f1;
+            }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        const float base = m[i] == kNegInf ? 0.f : m[i];   // nothing so far: every weight 2^-inf = 0
+#pragma unroll
+        for (int nt = 0; nt < 2 * KG; ++nt) {
+          const float p0 = ex2_approx(s[nt][2 * i] - base), p1 = ex2_approx(s[nt][2 * i + 1] - base);
+          l[i] += p0 + p1;
+          hi[i][nt] = pack16<T>(p0, p1);
+          const float2 back = unpack16<T>(hi[i][nt]);
+          lo[i][nt] = pack16<T>(p0 - back.x, p1 - back.y);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < KG; ++k)
 #pragma unroll
         for (int x = 0; x < VH; ++x)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            acc[x][j][i][0] *= f0;
-            acc[x][j][i][1] *= f1;
-            acc[x][j][i][2] *= f0;
-            acc[x][j][i][3] *= f1;
+            const uint32_t w0 = word(vr[x][4 * k], j), w1 = word(vr[x][4 * k + 1], j);
+            const uint32_t w2 = word(vr[x][4 * k + 2], j), w3 = word(vr[x][4 * k + 3], j);
+            const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+            const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+            for (int i = 0; i < QT; ++i) {
+              mma16816<T>(acc[x][j][i], a0, a1, a2, a3, hi[i][2 * k], hi[i][2 * k + 1]);
+              mma16816<T>(acc[x][j][i], a0, a1, a2, a3, lo[i][2 * k], lo[i][2 * k + 1]);
+            }
           }
+      if (more) R::load_v(vr, cur, g, c);
+    }
+
+    // ---------------------------------------------------------------- the prefix's parts
+    // Each part (a range of shared rows that one CTA of attend_prefix.cu took) joins
+    // one warp's sums as if it were another tile; the query rows b * N + q0 + q may
+    // lie in two blocks.
+    if (!STREAM && parts.plan.ctas) {
+      wait_for_primary();
+      const int RB = parts.plan.block_rows;
+      const int64_t r0 = (int64_t)b * N + q0;
+      for (int64_t blk = r0 / RB; blk <= (r0 + nq - 1) / RB; ++blk) {
+        const int u = h * parts.plan.blocks + (int)blk, off = (int)(r0 - blk * RB);   // query q is row off + q
+        const int c0 = parts.plan.cta_of((int64_t)u * parts.plan.nkt);
+        const int c1 = parts.plan.cta_of((int64_t)(u + 1) * parts.plan.nkt - 1);
+        auto inside = [&](int q) { return q < nq && off + q >= 0 && off + q < RB; };
+        for (int pc = c0 + rank * kWarps + warp; pc <= c1; pc += stride) {
+          const int64_t slot = parts.plan.slot(u, pc, pc == c0);
+          const float2* ml = parts.ml + slot * RB;
+          const float4* po = reinterpret_cast<const float4*>(parts.o) + slot * (RB * (D / 4));
+#pragma unroll
+          for (int i = 0; i < QT; ++i) {
+            float4 v[2][VH][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int q = 2 * c + k + 8 * i;
+              const bool in = inside(q);
+#pragma unroll
+              for (int x = 0; x < VH; ++x)
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+                  v[k][x][w] = in ? po[(16 * x + 2 * g + w) * RB + off + q] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            const int q = g + 8 * i;
+            float2 part = inside(q) ? ml[off + q] : make_float2(kNegInf, 0.f);
+            const float nm = fmaxf(m[i], part.x);
+            const float f = m[i] == nm ? 1.f : ex2_approx(m[i] - nm);
+            // a part without rows has left no O; a NaN sum passes on
+            const float fp = part.y == 0.f ? 0.f : part.x == nm ? 1.f : ex2_approx(part.x - nm);
+            m[i] = nm;
+            l[i] = l[i] * f + (c == 0 && fp != 0.f ? part.y * fp : 0.f);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float fa = __shfl_sync(~0u, f, 8 * c + 4 * k), fb = __shfl_sync(~0u, fp, 8 * c + 4 * k);
+#pragma unroll
+              for (int x = 0; x < VH; ++x)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                  const float4 y = fb != 0.f ? v[k][x][w] : make_float4(0.f, 0.f, 0.f, 0.f);
+                  acc[x][2 * w][i][k] = acc[x][2 * w][i][k] * fa + y.x * fb;
+                  acc[x][2 * w][i][k + 2] = acc[x][2 * w][i][k + 2] * fa + y.y * fb;
+                  acc[x][2 * w + 1][i][k] = acc[x][2 * w + 1][i][k] * fa + y.z * fb;
+                  acc[x][2 * w + 1][i][k + 2] = acc[x][2 * w + 1][i][k + 2] * fa + y.w * fb;
+                }
+            }
+          }
+        }
       }
     }
+
+    // ---------------------------------------------------------------- join the warps
 #pragma unroll
     for (int i = 0; i < QT; ++i) {
-      const float base = m[i] == kNegInf ? 0.f : m[i];   // nothing so far: every weight 2^-inf = 0
-#pragma unroll
-      for (int nt = 0; nt < 2 * KG; ++nt) {
-        const float p0 = ex2_approx(s[nt][2 * i] - base), p1 = ex2_approx(s[nt][2 * i + 1] - base);
-        l[i] += p0 + p1;
-        hi[i][nt] = pack16<T>(p0, p1);
-        const float2 back = unpack16<T>(hi[i][nt]);
-        lo[i][nt] = pack16<T>(p0 - back.x, p1 - back.y);
+      l[i] += __shfl_xor_sync(~0u, l[i], 1);
+      l[i] += __shfl_xor_sync(~0u, l[i], 2);
+      if (c == 0) {
+        part_ml[warp][g + 8 * i][0] = m[i];
+        part_ml[warp][g + 8 * i][1] = l[i];
       }
-    }
-#pragma unroll
-    for (int k = 0; k < KG; ++k)
 #pragma unroll
       for (int x = 0; x < VH; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t w0 = word(vr[x][4 * k], j), w1 = word(vr[x][4 * k + 1], j);
-          const uint32_t w2 = word(vr[x][4 * k + 2], j), w3 = word(vr[x][4 * k + 3], j);
-          const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-          const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
-#pragma unroll
-          for (int i = 0; i < QT; ++i) {
-            mma16816<T>(acc[x][j][i], a0, a1, a2, a3, hi[i][2 * k], hi[i][2 * k + 1]);
-            mma16816<T>(acc[x][j][i], a0, a1, a2, a3, lo[i][2 * k], lo[i][2 * k + 1]);
-          }
+          const int d = 64 * x + 8 * g + 2 * j;
+          *reinterpret_cast<float2*>(&part_o[warp][8 * i + 2 * c][d]) = make_float2(acc[x][j][i][0], acc[x][j][i][2]);
+          *reinterpret_cast<float2*>(&part_o[warp][8 * i + 2 * c + 1][d]) = make_float2(acc[x][j][i][1], acc[x][j][i][3]);
         }
-    if (more) R::load_v(vr, cur, g, c);
-  }
-
-  // ---------------------------------------------------------------- the prefix's parts
-  // Each part (a range of shared rows that one CTA of attend_prefix.cu took) joins
-  // one warp's sums as if it were another tile; the query rows b * N + q0 + q may
-  // lie in two blocks.
-  if (!STREAM && parts.plan.ctas) {
-    wait_for_primary();
-    const int RB = parts.plan.block_rows;
-    const int64_t r0 = (int64_t)b * N + q0;
-    for (int64_t blk = r0 / RB; blk <= (r0 + nq - 1) / RB; ++blk) {
-      const int u = h * parts.plan.blocks + (int)blk, off = (int)(r0 - blk * RB);   // query q is row off + q
-      const int c0 = parts.plan.cta_of((int64_t)u * parts.plan.nkt);
-      const int c1 = parts.plan.cta_of((int64_t)(u + 1) * parts.plan.nkt - 1);
-      auto inside = [&](int q) { return q < nq && off + q >= 0 && off + q < RB; };
-      for (int pc = c0 + rank * kWarps + warp; pc <= c1; pc += stride) {
-        const int64_t slot = parts.plan.slot(u, pc, pc == c0);
-        const float2* ml = parts.ml + slot * RB;
-        const float4* po = reinterpret_cast<const float4*>(parts.o) + slot * (RB * (D / 4));
+    }
+    __syncthreads();
+    constexpr int D4 = D / 4;
+    for (int x = tid; x < nq * D4; x += kThreads) {
+      const int q = x / D4, d = (x - q * D4) * 4;
+      float mm = kNegInf;
 #pragma unroll
-        for (int i = 0; i < QT; ++i) {
-          float4 v[2][VH][2];
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, part_ml[w][q][0]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ll = 0.f;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int q = 2 * c + k + 8 * i;
-            const bool in = inside(q);
-#pragma unroll
-            for (int x = 0; x < VH; ++x)
-#pragma unroll
-              for (int w = 0; w < 2; ++w)
-                v[k][x][w] = in ? po[(16 * x + 2 * g + w) * RB + off + q] : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-          const int q = g + 8 * i;
-          float2 part = inside(q) ? ml[off + q] : make_float2(kNegInf, 0.f);
-          const float nm = fmaxf(m[i], part.x);
-          const float f = m[i] == nm ? 1.f : ex2_approx(m[i] - nm);
-          // a part without rows has left no O; a NaN sum passes on
-          const float fp = part.y == 0.f ? 0.f : part.x == nm ? 1.f : ex2_approx(part.x - nm);
-          m[i] = nm;
-          l[i] = l[i] * f + (c == 0 && fp != 0.f ? part.y * fp : 0.f);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float fa = __shfl_sync(~0u, f, 8 * c + 4 * k), fb = __shfl_sync(~0u, fp, 8 * c + 4 * k);
-#pragma unroll
-            for (int x = 0; x < VH; ++x)
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const float4 y = fb != 0.f ? v[k][x][w] : make_float4(0.f, 0.f, 0.f, 0.f);
-                acc[x][2 * w][i][k] = acc[x][2 * w][i][k] * fa + y.x * fb;
-                acc[x][2 * w][i][k + 2] = acc[x][2 * w][i][k + 2] * fa + y.y * fb;
-                acc[x][2 * w + 1][i][k] = acc[x][2 * w + 1][i][k] * fa + y.z * fb;
-                acc[x][2 * w + 1][i][k + 2] = acc[x][2 * w + 1][i][k + 2] * fa + y.w * fb;
-              }
-          }
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = part_ml[w][q][0], f = mw == mm ? 1.f : ex2_approx(mw - mm);
+        const float4 v = *reinterpret_cast<const float4*>(&part_o[w][q][d]);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+        ll = fmaf(f, part_ml[w][q][1], ll);
+      }
+      if (!STREAM) {
+        *reinterpret_cast<float4*>(&cta_o[STREAM ? 0 : q][d]) = o;
+        if (d == 0) {
+          cta_ml[q][0] = mm;
+          cta_ml[q][1] = ll;
         }
+      } else if (whole) {
+        write_out<T>(a, b, h * N + q0 + q, d, mm, ll, o);
+      } else {
+        reinterpret_cast<float4*>(plan.part_o)[(slot * QN + q) * D4 + d / 4] = o;
+        if (d == 0) plan.part_ml[slot * QN + q] = make_float2(mm, ll);
       }
     }
-  }
-
-  // ---------------------------------------------------------------- join the warps
-#pragma unroll
-  for (int i = 0; i < QT; ++i) {
-    l[i] += __shfl_xor_sync(~0u, l[i], 1);
-    l[i] += __shfl_xor_sync(~0u, l[i], 2);
-    if (c == 0) {
-      part_ml[warp][g + 8 * i][0] = m[i];
-      part_ml[warp][g + 8 * i][1] = l[i];
+    if (STREAM) {
+      __syncthreads();                              // the next segment's sums go where these were
+      b = next_b;
+      if (b >= a.B) break;
+      continue;
     }
-#pragma unroll
-    for (int x = 0; x < VH; ++x)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int d = 64 * x + 8 * g + 2 * j;
-        *reinterpret_cast<float2*>(&part_o[warp][8 * i + 2 * c][d]) = make_float2(acc[x][j][i][0], acc[x][j][i][2]);
-        *reinterpret_cast<float2*>(&part_o[warp][8 * i + 2 * c + 1][d]) = make_float2(acc[x][j][i][1], acc[x][j][i][3]);
+    // ---------------------------------------------------------------- join the cluster
+    cluster.sync();
+    for (int x = rank * kThreads + tid; x < nq * D4; x += C * kThreads) {
+      const int q = x / D4, d = (x - q * D4) * 4;
+      float mm = kNegInf;
+      for (int r = 0; r < C; ++r) mm = fmaxf(mm, *cluster.map_shared_rank(&cta_ml[q][0], r));
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ll = 0.f;
+      for (int r = 0; r < C; ++r) {
+        const float mr = *cluster.map_shared_rank(&cta_ml[q][0], r), f = mr == mm ? 1.f : ex2_approx(mr - mm);
+        const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&cta_o[q][d], r));
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+        ll = fmaf(f, *cluster.map_shared_rank(&cta_ml[q][1], r), ll);
       }
-  }
-  __syncthreads();
-  constexpr int D4 = D / 4;
-  for (int x = tid; x < nq * D4; x += kThreads) {
-    const int q = x / D4, d = (x - q * D4) * 4;
-    float mm = kNegInf;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, part_ml[w][q][0]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ll = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float mw = part_ml[w][q][0], f = mw == mm ? 1.f : ex2_approx(mw - mm);
-      const float4 v = *reinterpret_cast<const float4*>(&part_o[w][q][d]);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
-      ll = fmaf(f, part_ml[w][q][1], ll);
-    }
-    if (!STREAM) {
-      *reinterpret_cast<float4*>(&cta_o[STREAM ? 0 : q][d]) = o;
-      if (d == 0) {
-        cta_ml[q][0] = mm;
-        cta_ml[q][1] = ll;
-      }
-    } else if (whole) {
       write_out<T>(a, b, h * N + q0 + q, d, mm, ll, o);
-    } else {
-      reinterpret_cast<float4*>(plan.part_o)[(slot * QN + q) * D4 + d / 4] = o;
-      if (d == 0) plan.part_ml[slot * QN + q] = make_float2(mm, ll);
     }
-  }
-  if (STREAM) {
-    __syncthreads();                              // the next segment's sums go where these were
-    b = next_b;
-    if (b >= a.B) break;
-    continue;
-  }
-  // ---------------------------------------------------------------- join the cluster
-  cluster.sync();
-  for (int x = rank * kThreads + tid; x < nq * D4; x += C * kThreads) {
-    const int q = x / D4, d = (x - q * D4) * 4;
-    float mm = kNegInf;
-    for (int r = 0; r < C; ++r) mm = fmaxf(mm, *cluster.map_shared_rank(&cta_ml[q][0], r));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ll = 0.f;
-    for (int r = 0; r < C; ++r) {
-      const float mr = *cluster.map_shared_rank(&cta_ml[q][0], r), f = mr == mm ? 1.f : ex2_approx(mr - mm);
-      const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&cta_o[q][d], r));
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
-      ll = fmaf(f, *cluster.map_shared_rank(&cta_ml[q][1], r), ll);
-    }
-    write_out<T>(a, b, h * N + q0 + q, d, mm, ll, o);
-  }
-  cluster.sync();   // no CTA leaves while another reads its shared memory
-  break;
+    cluster.sync();   // no CTA leaves while another reads its shared memory
+    break;
   }
   // The join that follows waits for this kernel alone, so its last CTA ends after
   // the prefix's kernel, beside which the others may have come and gone.
@@ -756,11 +766,13 @@ RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool 
 size_t RowsPlan::o_bytes(int D) const { return (size_t)slots() * qn * D * 4; }
 size_t RowsPlan::bytes(int D) const { return ctas ? o_bytes(D) + (size_t)slots() * qn * 8 : 0; }
 
-cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int D, int dtype, int sms, cudaStream_t s) {
+cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int D, int dtype,
+                               int sms, cudaStream_t s) {
+  using bf16 = __nv_bfloat16;
   if (a.pend)   // a handle's rows are fp16
     return D == 64 ? launch_q<__half, 64, true>(a, parts, plan, sms, s) : launch_q<__half, 128, true>(a, parts, plan, sms, s);
   if (dtype == kBf16)
-    return D == 64 ? launch_q<__nv_bfloat16, 64, false>(a, parts, plan, sms, s) : launch_q<__nv_bfloat16, 128, false>(a, parts, plan, sms, s);
+    return D == 64 ? launch_q<bf16, 64, false>(a, parts, plan, sms, s) : launch_q<bf16, 128, false>(a, parts, plan, sms, s);
   return D == 64 ? launch_q<__half, 64, false>(a, parts, plan, sms, s) : launch_q<__half, 128, false>(a, parts, plan, sms, s);
 }
 

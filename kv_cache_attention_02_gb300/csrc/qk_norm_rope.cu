@@ -18,6 +18,10 @@
 // of the frequency itself), so far positions lose nothing and no fp64
 // instruction runs. The lanes of a warp compute a token's D/2 angles once
 // between them, then take the warp's heads of that token with them.
+//
+// Measured on GB300: 32 x 4096 tokens of 40 heads of 128, bf16, 414-418 us, 6.4-6.5
+// TB/s (0.95 of the measured copy rate); 3 x 1021 fp32 tokens of 32 heads 13.5 us, 5.6
+// TB/s, 2.5 us of it the launch; one token of 8 heads 2.5-3 us.
 #include "kvevict_internal.cuh"
 #include "attend_internal.cuh"
 
