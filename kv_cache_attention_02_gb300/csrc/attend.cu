@@ -251,6 +251,7 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
   }
   rp.part_o = reinterpret_cast<float*>(space);
   rp.part_ml = reinterpret_cast<float2*>(space + rp.o_bytes(D));
+  rp.first = reinterpret_cast<int64_t*>(space + rp.o_bytes(D) + rp.ml_bytes());
   return cuda_result(launch_attend_rows(a, p.parts(), rp, D, d->dtype, dev.sms, s), "launch");
 }
 

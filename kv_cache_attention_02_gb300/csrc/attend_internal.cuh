@@ -120,12 +120,15 @@ cudaError_t launch_qk_norm_rope(QkArgs a, int D, int in_dtype, int out_dtype, in
 // contiguous range per CTA; otherwise a cluster per unit.
 struct RowsPlan {
   int ctas, qchunks, qn, final;   // a unit: qn query heads of a key head, qchunks units; final: no prefix parts to join
+  int batch;
   int64_t units;
+  int64_t* first;                 // [B + 1], unequal lengths: the first tile of each sequence, their total
   float* part_o;                  // [slot][qn][D]
   float2* part_ml;                // [slot][qn] maximum (base 2) and sum
   __host__ __device__ int64_t slot(int64_t u, int c, bool from_start) const { return final ? 2 * c + from_start : u + c; }
   int64_t slots() const { return final ? 2 * (int64_t)ctas : units + ctas; }
   size_t o_bytes(int D) const;
+  size_t ml_bytes() const;
   size_t bytes(int D) const;
 };
 RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool pend, bool prefix_parts, int sms);

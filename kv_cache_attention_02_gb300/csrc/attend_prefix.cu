@@ -51,6 +51,7 @@
 #include "tcgen05.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 namespace kvx {
 namespace {
@@ -711,12 +712,14 @@ cudaError_t launch_px(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pr
   auto kernel = attend_prefix_kernel<T, D, PAIR>;
   // The kernel's redistribution of registers needs the 168 a thread that its
   // launch bound gives it: checked, as it would wait forever with fewer.
-  static const cudaError_t regs = [&] {
+  static std::atomic<bool> checked{false};
+  if (!checked.load(std::memory_order_relaxed)) {
     cudaFuncAttributes f;
     const cudaError_t r = cudaFuncGetAttributes(&f, kernel);
-    return r != cudaSuccess ? r : f.numRegs == 168 ? cudaSuccess : cudaErrorLaunchOutOfResources;
-  }();
-  if (regs != cudaSuccess) return regs;
+    if (r != cudaSuccess) return r;
+    if (f.numRegs != 168) return cudaErrorLaunchOutOfResources;
+    checked.store(true, std::memory_order_relaxed);
+  }
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PxGeo<D>::SMEM);
   if (e != cudaSuccess) return e;
   kernel<<<p.plan.ctas, kPxThreads, PxGeo<D>::SMEM, s>>>(kmap, vmap, p);
@@ -769,7 +772,7 @@ PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int64_t own_
   // 8 x 2048 shared rows (67 MB) 12 | 13 us, 16 x 2048 12 | 21, 4 x 2048 12 | 10; beside
   // 256 own rows 16 x 2048 (134 MB) 16 | 22, 8 x 2048 16 | 14.
   const int64_t visits = (int64_t)B * ((G / H + 15) / 16);
-  if (visits < 2 || visits * H * P * D * 4 < (own ? 96 : 64) * 1000000ll) return pl;   // ctas = 0
+  if (visits < 2 || (double)visits * H * P * D * 4 < (own ? 96e6 : 64e6)) return pl;   // ctas = 0
   pl.pair = rows <= kT;
   pl.block_rows = pl.pair ? kT : 2 * kT;
   pl.blocks = (int)((rows + pl.block_rows - 1) / pl.block_rows);

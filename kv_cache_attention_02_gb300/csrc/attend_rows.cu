@@ -198,71 +198,53 @@ __device__ __forceinline__ int stream_tiles(const AttendArgs& a, int b) {
   return max(1, SeqRows<TR>(a, b).tiles(a));
 }
 
-// Where sequences lie in the row of all units' tiles (warp-collective): the
-// total, and the first tile of the sequence that `find` returns.
-template <int TR>
+// Where sequences lie in the row of all units' tiles. With unequal lengths the
+// stream kernel finds that out and leaves it in the workspace for the join: the
+// first tile of every sequence, and the total after them.
 struct Stream {
-  int64_t total, base;
+  int64_t total;
   int ctas;                                   // that have work: never more than there are tiles
-  int upb;                                    // units of a sequence
-  bool even;                                  // all sequences have as many tiles
-  __device__ __forceinline__ Stream(const AttendArgs& a, const RowsPlan& plan) : base(0), upb(a.H * plan.qchunks) {
-    even = !a.lens && !a.plens;
-    int64_t sum = 0;
-    if (even) {
-      sum = (int64_t)a.B * stream_tiles<TR>(a, 0);
-    } else {
-      for (int b = threadIdx.x & 31; b < a.B; b += 32) sum += stream_tiles<TR>(a, b);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    }
-    total = sum * upb;
-    ctas = (int)min((int64_t)plan.ctas, total);
-  }
-  // The sequence that tile x belongs to (x < total).
-  __device__ __forceinline__ int find(const AttendArgs& a, int64_t x) {
-    if (even) {
-      const int64_t per = (int64_t)upb * stream_tiles<TR>(a, 0);
-      const int b = (int)(x / per);
-      base = b * per;
-      return b;
-    }
-    return scan(a, [&](int, int64_t end) { return end * upb > x; });
-  }
-  // Sets base for sequence b.
-  __device__ __forceinline__ void seek(const AttendArgs& a, int b) {
-    if (even)
-      base = (int64_t)b * upb * stream_tiles<TR>(a, 0);
-    else
-      (void)scan(a, [&](int s, int64_t) { return s == b; });
-  }
+  __device__ __forceinline__ Stream(int64_t tiles, const RowsPlan& plan)
+      : total(tiles), ctas((int)min((int64_t)plan.ctas, tiles)) {}
   __device__ __forceinline__ int64_t start(int c) const { return c * total / ctas; }
   __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * ctas - 1) / total); }
-
- private:
-  template <typename F>
-  __device__ __forceinline__ int scan(const AttendArgs& a, F&& hit) {
-    const int lane = threadIdx.x & 31;
-    int64_t run = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int64_t own = b0 + lane < a.B ? stream_tiles<TR>(a, b0 + lane) : 0;
-      int64_t incl = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const uint32_t found = __ballot_sync(~0u, b0 + lane < a.B && hit(b0 + lane, run + incl));
-      if (found) {
-        const int f = __ffs(found) - 1;
-        base = (run + __shfl_sync(~0u, incl - own, f)) * upb;
-        return b0 + f;
-      }
-      run += __shfl_sync(~0u, incl, 31);
-    }
-    return a.B;   // not reached
-  }
 };
+__device__ __forceinline__ bool even_lengths(const AttendArgs& a) { return !a.lens && !a.plens; }
+
+// For a CTA of the stream: the sequence that its first tile belongs to (b) and
+// that sequence's first tile (base). All threads take a share of the sequences;
+// sums_s: [kThreads].
+template <int TR>
+__device__ __forceinline__ Stream find_range(const AttendArgs& a, const RowsPlan& plan, int64_t* sums_s, int& b,
+                                             int64_t& base) {
+  const int upb = a.H * plan.qchunks;          // units of a sequence
+  if (even_lengths(a)) {
+    const int64_t per = (int64_t)upb * stream_tiles<TR>(a, 0);
+    const Stream st(a.B * per, plan);
+    b = (int)min((int64_t)a.B - 1, st.start(min((int)blockIdx.x, st.ctas - 1)) / per);
+    base = b * per;
+    return st;
+  }
+  const int tid = threadIdx.x, share = (a.B + kThreads - 1) / kThreads;
+  int64_t own = 0;
+  for (int i = tid * share; i < min(a.B, (tid + 1) * share); ++i) own += stream_tiles<TR>(a, i);
+  sums_s[tid] = own;
+  __syncthreads();
+  int64_t sum = 0;
+  for (int i = 0; i < kThreads; ++i) sum += sums_s[i];
+  const Stream st(sum * upb, plan);
+  const int64_t x = st.start(min((int)blockIdx.x, st.ctas - 1));
+  base = 0;
+  int i = 0;
+  while (i < kThreads - 1 && (base + sums_s[i]) * upb <= x) base += sums_s[i++];
+  for (b = i * share; b < a.B - 1; ++b) {
+    const int t = stream_tiles<TR>(a, b);
+    if ((base + t) * upb > x) break;
+    base += t;
+  }
+  base *= upb;
+  return st;
+}
 
 // QT: groups of 8 query heads (1 or 2). STREAM: two CTAs an SM at D = 128, three
 // at 64 (the registers of a warp's tile, its sums and its queries).
@@ -288,16 +270,16 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   int64_t at = 0, end = 0, base = 0;              // STREAM: next tile, the range's end, the sequence's first tile
   int upb = 0;
   if (STREAM) {
-    Stream<TR> st(a, plan);
+    __shared__ int64_t sums_s[kThreads];
+    const Stream st = find_range<TR>(a, plan, sums_s, b, base);
     if ((int)blockIdx.x >= st.ctas) {
       if ((int)blockIdx.x == plan.ctas - 1) wait_for_primary();
       return;
     }
     at = st.start(blockIdx.x);
     end = st.start(blockIdx.x + 1);
-    b = st.find(a, at);
-    base = st.base;
-    upb = st.upb;
+    upb = a.H * qchunks;
+    if (blockIdx.x == 0 && tid == 0 && !even_lengths(a)) plan.first[a.B] = st.total;
     ub = 0;
   } else {
     const int unit = (int)(blockIdx.x / (unsigned)C);
@@ -322,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
       at += total - first;
       whole = plan.final && first == 0 && total == tb;
       slot = plan.slot((int64_t)b * upb + ub, blockIdx.x, first == 0);
+    if (rem == 0 && tid == 0 && !even_lengths(a)) plan.first[b] = base;
       if (at == base + (int64_t)upb * tb) {
         base = at;
         next_b = b + 1;
@@ -654,12 +637,12 @@ __global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_cons
   const int N = a.G / a.H, b = (int)(blockIdx.x / (unsigned)a.G), gq = (int)(blockIdx.x - (unsigned)b * a.G);
   const int h = gq / N, j = gq - h * N, qc = j / QN, q = j - qc * QN;
   constexpr int TR = tile_rows(QT, true);
-  Stream<TR> st(a, plan);
-  st.seek(a, b);
-  const int ub = h * plan.qchunks + qc, tb = stream_tiles<TR>(a, b);
-  const int64_t x = st.base + (int64_t)ub * tb, u = (int64_t)b * st.upb + ub;
-  const int c0 = st.cta_of(x), c1 = st.cta_of(x + tb - 1);
+  const int upb = a.H * plan.qchunks, ub = h * plan.qchunks + qc, tb = stream_tiles<TR>(a, b);
   wait_for_primary();                             // in every block: this kernel ends after the one before it
+  const bool even = even_lengths(a);
+  const Stream st(even ? (int64_t)a.B * upb * tb : plan.first[a.B], plan);
+  const int64_t x = (even ? (int64_t)b * upb * tb : plan.first[b]) + (int64_t)ub * tb, u = (int64_t)b * upb + ub;
+  const int c0 = st.cta_of(x), c1 = st.cta_of(x + tb - 1);
   if (plan.final && c0 == c1) return;             // written out by that CTA
   const int nr = c1 - c0 + 1;
   int np = 0, p0 = 0, pu = 0, prow = 0;
@@ -752,6 +735,7 @@ RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool 
   RowsPlan pl{};
   const int qt = rows_qt(G / H);
   pl.qn = 8 * qt;
+  pl.batch = B;
   pl.qchunks = (G / H + pl.qn - 1) / pl.qn;
   pl.units = (int64_t)B * H * pl.qchunks;
   pl.final = !prefix_parts;
@@ -764,7 +748,8 @@ RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool 
 }
 
 size_t RowsPlan::o_bytes(int D) const { return (size_t)slots() * qn * D * 4; }
-size_t RowsPlan::bytes(int D) const { return ctas ? o_bytes(D) + (size_t)slots() * qn * 8 : 0; }
+size_t RowsPlan::ml_bytes() const { return (size_t)slots() * qn * 8; }
+size_t RowsPlan::bytes(int D) const { return ctas ? o_bytes(D) + ml_bytes() + ((size_t)batch + 1) * 8 : 0; }
 
 cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int D, int dtype,
                                int sms, cudaStream_t s) {

@@ -80,6 +80,24 @@ def test_room_for_many_tiles_but_few_rows(kvx, B, N, H, D, n, top):
     ref.check_attend(kvx, q, lens=lens, **rows)
 
 
+def test_many_short_sequences(kvx):
+    """Thousands of sequences, most of them empty, over ranges that hold many each (checked where there are rows)."""
+    B, H, n = 6000, 8, 40
+    q, rows = _make(B, 2, H, 128, n=n, seed=16)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    some = torch.tensor([0, 1, 2, 700, 3001, 3002, 5998, 5999], device="cuda")
+    lens[some] = torch.tensor([1, n, 0, 33, n, 17, 16, n], dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, float("nan")), torch.empty(B, 2 * H, device="cuda")
+    kvx.attend(q, out, lens=lens, lse=lse, **rows)
+    torch.cuda.synchronize()
+    want = ref.attend_batch(q[some], k=rows["k"][some], v=rows["v"][some], lens=lens[some])
+    ref.check("out", out[some], want[0], want[2])
+    ref.check("lse", lse[some], want[1], want[3])
+    rest = torch.ones(B, dtype=torch.bool, device="cuda")
+    rest[some] = False
+    assert (out[rest] == 0).all() and (lse[rest] == -math.inf).all()
+
+
 @pytest.mark.parametrize("B,N,H,D,n,P", [(40, 4, 8, 128, 401, 700), (200, 3, 4, 64, 400, 300), (30, 20, 8, 128, 350, 1000),
                                         (1, 4, 2, 128, 30000, 20000)])
 def test_many_tiles_with_prefix(kvx, B, N, H, D, n, P):

@@ -84,6 +84,40 @@ def test_decode_loop(kvx, D, N, prefix):
     h.check()
 
 
+@pytest.mark.parametrize("B,budget,prefix", [(40, 20, 2500), (3, 20, 0), (60, 700, 0), (60, 300, 1700)])
+def test_cache_rows_beside_a_large_prefix(kvx, B, budget, prefix):
+    """Every way the rows are read (clusters, ranges, beside the tensor-core kernel) with a compaction pending; then after it."""
+    H, N, D, T = 2, 4, 128, 9
+    kw = dict(batch=B, n_layers=2, n_kv_heads=H, head_dim=D, layer_budgets=[budget, 12], n_sink=1, rope_theta=THETA,
+              max_prefill=budget, with_values=True)
+    h, twin = kvx.KVEvict(**kw), kvx.KVEvict(**kw)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def r(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda").half()
+    keys, values = r(B, 2, H, budget, D), r(B, 2, H, budget, D)
+    steps_k, steps_v = r(T, B, 2, H, D), r(T, B, 2, H, D)
+    for x in (h, twin):
+        x.prefill(keys, values=values)
+        x.decode(steps_k, values=steps_v)
+    q, k_new, v_new = r(B, N * H, D), r(B, H, D), r(B, H, D)
+    shared = {"prefix_k": r(H, prefix, D), "prefix_v": r(H, prefix, D)} if prefix else {}
+    for l, rows in ((0, budget), (1, 12)):
+        kv = [[_rows(twin, b, l, hh) for hh in range(H)] for b in range(B)]
+        k, v = (torch.stack([torch.stack([x[i] for x in row]) for row in kv]) for i in (0, 1))
+        assert k.shape == (B, H, rows, D)
+        want = ref.attend_batch(q, k=k, v=v, k_new=k_new, v_new=v_new, **shared)
+        for again in range(2):
+            out, lse = torch.full_like(q, float("nan")), torch.empty(B, N * H, device="cuda")
+            h.attend(l, q, out, k_new=k_new, v_new=v_new, lse=lse, **shared)
+            torch.cuda.synchronize()
+            ref.check("out", out, want[0], want[2])
+            ref.check("lse", lse, want[1], want[3])
+            if l == 1:
+                h.flush()                  # the second time with the compaction applied
+    h.check()
+
+
 def test_attend_refuses(kvx):
     q = torch.zeros(2, 4, 64, dtype=torch.float16, device="cuda")
     kw = dict(batch=2, n_layers=2, n_kv_heads=2, head_dim=64, avg_budget=16)
