@@ -143,12 +143,12 @@ int attend_check(const kvevict_attention* d) {
 
 // The prefix kernel's plan; not used (the row kernel reads the shared rows
 // itself) where TMA cannot describe the rows.
-PrefixPlan plan_prefix(const kvevict_attention* d, bool own, int64_t rows, int sms) {
+PrefixPlan plan_prefix(const kvevict_attention* d, bool own, Streamed stream, int sms) {
   const bool fit = d->prefix > 0 && prefix_strides_fit(d->prefix_k_stride, d->n_kv_heads, d->prefix, d->head_dim) &&
                    prefix_strides_fit(d->prefix_v_stride, d->n_kv_heads, d->prefix, d->head_dim);
   return fit
              ? prefix_plan(d->batch, d->n_heads, d->n_kv_heads, d->head_dim, d->prefix, own,
-                           rows * d->batch * d->n_kv_heads, sms)
+                           stream, sms)
              : PrefixPlan{};
 }
 
@@ -227,11 +227,15 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
   const int D = d->head_dim;
   PrefixArgs p{};
   const int own = a.n + (a.k_new ? 1 : 0);             // rows of a sequence, at most
-  p.plan = plan_prefix(d, rows || own, own, dev.sms);
+  p.plan = plan_prefix(d, rows || own, Streamed{}, dev.sms);
   const bool alone = p.plan.ctas && p.plan.final;      // the prefix is all there is
   RowsPlan rp{};
   if (!alone)
     rp = rows_plan(a.B, a.G, a.H, D, a.n, p.plan.ctas ? 0 : a.P, a.k_new, rows != nullptr, p.plan.ctas > 0, dev.sms);
+  if (p.plan.ctas && rp.ctas) {                        // both at once, each on its SMs
+    p.plan = plan_prefix(d, true, Streamed{(int64_t)a.B * a.H * own * D * 4, rp.units}, dev.sms);
+    rp.ctas = std::min(rp.ctas, stream_ctas(D, std::max(1, dev.sms - p.plan.ctas)));
+  }
   const size_t need = p.plan.bytes(D) + rp.bytes(D);
   if (need && (d->workspace_bytes < need || !d->workspace || !aligned(d->workspace)))
     return invalid("workspace must be 16-byte aligned and hold kvevict_attend_workspace bytes");
@@ -292,7 +296,7 @@ extern "C" int kvevict_attend_workspace(const kvevict_attention* args, int32_t w
     if (int rc = kvx::device_info(&dev)) return rc;
     const int B = args->batch, G = args->n_heads, H = args->n_kv_heads, D = args->head_dim;
     const bool own = with_cache || args->n > 0 || args->k_new;
-    const kvx::PrefixPlan pp = kvx::plan_prefix(args, own, 0, dev.sms);
+    const kvx::PrefixPlan pp = kvx::plan_prefix(args, own, kvx::Streamed{}, dev.sms);
     *bytes = pp.bytes(D);
     if (pp.ctas && !own) return KVEVICT_OK;
     // a handle's rows are not in the description: as many as there can be

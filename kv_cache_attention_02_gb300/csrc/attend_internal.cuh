@@ -83,9 +83,12 @@ struct PrefixPlan {
   bool shared_blocks() const;   // whether any block is cut
 };
 bool prefix_strides_fit(const int64_t* stride, int H, int P, int D);
-// own_rows: rows of all sequences and key heads that the row kernel reads beside
-// it (the workspace does not depend on their number); own: whether there are any.
-PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int64_t own_rows, int sms);
+// What the row kernel streams beside the prefix's.
+struct Streamed {
+  int64_t bytes, units;
+};
+// own: whether there are own rows to join; the workspace does not depend on `stream`.
+PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, Streamed stream, int sms);
 
 // The parts of the prefix's attention in the workspace: per slot O as
 // [D/4][block_rows] float4 and (m, l) as [block_rows] float2, base-2 units.
@@ -126,12 +129,14 @@ struct RowsPlan {
   float* part_o;                  // [slot][qn][D]
   float2* part_ml;                // [slot][qn] maximum (base 2) and sum
   __host__ __device__ int64_t slot(int64_t u, int c, bool from_start) const { return final ? 2 * c + from_start : u + c; }
-  int64_t slots() const { return final ? 2 * (int64_t)ctas : units + ctas; }
+  int64_t slots;                  // parts that the workspace has room for
   size_t o_bytes(int D) const;
   size_t ml_bytes() const;
   size_t bytes(int D) const;
 };
+// prefix_parts: the prefix's kernel runs beside it.
 RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool pend, bool prefix_parts, int sms);
+int stream_ctas(int D, int sms);   // resident on so many SMs
 // parts.plan.ctas > 0: joins the prefix's parts too (a.P is 0 then).
 cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int D, int dtype,
                                int sms, cudaStream_t s);

@@ -763,7 +763,7 @@ bool prefix_strides_fit(const int64_t* stride, int H, int P, int D) {
   return hs >= D && rs >= D && hs < ((int64_t)1 << 39) && rs < ((int64_t)1 << 39);
 }
 
-PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int64_t own_rows, int sms) {
+PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, Streamed stream, int sms) {
   PrefixPlan pl{};
   const int64_t rows = (int64_t)B * (G / H);
   // The row kernel reads the prefix once for every sequence (and 16 query heads),
@@ -780,14 +780,27 @@ PrefixPlan prefix_plan(int B, int G, int H, int D, int P, bool own, int64_t own_
   pl.units = H * pl.blocks;
   pl.final = !own;
   const int64_t total = pl.total();
-  // The row kernel of the same call starts as soon as SMs are free, so with own
-  // rows the prefix takes only its share of them, by rows read: both then end
-  // together (32 sequences on 16384 shared + 512 own rows: 35 us against
-  // 44 us one after the other).
-  const int64_t share = own_rows > 0 ? sms * total / (total + own_rows / kT) : sms;
-  // (not so few that a CTA has more than 16 tiles, or two blocks, beside little)
-  const int64_t least = std::max<int64_t>(pl.units, total / 16);
-  const int64_t most = std::min<int64_t>({std::max(share, least), sms, pl.pair ? (total + 1) / 2 : total});
+  int64_t most = std::min<int64_t>(sms, pl.pair ? (total + 1) / 2 : total);
+  if (stream.bytes > 0) {
+    // The row kernel streams its rows on the other SMs meanwhile. Both times by SM
+    // count, in us: this kernel's start and end and its longest range of tiles; the
+    // stream's, 1.8 a unit of its CTAs and its bytes at 50 GB/s a SM. The split whose longer one is
+    // shortest (32 sequences on 16384 shared + 512 own rows: 33 us against 44
+    // one after the other; 8192 + 2048: 51 against 84 with the SMs shared by rows read).
+    const double tile = pl.pair ? (D == 128 ? 1.4 : 0.9) : (D == 128 ? 1.9 : 1.5);
+    double best = 1e30;
+    int64_t at = most;
+    for (int64_t p = 1; p <= std::min<int64_t>(most, sms - 4); ++p) {
+      const double mine = 8.0 + tile * (double)((total + p - 1) / p);
+      const double rows = 3.0 + 1.8 * (double)stream.units / stream_ctas(D, (int)(sms - p)) +
+                          (double)stream.bytes / (50e3 * (double)(sms - p));
+      if (std::max(mine, rows) < best) {
+        best = std::max(mine, rows);
+        at = p;
+      }
+    }
+    most = at;
+  }
   pl.ctas = (int)most;
   if (pl.units <= most) {
     const int split = (int)std::min<int64_t>(most / pl.units, pl.nkt);

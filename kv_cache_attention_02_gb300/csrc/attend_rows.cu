@@ -65,6 +65,10 @@ constexpr int kStreamTiles = 8, kBesideTiles = 1;
 // A stream too where a cluster's warps would have this many tiles each: few, long
 // units that a cluster cannot spread over the GPU.
 constexpr int kClusterTiles = 8;
+// Parts of a head that one warp joins, with many heads (half as many with few): 32
+// sequences of 1024 rows 24.8 us, 28.3 with eight warps a head; 2 of 4096, 40 parts,
+// 10.0 with eight, 11.5 with one.
+constexpr int kFewParts = 32;
 
 constexpr int stream_ctas_per_sm(int D) { return D == 64 ? 3 : 2; }
 int rows_qt(int N) { return N <= 8 ? 1 : 2; }
@@ -624,27 +628,32 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
   if (STREAM && (int)blockIdx.x == plan.ctas - 1) wait_for_primary();
 }
 
-// Joins the parts of a stream's cut units, and the prefix's: one block a query
-// head, a lane for four columns, the parts dealt to the warps.
-template <typename T, int D, int QT>
-__global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_constant__ AttendArgs a,
-                                                               const __grid_constant__ PrefixParts parts,
-                                                               const __grid_constant__ RowsPlan plan) {
-  constexpr int D4 = D / 4, QN = 8 * QT;
-  __shared__ float2 ml_s[8];
-  __shared__ float4 o_s[8][D4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int N = a.G / a.H, b = (int)(blockIdx.x / (unsigned)a.G), gq = (int)(blockIdx.x - (unsigned)b * a.G);
-  const int h = gq / N, j = gq - h * N, qc = j / QN, q = j - qc * QN;
-  constexpr int TR = tile_rows(QT, true);
+// Joins the parts of a stream's cut units, and the prefix's: JW warps a query
+// head (one, in blocks of four heads, where a head has few parts), a lane for four
+// columns, the parts dealt to the warps and eight loads under way at once.
+template <typename T, int D, int QT, int JW>
+__global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW)
+    attend_rows_join_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ PrefixParts parts,
+                            const __grid_constant__ RowsPlan plan) {
+  constexpr int D4 = D / 4, QN = 8 * QT, TR = tile_rows(QT, true), LOADS = 8;
+  __shared__ float2 ml_s[JW];
+  __shared__ float4 o_s[JW][D4];
+  const int warp = JW == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned head = JW == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const bool there = head < (unsigned)a.B * (unsigned)a.G;
+  const int b = there ? (int)(head / (unsigned)a.G) : 0, gq = there ? (int)(head - (unsigned)b * a.G) : 0;
+  // where the head's parts are: all but unequal lengths' before the wait
+  const int N = a.G / a.H, h = gq / N, j = gq - h * N, qc = j / QN, q = j - qc * QN;
   const int upb = a.H * plan.qchunks, ub = h * plan.qchunks + qc, tb = stream_tiles<TR>(a, b);
-  wait_for_primary();                             // in every block: this kernel ends after the one before it
+  const int64_t u = (int64_t)b * upb + ub;
+  int c0 = 0, c1 = 0;
+  auto range = [&](int64_t total, int64_t first) {
+    const Stream st(total, plan);
+    c0 = st.cta_of(first + (int64_t)ub * tb);
+    c1 = st.cta_of(first + (int64_t)ub * tb + tb - 1);
+  };
   const bool even = even_lengths(a);
-  const Stream st(even ? (int64_t)a.B * upb * tb : plan.first[a.B], plan);
-  const int64_t x = (even ? (int64_t)b * upb * tb : plan.first[b]) + (int64_t)ub * tb, u = (int64_t)b * upb + ub;
-  const int c0 = st.cta_of(x), c1 = st.cta_of(x + tb - 1);
-  if (plan.final && c0 == c1) return;             // written out by that CTA
-  const int nr = c1 - c0 + 1;
+  if (even) range((int64_t)a.B * upb * tb, (int64_t)b * upb * tb);
   int np = 0, p0 = 0, pu = 0, prow = 0;
   if (parts.plan.ctas) {
     const int64_t r = (int64_t)b * N + j;
@@ -654,14 +663,19 @@ __global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_cons
     p0 = parts.plan.cta_of((int64_t)pu * parts.plan.nkt);
     np = parts.plan.cta_of((int64_t)(pu + 1) * parts.plan.nkt - 1) - p0 + 1;
   }
+  wait_for_primary();                             // in every block: this kernel ends after the one before it
+  if (!there) return;
+  if (!even) range(plan.first[a.B], plan.first[b]);
+  if (plan.final && c0 == c1) return;             // written out by that CTA
+  const int nr = c1 - c0 + 1;
   float m = kNegInf, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = warp; i0 < nr + np; i0 += 32) {    // four parts' loads under way at once
-    float2 ml[4];
-    float4 v[4];
+  for (int i0 = warp; i0 < nr + np; i0 += LOADS * JW) {
+    float2 ml[LOADS];
+    float4 v[LOADS];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + 8 * k;
+    for (int k = 0; k < LOADS; ++k) {
+      const int i = i0 + JW * k;
       ml[k] = make_float2(kNegInf, 0.f);
       v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < nr) {
@@ -677,31 +691,33 @@ __global__ void __launch_bounds__(256) attend_rows_join_kernel(const __grid_cons
     }
     float nm = m;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) nm = fmaxf(nm, ml[k].x);
+    for (int k = 0; k < LOADS; ++k) nm = fmaxf(nm, ml[k].x);
     const float f = m == nm ? 1.f : ex2_approx(m - nm);
     m = nm;
     l *= f;
     o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < LOADS; ++k) {
       const float w = ml[k].x == nm ? 1.f : ex2_approx(ml[k].x - nm);
       l = fmaf(ml[k].y, w, l);
       o = make_float4(fmaf(v[k].x, w, o.x), fmaf(v[k].y, w, o.y), fmaf(v[k].z, w, o.z), fmaf(v[k].w, w, o.w));
     }
   }
-  if (lane == 0) ml_s[warp] = make_float2(m, l);
-  if (lane < D4) o_s[warp][lane] = o;
-  __syncthreads();
-  if (warp != 0 || lane >= D4) return;
-  for (int w = 1; w < 8; ++w) {
-    const float2 ml = ml_s[w];
-    const float4 v = o_s[w][lane];
-    const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2_approx(m - nm), y = ml.x == nm ? 1.f : ex2_approx(ml.x - nm);
-    m = nm;
-    l = l * f + ml.y * y;
-    o = make_float4(o.x * f + v.x * y, o.y * f + v.y * y, o.z * f + v.z * y, o.w * f + v.w * y);
+  if (JW > 1) {
+    if (lane == 0) ml_s[warp] = make_float2(m, l);
+    if (lane < D4) o_s[warp][lane] = o;
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < JW; ++w) {
+      const float2 ml = ml_s[w];
+      const float4 v = o_s[w][min(lane, D4 - 1)];
+      const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2_approx(m - nm), y = ml.x == nm ? 1.f : ex2_approx(ml.x - nm);
+      m = nm;
+      l = l * f + ml.y * y;
+      o = make_float4(o.x * f + v.x * y, o.y * f + v.y * y, o.z * f + v.z * y, o.w * f + v.w * y);
+    }
   }
-  write_out<T>(a, b, gq, 4 * lane, m, l, o);
+  if (lane < D4) write_out<T>(a, b, gq, 4 * lane, m, l, o);
 }
 
 template <typename T, int D, int QT, bool PEND>
@@ -712,8 +728,13 @@ cudaError_t launch_one(const AttendArgs& a, const PrefixParts& parts, const Rows
     const cudaError_t e = launch_after(attend_rows_kernel<T, D, QT, PEND, true>, plan.ctas, kThreads, 0, 1,
                                        parts.plan.ctas > 0, s, a, parts, plan);
     if (e != cudaSuccess) return e;
-    return launch_after(attend_rows_join_kernel<T, D, QT>, dim3((unsigned)((int64_t)a.B * a.G)), 256, 0, 1, true, s, a,
-                        parts, plan);
+    // parts of a head, about: the prefix's and its unit's
+    const int64_t heads = (int64_t)a.B * a.G;
+    const int64_t count = parts.plan.ctas / std::max(1, parts.plan.units) + plan.ctas / plan.units + 2;
+    if (count <= (heads >= 4 * sms ? kFewParts : kFewParts / 2))
+      return launch_after(attend_rows_join_kernel<T, D, QT, 1>, dim3((unsigned)((heads + 3) / 4)), 128, 0, 1, true, s, a,
+                          parts, plan);
+    return launch_after(attend_rows_join_kernel<T, D, QT, 8>, dim3((unsigned)heads), 256, 0, 1, true, s, a, parts, plan);
   }
   const int64_t units = (int64_t)a.B * a.H * plan.qchunks;
   const int64_t tiles = rows_tiles(tile_rows(QT, false), a.n, a.P, a.k_new, a.pend) + parts.plan.ctas / a.H;
@@ -744,11 +765,14 @@ RowsPlan rows_plan(int B, int G, int H, int D, int n, int P, bool has_new, bool 
   if ((int64_t)B * G <= 0x7FFFFFFF && (total >= ctas * kWarps * (prefix_parts ? kBesideTiles : kStreamTiles) ||
                                        tiles >= (int64_t)cluster_ctas(pl.units, tiles, sms) * kWarps * kClusterTiles))
     pl.ctas = (int)std::min<int64_t>(ctas, (total + kWarps - 1) / kWarps);
+  pl.slots = pl.final ? 2 * (int64_t)pl.ctas : pl.units + ctas;
   return pl;
 }
 
-size_t RowsPlan::o_bytes(int D) const { return (size_t)slots() * qn * D * 4; }
-size_t RowsPlan::ml_bytes() const { return (size_t)slots() * qn * 8; }
+int stream_ctas(int D, int sms) { return sms * stream_ctas_per_sm(D); }
+
+size_t RowsPlan::o_bytes(int D) const { return (size_t)slots * qn * D * 4; }
+size_t RowsPlan::ml_bytes() const { return (size_t)slots * qn * 8; }
 size_t RowsPlan::bytes(int D) const { return ctas ? o_bytes(D) + ml_bytes() + ((size_t)batch + 1) * 8 : 0; }
 
 cudaError_t launch_attend_rows(const AttendArgs& a, const PrefixParts& parts, const RowsPlan& plan, int D, int dtype,
