@@ -411,22 +411,34 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       const int limit = block_limit(p, u);
       const int n = max(0, min(k1, (limit + kT - 1) / kT) - k0);
       const int h = u / p.plan.blocks;
-      const int64_t r = (int64_t)(u % p.plan.blocks) * p.plan.block_rows + (PAIR ? 0 : w * kT) + row;
-      const bool valid = r < (int64_t)a.B * N;
-      const int b = valid ? (int)(r / N) : 0, head = h * N + (valid ? (int)(r - (int64_t)b * N) : 0);
+      const int r = (u - h * p.plan.blocks) * p.plan.block_rows + (PAIR ? 0 : w * kT) + row;   // below 2^26 + 256
+      const bool valid = r < a.B * N;
+      const int b = valid ? r / N : 0, head = h * N + (valid ? r - b * N : 0);
       const int rows = valid && a.plens ? max(0, min(a.plens[b], a.P)) : a.P;
-      if (n > 0) {
-        // the queries into shared memory as TMA would swizzle them; PAIR: each
-        // warpgroup brings half of every row
-        const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0] + (int64_t)head * a.q_stride[1];
-        unsigned char* dst = smem + Gm::Q + (PAIR ? 0 : w) * Gm::TILEB + row * 128;
-        constexpr int CH = PAIR ? D / 16 : D / 8;
+      // The warp's 32 rows of the query block, as TMA would swizzle them; PAIR: each
+      // warpgroup has half of every row's pieces. Between global and shared memory
+      // neighbouring lanes move neighbouring pieces of a row (a lane a row would
+      // touch 32 lines an instruction, 2 to 4 us a block).
+      constexpr int CPR = PAIR ? D / 16 : D / 8;     // 16-byte pieces of a row
+      unsigned char* const mine = smem + Gm::Q + (PAIR ? 0 : w) * Gm::TILEB;
+      auto piece_of = [&](int r_, int c) { return mine + r_ * 128 + (c >> 3) * Gm::HALFB + (((c ^ r_) & 7) << 4); };
+      auto each_piece = [&](int64_t offset, auto&& move) {   // offset: of this lane's row
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int c = (PAIR ? w * CH : 0) + i;
-          const uint4 v = valid ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * Gm::HALFB + (((c ^ row) & 7) << 4)) = v;
+        for (int i = 0; i < CPR; ++i) {
+          const int from = i * (32 / CPR) + lane / CPR, c = (PAIR ? w * CPR : 0) + lane % CPR;
+          const int64_t at = __shfl_sync(~0u, offset, from);
+          const bool on = __shfl_sync(~0u, (int)valid, from);
+          move(i, on, at + 8 * c, piece_of((warp & 3) * 32 + from, c));
         }
+      };
+      if (n > 0) {
+        uint4 v[CPR];                                // all on their way before the first is stored
+        const T* const q = static_cast<const T*>(a.q);
+        const int64_t at = b * a.q_stride[0] + (int64_t)head * a.q_stride[1];
+        each_piece(at, [&](int i, bool on, int64_t from, unsigned char*) {
+          v[i] = on ? *reinterpret_cast<const uint4*>(q + from) : make_uint4(0, 0, 0, 0);
+        });
+        each_piece(at, [&](int i, bool, int64_t, unsigned char* to) { *reinterpret_cast<uint4*>(to) = v[i]; });
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
@@ -554,7 +566,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       // a block of this CTA alone goes to the output, any other to the workspace
       if (p.plan.final && k0 == 0 && k1 == p.plan.nkt) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        T* dst = static_cast<T*>(a.out) + b * a.out_stride[0] + (int64_t)head * a.out_stride[1];
 #pragma unroll 1
         for (int i = 0; i < CC; ++i) {
           const int c = (PAIR ? w * CC : 0) + i;
@@ -565,9 +576,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             uint32_t o[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[x] = pack16<T>(v[e + 2 * x] * inv, v[e + 2 * x + 1] * inv);
-            if (valid) *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(piece_of(row, 4 * c + e / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
+        __syncwarp();                                // the queries' place serves: their products are done
+        T* const out = static_cast<T*>(a.out);
+        each_piece(b * a.out_stride[0] + (int64_t)head * a.out_stride[1], [&](int, bool on, int64_t to, unsigned char* from) {
+          if (on) *reinterpret_cast<uint4*>(out + to) = *reinterpret_cast<const uint4*>(from);
+        });
         if (valid && a.lse && !(PAIR && w))
           a.lse[(int64_t)b * a.G + head] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
       } else {
