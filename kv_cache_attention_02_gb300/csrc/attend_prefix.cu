@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             tc_commit(s_full(w));
           }
         };
+        // (TILES: the softmax warps give the stages back)
         auto release = [&](int s) {
           if (elect_one()) tc_commit(empty(s));
         };
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           }
         } else {
           ok = (s = tile()) >= 0;
-          if (ok) mma_s(0, s), mma_s(1, s), release(s);
+          if (ok) mma_s(0, s), mma_s(1, s);
           for (int i = 0; i < n && ok; ++i) {
             const bool more = i + 1 < n;
             int sk = 0;
@@ -389,10 +390,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
               tc_commit(o_done(0));
             }
             if (!(ok = mma_o(1, s, i == 0))) break;
-            release(s);
             if (more) {
               mma_s(1, sk);
-              release(sk);
             } else if (elect_one()) {
               tc_commit(o_done(1));
             }
@@ -407,6 +406,16 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const int row = (warp & 3) * 32 + lane;          // query row of the stream = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t ns = 0, no = 0;                         // logits tiles and finished outputs seen
+    int ring = 0;                                    // stage of the segment's first tile
+    // TILES: the second stream gives the ring's stages back. When it sees its logits
+    // of key tile i (the segment's tile 2 i), those keys have been read, and the values
+    // of tile i - 1 (2 i - 1) by the products before. A commit by the MMA warp for
+    // each would be one more stop in its stream of products (368 against 383 us for 16 x
+    // 256-token chunks on 8192 keys); PAIR waits for memory and wants its stages
+    // sooner.
+    auto release = [&](int nth) {
+      if (lane == 0 && (warp & 3) == 0) mbar_arrive(empty((ring + nth) % NS));
+    };
     while (walk.next(u, k0, k1)) {
       const int limit = block_limit(p, u);
       const int n = max(0, min(k1, (limit + kT - 1) / kT) - k0);
@@ -451,6 +460,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (!ok) break;
         ++ns;
         tc_fence_after();
+        if (!PAIR && w == 1) {
+          release(2 * i);
+          if (i > 0) release(2 * i - 1);
+        }
         const int left = rows - (k0 + i) * kT;       // columns from here on are masked
         const bool none = left <= 0;
         // a length ends inside this tile, or rows that no sequence has begin in it
@@ -527,7 +540,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         ok = __all_sync(~0u, wait_or_abort(o_done(w), no & 1, abort_flag, p.err));
         ++no;
         tc_fence_after();
+        if (!PAIR && w == 1) release(2 * n - 1);
       }
+      ring = (ring + 2 * n) % NS;
       if (!ok) l = __int_as_float(0x7FFFFFFF);       // NaN: this row's result is lost
       float f0 = 1.f, f1 = 0.f;
       if (PAIR) {
