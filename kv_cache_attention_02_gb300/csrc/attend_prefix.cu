@@ -39,14 +39,14 @@
 // that has seen S may rescale O without another wait.
 // Every mbarrier wait is bounded; on expiry the CTA leaves NaN in its rows.
 //
-// Measured on GB300: 4096 x 32 query rows on 8192 keys, D = 128, bf16, 365-410 us
-// by the box, 1.34-1.51 PFLOP/s (0.72-0.81 of the measured matrix rate, 62% of the
-// tensor pipe's cycles); its MMAs with no softmax between them take 327 us, without
-// waits 309. 32 sequences on 65536 rows 50 us for the kernel, 5.4 TB/s; a call's start,
-// one tile and its end are 9.7 us of that (2.5 launch and set-up, 5 the chain of one
-// tile, 2 the parts), which is most of a short prefix's time. Tried and slower: three
-// logits buffers at D = 64 with one general issue loop (53 against 47 us), a
-// suspended or a longer plain poll of the barriers (524, 542 against 505).
+// Measured on GB300: 4096 x 32 query rows on 8192 keys, D = 128, bf16, 365-408 us by
+// the GPU's clocks, 1.35-1.51 PFLOP/s (0.72-0.81 of the measured matrix rate); its MMAs
+// with no softmax between them take 327 us, without waits 309. 32 sequences on 65536
+// rows 50 us for the kernel, 5.4 TB/s, and 6 us for the join. A call's start, one tile and
+// its end are 8 us (setup 0.9, queries 2, first tile and its softmax 2, end 2), which
+// is most of a short prefix's time. Tried and slower: three logits buffers at D = 64
+// with one general issue loop (53 against 47 us), a suspended or a longer plain poll
+// of the barriers (524, 542 against 505), the operands' low words added apart (no change).
 #include "attend_internal.cuh"
 #include "tcgen05.cuh"
 

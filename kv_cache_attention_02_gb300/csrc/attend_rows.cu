@@ -40,12 +40,12 @@
 //     fixed order, with the shared prefix's parts if there are any.
 //
 // Measured on GB300 (D = 128, 32 query heads on 8, fp16): 32 sequences of 2048 rows
-// 45-46 us, 5.8-6.0 TB/s of rows (0.87 of the measured copy rate); 7 unequal ones of
-// up to 65521 rows 139 us, 6.0 TB/s; one of 512 rows 5 us, all latency. Tried and
-// slower: the tiles through shared memory by cp.async, two more in flight (63 against
-// 50 us), 32-byte loads (53 against 50), more and smaller ranges (54-59), L2
-// prefetches throughout (150 against 139 on the unequal lengths). Bound by loads
-// in flight a warp's registers hold: 16 KB of them, 8 warps an SM, the
+// 44-46 us, 5.8-6.1 TB/s of rows (0.88 of the measured copy rate), 64 of them 80 us, 6.7
+// TB/s; 7 unequal ones of up to 65521 rows 139-142 us, 6.0 TB/s; one of 512 rows 5-6 us,
+// all latency. Tried and slower: the tiles through shared memory by cp.async, two more in
+// flight (63 against 50 us), 32-byte loads (53 against 50), more and smaller ranges
+// (54-59), L2 prefetches throughout (150 against 139 on the unequal lengths). Bound by
+// the loads that a warp's registers hold in flight, 16 KB, 8 warps an SM, with the
 // latencies of start, join and unequal SMs on top (SMs are busy 84% of the time).
 #include "attend_internal.cuh"
 
