@@ -50,6 +50,7 @@ extern "C" {
 #define KVEVICT_ERR_CUDA (-3)         /* a CUDA runtime call failed */
 #define KVEVICT_ERR_OOM (-4)          /* device allocation failed */
 #define KVEVICT_ERR_DEVICE_CHECK (-5) /* a kernel raised its error word (bounded wait ran out) */
+#define KVEVICT_ERR_WORKSPACE (-6)    /* kvevict_attend: the workspace is missing, too small or not aligned */
 
 #define KVEVICT_MAX_LAYERS 256
 #define KVEVICT_MAX_PREFILL 16384
@@ -464,7 +465,8 @@ typedef struct kvevict_attention {
  * error word (kvevict_check).
  * The workspace holds nothing between calls and needs no initial value; calls
  * that may run at the same time (captured graphs too) need one each.
- * Errors: INVALID_ARG, CUDA. */
+ * Errors: INVALID_ARG, CUDA, WORKSPACE (nothing has been launched: ask
+ * kvevict_attend_workspace for the size and call again). */
 int kvevict_attend(const kvevict_attention* args, void* stream);
 
 /* Device bytes that a call of this description needs as workspace, on the

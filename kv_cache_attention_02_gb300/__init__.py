@@ -20,7 +20,7 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvevict.so")
 
-OK, ERR_INVALID_ARG, ERR_BAD_STATE, ERR_CUDA, ERR_OOM, ERR_DEVICE_CHECK = 0, -1, -2, -3, -4, -5
+OK, ERR_INVALID_ARG, ERR_BAD_STATE, ERR_CUDA, ERR_OOM, ERR_DEVICE_CHECK, ERR_WORKSPACE = 0, -1, -2, -3, -4, -5, -6
 SCORE_CUMULATIVE, SCORE_CURRENT = 0, 1
 PREFILL_BULK, PREFILL_SEQUENTIAL = 0, 1
 DTYPE_FP16, DTYPE_BF16, DTYPE_FP32 = 0, 1, 2
@@ -292,8 +292,6 @@ def _with_workspace(args, cache, device, stream):
     """The same call with the workspace it needs, taken from torch's allocator for its stream, and that tensor."""
     torch, need = _torch(), ctypes.c_size_t(0)
     _check(lib().kvevict_attend_workspace(args, cache, ctypes.addressof(need)))
-    if need.value == 0:
-        return args, None
     if stream == torch._C._cuda_getCurrentRawStream(device):
         space = torch.empty(need.value, dtype=torch.uint8, device="cuda")
     else:
@@ -316,8 +314,10 @@ def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_
     whole 16-byte pieces. Errors: ValueError, KVEvictError.
     """
     args, s = _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream, None)
-    args, space = _with_workspace(args, 0, q.get_device(), s)
     rc = lib().kvevict_attend(args, s)
+    if rc == ERR_WORKSPACE:                 # most calls need none
+        args, space = _with_workspace(args, 0, q.get_device(), s)
+        rc = lib().kvevict_attend(args, s)
     if rc:
         _check(rc)
 
@@ -422,8 +422,11 @@ class KVEvict:
         """
         args, s = _attention(q, out, None, None, None, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream,
                              self.H)
-        args, space = _with_workspace(args, 1, q.get_device(), s)
-        _check(lib().kvevict_attend_cache(self._h, l, args, s))
+        rc = lib().kvevict_attend_cache(self._h, l, args, s)
+        if rc == ERR_WORKSPACE:
+            args, space = _with_workspace(args, 1, q.get_device(), s)
+            rc = lib().kvevict_attend_cache(self._h, l, args, s)
+        _check(rc)
 
     def run_host(self, prefill_keys, decode_keys, evicted=None, stream=None):
         """End to end from host memory (pinned tensors or numpy uint16 arrays)."""

@@ -237,8 +237,10 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
     rp.ctas = std::min(rp.ctas, stream_ctas(D, std::max(1, dev.sms - p.plan.ctas)));
   }
   const size_t need = p.plan.bytes(D) + rp.bytes(D);
-  if (need && (d->workspace_bytes < need || !d->workspace || !aligned(d->workspace)))
-    return invalid("workspace must be 16-byte aligned and hold kvevict_attend_workspace bytes");
+  if (need && (d->workspace_bytes < need || !d->workspace || !aligned(d->workspace))) {
+    set_last_error("workspace must be 16-byte aligned and hold kvevict_attend_workspace bytes");
+    return KVEVICT_ERR_WORKSPACE;
+  }
   char* space = static_cast<char*>(d->workspace);
   if (p.plan.ctas) {
     p.a = a;

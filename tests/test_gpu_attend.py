@@ -362,6 +362,50 @@ def test_parts_join_by_lse(kvx, B, P):
     torch.testing.assert_close(total, lse, rtol=1e-6, atol=1e-5)
 
 
+@pytest.mark.parametrize("n,P", [(2100, 0), (10, 3000)])
+def test_workspace_of_the_c_call(kvx, n, P):
+    """Too little workspace launches nothing; the size asked for is enough, and nothing past it is written."""
+    import ctypes
+    B, G, H, D = 40, 8, 2, 128
+    q, rows = _make(B, G // H, H, D, n=n, P=P, seed=17)
+    want, wlse = ref.check_attend(kvx, q, **rows)
+    out, lse = torch.full_like(q, 5.0), torch.empty_like(wlse)
+    args, stream = kvx._attention(q, out, rows["k"], rows["v"], None, None, None, rows.get("prefix_k"), rows.get("prefix_v"),
+                                  None, lse, None, None, None)
+    need = ctypes.c_size_t(0)
+    assert kvx.lib().kvevict_attend_workspace(args, 0, ctypes.addressof(need)) == kvx.OK and need.value > 0
+    space = torch.full((need.value + 4096,), 7, dtype=torch.uint8, device="cuda")
+
+    def call(at, size):
+        filled = bytearray(args)
+        kvx.struct.pack_into("=Q", filled, kvx._WORKSPACE_AT, at)
+        kvx.struct.pack_into("=Q", filled, kvx._WORKSPACE_BYTES_AT, size)
+        rc = kvx.lib().kvevict_attend(bytes(filled), stream)
+        torch.cuda.synchronize()
+        return rc
+    for at, size in ((0, 0), (0, need.value), (space.data_ptr(), need.value - 1), (space.data_ptr() + 8, need.value)):
+        assert call(at, size) == kvx.ERR_WORKSPACE and "workspace" in kvx.last_error()
+    assert (out == 5).all()
+    assert call(space.data_ptr(), need.value) == kvx.OK
+    assert torch.equal(out, want) and torch.equal(lse, wlse) and (space[need.value:] == 7).all()
+
+
+@pytest.mark.parametrize("n,P", [(300, 0), (2100, 0), (10, 3000)])
+def test_other_stream_than_the_current_one(kvx, n, P):
+    """The workspace belongs to the call's stream: by handle, by object, and the default stream from a side stream."""
+    q, rows = _make(40, 4, 2, 128, n=n, P=P, seed=18)
+    want, _ = ref.check_attend(kvx, q, **rows)
+    side = torch.cuda.Stream()
+    for given, current in ((side, None), (side.cuda_stream, None), (0, side), (torch.cuda.default_stream(), side)):
+        out = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(current):
+            for _ in range(3):
+                kvx.attend(q, out, stream=given, **rows)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_bounded_wait_leaves_nan(kvx):
     """A wait that runs out cannot reach the return code: NaN in every output instead, and the next call is unaffected.
     The library's test hook leaves one copy unissued; nothing faults or hangs."""
