@@ -132,6 +132,7 @@ def prefill_scores_noalloc(keys, colsum, stream=None):
 # ``kvevict_qk`` and ``kvevict_attention`` of include/kvevict.h, field by field.
 _QK = struct.Struct("=8i f i d q 7Q 12q")
 _ATTENTION = struct.Struct("=8i f i 12Q 18q Q")
+_U64 = struct.Struct("=Q")
 _WORKSPACE_AT, _WORKSPACE_BYTES_AT = 40 + 11 * 8, 40 + 12 * 8 + 18 * 8   # offsets in kvevict_attention
 _NO3, _NO4 = (0, 0, 0), (0, 0, 0, 0)     # strides of tensors that are not there
 
@@ -288,19 +289,17 @@ def _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens
         spv[0], spv[1], 0), s
 
 
-def _with_workspace(args, cache, device, stream):
+def _with_workspace(args, cache, q, stream):
     """The same call with the workspace it needs, taken from torch's allocator for its stream, and that tensor."""
     torch, need = _torch(), ctypes.c_size_t(0)
     _check(lib().kvevict_attend_workspace(args, cache, ctypes.addressof(need)))
-    if stream == torch._C._cuda_getCurrentRawStream(device):
-        space = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+    if stream == torch._C._cuda_getCurrentRawStream(q.get_device()):
+        space = torch.empty(need.value, dtype=torch.uint8, device=q.device)
     else:
         with torch.cuda.stream(torch.cuda.ExternalStream(stream or 0)):
-            space = torch.empty(need.value, dtype=torch.uint8, device="cuda")
-    filled = bytearray(args)
-    struct.pack_into("=Q", filled, _WORKSPACE_AT, space.data_ptr())
-    struct.pack_into("=Q", filled, _WORKSPACE_BYTES_AT, need.value)
-    return bytes(filled), space
+            space = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+    return b"".join((args[:_WORKSPACE_AT], _U64.pack(space.data_ptr()), args[_WORKSPACE_AT + 8:_WORKSPACE_BYTES_AT],
+                     _U64.pack(need.value))), space
 
 
 def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_k=None, prefix_v=None,
@@ -316,7 +315,7 @@ def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_
     args, s = _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream, None)
     rc = lib().kvevict_attend(args, s)
     if rc == ERR_WORKSPACE:                 # most calls need none
-        args, space = _with_workspace(args, 0, q.get_device(), s)
+        args, space = _with_workspace(args, 0, q, s)
         rc = lib().kvevict_attend(args, s)
     if rc:
         _check(rc)
@@ -424,7 +423,7 @@ class KVEvict:
                              self.H)
         rc = lib().kvevict_attend_cache(self._h, l, args, s)
         if rc == ERR_WORKSPACE:
-            args, space = _with_workspace(args, 1, q.get_device(), s)
+            args, space = _with_workspace(args, 1, q, s)
             rc = lib().kvevict_attend_cache(self._h, l, args, s)
         _check(rc)
 

@@ -51,6 +51,7 @@ int device_info(DeviceInfo* out) {
     g_sms[dev].store(sms, std::memory_order_relaxed);
   }
   out->sms = sms;
+  out->device = dev;
   return KVEVICT_OK;
 }
 
@@ -248,6 +249,7 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
     p.part_ml = reinterpret_cast<float2*>(space + p.plan.o_bytes(D));
     p.err = rows ? rows->err : nullptr;
     p.stall = take_scorer_stall() ? 1 : 0;
+    p.device = dev.device;
     const cudaError_t e = launch_attend_prefix(p, D, d->dtype, s);
     if (e != cudaSuccess) return cuda_result(e, "launch");
     if (alone) return KVEVICT_OK;

@@ -105,6 +105,7 @@ struct PrefixArgs {
   float2* part_ml;
   int* err;                // error word for bounded waits, or null
   int stall;               // test hook: CTA 0's first tile is never issued
+  int device;              // the current one, below 64
   bool k_row_first, v_row_first;
   __host__ __device__ PrefixParts parts() const { return PrefixParts{plan, part_o, part_ml}; }
 };
@@ -113,6 +114,7 @@ cudaError_t launch_attend_prefix(const PrefixArgs& p, int D, int dtype, cudaStre
 // What a launch needs to know of the current device, looked up once.
 struct DeviceInfo {
   int sms = 0;
+  int device = 0;
 };
 int device_info(DeviceInfo* out);   // KVEVICT_* code; sets the last error
 void set_last_error(const std::string& msg);

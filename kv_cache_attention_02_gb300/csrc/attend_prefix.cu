@@ -743,16 +743,17 @@ cudaError_t launch_px(const CUtensorMap& kmap, const CUtensorMap& vmap, const Pr
   auto kernel = attend_prefix_kernel<T, D, PAIR>;
   // The kernel's redistribution of registers needs the 168 a thread that its
   // launch bound gives it: checked, as it would wait forever with fewer.
-  static std::atomic<bool> checked{false};
-  if (!checked.load(std::memory_order_relaxed)) {
+  static std::atomic<uint64_t> ready{0};   // devices on which that, and its shared memory, are settled
+  const uint64_t bit = 1ull << p.device;
+  cudaError_t e;
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
     cudaFuncAttributes f;
-    const cudaError_t r = cudaFuncGetAttributes(&f, kernel);
-    if (r != cudaSuccess) return r;
-    if (f.numRegs != 168) return cudaErrorLaunchOutOfResources;
-    checked.store(true, std::memory_order_relaxed);
+    e = cudaFuncGetAttributes(&f, kernel);
+    if (e == cudaSuccess && f.numRegs != 168) e = cudaErrorLaunchOutOfResources;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PxGeo<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PxGeo<D>::SMEM);
-  if (e != cudaSuccess) return e;
   kernel<<<p.plan.ctas, kPxThreads, PxGeo<D>::SMEM, s>>>(kmap, vmap, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !p.plan.final || !p.plan.shared_blocks()) return e;
