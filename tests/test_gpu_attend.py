@@ -223,7 +223,22 @@ def test_prefix_rows_past_every_length_are_not_used(kvx):
     ref.check_attend(kvx, q, prefix_lens=plens, **rows)
 
 
-@pytest.mark.parametrize("P", [0, 300])
+@pytest.mark.parametrize("B,N,H", [(130, 4, 2), (30, 4, 8), (300, 3, 2)])
+def test_strides_of_a_large_prefix(kvx, B, N, H):
+    """Queries inside a fused projection, outputs inside a larger buffer whose other rows stay; lengths out of range."""
+    D, P = 128, 1300
+    q, rows = _make(B, N, H, D, P=P, seed=21)
+    qkv = torch.cat([q, q * 3, q], 1)
+    big = torch.full((B + 1, 2 * N * H, D), 3.0, dtype=F16, device="cuda")
+    ref.check_attend(kvx, qkv[:, N * H:2 * N * H], out=big[:B, N * H:], **rows)
+    assert (big[:, :N * H] == 3).all() and (big[B] == 3).all()
+    plens = torch.full((B,), P + 7, dtype=torch.int32, device="cuda")
+    plens[::3] = -5
+    ref.check_attend(kvx, qkv[:, N * H:2 * N * H], out=big[:B, N * H:], prefix_lens=plens, **rows)
+    assert (big[:, :N * H] == 3).all() and (big[B] == 3).all()
+
+
+@pytest.mark.parametrize("P", [0, 300, 2500])
 @pytest.mark.parametrize("B", [3, 50])
 def test_strides(kvx, B, P):
     """Rows between sequences ([B, n, H, D]), queries inside a fused projection, outputs inside a larger buffer."""
