@@ -424,7 +424,7 @@ typedef struct kvevict_attention {
   int32_t n;              /* own rows a sequence has room for, >= 0 */
   int32_t prefix;         /* shared rows P, >= 0; n + prefix < 2^30 */
   int32_t reserved;       /* 0 */
-  float scale;            /* of the logits, > 0 and finite; 0 = 1/sqrt(D) */
+  float scale;            /* of the logits, 2^-126 to 2^127; 0 = 1/sqrt(D) */
   int32_t reserved2;      /* 0 */
   const void* q;          /* device [B, G, D] */
   void* out;              /* device [B, G, D] */

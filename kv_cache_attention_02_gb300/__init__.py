@@ -247,8 +247,8 @@ def _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens
         raise ValueError("k and v, k_new and v_new, prefix_k and prefix_v go together")
     if lens is not None and k is None or prefix_lens is not None and prefix_k is None:
         raise ValueError("lens goes with k and prefix_lens with prefix_k")
-    if scale is not None and not scale > 0:
-        raise ValueError("scale must be > 0")
+    if scale is not None and not 2.0**-126 <= scale <= 2.0**127:
+        raise ValueError("scale must be from 2^-126 to 2^127")
     H, n, prefix = kv_heads, 0, 0
     if k is not None:
         if k.dim() != 4:
@@ -308,9 +308,9 @@ def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_
 
     q, out [B, G, D] fp16 or bf16, everything else of q's type; k, v [B, H, n, D] with lens int32 [B] or None (n);
     k_new, v_new [B, H, D]; prefix_k, prefix_v [H, P, D], read once for the whole batch, with prefix_lens int32 [B] or
-    None (P). Query head i reads key head i // (G // H). lse: float32 [B, G] output or None. scale: 1/sqrt(D) unless
-    given. A sequence with no rows gets out 0 and lse -inf. Any layout with a contiguous last dimension and strides of
-    whole 16-byte pieces. Errors: ValueError, KVEvictError.
+    None (P). Query head i reads key head i // (G // H). lse: float32 [B, G] output or None. scale: 2^-126 to 2^127,
+    1/sqrt(D) unless given. A sequence with no rows gets out 0 and lse -inf. Any layout with a contiguous last
+    dimension and strides of whole 16-byte pieces. Errors: ValueError, KVEvictError.
     """
     args, s = _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens, lse, scale, stream, None)
     rc = lib().kvevict_attend(args, s)

@@ -137,7 +137,9 @@ int attend_check(const kvevict_attention* d) {
   if (d->n < 0 || d->prefix < 0 || (int64_t)d->n + d->prefix >= (1 << 30))
     return invalid("n and prefix must be >= 0 and below 2^30 together");
   if ((int64_t)d->batch * d->n_heads > (1 << 26)) return invalid("batch * n_heads must be at most 2^26");
-  if (!(d->scale >= 0.f) || !std::isfinite(d->scale)) return invalid("scale must be >= 0 and finite");
+  // more than 2^127 could overflow with the factor log2(e)
+  if (d->scale != 0.f && !(d->scale >= 0x1p-126f && d->scale <= 0x1p127f))
+    return invalid("scale must be 0, or from 2^-126 to 2^127");
   if (d->reserved || d->reserved2) return invalid("reserved must be 0");
   return KVEVICT_OK;
 }

@@ -108,3 +108,17 @@ def test_tensors_are_checked(kvx):
         kvx.qk_norm_rope(x, None, None, None, rope_theta=1e4)
     with pytest.raises(ValueError, match="fp16 or bf16"):
         kvx.qk_norm_rope(x, None, x, None, rope_theta=1e4)
+
+
+@pytest.mark.parametrize("scale", [1e-39, 3e38])
+def test_scales_outside_the_normal_floats_are_refused(kvx, scale):
+    """Below them a scale would round towards 0, the default's mark; above 2^127 its base-2 form overflows."""
+    assert kvx.lib().kvevict_attend(_attention(kvx, scale=scale), None) == kvx.ERR_INVALID_ARG
+    assert "scale" in kvx.last_error()
+
+
+@pytest.mark.parametrize("scale", [1e-60, 1e-39, 3e38, 1e60, 10**400, float("inf"), float("nan")])
+def test_python_scales_outside_the_normal_floats_are_refused(kvx, scale):
+    q, k = torch.zeros(2, 4, 64, dtype=torch.float16), torch.zeros(2, 2, 5, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="scale"):
+        kvx.attend(q, q, k=k, v=k, scale=scale)
