@@ -393,7 +393,7 @@ typedef struct kvevict_qk {
   int32_t head_dim;       /* D, 64 or 128 */
   float eps;              /* of the norm, >= 0 */
   int32_t reserved;       /* 0 */
-  double rope_theta;      /* RoPE base, > 0; the cache's kvevict_config.rope_theta */
+  double rope_theta;      /* RoPE base, > 0 and normal; the cache's kvevict_config.rope_theta */
   int64_t pos0;           /* position of token 0 where positions is null */
   const void* q;          /* device [batch, seq, n_heads, D]; null if n_heads = 0 */
   const void* k;          /* device [batch, seq, n_kv_heads, D]; null if n_kv_heads = 0 */

@@ -207,6 +207,12 @@ def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None
     some, some_out = (q, q_out) if q is not None else (k, k_out)
     if some.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q and k must have shape [batch, seq, heads, head_dim]")
+    if not 2.0**-1022 <= rope_theta <= 1.7e308:
+        raise ValueError("rope_theta must be > 0, normal and finite")
+    if not 0 <= eps <= 3.4e38:
+        raise ValueError("eps must be >= 0 and finite")
+    if not -1 << 63 <= pos0 < 1 << 63:
+        raise ValueError("pos0 must fit 64 bits")
     B, S, _, D = some.shape
     kind, kind_out = some.dtype, some_out.dtype
     if kind not in _IN or kind_out not in _OUT:

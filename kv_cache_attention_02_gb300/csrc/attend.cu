@@ -68,7 +68,8 @@ int qk_run(const kvevict_qk* d, cudaStream_t s) {
   if ((int64_t)d->n_heads + d->n_kv_heads > 65536) return invalid("more than 65536 heads");
   if (d->head_dim != 64 && d->head_dim != 128) return invalid("head_dim must be 64 or 128");
   if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return invalid("eps must be >= 0 and finite");
-  if (!(d->rope_theta > 0.0) || !std::isfinite(d->rope_theta)) return invalid("rope_theta must be > 0 and finite");
+  if (!(d->rope_theta > 0.0) || !std::isnormal(d->rope_theta))   // a subnormal's powers overflow
+    return invalid("rope_theta must be > 0, normal and finite");
   if (d->reserved) return invalid("reserved must be 0");
   if (d->batch == 0 || d->seq == 0 || d->n_heads + d->n_kv_heads == 0) return KVEVICT_OK;
   if (d->n_heads > 0 && (!d->q || !d->q_out)) return invalid("q and q_out must not be null");

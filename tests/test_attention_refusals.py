@@ -122,3 +122,20 @@ def test_python_scales_outside_the_normal_floats_are_refused(kvx, scale):
     q, k = torch.zeros(2, 4, 64, dtype=torch.float16), torch.zeros(2, 2, 5, 64, dtype=torch.float16)
     with pytest.raises(ValueError, match="scale"):
         kvx.attend(q, q, k=k, v=k, scale=scale)
+
+
+def test_subnormal_rope_theta_is_refused(kvx):
+    """Its highest power overflows a double."""
+    assert kvx.lib().kvevict_qk_norm_rope(_qk(kvx, rope_theta=1e-320), None) == kvx.ERR_INVALID_ARG
+    assert "rope_theta" in kvx.last_error()
+
+
+@pytest.mark.parametrize("kw,frag", [
+    (dict(eps=1e39), "eps"), (dict(eps=-1e-6), "eps"), (dict(eps=float("nan")), "eps"), (dict(pos0=1 << 63), "pos0"),
+    (dict(pos0=-(1 << 63) - 1), "pos0"), (dict(rope_theta=10**400), "rope_theta"), (dict(rope_theta=0.0), "rope_theta"),
+    (dict(rope_theta=float("nan")), "rope_theta"), (dict(rope_theta=1e-320), "rope_theta"),
+])
+def test_python_numbers_out_of_range_are_refused(kvx, kw, frag):
+    x = torch.zeros(2, 3, 4, 64)
+    with pytest.raises(ValueError, match=frag):
+        kvx.qk_norm_rope(x, None, x.half(), None, **{"rope_theta": 1e4, **kw})
