@@ -142,6 +142,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 // One thread of the warp, always the same, chosen in a way that tells the
 // compiler that the warp stays uniform: descriptors then live in uniform
 // registers. With `lane == 0` instead, moving them there bound the rate at which
@@ -474,13 +480,21 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
           for (int e = 0; e < kT; ++e) v[e] = e < left ? v[e] : kNegInf;
         }
+        // (a NaN stays in the maximum, so that one compare finds logits that are not finite)
         float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
         for (int e = 4; e < kT; e += 8)
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            m4[x] = e + 4 < kT ? fmaxf(m4[x], fmaxf(v[e + x], v[e + 4 + x])) : fmaxf(m4[x], v[e + x]);
-        const float mx = none ? kNegInf : fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale2;
+            m4[x] = e + 4 < kT ? max_nan(m4[x], max_nan(v[e + x], v[e + 4 + x])) : max_nan(m4[x], v[e + x]);
+        const float top = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+        const float mx = none ? kNegInf : top * a.scale2;
+        // A row past its length: the addend -inf below makes its weights 0, but for logits
+        // of NaN and +inf (keys that other rows have): they go, where there are any.
+        if (__any_sync(~0u, none && !(top < -kNegInf))) {
+#pragma unroll
+          for (int e = 0; e < kT; ++e) v[e] = none ? kNegInf : v[e];
+        }
         const bool up = mx > m + kLazy;
         if (__any_sync(~0u, up)) {
           const float nm = up ? mx : m, f = nm == m ? 1.f : ex2(m - nm);
@@ -499,8 +513,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           }
         }
         begun = true;
-        // a row past its length: every weight 2^-inf = 0 (and so are masked ones,
-        // with a row that has had nothing so far)
+        // (a row that has had nothing so far: masked logits still give 2^-inf = 0)
         const float nb = none ? kNegInf : m == kNegInf ? 0.f : -m;
         const float2 sc2 = make_float2(a.scale2, a.scale2), nb2 = make_float2(nb, nb);
         float2 l4[4];
