@@ -522,8 +522,9 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
             float2 part = inside(q) ? ml[off + q] : make_float2(kNegInf, 0.f);
             const float nm = fmaxf(m[i], part.x);
             const float f = m[i] == nm ? 1.f : ex2_approx(m[i] - nm);
-            // a part without rows has left no O; a NaN sum passes on
-            const float fp = part.y == 0.f ? 0.f : part.x == nm ? 1.f : ex2_approx(part.x - nm);
+            // a part without rows has left no O; a NaN sum (NaN logits, a wait that ran out)
+            // passes on, however far its maximum is below the others
+            const float fp = part.y == 0.f ? 0.f : part.y != part.y ? part.y : part.x == nm ? 1.f : ex2_approx(part.x - nm);
             m[i] = nm;
             l[i] = l[i] * f + (c == 0 && fp != 0.f ? part.y * fp : 0.f);
 #pragma unroll

@@ -65,3 +65,74 @@ def test_a_logit_of_minus_infinity_takes_no_weight(kvx, B, N, H, D, P, dtype):
     want = ref.attend_batch(q, prefix_lens=torch.where(lens > 15, lens - 10, lens.clamp(max=5)), **less)
     ref.check("out", out, want[0], want[2])
     ref.check("lse", lse, want[1], want[3])
+
+
+# Few own rows beside a large prefix (joined in the clusters' kernel), and many (in the ranges' join).
+BESIDE = [(32, 4, 8, 128, 1100, 0), (40, 3, 8, 128, 900, 5), (300, 2, 2, 128, 901, 0), (32, 4, 8, 128, 1100, 400),
+          (300, 2, 2, 128, 901, 200)]
+
+
+@pytest.mark.parametrize("B,N,H,D,P,n", BESIDE)
+def test_shared_keys_of_nan_beside_finite_own_rows(kvx, B, N, H, D, P, n):
+    """A head whose shared keys are all NaN answers with NaN in every sequence that shares some; the others are untouched."""
+    q, rows = make(B, N, H, D, P=P, n=n, new=True, seed=P + n)
+    lens = torch.full((B,), P, dtype=torch.int32, device="cuda")
+    lens[5:9] = 0
+    assert prefix_kernel(kvx, q, prefix_lens=lens, **rows)
+    want, wlse = ref.check_attend(kvx, q, prefix_lens=lens, **rows)
+    rows["prefix_k"][1] = float("nan")
+    out, lse = torch.empty_like(q), torch.empty_like(wlse)
+    kvx.attend(q, out, lse=lse, prefix_lens=lens, **rows)
+    torch.cuda.synchronize()
+    hit = torch.zeros(B, N * H, dtype=torch.bool, device="cuda")
+    hit[lens > 0, N:2 * N] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wlse[~hit])
+
+
+@pytest.mark.parametrize("B,N,H,D,P,n", BESIDE + [(4000, 4, 8, 64, 130, 0)])
+def test_a_wait_that_runs_out_beside_own_rows(kvx, B, N, H, D, P, n):
+    """NaN wherever the lost part belongs, however far the own rows' logits are above it; right results next time. (The
+    library's test hook leaves one copy unissued: the bounded wait runs out, nothing hangs.)"""
+    q, rows = make(B, N, H, D, P=P, n=n, new=True, seed=P + n)
+    rows["k_new"] = (q[:, ::N] * 40).contiguous()            # own logits far above the shared rows'
+    assert prefix_kernel(kvx, q, **rows)
+    want, wlse = torch.empty_like(q), torch.empty(B, N * H, device="cuda")
+    kvx.attend(q, want, lse=wlse, **rows)
+    torch.cuda.synchronize()
+    assert torch.isfinite(want).all() and torch.isfinite(wlse).all()
+    out, lse = torch.zeros_like(q), torch.zeros_like(wlse)
+    assert kvx.lib().kvevict_test_stall_next_step(None) == kvx.OK
+    kvx.attend(q, out, lse=lse, **rows)
+    torch.cuda.synchronize()
+    # the first CTA's first block of query rows: the first key head's, 128 of them, or 256 where there are more
+    first = min(B, 128 // N if B * N <= 128 else 256 // N)
+    assert torch.isnan(out[:first, :N]).all() and torch.isnan(lse[:first, :N]).all()
+    # lost or right, nothing in between
+    lost = torch.isnan(lse)
+    assert torch.equal(torch.isnan(out), lost[..., None].expand_as(out))
+    assert torch.equal(out[~lost], want[~lost]) and torch.equal(lse[~lost], wlse[~lost])
+    kvx.attend(q, out, lse=lse, **rows)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+def test_a_wait_that_runs_out_on_a_handle(kvx):
+    """The handle reports it, too, and attention that waits for nothing goes on."""
+    B, N, H, D, P = 32, 4, 8, 128, 1100
+    q, rows = make(B, N, H, D, P=P, new=True, seed=1)
+    h = kvx.KVEvict(batch=B, n_layers=1, n_kv_heads=H, head_dim=D, layer_budgets=[8], n_sink=1, max_prefill=4, with_values=True)
+    want, out = torch.empty_like(q), torch.zeros_like(q)
+    h.attend(0, q, want, **rows)
+    torch.cuda.synchronize()
+    h.check()
+    assert kvx.lib().kvevict_test_stall_next_step(None) == kvx.OK
+    h.attend(0, q, out, **rows)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:, :N]).all()
+    with pytest.raises(kvx.KVEvictError) as e:
+        h.check()
+    assert e.value.code == kvx.ERR_DEVICE_CHECK
+    h.attend(0, q, out, **rows)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
