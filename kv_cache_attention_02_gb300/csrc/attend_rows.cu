@@ -25,9 +25,11 @@
 // some lane exceeds it.
 //
 // The weights go into the second product as a sum of two 16-bit parts
-// (p = hi + lo), 22 bits in all for fp16 and 16 for bf16: the matrix pipe has
-// room for the second instruction here, and the output keeps the accuracy of
-// its own rounding.
+// (p = hi + lo): the matrix pipe has room for the second instruction here, and the
+// output keeps the accuracy of its own rounding. In bf16 that is 16 bits of every
+// weight. fp16's smallest step is 2^-24, so its weights, at most 1, go in times 2^15
+// (and out again, both exact): 22 bits down to 2^-17 of the largest weight, and steps
+// of 2^-39 of it below, which leave a tail of a million rows its sum.
 //
 // Work: a unit is a sequence's key head with up to 16 of its query heads.
 //   Few tiles (a latency, mostly): one cluster of CTAs a unit, its tiles dealt to
@@ -51,6 +53,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 namespace kvx {
 namespace {
 
@@ -69,6 +73,11 @@ constexpr int kClusterTiles = 8;
 // sequences of 1024 rows 24.8 us, 28.3 with eight warps a head; 2 of 4096, 40 parts,
 // 10.0 with eight, 11.5 with one.
 constexpr int kFewParts = 32;
+
+// What the weights of the second product are multiplied by: the top of fp16's range
+// (65504) is used, with a factor of two to spare.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 32768.f : 1.f;
 
 constexpr int stream_ctas_per_sm(int D) { return D == 64 ? 3 : 2; }
 int rows_qt(int N) { return N <= 8 ? 1 : 2; }
@@ -464,9 +473,10 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
         for (int nt = 0; nt < 2 * KG; ++nt) {
           const float p0 = ex2_approx(s[nt][2 * i] - base), p1 = ex2_approx(s[nt][2 * i + 1] - base);
           l[i] += p0 + p1;
-          hi[i][nt] = pack16<T>(p0, p1);
+          const float2 w = make_float2(p0 * kLift<T>, p1 * kLift<T>);
+          hi[i][nt] = pack16<T>(w.x, w.y);
           const float2 back = unpack16<T>(hi[i][nt]);
-          lo[i][nt] = pack16<T>(p0 - back.x, p1 - back.y);
+          lo[i][nt] = pack16<T>(w.x - back.x, w.y - back.y);
         }
       }
 #pragma unroll
@@ -487,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
           }
       if (more) R::load_v(vr, cur, g, c);
     }
+#pragma unroll
+    for (int x = 0; x < VH * 4 * QT * 4; ++x) (&acc[0][0][0][0])[x] *= 1.f / kLift<T>;
 
     // ---------------------------------------------------------------- the prefix's parts
     // Each part (a range of shared rows that one CTA of attend_prefix.cu took) joins
