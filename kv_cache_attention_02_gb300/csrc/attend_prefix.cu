@@ -61,6 +61,7 @@ constexpr int kPxThreads = 384;
 constexpr int kPxTmem = 512;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazy = 8.f;           // log2 of how far a weight may exceed 1
+constexpr float kFar = 0x1p23f;        // base-2 logits from here on are whole numbers
 
 template <int D>
 struct PxGeo {
@@ -489,15 +490,17 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             m4[x] = e + 4 < kT ? max_nan(m4[x], max_nan(v[e + x], v[e + 4 + x])) : max_nan(m4[x], v[e + x]);
         const float top = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
         const float mx = none ? kNegInf : top * a.scale2;
-        // A row past its length: the addend -inf below makes its weights 0, but for logits
-        // of NaN and +inf (keys that other rows have): they go, where there are any.
-        if (__any_sync(~0u, none && !(top < -kNegInf))) {
-#pragma unroll
-          for (int e = 0; e < kT; ++e) v[e] = none ? kNegInf : v[e];
-        }
-        const bool up = mx > m + kLazy;
-        if (__any_sync(~0u, up)) {
-          const float nm = up ? mx : m, f = nm == m ? 1.f : ex2(m - nm);
+        // Rare: logits of NaN or +inf in a row past its length (keys that other rows have),
+        // which the addend -inf below would leave NaN; and a maximum so large that it is
+        // rounded by a half or more, as its own logit need not be near it in the fused
+        // product and difference below. (One vote with the common case, as each one stands
+        // in the way of everything after it: 51.3 us for the unequal lengths so, 52.5 with two.)
+        const bool odd = none ? !(top < -kNegInf) : !(fabsf(mx) < kFar), up = mx > m + kLazy;
+        // a row past its length: every weight 2^-inf = 0 (and so are masked ones, with a
+        // row that has had nothing so far)
+        float nb = none ? kNegInf : m == kNegInf ? 0.f : -m;
+        if (__any_sync(~0u, up || odd)) {
+          const float nm = up || (odd && mx > m) ? mx : m, f = nm == m ? 1.f : ex2(m - nm);
           m = nm;
           l *= f;
           if (begun) {
@@ -511,10 +514,27 @@ __global__ void __launch_bounds__(kPxThreads, 1)
               tmem_st16(to + 16 * c, o);
             }
           }
+          nb = none ? kNegInf : m == kNegInf ? 0.f : -m;
+          if (__builtin_expect(__any_sync(~0u, odd), 0)) {
+            // the difference, of a product rounded as the maximum was, goes through the
+            // fused product instead
+            const float inv = 1.f / a.scale2;
+#pragma unroll 1
+            for (int c = 0; c < kT / 16; ++c) {
+              float x[16];
+              uint32_t o[16];
+              tmem_ld16(ts + 16 * c, x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = __float_as_uint(16 * c + e < left ? __fadd_rn(__fmul_rn(x[e], a.scale2), nb) * inv : kNegInf);
+              tmem_st16(ts + 16 * c, o);
+            }
+            tmem_st_wait();
+            tmem_ld128(ts, v);
+            nb = 0.f;
+          }
         }
         begun = true;
-        // (a row that has had nothing so far: masked logits still give 2^-inf = 0)
-        const float nb = none ? kNegInf : m == kNegInf ? 0.f : -m;
         const float2 sc2 = make_float2(a.scale2, a.scale2), nb2 = make_float2(nb, nb);
         float2 l4[4];
 #pragma unroll

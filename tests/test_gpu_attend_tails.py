@@ -1,11 +1,11 @@
-"""Weights far below the largest one: a dominant key in front of a long tail."""
+"""Weights far below the largest one: a dominant key in front of a long tail, and logits of any size."""
 import math
 
 import pytest
 
 torch = pytest.importorskip("torch")
 import attention_reference as ref  # noqa: E402
-from attention_paths import make  # noqa: E402
+from attention_paths import make, prefix_kernel, workspace  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
@@ -66,3 +66,41 @@ def test_own_rows(kvx, B, N, H, D, n, nats, dtype, sink):
             want = _tight(q[b, some], rows["k"][b, h], rows["v"][b, h], LIFT_ROWS)
             ref.check("out", out[b, some], want[0], want[2])
             ref.check("lse", lse[b, some], want[1], want[3])
+
+
+@pytest.mark.parametrize("path", ["clusters", "ranges", "pair", "tiles"])
+@pytest.mark.parametrize("size,dtype", [(1e3, F16), (3e4, F16), (1e6, F16), (1e8, F16), (3e4, BF16), (1e8, BF16), (1e11, BF16),
+                                        (1e30, BF16)])
+def test_logits_of_any_size(kvx, path, size, dtype):
+    """Logits of the given size, in steps that the largest one grows by again and again, and the largest twice: the output
+    is the mean of those two rows' values."""
+    D, n = 128, 1200
+    shape = {"clusters": (2, 2, 2), "ranges": (40, 2, 8), "pair": (64, 2, 4), "tiles": (64, 5, 4)}[path]
+    shared = path in ("pair", "tiles")
+    q, rows = make(*shape, D, dtype=dtype, seed=8, **({"P": n} if shared else {"n": n if path == "ranges" else 300}))
+    k, v = (rows["prefix_k"], rows["prefix_v"]) if shared else (rows["k"], rows["v"])
+    count = k.shape[-2]
+    assert prefix_kernel(kvx, q, **rows) == shared and (workspace(kvx, q, **rows) > 0) == (path != "clusters")
+    q.zero_()
+    k.zero_()
+    # q . k * scale = size * (step of the row), steps 2^-3 apart in size: exact products, sums of one term
+    root = 2.0 ** (math.ceil(math.log2(size) / 2) + 1)
+    q[..., 0] = root
+    steps = (torch.arange(count, device="cuda") // (count // 8)).clamp(max=8) / 8 - 0.5
+    steps[steps == steps.max()] = -0.5
+    a, b = count - 3, count // 2
+    steps[a] = steps[b] = 1.0
+    k[..., 0] = (steps * (size / root) * math.sqrt(D)).to(dtype)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    kvx.attend(q, out, lse=lse, **rows)
+    torch.cuda.synchronize()
+    B, H, N = shape[0], shape[2], shape[1]
+    # Two equal logits, so two equal weights w', each w rounded once to 16 bits, over a sum of two unrounded w: w' / w is
+    # within half a step of 1, and the output is rounded once. (A weight that is not exactly 1, as the logit and the
+    # maximum may be rounded apart, cancels.) The rest of the weights are below 2^-700. fp32: four roundings and an exp2.
+    va, vb = v[..., a, :].double(), v[..., b, :].double()
+    mean, size = [(x / 2).expand(B, H, D).repeat_interleave(N, 1) for x in (va + vb, va.abs() + vb.abs())]
+    half = ref.HALF_STEP[dtype]
+    ref.check("out", out, mean, half * (mean.abs() + size) + 2.0 ** -20 * size + (2.0 ** -25 if dtype is F16 else 0.0))
+    top = float(q[0, 0, 0].double()) * float(k.reshape(-1, count, D)[0, a, 0].double()) * D ** -0.5
+    assert (lse - (top + math.log(2))).abs().max() <= 2.0 ** -21 * abs(top) + 2.0 ** -20
