@@ -5,12 +5,14 @@
 // For one key head the queries of all sequences and of its N = G / H query
 // heads are the rows of one matrix Q [B*N, D], row b*N + j:
 //   S = Q K^T * scale,  P = e^(S - m),  O = P V,  l = sum P,
-// with the running maximum m and sum l of each row in fp32. P is rounded to
-// the inputs' 16-bit type for the second product and l is summed before that
-// rounding, so the roundings average out; with few rows (see PAIR) it goes in
-// as the sum of two 16-bit parts, as in attend_rows.cu. m follows the true
-// maximum only when it would be exceeded by more than 2^8, which P and l carry
-// without loss: most tiles then need no rescaling of O.
+// with the running sum l of each row in fp32, relative to m: the running maximum, or
+// less. P is rounded to the inputs' 16-bit type for the second product and l is summed
+// before that rounding, so the roundings average out; with few rows (see PAIR) it goes
+// in as the sum of two 16-bit parts, as in attend_rows.cu. m moves only when the true
+// maximum is more than 2^8 above the one it was set by, which P and l carry without
+// loss: most tiles then need no rescaling of O. In fp16 m is set 2^7 below that maximum,
+// so that P uses the type's upper range and only weights below 2^-32 of the largest
+// vanish (2^16 rows of them are 2^-16 of the sum).
 //
 // Work: the (key head, block of query rows, 128-key tile) triples, in that
 // order, are cut into one contiguous range per CTA (one CTA an SM, which holds
@@ -60,7 +62,10 @@ constexpr int kT = 128;                // query rows of a stream, keys of a tile
 constexpr int kPxThreads = 384;
 constexpr int kPxTmem = 512;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLazy = 8.f;           // log2 of how far a weight may exceed 1
+constexpr float kLazy = 8.f;           // log2 of how far a weight may exceed the first maximum's
+// log2 of the first maximum's weight: with kLazy on top, half of fp16's range. bf16 has fp32's exponents.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 constexpr float kFar = 0x1p23f;        // base-2 logits from here on are whole numbers
 
 template <int D>
@@ -495,12 +500,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         // rounded by a half or more, as its own logit need not be near it in the fused
         // product and difference below. (One vote with the common case, as each one stands
         // in the way of everything after it: 51.3 us for the unequal lengths so, 52.5 with two.)
-        const bool odd = none ? !(top < -kNegInf) : !(fabsf(mx) < kFar), up = mx > m + kLazy;
+        const bool odd = none ? !(top < -kNegInf) : !(fabsf(mx) < kFar), up = mx > m + (kLazy + kLift<T>);
         // a row past its length: every weight 2^-inf = 0 (and so are masked ones, with a
         // row that has had nothing so far)
         float nb = none ? kNegInf : m == kNegInf ? 0.f : -m;
         if (__any_sync(~0u, up || odd)) {
-          const float nm = up || (odd && mx > m) ? mx : m, f = nm == m ? 1.f : ex2(m - nm);
+          const float nm = odd ? fmaxf(m, mx) : up ? mx - kLift<T> : m, f = nm == m ? 1.f : ex2(m - nm);
           m = nm;
           l *= f;
           if (begun) {

@@ -9,9 +9,8 @@ from attention_paths import make, prefix_kernel, workspace  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
-# The power of two by which fp16 weights are multiplied: the smallest step of fp16, 2^-24, is that much less beside the
-# largest weight.
-LIFT_ROWS = 15
+# The power of two that the largest fp16 weight is at least: the smallest step of fp16, 2^-24, is that much less beside it.
+LIFT_ROWS, LIFT_PREFIX = 15, 7
 
 
 @pytest.fixture(scope="module")
@@ -64,6 +63,30 @@ def test_own_rows(kvx, B, N, H, D, n, nats, dtype, sink):
         for h in range(H):
             some = slice(h * N, h * N + N)
             want = _tight(q[b, some], rows["k"][b, h], rows["v"][b, h], LIFT_ROWS)
+            ref.check("out", out[b, some], want[0], want[2])
+            ref.check("lse", lse[b, some], want[1], want[3])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("nats", [12.0, 17.8, 20.5])
+@pytest.mark.parametrize("B,N,H,D,P", [(32, 4, 1, 128, 65521), (32, 4, 64, 128, 1300), (1024, 4, 8, 128, 1300), (700, 5, 8, 64, 1100)])
+@pytest.mark.parametrize("sink", ["first", "middle", "last"])
+@pytest.mark.parametrize("new", [False, True])
+def test_shared_rows(kvx, B, N, H, D, P, nats, dtype, sink, new):
+    at = {"first": 0, "middle": P // 2, "last": P - 1}[sink]
+    q, rows = _tailed(B, N, H, D, dict(P=P, new=new), [("prefix_k", "prefix_v")], at, nats, dtype)
+    if new:
+        rows["k_new"][..., 0] = -8.0
+    assert prefix_kernel(kvx, q, **rows)
+    out, lse = torch.empty_like(q), torch.empty(B, N * H, device="cuda")
+    kvx.attend(q, out, lse=lse, **rows)
+    torch.cuda.synchronize()
+    for b in range(0, B, B // 3):
+        for h in range(0, H, 3):
+            keys, values, some = rows["prefix_k"][h], rows["prefix_v"][h], slice(h * N, h * N + N)
+            if new:
+                keys, values = torch.cat([keys, rows["k_new"][b, h, None]]), torch.cat([values, rows["v_new"][b, h, None]])
+            want = _tight(q[b, some], keys, values, LIFT_PREFIX)
             ref.check("out", out[b, some], want[0], want[2])
             ref.check("lse", lse[b, some], want[1], want[3])
 
