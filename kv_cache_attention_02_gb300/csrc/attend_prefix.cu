@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           nb = none ? kNegInf : m == kNegInf ? 0.f : -m;
           if (__builtin_expect(__any_sync(~0u, odd), 0)) {
             // the difference, of a product rounded as the maximum was, goes through the
-            // fused product instead
+            // fused product instead (in such rows alone: no row's bits depend on its neighbours)
             const float inv = 1.f / a.scale2;
 #pragma unroll 1
             for (int c = 0; c < kT / 16; ++c) {
@@ -531,12 +531,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
               tmem_ld16(ts + 16 * c, x);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                o[e] = __float_as_uint(16 * c + e < left ? __fadd_rn(__fmul_rn(x[e], a.scale2), nb) * inv : kNegInf);
+                o[e] = __float_as_uint(16 * c + e >= left ? kNegInf
+                                       : odd ? __fadd_rn(__fmul_rn(x[e], a.scale2), nb) * inv : x[e]);
               tmem_st16(ts + 16 * c, o);
             }
             tmem_st_wait();
             tmem_ld128(ts, v);
-            nb = 0.f;
+            if (odd) nb = 0.f;
           }
         }
         begun = true;

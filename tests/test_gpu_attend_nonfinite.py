@@ -67,6 +67,29 @@ def test_a_logit_of_minus_infinity_takes_no_weight(kvx, B, N, H, D, P, dtype):
     ref.check("lse", lse, want[1], want[3])
 
 
+@pytest.mark.parametrize("B,N,H,D,P", [(64, 2, 4, 128, 2000), (64, 5, 4, 64, 2000), (3, 2, 2, 64, 100)])
+def test_a_logit_of_infinity(kvx, B, N, H, D, P):
+    """+inf: NaN in the sequences that have the row. Nothing but -inf: as if there were no rows."""
+    q, rows = make(B, N, H, D, P=P, seed=6)
+    lens = torch.tensor([P, 17], dtype=torch.int32, device="cuda").repeat(B)[:B]
+    want, wlse = ref.check_attend(kvx, q, prefix_lens=lens, **rows)
+    q[:, :N, 0] = 1.0                                                  # the first key head's queries
+    want[:, :N], wlse[:, :N] = [x[:, :N] for x in ref.check_attend(kvx, q, prefix_lens=lens, **rows)]
+    rows["prefix_k"][0, 40, 0] = float("inf")
+    out, lse = torch.empty_like(q), torch.empty_like(wlse)
+    kvx.attend(q, out, lse=lse, prefix_lens=lens, **rows)
+    torch.cuda.synchronize()
+    hit = torch.zeros(B, N * H, dtype=torch.bool, device="cuda")
+    hit[::2, :N] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wlse[~hit])
+    rows["prefix_k"][0, :, 0] = -float("inf")
+    kvx.attend(q, out, lse=lse, prefix_lens=lens, **rows)
+    torch.cuda.synchronize()
+    assert (out[:, :N] == 0).all() and (lse[:, :N] == -float("inf")).all()
+    assert torch.equal(out[:, N:], want[:, N:]) and torch.equal(lse[:, N:], wlse[:, N:])
+
+
 # Few own rows beside a large prefix (joined in the clusters' kernel), and many (in the ranges' join).
 BESIDE = [(32, 4, 8, 128, 1100, 0), (40, 3, 8, 128, 900, 5), (300, 2, 2, 128, 901, 0), (32, 4, 8, 128, 1100, 400),
           (300, 2, 2, 128, 901, 200)]
