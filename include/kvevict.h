@@ -458,9 +458,13 @@ typedef struct kvevict_attention {
  * own rows the call is the prefix's part of a longer attention (a prompt
  * chunk's tokens given as sequences), and lse joins it with the rest. Logits,
  * softmax and sums are fp32; out is rounded once. out and lse overlap no input.
- * Where prefix_lens differ, a shared value that is NaN or infinite may show in
- * sequences that do not share its row (their weight of it is 0); rows past the
- * longest length are not looked at. Waits in the prefix's kernel are bounded
+ * A key whose logit is NaN or +inf makes its sequences' out and lse NaN; one of
+ * -inf takes no weight. A value that is NaN or infinite shows in its column of
+ * out as NaN or infinite (which of the two depends on the sizes: a weight is
+ * split in two, and 0 times infinity is NaN), whatever its row's weight. Where
+ * prefix_lens differ, such a value may show in sequences that do not share
+ * its row (their weight of it is 0), such a key does not; rows past the longest
+ * length are not looked at. Waits in the prefix's kernel are bounded
  * (4 s); one that runs out leaves NaN in out and lse, and on a handle sets its
  * error word (kvevict_check).
  * The workspace holds nothing between calls and needs no initial value; calls

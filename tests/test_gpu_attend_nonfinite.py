@@ -49,6 +49,34 @@ def test_keys_of_rows_that_a_sequence_does_not_share(kvx, B, N, H, D, P, dtype, 
     assert torch.isnan(out[~short]).all() and torch.isnan(lse[~short]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("path", ["clusters", "ranges", "pair", "tiles"])
+def test_a_value_that_counts_and_is_not_finite(kvx, path, value, D):
+    """It shows: its column is not finite in the sequences that have the row, whichever kernel runs. Everything else,
+    the log sums among it, is as it was."""
+    if path in ("pair", "tiles"):
+        B, N, H = 64, 2 if path == "pair" else 5, 4
+        q, rows = make(B, N, H, D, P=2000 * 128 // D, seed=3)
+    else:
+        B, N, H = (3, 2, 2) if path == "clusters" else (60, 2, 8)
+        q, rows = make(B, N, H, D, n=50 if path == "clusters" else 600, seed=3)
+    assert prefix_kernel(kvx, q, **rows) == (path in ("pair", "tiles"))
+    want, lse = ref.check_attend(kvx, q, **rows)
+    rows["v" if "v" in rows else "prefix_v"][..., 0, 17, 9] = float(value)      # of the first key head
+    if "v" in rows:
+        rows["v"][1:, 0, 17, 9] = 1.0                                           # of the first sequence
+    out, again = torch.empty_like(q), torch.empty_like(lse)
+    kvx.attend(q, out, lse=again, **rows)
+    torch.cuda.synchronize()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[:1 if "v" in rows else B, :N, 9] = True
+    assert not torch.isfinite(out[hit]).any()
+    if "v" in rows:
+        hit[:, :N, 9] = True
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(again, lse)
+
+
 @pytest.mark.parametrize("B,N,H,D,P", [(32, 4, 8, 128, 1100), (300, 2, 2, 128, 901), (4, 2, 2, 64, 100)])
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_a_logit_of_minus_infinity_takes_no_weight(kvx, B, N, H, D, P, dtype):
