@@ -196,7 +196,7 @@ def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None
     q [B, S, G, D], k [B, S, H, D]: fp16, bf16 or fp32 (views of a fused projection are fine). q_out, k_out: their
     shapes in fp16 or bf16, in any layout with a contiguous last dimension; ``prompt_keys[:, l].transpose(1, 2)``
     writes layer l of what ``KVEvict.prefill`` takes, ``k_new[:, l, None]`` of what ``KVEvict.step`` takes. q_weight,
-    k_weight [D] or None (no norm). positions: int32 [B, S], else token s is at pos0 + s. Either of q and k may be
+    k_weight [D] or None (no norm). positions: int32 [B, S], else token s is at pos0 + s, in 32 bits too. Either of q and k may be
     None with its output. Errors: ValueError, KVEvictError.
     """
     torch = _torch()
@@ -214,6 +214,8 @@ def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None
     if not -1 << 63 <= pos0 < 1 << 63:
         raise ValueError("pos0 must fit 64 bits")
     B, S, _, D = some.shape
+    if positions is None and not -1 << 31 <= pos0 <= (1 << 31) - max(S, 1):
+        raise ValueError("pos0 and the positions after it must fit 32 bits")
     kind, kind_out = some.dtype, some_out.dtype
     if kind not in _IN or kind_out not in _OUT:
         raise ValueError("q and k must be fp16, bf16 or fp32, q_out and k_out fp16 or bf16")

@@ -70,6 +70,9 @@ int qk_run(const kvevict_qk* d, cudaStream_t s) {
   if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return invalid("eps must be >= 0 and finite");
   if (!(d->rope_theta > 0.0) || !std::isnormal(d->rope_theta))   // a subnormal's powers overflow
     return invalid("rope_theta must be > 0, normal and finite");
+  // a frequency's 53 bits leave a position of 2^31 an angle within 2^-21, one of 2^50 none
+  if (!d->positions && (d->pos0 < INT32_MIN || d->pos0 > (int64_t)INT32_MAX + 1 - std::max(d->seq, 1)))
+    return invalid("pos0 and the positions after it must fit 32 bits");
   if (d->reserved) return invalid("reserved must be 0");
   if (d->batch == 0 || d->seq == 0 || d->n_heads + d->n_kv_heads == 0) return KVEVICT_OK;
   if (d->n_heads > 0 && (!d->q || !d->q_out)) return invalid("q and q_out must not be null");

@@ -15,8 +15,8 @@
 //
 // Angles: the turn count p * w / 2 pi is taken modulo 1 in 64-bit fixed point
 // (one integer product; the fraction is exact up to p * 2^-65 plus the 2^-53
-// of the frequency itself), so far positions lose nothing and no fp64
-// instruction runs. The lanes of a warp compute a token's D/2 angles once
+// of the frequency itself: within 2^-21 rad at the farthest positions, +-2^31), and
+// no fp64 instruction runs. The lanes of a warp compute a token's D/2 angles once
 // between them, then take the warp's heads of that token with them.
 //
 // Measured on GB300: 32 x 4096 tokens of 40 heads of 128, bf16, 414-418 us, 6.4-6.5

@@ -1,0 +1,16 @@
+"""Numbers that kvevict_qk_norm_rope cannot compute with: refused, in C and from Python, before anything runs."""
+import pytest
+
+torch = pytest.importorskip("torch")
+from test_attention_refusals import _qk, kvx  # noqa: E402,F401
+
+
+@pytest.mark.parametrize("pos0,seq", [(1 << 31, 1), ((1 << 31) - 1, 2), (-(1 << 31) - 1, 1), (1 << 40, 1), ((1 << 63) - 1, 3),
+                                      (-(1 << 63), 1)])
+def test_positions_past_32_bits(kvx, pos0, seq):  # noqa: F811
+    """A frequency of 53 bits leaves a position of 2^33 an angle's error of 2^-20, one of 2^50 no angle at all."""
+    assert kvx.lib().kvevict_qk_norm_rope(_qk(kvx, pos0=pos0, seq=seq), None) == kvx.ERR_INVALID_ARG
+    assert "pos0" in kvx.last_error()
+    x = torch.zeros(2, seq, 4, 64)
+    with pytest.raises((ValueError, kvx.KVEvictError), match="pos0"):
+        kvx.qk_norm_rope(x, None, x.half(), None, rope_theta=1e4, pos0=pos0)
