@@ -410,7 +410,8 @@ typedef struct kvevict_qk {
 
 /* RMS norm of every query and key head, y = x * w / sqrt(mean(x^2) + eps), and
  * the rotation of the pairs (i, i + D/2) by p * theta^(-2i/D), in fp32 with one
- * rounding to out_dtype. q_out may be q itself, and k_out k, with the same type
+ * rounding to out_dtype. (Squares are summed in fp32, too: a head of elements
+ * beyond 1e18 overflows to 0.) q_out may be q itself, and k_out k, with the same type
  * and strides; outputs overlap nothing else. Positions are any int32 (pos0 + s
  * too); angles are within 2^-21 of exact for rope_theta >= 1. One kernel launch. Errors: INVALID_ARG, CUDA. */
 int kvevict_qk_norm_rope(const kvevict_qk* args, void* stream);

@@ -209,8 +209,8 @@ def qk_norm_rope(q, k, q_out, k_out, *, rope_theta, q_weight=None, k_weight=None
         raise ValueError("q and k must have shape [batch, seq, heads, head_dim]")
     if not 2.0**-1022 <= rope_theta <= 1.7e308:
         raise ValueError("rope_theta must be > 0, normal and finite")
-    if not 0 <= eps <= 3.4e38:
-        raise ValueError("eps must be >= 0 and finite")
+    if not (eps == 0 or 2.0**-149 <= eps <= 3.4e38):         # (below, it would round to 0)
+        raise ValueError("eps must be 0, or from 2^-149 and finite")
     if not -1 << 63 <= pos0 < 1 << 63:
         raise ValueError("pos0 must fit 64 bits")
     B, S, _, D = some.shape

@@ -14,3 +14,11 @@ def test_positions_past_32_bits(kvx, pos0, seq):  # noqa: F811
     x = torch.zeros(2, seq, 4, 64)
     with pytest.raises((ValueError, kvx.KVEvictError), match="pos0"):
         kvx.qk_norm_rope(x, None, x.half(), None, rope_theta=1e4, pos0=pos0)
+
+
+@pytest.mark.parametrize("eps", [1e-46, 1e-60, 5e-324])
+def test_eps_that_is_zero_in_32_bits(kvx, eps):  # noqa: F811
+    """It would make a row of zeros NaN where the formula has 0."""
+    x = torch.zeros(2, 3, 4, 64)
+    with pytest.raises(ValueError, match="eps"):
+        kvx.qk_norm_rope(x, None, x.half(), None, rope_theta=1e4, eps=eps)
