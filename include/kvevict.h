@@ -474,6 +474,12 @@ typedef struct kvevict_attention {
  * kvevict_attend_workspace for the size and call again). */
 int kvevict_attend(const kvevict_attention* args, void* stream);
 
+/* Test hook: while `without` is not 0, calls of this process are planned as if
+ * the prefix's tensor-core kernel could not be launched (a driver without tensor maps, a
+ * compiler that gave the kernel other registers): the row kernel then reads the shared rows
+ * itself, with the same results. Not while a call is under way. Errors: none. */
+int kvevict_test_without_prefix_kernel(int32_t without);
+
 /* Device bytes that a call of this description needs as workspace, on the
  * current device; of the pointers only k_new counts (whether it is null).
  * with_cache: 1 for

@@ -81,6 +81,7 @@ SIGNATURES = {
     "kvevict_qk_norm_rope": (ctypes.c_int, [P, P]),
     "kvevict_attend": (ctypes.c_int, [P, P]),
     "kvevict_attend_workspace": (ctypes.c_int, [P, i32, P]),
+    "kvevict_test_without_prefix_kernel": (ctypes.c_int, [i32]),
     "kvevict_attend_cache": (ctypes.c_int, [P, i32, P, P]),
 }
 

@@ -149,14 +149,13 @@ int attend_check(const kvevict_attention* d) {
 }
 
 // The prefix kernel's plan; not used (the row kernel reads the shared rows
-// itself) where TMA cannot describe the rows.
-PrefixPlan plan_prefix(const kvevict_attention* d, bool own, Streamed stream, int sms) {
-  const bool fit = d->prefix > 0 && prefix_strides_fit(d->prefix_k_stride, d->n_kv_heads, d->prefix, d->head_dim) &&
-                   prefix_strides_fit(d->prefix_v_stride, d->n_kv_heads, d->prefix, d->head_dim);
-  return fit
-             ? prefix_plan(d->batch, d->n_heads, d->n_kv_heads, d->head_dim, d->prefix, own,
-                           stream, sms)
-             : PrefixPlan{};
+// itself) where TMA cannot describe the rows, or the kernel cannot be launched.
+PrefixPlan plan_prefix(const kvevict_attention* d, bool own, Streamed stream, const DeviceInfo& dev) {
+  if (d->prefix == 0 || !prefix_strides_fit(d->prefix_k_stride, d->n_kv_heads, d->prefix, d->head_dim) ||
+      !prefix_strides_fit(d->prefix_v_stride, d->n_kv_heads, d->prefix, d->head_dim))
+    return PrefixPlan{};
+  const PrefixPlan plan = prefix_plan(d->batch, d->n_heads, d->n_kv_heads, d->head_dim, d->prefix, own, stream, dev.sms);
+  return plan.ctas && prefix_kernel_ready(d->head_dim, d->dtype, plan.pair, dev.device) ? plan : PrefixPlan{};
 }
 
 }  // namespace
@@ -234,13 +233,13 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
   const int D = d->head_dim;
   PrefixArgs p{};
   const int own = a.n + (a.k_new ? 1 : 0);             // rows of a sequence, at most
-  p.plan = plan_prefix(d, rows || own, Streamed{}, dev.sms);
+  p.plan = plan_prefix(d, rows || own, Streamed{}, dev);
   const bool alone = p.plan.ctas && p.plan.final;      // the prefix is all there is
   RowsPlan rp{};
   if (!alone)
     rp = rows_plan(a.B, a.G, a.H, D, a.n, p.plan.ctas ? 0 : a.P, a.k_new, rows != nullptr, p.plan.ctas > 0, dev.sms);
   if (p.plan.ctas && rp.ctas) {                        // both at once, each on its SMs
-    p.plan = plan_prefix(d, true, Streamed{(int64_t)a.B * a.H * own * D * 4, rp.units}, dev.sms);
+    p.plan = plan_prefix(d, true, Streamed{(int64_t)a.B * a.H * own * D * 4, rp.units}, dev);
     rp.ctas = std::min(rp.ctas, stream_ctas(D, std::max(1, dev.sms - p.plan.ctas)));
   }
   const size_t need = p.plan.bytes(D) + rp.bytes(D);
@@ -255,7 +254,6 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
     p.part_ml = reinterpret_cast<float2*>(space + p.plan.o_bytes(D));
     p.err = rows ? rows->err : nullptr;
     p.stall = take_scorer_stall() ? 1 : 0;
-    p.device = dev.device;
     const cudaError_t e = launch_attend_prefix(p, D, d->dtype, s);
     if (e != cudaSuccess) return cuda_result(e, "launch");
     if (alone) return KVEVICT_OK;
@@ -306,7 +304,7 @@ extern "C" int kvevict_attend_workspace(const kvevict_attention* args, int32_t w
     if (int rc = kvx::device_info(&dev)) return rc;
     const int B = args->batch, G = args->n_heads, H = args->n_kv_heads, D = args->head_dim;
     const bool own = with_cache || args->n > 0 || args->k_new;
-    const kvx::PrefixPlan pp = kvx::plan_prefix(args, own, kvx::Streamed{}, dev.sms);
+    const kvx::PrefixPlan pp = kvx::plan_prefix(args, own, kvx::Streamed{}, dev);
     *bytes = pp.bytes(D);
     if (pp.ctas && !own) return KVEVICT_OK;
     // a handle's rows are not in the description: as many as there can be
@@ -315,4 +313,9 @@ extern "C" int kvevict_attend_workspace(const kvevict_attention* args, int32_t w
                              pp.ctas > 0, dev.sms).bytes(D);
     return KVEVICT_OK;
   });
+}
+
+extern "C" int kvevict_test_without_prefix_kernel(int32_t without) {
+  kvx::prefix_kernel_off(without != 0);
+  return KVEVICT_OK;
 }

@@ -83,6 +83,9 @@ struct PrefixPlan {
   bool shared_blocks() const;   // whether any block is cut
 };
 bool prefix_strides_fit(const int64_t* stride, int H, int P, int D);
+// Whether the kernel can be launched as it was compiled, on a device below 64 (looked up once).
+bool prefix_kernel_ready(int D, int dtype, bool pair, int device);
+void prefix_kernel_off(bool off);   // test hook: never ready
 // What the row kernel streams beside the prefix's.
 struct Streamed {
   int64_t bytes, units;
@@ -105,7 +108,6 @@ struct PrefixArgs {
   float2* part_ml;
   int* err;                // error word for bounded waits, or null
   int stall;               // test hook: CTA 0's first tile is never issued
-  int device;              // the current one, below 64
   bool k_row_first, v_row_first;
   __host__ __device__ PrefixParts parts() const { return PrefixParts{plan, part_o, part_ml}; }
 };

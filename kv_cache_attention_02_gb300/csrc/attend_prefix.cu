@@ -777,28 +777,24 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   if (d4 + warp == 0 && a.lse) a.lse[(int64_t)b * a.G + head] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-template <typename T, int D, bool PAIR>
-cudaError_t launch_px(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefixArgs& p, cudaStream_t s) {
-  auto kernel = attend_prefix_kernel<T, D, PAIR>;
-  // The kernel's redistribution of registers needs the 168 a thread that its
-  // launch bound gives it: checked, as it would wait forever with fewer.
-  static std::atomic<uint64_t> ready{0};   // devices on which that, and its shared memory, are settled
-  const uint64_t bit = 1ull << p.device;
-  cudaError_t e;
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    cudaFuncAttributes f;
-    e = cudaFuncGetAttributes(&f, kernel);
-    if (e == cudaSuccess && f.numRegs != 168) e = cudaErrorLaunchOutOfResources;
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PxGeo<D>::SMEM);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_relaxed);
+// One instantiation of the kernel.
+template <typename Elem, int Dim, bool Pair>
+struct PxKind {
+  using T = Elem;
+  static constexpr int D = Dim;
+  static constexpr auto kernel = attend_prefix_kernel<Elem, Dim, Pair>;
+};
+template <typename F>
+auto px_pick(int D, int dtype, bool pair, F&& f) {
+  if (dtype == kBf16) {
+    if (D == 64) return pair ? f(PxKind<__nv_bfloat16, 64, true>{}) : f(PxKind<__nv_bfloat16, 64, false>{});
+    return pair ? f(PxKind<__nv_bfloat16, 128, true>{}) : f(PxKind<__nv_bfloat16, 128, false>{});
   }
-  kernel<<<p.plan.ctas, kPxThreads, PxGeo<D>::SMEM, s>>>(kmap, vmap, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !p.plan.final || !p.plan.shared_blocks()) return e;
-  const dim3 grid(std::min(p.plan.units, p.plan.ctas - 1), p.plan.block_rows / 32, D / 32);
-  return launch_after(attend_join_kernel<T, D>, grid, 256, 0, 1, true, s, p);
+  if (D == 64) return pair ? f(PxKind<__half, 64, true>{}) : f(PxKind<__half, 64, false>{});
+  return pair ? f(PxKind<__half, 128, true>{}) : f(PxKind<__half, 128, false>{});
 }
+
+std::atomic<bool> g_off{false};   // test hook
 
 // Strides between heads and rows, where a dimension of one has none of its own.
 void row_strides(const int64_t* stride, int H, int P, int D, int64_t* hs, int64_t* rs) {
@@ -892,22 +888,42 @@ bool PrefixPlan::shared_blocks() const {
   return false;
 }
 
+bool prefix_kernel_ready(int D, int dtype, bool pair, int device) {
+  if (g_off.load(std::memory_order_relaxed) || !encode_fn()) return false;
+  return px_pick(D, dtype, pair, [&](auto kind) {
+    using K = decltype(kind);
+    // The kernel's redistribution of registers needs the 168 a thread that its
+    // launch bound gives it: checked, as it would wait forever with fewer.
+    static std::atomic<uint64_t> ready{0};   // devices on which that, and its shared memory, are settled
+    const uint64_t bit = 1ull << device;
+    if (ready.load(std::memory_order_relaxed) & bit) return true;
+    cudaFuncAttributes f;
+    if (cudaFuncGetAttributes(&f, K::kernel) != cudaSuccess || f.numRegs != 168 ||
+        cudaFuncSetAttribute(K::kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PxGeo<K::D>::SMEM) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    ready.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+  });
+}
+
+void prefix_kernel_off(bool off) { g_off.store(off); }
+
 cudaError_t launch_attend_prefix(const PrefixArgs& args, int D, int dtype, cudaStream_t s) {
   PrefixArgs p = args;
   CUtensorMap kmap, vmap;
   if (!encode_rows(&kmap, p.a.pk, p.a.pk_stride, p.a.H, p.a.P, D, dtype, &p.k_row_first) ||
       !encode_rows(&vmap, p.a.pv, p.a.pv_stride, p.a.H, p.a.P, D, dtype, &p.v_row_first))
     return cudaErrorInvalidValue;
-  if (dtype == kBf16) {
-    if (D == 64)
-      return p.plan.pair ? launch_px<__nv_bfloat16, 64, true>(kmap, vmap, p, s)
-                         : launch_px<__nv_bfloat16, 64, false>(kmap, vmap, p, s);
-    return p.plan.pair ? launch_px<__nv_bfloat16, 128, true>(kmap, vmap, p, s)
-                       : launch_px<__nv_bfloat16, 128, false>(kmap, vmap, p, s);
-  }
-  if (D == 64)
-    return p.plan.pair ? launch_px<__half, 64, true>(kmap, vmap, p, s) : launch_px<__half, 64, false>(kmap, vmap, p, s);
-  return p.plan.pair ? launch_px<__half, 128, true>(kmap, vmap, p, s) : launch_px<__half, 128, false>(kmap, vmap, p, s);
+  return px_pick(D, dtype, p.plan.pair, [&](auto kind) {
+    using K = decltype(kind);
+    K::kernel<<<p.plan.ctas, kPxThreads, PxGeo<K::D>::SMEM, s>>>(kmap, vmap, p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !p.plan.final || !p.plan.shared_blocks()) return e;
+    const dim3 grid(std::min(p.plan.units, p.plan.ctas - 1), p.plan.block_rows / 32, K::D / 32);
+    return launch_after(attend_join_kernel<typename K::T, K::D>, grid, 256, 0, 1, true, s, p);
+  });
 }
 
 }  // namespace kvx
