@@ -493,7 +493,10 @@ int kvevict_attend_workspace(const kvevict_attention* args, int32_t with_cache, 
  * n_kv_heads and head_dim are the handle's, dtype is FP16, and n, k, v and lens
  * must be 0 and null (the row count is min(next_pos, budget_l) when the call is
  * made: a captured call keeps it). q and k_new are rotated at position
- * kvevict_next_pos. Errors: as kvevict_attend; INVALID_ARG (a key-only handle,
+ * kvevict_next_pos, or at `prefix` + kvevict_next_pos behind a prefix, whose rows
+ * have the positions from 0 on: the prompt's keys were then rotated from `prefix`
+ * on, too (the cache's own positions start at 0 all the same; only differences
+ * count). Errors: as kvevict_attend; INVALID_ARG (a key-only handle,
  * another device current than the handle's, layer out of range). */
 int kvevict_attend_cache(const kvevict_t* h, int32_t l, const kvevict_attention* args, void* stream);
 

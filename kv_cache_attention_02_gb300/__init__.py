@@ -424,7 +424,8 @@ class KVEvict:
                scale=None, stream=None):
         """``attend`` with layer l's kept keys and values as the own rows (a value-carrying handle; fp16).
 
-        q, out [B, G, D]; k_new, v_new [B, H, D]: the token's own, before the step that inserts them. Rows are as
+        q, out [B, G, D]; k_new, v_new [B, H, D]: the token's own, before the step that inserts them, rotated at
+        position next_pos, behind P shared rows at P + next_pos (and the prompt's keys from P on). Rows are as
         ``read_state`` and ``read_values`` give them; the handle is not changed. A captured call keeps the row count
         of its capture.
         """
