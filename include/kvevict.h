@@ -377,8 +377,9 @@ int kvevict_prefill_scores_noalloc(const uint16_t* keys, int32_t heads, int32_t 
  * device that is current, which must be the one the pointers belong to. Their
  * descriptions are read before the call returns. Strides count elements; the
  * last dimension is contiguous, pointers start on a 16-byte boundary and the
- * stride of every dimension of more than one entry is a multiple of 16 bytes. Calls may overlap on any streams and
- * threads as long as none writes what another uses. */
+ * stride of every dimension of more than one entry is a multiple of 16 bytes;
+ * inputs may broadcast (strides of 0), the rows of outputs lie apart. Calls may
+ * overlap on any streams and threads as long as none writes what another uses. */
 #define KVEVICT_DTYPE_FP16 0
 #define KVEVICT_DTYPE_BF16 1
 #define KVEVICT_DTYPE_FP32 2   /* inputs and weights of kvevict_qk_norm_rope only */

@@ -35,6 +35,14 @@ bool strides16(const int64_t (&s)[K], const int32_t (&extent)[K], int elem) {
   return true;
 }
 
+// Rows of D elements that cannot lie apart (written by several threads at once).
+template <int K>
+bool rows_overlap(const int64_t (&s)[K], const int32_t (&extent)[K], int D) {
+  for (int i = 0; i < K; ++i)
+    if (extent[i] > 1 && s[i] < D && s[i] > -D) return true;
+  return false;
+}
+
 bool is16(int dtype) { return dtype == kFp16 || dtype == kBf16; }
 
 }  // namespace
@@ -85,6 +93,9 @@ int qk_run(const kvevict_qk* d, cudaStream_t s) {
   if (d->n_kv_heads > 0 && (!aligned(d->k) || !aligned(d->k_out) || !strides16(d->k_stride, kx, ie) ||
                             !strides16(d->k_out_stride, kx, 2)))
     return invalid("k and k_out must be 16-byte aligned, with strides of multiples of 16 bytes");
+  if ((d->n_heads > 0 && rows_overlap(d->q_out_stride, qx, d->head_dim)) ||
+      (d->n_kv_heads > 0 && rows_overlap(d->k_out_stride, kx, d->head_dim)))
+    return invalid("the rows of q_out and of k_out must not overlap: strides of at least head_dim");
   const unsigned we = d->weight_dtype == kFp32 ? 4 : 2;
   if (!aligned(d->q_weight, we) || !aligned(d->k_weight, we) || !aligned(d->positions, 4))
     return invalid("q_weight, k_weight and positions must be aligned to their elements");
@@ -177,6 +188,8 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
   const int32_t nx[2] = {d->batch, d->n_kv_heads}, px[2] = {d->n_kv_heads, d->prefix};
   if (!aligned(d->q) || !aligned(d->out) || !strides16(d->q_stride, qx, 2) || !strides16(d->out_stride, qx, 2))
     return invalid("q and out must be 16-byte aligned, with strides of multiples of 16 bytes");
+  if (rows_overlap(d->out_stride, qx, d->head_dim))
+    return invalid("the rows of out must not overlap: strides of at least head_dim");
   if (d->n > 0 && (!aligned(d->k) || !aligned(d->v) || !strides16(d->k_stride, kx, 2) || !strides16(d->v_stride, kx, 2)))
     return invalid("k and v must be 16-byte aligned, with strides of multiples of 16 bytes");
   if (d->k_new && (!aligned(d->k_new) || !aligned(d->v_new) || !strides16(d->k_new_stride, nx, 2) ||
