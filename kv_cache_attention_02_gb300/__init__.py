@@ -93,11 +93,12 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build the CUDA library first "
                               "(python -c 'import __graft_entry__ as g; g.build()')")
-        _lib = ctypes.CDLL(LIB_PATH)
+        found = ctypes.CDLL(LIB_PATH)
         for name, (res, args) in SIGNATURES.items():
-            fn = getattr(_lib, name)
+            fn = getattr(found, name)
             fn.restype = res
             fn.argtypes = args
+        _lib = found                  # whole: other threads may be here, too
     return _lib
 
 
@@ -144,9 +145,9 @@ def _torch():
     if _loaded is not None:
         return _loaded
     import torch
-    _loaded = torch
     _IN = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
     _OUT = {torch.float16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
+    _loaded = torch                   # last: other threads may be here, too
     return torch
 
 
