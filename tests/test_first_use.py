@@ -22,7 +22,7 @@ def test_the_library_is_published_with_its_signatures(kvx, monkeypatch):
                 yield x
     monkeypatch.setattr(kvx, "SIGNATURES", Watched(kvx.SIGNATURES))
     found = kvx.lib()
-    assert found is kvx._lib and all(getattr(found, name).argtypes == args for name, (_, args) in kvx.SIGNATURES.items())
+    assert found is kvx._lib and all(getattr(found, name).argtypes == args for name, (_, args) in dict.items(kvx.SIGNATURES))
 
 
 def test_torch_is_published_with_its_types(kvx):
