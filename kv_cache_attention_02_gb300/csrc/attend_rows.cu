@@ -44,7 +44,8 @@
 // Measured on GB300 (D = 128, 32 query heads on 8, fp16): 32 sequences of 2048 rows
 // 44-46 us, 5.8-6.1 TB/s of rows (0.88 of the measured copy rate), 64 of them 80 us, 6.7
 // TB/s; 7 unequal ones of up to 65521 rows 139-142 us, 6.0 TB/s; one of 512 rows 5-6 us,
-// all latency. Tried and slower: the tiles through shared memory by cp.async, two more in
+// all latency. A cache's rows 46-47 us for the same 32 x 2048, 51 us with a compaction
+// pending (its rows re-rotated on the way). Tried and slower: the tiles through shared memory by cp.async, two more in
 // flight (63 against 50 us), 32-byte loads (53 against 50), more and smaller ranges
 // (54-59), L2 prefetches throughout (150 against 139 on the unequal lengths). Bound by
 // the loads that a warp's registers hold in flight, 16 KB, 8 warps an SM, with the
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
       at += total - first;
       whole = plan.final && first == 0 && total == tb;
       slot = plan.slot((int64_t)b * upb + ub, blockIdx.x, first == 0);
-    if (rem == 0 && tid == 0 && !even_lengths(a)) plan.first[b] = base;
+      if (rem == 0 && tid == 0 && !even_lengths(a)) plan.first[b] = base;
       if (at == base + (int64_t)upb * tb) {
         base = at;
         next_b = b + 1;
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
           tm = fmaxf(tm, __shfl_xor_sync(~0u, tm, 1));
           tm = fmaxf(tm, __shfl_xor_sync(~0u, tm, 2));
           const float nm = fmaxf(m[i], tm);
-          const float f = nm == m[i] ? 1.f : ex2_approx(m[i] - nm);   // first rows: 2^-inf = 0
+          const float f = nm == m[i] ? 1.f : ex2(m[i] - nm);   // first rows: 2^-inf = 0
           m[i] = nm;
           l[i] *= f;
           // the accumulators' columns are queries 2c and 2c + 1
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
         const float base = m[i] == kNegInf ? 0.f : m[i];   // nothing so far: every weight 2^-inf = 0
 #pragma unroll
         for (int nt = 0; nt < 2 * KG; ++nt) {
-          const float p0 = ex2_approx(s[nt][2 * i] - base), p1 = ex2_approx(s[nt][2 * i + 1] - base);
+          const float p0 = ex2(s[nt][2 * i] - base), p1 = ex2(s[nt][2 * i + 1] - base);
           l[i] += p0 + p1;
           const float2 w = make_float2(p0 * kLift<T>, p1 * kLift<T>);
           hi[i][nt] = pack16<T>(w.x, w.y);
@@ -533,10 +534,10 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
             const int q = g + 8 * i;
             float2 part = inside(q) ? ml[off + q] : make_float2(kNegInf, 0.f);
             const float nm = fmaxf(m[i], part.x);
-            const float f = m[i] == nm ? 1.f : ex2_approx(m[i] - nm);
+            const float f = m[i] == nm ? 1.f : ex2(m[i] - nm);
             // a part without rows has left no O; a NaN sum (NaN logits, a wait that ran out)
             // passes on, however far its maximum is below the others
-            const float fp = part.y == 0.f ? 0.f : part.y != part.y ? part.y : part.x == nm ? 1.f : ex2_approx(part.x - nm);
+            const float fp = part.y == 0.f ? 0.f : part.y != part.y ? part.y : part.x == nm ? 1.f : ex2(part.x - nm);
             m[i] = nm;
             l[i] = l[i] * f + (c == 0 && fp != 0.f ? part.y * fp : 0.f);
 #pragma unroll
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
       float ll = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float mw = part_ml[w][q][0], f = mw == mm ? 1.f : ex2_approx(mw - mm);
+        const float mw = part_ml[w][q][0], f = mw == mm ? 1.f : ex2(mw - mm);
         const float4 v = *reinterpret_cast<const float4*>(&part_o[w][q][d]);
         o.x = fmaf(f, v.x, o.x);
         o.y = fmaf(f, v.y, o.y);
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float ll = 0.f;
       for (int r = 0; r < C; ++r) {
-        const float mr = *cluster.map_shared_rank(&cta_ml[q][0], r), f = mr == mm ? 1.f : ex2_approx(mr - mm);
+        const float mr = *cluster.map_shared_rank(&cta_ml[q][0], r), f = mr == mm ? 1.f : ex2(mr - mm);
         const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&cta_o[q][d], r));
         o.x = fmaf(f, v.x, o.x);
         o.y = fmaf(f, v.y, o.y);
@@ -705,13 +706,13 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW)
     float nm = m;
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) nm = fmaxf(nm, ml[k].x);
-    const float f = m == nm ? 1.f : ex2_approx(m - nm);
+    const float f = m == nm ? 1.f : ex2(m - nm);
     m = nm;
     l *= f;
     o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
-      const float w = ml[k].x == nm ? 1.f : ex2_approx(ml[k].x - nm);
+      const float w = ml[k].x == nm ? 1.f : ex2(ml[k].x - nm);
       l = fmaf(ml[k].y, w, l);
       o = make_float4(fmaf(v[k].x, w, o.x), fmaf(v[k].y, w, o.y), fmaf(v[k].z, w, o.z), fmaf(v[k].w, w, o.w));
     }
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW)
     for (int w = 1; w < JW; ++w) {
       const float2 ml = ml_s[w];
       const float4 v = o_s[w][min(lane, D4 - 1)];
-      const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2_approx(m - nm), y = ml.x == nm ? 1.f : ex2_approx(ml.x - nm);
+      const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2(m - nm), y = ml.x == nm ? 1.f : ex2(ml.x - nm);
       m = nm;
       l = l * f + ml.y * y;
       o = make_float4(o.x * f + v.x * y, o.y * f + v.y * y, o.z * f + v.z * y, o.w * f + v.w * y);

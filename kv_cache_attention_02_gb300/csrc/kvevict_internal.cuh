@@ -257,4 +257,12 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// 2^x on the MUFU (ex2.approx: relative error below 2^-22; subnormal results
+// flush to zero, which only drops terms below 2^-126 from a sum of terms <= 1).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 }  // namespace kvx

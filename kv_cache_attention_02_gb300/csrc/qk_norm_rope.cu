@@ -20,8 +20,9 @@
 // between them, then take the warp's heads of that token with them.
 //
 // Measured on GB300: 32 x 4096 tokens of 40 heads of 128, bf16, 414-418 us, 6.4-6.5
-// TB/s (0.95 of the measured copy rate); 3 x 1021 fp32 tokens of 32 heads 13.5 us, 5.6
-// TB/s, 2.5 us of it the launch; one token of 8 heads 2.5-3 us.
+// TB/s (0.95 of the measured copy rate); 3 x 1021 fp32 tokens of 32 heads 17.1 us, 4.4
+// TB/s, 4 us of it launch and first loads (13.5 us with its 75 MB in L2); one token of 8
+// heads 4.3 us.
 #include "kvevict_internal.cuh"
 #include "attend_internal.cuh"
 

@@ -95,14 +95,6 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
   for (int e = 0; e < 64; ++e) v[e] = __uint_as_float(r[e]);
 }
 
-// 2^x on the MUFU (ex2.approx: relative error below 2^-22; subnormal results
-// flush to zero, which only drops terms below 2^-126 from a sum of terms <= 1).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
