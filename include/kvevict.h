@@ -50,7 +50,7 @@ extern "C" {
 #define KVEVICT_ERR_CUDA (-3)         /* a CUDA runtime call failed */
 #define KVEVICT_ERR_OOM (-4)          /* device allocation failed */
 #define KVEVICT_ERR_DEVICE_CHECK (-5) /* a kernel raised its error word (bounded wait ran out) */
-#define KVEVICT_ERR_WORKSPACE (-6)    /* kvevict_attend: the workspace is missing, too small or not aligned */
+#define KVEVICT_ERR_WORKSPACE (-6)    /* kvevict_attend*: the workspace is missing, too small or not aligned */
 
 #define KVEVICT_MAX_LAYERS 256
 #define KVEVICT_MAX_PREFILL 16384
@@ -261,7 +261,8 @@ int kvevict_check(kvevict_t* h, void* stream);
  * outcome: a
  * handle then reports DEVICE_CHECK, the allocation-free call writes NaN
  * scores. A launch of kvevict_attend's prefix kernel that comes first takes the
- * hook instead (its first key tile), and writes NaN. Nothing faults or hangs. One-shot. Errors: none. */
+ * hook instead (its first key tile), and writes NaN; so does one of
+ * kvevict_attend_prompt or kvevict_attend_tree. Nothing faults or hangs. One-shot. Errors: none. */
 int kvevict_test_stall_next_step(kvevict_t* h);
 
 /* Position the next decode key will occupy (= tokens absorbed so far): the
@@ -500,6 +501,111 @@ int kvevict_attend_workspace(const kvevict_attention* args, int32_t with_cache, 
  * count). Errors: as kvevict_attend; INVALID_ARG (a key-only handle,
  * another device current than the handle's, layer out of range). */
 int kvevict_attend_cache(const kvevict_t* h, int32_t l, const kvevict_attention* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Several tokens a sequence: the attention of whole prompts, before
+ * kvevict_prefill takes their keys, and of trees of drafted tokens, before those
+ * that are accepted go into the cache as steps (kvevict_decode_kv takes several).
+ * The rules of the block above hold: no state, nothing allocated, the current
+ * device, strides in elements. Keys and values are read through tensor maps: their
+ * strides are >= 0 and below 2^39, and tokens (rows) lie at least D apart. */
+#define KVEVICT_MAX_TREE 64   /* tokens of a tree */
+#define KVEVICT_MAX_JOIN 8    /* parts that one join takes */
+
+typedef struct kvevict_tokens {
+  int32_t dtype;          /* FP16 or BF16: q, out and every key and value */
+  int32_t batch;          /* B sequences, >= 0 */
+  int32_t seq;            /* tokens a sequence has room for, S; with starts: of all sequences together, T */
+  int32_t n_heads;        /* G query heads, a multiple of n_kv_heads */
+  int32_t n_kv_heads;     /* H >= 1 */
+  int32_t head_dim;       /* D, 64 or 128 */
+  int32_t n;              /* own rows a sequence has room for, >= 0; n + seq < 2^30 */
+  int32_t reserved;       /* 0 */
+  float scale;            /* of the logits, 2^-126 to 2^127; 0 = 1/sqrt(D) */
+  int32_t reserved2;      /* 0 */
+  const void* q;          /* device [B, S, G, D]; with starts [T, G, D] */
+  void* out;              /* device, the shape of q */
+  float* lse;             /* device float [B, S, G] or [T, G], contiguous, or null */
+  const void* k_new;      /* device [B, S, H, D] or [T, H, D]: the tokens' own keys and values */
+  const void* v_new;
+  const int32_t* starts;  /* device int32 [B + 1], ascending, or null: sequence b has the tokens
+                             starts[b] .. starts[b + 1] - 1 of T (clamped to it) */
+  const int32_t* new_lens; /* device int32 [B]: sequence b has min(max(new_lens[b], 0), S) tokens; null: S */
+  const int32_t* parents; /* trees: device int32 [B, S], the token that each one continues, -1 where it
+                             continues the sequence itself; null: the one before it */
+  const void* k;          /* device [B, H, n, D]; null if n = 0: rows before the tokens */
+  const void* v;
+  const int32_t* lens;    /* device int32 [B]: sequence b has min(max(lens[b], 0), n) rows; null: n */
+  void* workspace;        /* device, kvevict_attend_tokens_workspace bytes, 16-byte aligned; null if that is 0 */
+  int64_t q_stride[3];    /* between sequences (with starts: not used), tokens and heads */
+  int64_t out_stride[3];
+  int64_t k_new_stride[3]; /* any order: [B, H, S, D] is what kvevict_prefill takes */
+  int64_t v_new_stride[3];
+  int64_t k_stride[3];    /* between sequences, heads and rows */
+  int64_t v_stride[3];
+  int64_t parents_stride; /* between sequences; 0: the same tree for all */
+  uint64_t workspace_bytes;
+} kvevict_tokens;
+
+/* Causal attention of prompts: token i of a sequence sees the sequence's own rows
+ * (k, v: an earlier chunk's) and its tokens 0 .. i; with s_j = q . k_j * scale over
+ * those,
+ *   out = sum_j e^(s_j) v_j / sum_j e^(s_j),   lse = log sum_j e^(s_j).
+ * Query head i reads key head i / (G / H). Tokens behind a sequence's last are neither
+ * read nor written: their out and lse stay as they are. Logits, softmax and sums are
+ * fp32; out is rounded once. out and lse overlap no input.
+ * A key whose logit is NaN or +inf makes out and lse of the query heads that see it
+ * NaN; one of -inf takes no weight. A value that is NaN or infinite shows in its
+ * column of out, as NaN or infinite, wherever it is seen and nowhere else. Rows and
+ * tokens past a length may hold anything. Waits in the kernel are bounded (4 s); one
+ * that runs out leaves NaN in out and lse, and on a handle sets its error word.
+ * The workspace holds nothing between calls and needs no initial value; calls that
+ * may run at the same time (captured graphs too) need one each.
+ * Errors: INVALID_ARG (parents not null), CUDA, WORKSPACE (nothing has been launched:
+ * ask kvevict_attend_tokens_workspace for the size and call again). */
+int kvevict_attend_prompt(const kvevict_tokens* args, void* stream);
+
+/* The same for drafted tokens that form a tree: token i sees the sequence's own rows,
+ * itself, its parent, the parent's parent and so on. seq is at most KVEVICT_MAX_TREE
+ * and starts null; a parent that is not before its token (or negative) counts as -1.
+ * Errors: as kvevict_attend_prompt. */
+int kvevict_attend_tree(const kvevict_tokens* args, void* stream);
+
+/* kvevict_attend_tree with layer l's kept rows of a value-carrying handle as the own
+ * rows, as kvevict_attend_cache has them (a compaction still pending included, the
+ * handle unchanged). batch, n_kv_heads and head_dim are the handle's, dtype is FP16,
+ * and n, k, v and lens must be 0 and null. A token at depth d of its tree (0: it
+ * continues the sequence) is rotated at kvevict_next_pos + d. Errors: as
+ * kvevict_attend_tree and kvevict_attend_cache. */
+int kvevict_attend_tree_cache(const kvevict_t* h, int32_t l, const kvevict_tokens* args, void* stream);
+
+/* Device bytes that a call of this description needs as workspace, on the current
+ * device; of the pointers only starts counts (whether it is null). with_cache: 1 for
+ * kvevict_attend_tree_cache, else 0. *bytes: host. Errors: INVALID_ARG, CUDA. */
+int kvevict_attend_tokens_workspace(const kvevict_tokens* args, int32_t with_cache, size_t* bytes);
+
+typedef struct kvevict_join {
+  int32_t dtype;          /* FP16 or BF16: of the parts and of out */
+  int32_t batch, seq;     /* >= 0 */
+  int32_t n_heads;        /* G >= 0 */
+  int32_t head_dim;       /* D, 64 or 128 */
+  int32_t parts;          /* 1 .. KVEVICT_MAX_JOIN */
+  int32_t reserved[2];    /* 0 */
+  const void* part[8];    /* device [batch, seq, G, D] each: outputs of attention over disjoint rows */
+  const float* part_lse[8]; /* device float [batch, seq, G] each, contiguous: their lse */
+  void* out;              /* device [batch, seq, G, D] */
+  float* lse;             /* device float [batch, seq, G], contiguous, or null */
+  int64_t part_stride[8][3]; /* between sequences, tokens and heads */
+  int64_t out_stride[3];
+} kvevict_join;
+
+/* Joins parts of an attention over disjoint rows: lse = log sum_p e^(lse_p) and
+ * out = sum_p e^(lse_p - lse) part_p, in fp32, rounded once. A part whose lse is -inf
+ * takes no weight, whatever it holds; a head with no other gets out 0 and lse -inf. A
+ * lse that is NaN or +inf makes out and lse NaN. out may be one of the parts, with the
+ * same strides, and lse its lse; otherwise they overlap no input. One kernel launch.
+ * Errors: INVALID_ARG, CUDA. */
+int kvevict_attend_join(const kvevict_join* args, void* stream);
 
 /* Message of the last failure on the calling thread ("" if none). */
 const char* kvevict_last_error(void);

@@ -27,6 +27,7 @@ DTYPE_FP16, DTYPE_BF16, DTYPE_FP32 = 0, 1, 2
 DECODE_AUTO, DECODE_STREAM, DECODE_RESIDENT = 0, 1, 2
 MAX_LAYERS = 256
 MAX_PREFILL = 16384
+MAX_TREE, MAX_JOIN = 64, 8
 
 i32, i64, u64, f32, f64, P = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float,
                               ctypes.c_double, ctypes.c_void_p)
@@ -83,6 +84,11 @@ SIGNATURES = {
     "kvevict_attend_workspace": (ctypes.c_int, [P, i32, P]),
     "kvevict_test_without_prefix_kernel": (ctypes.c_int, [i32]),
     "kvevict_attend_cache": (ctypes.c_int, [P, i32, P, P]),
+    "kvevict_attend_prompt": (ctypes.c_int, [P, P]),
+    "kvevict_attend_tree": (ctypes.c_int, [P, P]),
+    "kvevict_attend_tree_cache": (ctypes.c_int, [P, i32, P, P]),
+    "kvevict_attend_tokens_workspace": (ctypes.c_int, [P, i32, P]),
+    "kvevict_attend_join": (ctypes.c_int, [P, P]),
 }
 
 
@@ -131,11 +137,13 @@ def prefill_scores_noalloc(keys, colsum, stream=None):
                                                 _stream(stream)))
 
 
-# ``kvevict_qk`` and ``kvevict_attention`` of include/kvevict.h, field by field.
+# ``kvevict_qk``, ``kvevict_attention``, ``kvevict_tokens`` and ``kvevict_join`` of include/kvevict.h, field by field.
 _QK = struct.Struct("=8i f i d q 7Q 12q")
 _ATTENTION = struct.Struct("=8i f i 12Q 18q Q")
+_TOKENS = struct.Struct("=8i f i 12Q 19q Q")
+_JOIN = struct.Struct("=8i 18Q 27q")
 _U64 = struct.Struct("=Q")
-_WORKSPACE_AT, _WORKSPACE_BYTES_AT = 40 + 11 * 8, 40 + 12 * 8 + 18 * 8   # offsets in kvevict_attention
+_WORKSPACE_AT = 40 + 11 * 8              # offset in kvevict_attention and kvevict_tokens (workspace_bytes is the last)
 _NO3, _NO4 = (0, 0, 0), (0, 0, 0, 0)     # strides of tensors that are not there
 
 
@@ -299,16 +307,16 @@ def _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens
         spv[0], spv[1], 0), s
 
 
-def _with_workspace(args, cache, q, stream):
+def _with_workspace(args, cache, q, stream, size=None):
     """The same call with the workspace it needs, taken from torch's allocator for its stream, and that tensor."""
     torch, need = _torch(), ctypes.c_size_t(0)
-    _check(lib().kvevict_attend_workspace(args, cache, ctypes.addressof(need)))
+    _check((size or lib().kvevict_attend_workspace)(args, cache, ctypes.addressof(need)))
     if stream == torch._C._cuda_getCurrentRawStream(q.get_device()):
         space = torch.empty(need.value, dtype=torch.uint8, device=q.device)
     else:
         with torch.cuda.stream(torch.cuda.ExternalStream(stream or 0)):
             space = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    return b"".join((args[:_WORKSPACE_AT], _U64.pack(space.data_ptr()), args[_WORKSPACE_AT + 8:_WORKSPACE_BYTES_AT],
+    return b"".join((args[:_WORKSPACE_AT], _U64.pack(space.data_ptr()), args[_WORKSPACE_AT + 8:-8],
                      _U64.pack(need.value))), space
 
 
@@ -327,6 +335,140 @@ def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_
     if rc == ERR_WORKSPACE:                 # most calls need none
         args, space = _with_workspace(args, 0, q, s)
         rc = lib().kvevict_attend(args, s)
+    if rc:
+        _check(rc)
+
+
+def _tokens(q, out, k_new, v_new, starts, new_lens, parents, k, v, lens, lse, scale, stream, tree):
+    """The ``kvevict_tokens`` of a call and its stream."""
+    torch = _torch()
+    packed = q.dim() == 3 and not tree
+    if q.dim() != 4 and not packed:
+        raise ValueError("q must have shape [batch, tokens, heads, head_dim]" + ("" if tree else " or [tokens, heads, head_dim]"))
+    kind, heads = q.dtype, q.shape[-2]
+    if kind not in _OUT:
+        raise ValueError("q must be fp16 or bf16")
+    if (k is None) != (v is None):
+        raise ValueError("k and v go together")
+    if lens is not None and k is None:
+        raise ValueError("lens goes with k")
+    if scale is not None and not 2.0**-126 <= scale <= 2.0**127:
+        raise ValueError("scale must be from 2^-126 to 2^127")
+    if k_new.dim() != q.dim():
+        raise ValueError("k_new must have as many dimensions as q")
+    B, S, H, D = 1, q.shape[-3], k_new.shape[-2], q.shape[-1]
+    if packed:
+        if new_lens is not None:
+            raise ValueError("new_lens goes with a batch [batch, tokens, heads, head_dim], starts with packed tokens")
+        if starts is not None:
+            if starts.dim() != 1 or starts.shape[0] < 1:
+                raise ValueError("starts must have shape [batch + 1]")
+            B = starts.shape[0] - 1
+        room = (S,)
+    else:
+        if starts is not None:
+            raise ValueError("starts goes with packed tokens [tokens, heads, head_dim]")
+        B = q.shape[0]
+        room = (B, S)
+    n = 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("k must have shape [batch, kv_heads, rows, head_dim]")
+        n = k.shape[2]
+    device, s = _place(torch, q, stream)
+    own = (S, H, D) if packed else (B, S, H, D)
+    pointers, strides = [], []
+    for name, t, shape in (("q", q, q.shape), ("out", out, q.shape), ("k_new", k_new, own), ("v_new", v_new, own)):
+        at, st = _strided(name, t, shape, kind, device)
+        pointers.append(at)
+        strides += (0, *st[:2]) if packed else st[:3]
+    pk = pv = pp = tree_stride = 0
+    sk = sv = _NO4
+    if n:
+        pk, sk = _strided("k", k, (B, H, n, D), kind, device)
+        pv, sv = _strided("v", v, (B, H, n, D), kind, device)
+    if parents is not None:
+        if parents.dim() == 1:
+            parents = parents.expand(B, -1)
+        if parents.shape[-1:] == (1,):                          # (a single token's stride may be anything)
+            parents = parents.as_strided((parents.shape[0], 1), (parents.stride(0), 1))
+        pp, st = _strided("parents", parents, (B, S), torch.int32, device)
+        tree_stride = st[0]
+    ints = torch.int32
+    return _TOKENS.pack(
+        _OUT[kind], B, S, heads, H, D, n, 0, scale or 0.0, 0, pointers[0], pointers[1],
+        _dense("lse", lse, (*room, heads), torch.float32, device), pointers[2], pointers[3],
+        _dense("starts", starts, (B + 1,), ints, device), _dense("new_lens", new_lens, (B,), ints, device), pp, pk, pv,
+        _dense("lens", lens, (B,), ints, device), 0, *strides, *sk[:3], *sv[:3], tree_stride, 0), s
+
+
+def _call_tokens(call, cache, q, args, stream):
+    """Makes a call that takes a ``kvevict_tokens``, with a workspace where it needs one."""
+    rc = call(args, stream)
+    if rc == ERR_WORKSPACE:
+        args, space = _with_workspace(args, cache, q, stream, lib().kvevict_attend_tokens_workspace)
+        rc = call(args, stream)
+    if rc:
+        _check(rc)
+
+
+def attend_prompt(q, out, *, k_new, v_new, starts=None, new_lens=None, k=None, v=None, lens=None, lse=None, scale=None,
+                  stream=None):
+    """Causal attention of whole prompts: every token over its sequence's own rows and its tokens up to itself.
+
+    A batch: q, out [B, S, G, D], k_new, v_new [B, S, H, D] with new_lens int32 [B] or None (S). Packed: q, out [T, G, D],
+    k_new, v_new [T, H, D] with starts int32 [B + 1] (sequence b: starts[b] .. starts[b + 1] - 1; None: one sequence). fp16 or
+    bf16. k, v [B, H, n, D] with lens int32 [B] or None (n): rows before the tokens, an earlier chunk's. Query head i
+    reads key head i // (G // H). lse: float32, q's shape without D, or None. Tokens behind a sequence's last are not
+    written. ``prompt_keys[:, l].transpose(1, 2)`` reads layer l of what ``KVEvict.prefill`` takes. Layouts and
+    scale as in ``attend``. Errors: ValueError, KVEvictError.
+    """
+    args, s = _tokens(q, out, k_new, v_new, starts, new_lens, None, k, v, lens, lse, scale, stream, False)
+    _call_tokens(lib().kvevict_attend_prompt, 0, q, args, s)
+
+
+def attend_tree(q, out, *, k_new, v_new, parents=None, new_lens=None, k=None, v=None, lens=None, lse=None, scale=None,
+                stream=None):
+    """Attention of a tree of drafted tokens per sequence: each over the sequence's own rows, itself and its ancestors.
+
+    q, out [B, T, G, D], k_new, v_new [B, T, H, D], T at most MAX_TREE, with new_lens int32 [B] or None (T). parents:
+    int32 [B, T] or [T] (the same tree for all), the token that each one continues, always one before it, or -1
+    where it continues the sequence itself; None: a chain. Everything else as in ``attend_prompt``.
+    """
+    args, s = _tokens(q, out, k_new, v_new, None, new_lens, parents, k, v, lens, lse, scale, stream, True)
+    _call_tokens(lib().kvevict_attend_tree, 0, q, args, s)
+
+
+def attend_join(out, parts, *, lse=None, stream=None):
+    """Joins parts of an attention over disjoint rows (a shared prefix's and the rest) by their log sums.
+
+    parts: 1 to MAX_JOIN pairs (part, its lse); out and every part [B, S, G, D] or [T, G, D], fp16 or bf16; lse, theirs and
+    the output: float32, that shape without D. out may be one of the parts, and lse its lse. A part whose lse is -inf
+    takes no weight. Layouts as in ``attend``. Errors: ValueError, KVEvictError.
+    """
+    torch = _torch()
+    if out.dim() not in (3, 4):
+        raise ValueError("out must have shape [batch, tokens, heads, head_dim] or [tokens, heads, head_dim]")
+    kind, shape = out.dtype, out.shape
+    if kind not in _OUT:
+        raise ValueError("out must be fp16 or bf16")
+    parts = list(parts)
+    if not 1 <= len(parts) <= MAX_JOIN:
+        raise ValueError(f"1 to {MAX_JOIN} parts can be joined, got {len(parts)}")
+    device, s = _place(torch, out, stream)
+    flat = len(shape) == 3
+    pointers, lses, strides = [0] * MAX_JOIN, [0] * MAX_JOIN, [0] * (3 * MAX_JOIN)
+    for i, (part, part_lse) in enumerate(parts):
+        pointers[i], st = _strided(f"part {i}", part, shape, kind, device)
+        strides[3 * i:3 * i + 3] = (0, *st[:2]) if flat else st[:3]
+        if part_lse is None:
+            raise ValueError(f"part {i} needs its lse")
+        lses[i] = _dense(f"lse of part {i}", part_lse, shape[:-1], torch.float32, device)
+    to, st = _strided("out", out, shape, kind, device)
+    B, S, G, D = (1, *shape) if flat else shape
+    args = _JOIN.pack(_OUT[kind], B, S, G, D, len(parts), 0, 0, *pointers, *lses, to,
+                      _dense("lse", lse, shape[:-1], torch.float32, device), *strides, *((0, *st[:2]) if flat else st[:3]))
+    rc = lib().kvevict_attend_join(args, s)
     if rc:
         _check(rc)
 
@@ -437,6 +579,16 @@ class KVEvict:
             args, space = _with_workspace(args, 1, q, s)
             rc = lib().kvevict_attend_cache(self._h, l, args, s)
         _check(rc)
+
+    def attend_tree(self, l: int, q, out, *, k_new, v_new, parents=None, new_lens=None, lse=None, scale=None, stream=None):
+        """``attend_tree`` with layer l's kept keys and values as the own rows (a value-carrying handle; fp16).
+
+        A token at depth d of its tree (0: it continues the sequence) is rotated at position next_pos + d. Rows are as
+        ``read_state`` and ``read_values`` give them; the handle is not changed: the tokens that are accepted go in by
+        ``step`` or ``decode``. A captured call keeps the row count of its capture.
+        """
+        args, s = _tokens(q, out, k_new, v_new, None, new_lens, parents, None, None, None, lse, scale, stream, True)
+        _call_tokens(lambda d, at: lib().kvevict_attend_tree_cache(self._h, l, d, at), 1, q, args, s)
 
     def run_host(self, prefill_keys, decode_keys, evicted=None, stream=None):
         """End to end from host memory (pinned tensors or numpy uint16 arrays)."""

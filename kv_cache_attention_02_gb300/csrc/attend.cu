@@ -1,9 +1,7 @@
 // attend.cu -- the entry points kvevict_qk_norm_rope, kvevict_attend and
 // kvevict_attend_workspace of include/kvevict.h: argument checks and dispatch.
 // Host code only; nothing on the device is touched before the checks pass.
-#include "attend_internal.cuh"
-
-#include <nvtx3/nvToolsExt.h>
+#include "entry.cuh"
 
 #include <atomic>
 #include <cmath>
@@ -13,37 +11,6 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];   // multiprocessors of each device, 0: not looked up yet
-
-int invalid(const char* msg) {
-  set_last_error(msg);
-  return KVEVICT_ERR_INVALID_ARG;
-}
-
-int cuda_result(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return KVEVICT_OK;
-  set_last_error(std::string(what) + ": " + cudaGetErrorString(e));
-  return e == cudaErrorMemoryAllocation ? KVEVICT_ERR_OOM : KVEVICT_ERR_CUDA;
-}
-
-bool aligned(const void* p, unsigned to = 16) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-// Whole 16-byte pieces between the entries of every dimension that has several.
-template <int K>
-bool strides16(const int64_t (&s)[K], const int32_t (&extent)[K], int elem) {
-  for (int i = 0; i < K; ++i)
-    if (extent[i] > 1 && ((s[i] * elem) & 15)) return false;
-  return true;
-}
-
-// Rows of D elements that cannot lie apart (written by several threads at once).
-template <int K>
-bool rows_overlap(const int64_t (&s)[K], const int32_t (&extent)[K], int D) {
-  for (int i = 0; i < K; ++i)
-    if (extent[i] > 1 && s[i] < D && s[i] > -D) return true;
-  return false;
-}
-
-bool is16(int dtype) { return dtype == kFp16 || dtype == kBf16; }
 
 }  // namespace
 
@@ -282,33 +249,16 @@ int attend_run(const kvevict_attention* d, const CacheRows* rows, cudaStream_t s
 
 }  // namespace kvx
 
-namespace {
-// An NVTX range named after the entry point, and no C++ exception past it (an
-// error message is the only thing that allocates).
-template <typename F>
-int entry(const char* name, F&& body) {
-  nvtxRangePushA(name);
-  int rc;
-  try {
-    rc = body();
-  } catch (...) {
-    rc = KVEVICT_ERR_OOM;
-  }
-  nvtxRangePop();
-  return rc;
-}
-}  // namespace
-
 extern "C" int kvevict_qk_norm_rope(const kvevict_qk* args, void* stream) {
-  return entry(__func__, [&] { return kvx::qk_run(args, (cudaStream_t)stream); });
+  return kvx::entry(__func__, [&] { return kvx::qk_run(args, (cudaStream_t)stream); });
 }
 
 extern "C" int kvevict_attend(const kvevict_attention* args, void* stream) {
-  return entry(__func__, [&] { return kvx::attend_run(args, nullptr, (cudaStream_t)stream); });
+  return kvx::entry(__func__, [&] { return kvx::attend_run(args, nullptr, (cudaStream_t)stream); });
 }
 
 extern "C" int kvevict_attend_workspace(const kvevict_attention* args, int32_t with_cache, size_t* bytes) {
-  return entry(__func__, [&] {
+  return kvx::entry(__func__, [&] {
     if (!bytes) return kvx::invalid("bytes must not be null");
     if (int rc = kvx::attend_check(args)) return rc;
     *bytes = 0;

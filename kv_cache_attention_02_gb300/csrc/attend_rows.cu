@@ -166,25 +166,6 @@ __device__ __forceinline__ void prefetch_tile(const Tile<T>& t, int lane) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lane ? t.v : t.k), "r"(rows * D * 2) : "memory");
 }
 
-// A cache key whose compaction is pending: rotated by -1 position, every
-// product and sum rounded to fp32, then to fp16, as the step kernel and the
-// flush do it, so the logits see the very key the cache will hold. lo and hi
-// are the pieces with elements i and i + D/2.
-__device__ __forceinline__ void rotate_back(uint4& lo, uint4& hi, const float* rc, const float* rs) {
-  uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = unpack16<__half>(a[i]), y = unpack16<__half>(b[i]);
-    const float2 c = *reinterpret_cast<const float2*>(rc + 2 * i), s = *reinterpret_cast<const float2*>(rs + 2 * i);
-    a[i] = pack16<__half>(__fsub_rn(__fmul_rn(x.x, c.x), __fmul_rn(y.x, s.x)),
-                          __fsub_rn(__fmul_rn(x.y, c.y), __fmul_rn(y.y, s.y)));
-    b[i] = pack16<__half>(__fadd_rn(__fmul_rn(x.x, s.x), __fmul_rn(y.x, c.x)),
-                          __fadd_rn(__fmul_rn(x.y, s.y), __fmul_rn(y.y, c.y)));
-  }
-  lo = make_uint4(a[0], a[1], a[2], a[3]);
-  hi = make_uint4(b[0], b[1], b[2], b[3]);
-}
-
 // Columns d .. d + 3 of query head gq from its sums, and the head's log sum.
 template <typename T>
 __device__ __forceinline__ void write_out(const AttendArgs& a, int b, int gq, int d, float m, float l, float4 o) {

@@ -1,0 +1,1152 @@
+// attend_tokens.cu -- attention of several query tokens a sequence, on the
+// 5th-generation tensor cores: whole prompts (causal, packed or padded, behind rows
+// that the sequence already has or none) and trees of drafted tokens over a cache.
+//
+// For one sequence and key head the query rows are those of one matrix Q [nq*N, D], N =
+// G / H, row t*N + j for token t and query head j:
+//   S = Q K^T * scale,  P = e^(S - m),  O = P V,  l = sum P,
+// over the sequence's own rows, which every token sees, and its tokens' keys, of which
+// token t sees 0..t (a prompt) or itself and its ancestors (a tree). The arithmetic is
+// that of attend_prefix.cu: 16-bit weights for the second product (the sum of two 16-bit
+// parts with up to 128 query rows), the sum l of the unrounded ones in fp32 relative to
+// m, which moves only when the maximum has grown by 2^8.
+//
+// Work: see TokensPlan. A block is PAIR: 128 query rows, its key tiles dealt alternately
+// to two streams; else 256 rows, a stream for either half, both on every tile. Key tiles
+// past the last row's are not visited. A piece of a block that another CTA finishes
+// leaves its unnormalised O, m and l in the workspace for the join kernel below.
+//
+// Roles in a 384-thread CTA, one an SM:
+//   warp 0      one thread issues TMA loads of key and value tiles (128 rows, 128-byte
+//               swizzle) into one ring, in the order they are used;
+//   warp 1      issues tcgen05.mma: S = Q K^T from shared memory, then O += P V with P
+//               from TMEM and V as it lies in memory;
+//   warps 2, 3  mend tiles on their way: values that no row of the block sees, or some
+//               rows do not and that are not finite, become zeros (0 * NaN would spoil
+//               the sums); a cache's keys whose compaction is pending are re-rotated;
+//   warps 4..11 two softmax warpgroups, one per stream, a query row a thread. The next
+//               block's queries are loaded while the last products run, and its first
+//               logits computed while the outputs are written.
+// A value that is not finite, in a tile that some rows see in part, is added to the
+// output of the rows that see it at the end, from memory.
+// Every mbarrier wait is bounded; on expiry the CTA leaves NaN in its rows.
+#include "attend_tokens.cuh"
+#include "tcgen05.cuh"
+
+#include <algorithm>
+#include <atomic>
+
+namespace kvx {
+namespace {
+
+constexpr int kT = 128;                // query rows of a stream, keys of a tile
+constexpr int kThreads = 384;
+constexpr int kTmem = 512;
+constexpr float kNegInf = -__builtin_huge_valf();
+// As in attend_prefix.cu: how far (log2) a weight may exceed the first maximum's, and
+// that maximum's own weight.
+constexpr float kLazy = 8.f;
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
+constexpr float kFar = 0x1p23f;        // base-2 logits from here on are whole numbers
+// What the start of a block costs, in tiles of half a block.
+constexpr int kStartTiles = 2;
+constexpr int kMarks = 8;              // more segments than the ring can hold tiles of, at once
+
+template <int D, bool PAIR>
+struct Geo {
+  static constexpr int KH = D / 64;              // 128-byte halves of a row
+  static constexpr int HALFB = kT * 128;         // one half tile, 16 KB
+  static constexpr int TILEB = KH * HALFB;
+  static constexpr int STAGES = (PAIR ? 160 : 128) * 1024 / TILEB;
+  static constexpr int CW = PAIR ? 32 : 64;      // output columns staged at a time
+  static constexpr int Q = 0, RING = (PAIR ? 1 : 2) * TILEB, STAGE = RING + STAGES * TILEB;
+  static constexpr int ML = STAGE + 8 * 32 * CW * 2;   // PAIR: the streams' maxima and sums
+  static constexpr int BARS = ML + (PAIR ? 2 * kT * 8 : 0);
+  static constexpr int NBARS = 3 * STAGES + 11;
+  static constexpr int SMEM = BARS + NBARS * 8 + 16 + kMarks * 4 + 1024;   // slack to align to 1024 bytes
+};
+
+// TMA coordinates of a row tensor: which of the map's dimensions 1..3 is which.
+struct Coords {
+  int row, h, b;           // their places, 0..2
+  int hm, bm;              // 0 where all heads (sequences) share the rows
+};
+struct MapArgs {
+  Coords k, v, kn, vn;
+};
+
+struct Params {
+  TokensArgs a;
+  TokensPlan plan;
+  MapArgs at;
+  float* part_o;           // [slot][D/4][block_rows] float4
+  float2* part_ml;         // [slot][block_rows]
+  TokensAt* first;         // [ctas + 1]
+  int* err;
+  int stall;
+};
+
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, const Coords& c, int d, int row, int h,
+                                              int b, uint32_t bar) {
+  h *= c.hm;
+  b *= c.bm;
+  const int x0 = c.row == 0 ? row : c.h == 0 ? h : b;
+  const int x1 = c.row == 1 ? row : c.h == 1 ? h : b;
+  const int x2 = c.row == 2 ? row : c.h == 2 ? h : b;
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(x0), "r"(x1), "r"(x2), "r"(bar)
+      : "memory");
+}
+
+// ---------------------------------------------------------------- the work
+struct Seq {
+  int tok0, nq, n, ta;     // first token (packed), tokens, own rows, tiles of own rows
+};
+__device__ __forceinline__ Seq load_seq(const TokensArgs& a, int b) {
+  Seq s;
+  s.tok0 = 0;
+  s.nq = a.S;
+  if (a.starts) {
+    s.tok0 = max(0, min(a.starts[b], a.S));
+    s.nq = max(0, min(a.starts[b + 1], a.S) - s.tok0);
+  } else if (a.new_lens) {
+    s.nq = max(0, min(a.new_lens[b], a.S));
+  }
+  s.n = a.lens ? max(0, min(a.lens[b], a.n)) : a.n;
+  s.ta = (s.n + (a.pend ? 1 : 0) + kT - 1) / kT;     // an evicted row may still be in place
+  return s;
+}
+
+// Costs of one key head's half blocks (PAIR: blocks) of a sequence: j costs base + j / N
+// for causal tokens (rows 128 j .. are tokens up to (128 j + 127) / N, which see 1 + j / N
+// tiles), base alone for a tree or where all are to count the same.
+struct Cost {
+  int64_t base, N;         // N = 0: base alone
+  int halves;
+  __device__ __forceinline__ Cost(const TokensArgs& a, const TokensPlan& p, const Seq& s) {
+    const int n = a.G / a.H;
+    const int64_t rows = (int64_t)s.nq * n;
+    halves = p.pair ? (int)((rows + kT - 1) / kT) : 2 * (int)((rows + 2 * kT - 1) / (2 * kT));
+    base = p.even ? 1 : 1 + s.ta + kStartTiles;
+    N = p.even || a.parents ? 0 : n;
+  }
+  __device__ __forceinline__ int64_t before(int64_t j) const {   // of 0 .. j - 1
+    if (!N) return j * base;
+    const int64_t q = (unsigned)j / (unsigned)N, r = j - q * N;
+    return j * base + N * (q * (q - 1) / 2) + q * r;
+  }
+  __device__ __forceinline__ int64_t head() const { return before(halves); }
+  // The last j with before(j) <= y, 0 <= y < head().
+  __device__ __forceinline__ int find(int64_t y) const {
+    int64_t j;
+    if (!N) {
+      j = y / base;
+    } else {
+      const float b = (float)base - 0.5f, n = (float)N;
+      j = (int64_t)(n * (sqrtf(b * b + 2.f * (float)y / n) - b));
+    }
+    j = max((int64_t)0, min(j, (int64_t)halves - 1));
+    while (j > 0 && before(j) > y) --j;
+    while (j < halves - 1 && before(j + 1) <= y) ++j;
+    return (int)j;
+  }
+};
+
+// Tiles that the first `rows` query rows of a sequence visit.
+__device__ __forceinline__ int tiles_of(const TokensArgs& a, const Seq& s, int rows) {
+  const int N = a.G / a.H;
+  const int keys = a.parents ? s.nq : min(s.nq, (rows + N - 1) / N);
+  return s.ta + (keys + kT - 1) / kT;
+}
+__device__ __forceinline__ int block_tiles(const TokensArgs& a, const TokensPlan& p, const Seq& s, int i) {
+  return tiles_of(a, s, min(s.nq * (a.G / a.H), (i + 1) * p.block_rows));
+}
+
+// Start of the range that begins at cost y of sequence b, which is in it.
+__device__ __forceinline__ TokensAt locate(const TokensArgs& a, const TokensPlan& p, int b, int64_t y) {
+  const Seq s = load_seq(a, b);
+  const Cost c(a, p, s);
+  TokensAt at;
+  at.b = b;
+  at.h = (int)(y / c.head());
+  y -= at.h * c.head();
+  const int per = p.pair ? 1 : 2;
+  at.i = c.find(y) / per;
+  at.k = 0;
+  if (!p.whole) {
+    const int64_t c0 = c.before((int64_t)at.i * per), c1 = c.before((int64_t)(at.i + 1) * per);
+    at.k = (int)((y - c0) * block_tiles(a, p, s, at.i) / (c1 - c0));
+  }
+  return at;
+}
+
+// The range of this CTA, [ends_s[0], ends_s[1]); all threads, with barriers.
+__device__ __forceinline__ void find_range(const TokensArgs& a, const TokensPlan& p, int64_t* sums_s, TokensAt* ends_s) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int share = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(a.B, tid * share), b1 = min(a.B, b0 + share);
+  int64_t own = 0;
+  for (int b = b0; b < b1; ++b) own += a.H * Cost(a, p, load_seq(a, b)).head();
+  int64_t to = own;                                  // of this and lower lanes
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t x = __shfl_up_sync(~0u, to, d);
+    if (lane >= d) to += x;
+  }
+  if (lane == 31) sums_s[warp] = to;
+  if (tid < 2) ends_s[tid] = TokensAt{a.B, 0, 0, 0};
+  __syncthreads();
+  int64_t total = 0, from = to - own;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) from += sums_s[w];
+    total += sums_s[w];
+  }
+  for (int e = 0; e < 2; ++e) {
+    const int64_t x = (blockIdx.x + e) * total / p.ctas;
+    if (x < from || x >= from + own) continue;
+    int64_t y = x - from;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t seq = a.H * Cost(a, p, load_seq(a, b)).head();
+      if (y < seq) {
+        ends_s[e] = locate(a, p, b, y);
+        break;
+      }
+      y -= seq;
+    }
+  }
+  __syncthreads();
+}
+
+// A block's tiles k0 .. k1 - 1.
+struct Seg {
+  int b, h, i, k0, k1;
+  int e;                   // the evicted row still in place, or -1
+  int n;                   // own rows as they lie, that one included
+  bool whole;
+  Seq s;
+};
+
+// The walk over a CTA's range, the same in every role (warp-collective).
+struct Walk {
+  TokensAt at, end;
+  int loaded;
+  Seq s;
+  __device__ __forceinline__ Walk(const TokensAt* ends) : at(ends[0]), end(ends[1]), loaded(-1) {}
+  __device__ __forceinline__ bool next(const TokensArgs& a, const TokensPlan& p, Seg& g) {
+    while (true) {
+      if (at.b > end.b || (at.b == end.b && (at.h > end.h || (at.h == end.h && (at.i > end.i || (at.i == end.i && at.k >= end.k))))))
+        return false;
+      if (at.b != loaded) {
+        s = load_seq(a, at.b);
+        loaded = at.b;
+      }
+      const int rows = s.nq * (a.G / a.H);
+      if (rows == 0) {                               // on to the next sequence that has tokens
+        const int lane = threadIdx.x & 31;
+        const bool some = at.b + 1 + lane >= a.B || load_seq(a, at.b + 1 + lane).nq > 0;
+        const unsigned found = __ballot_sync(~0u, some);
+        at = TokensAt{at.b + (found ? __ffs(found) : 32), 0, 0, 0};
+        if (at.b >= a.B) return false;
+        continue;
+      }
+      const int tiles = block_tiles(a, p, s, at.i);
+      g.b = at.b;
+      g.h = at.h;
+      g.i = at.i;
+      g.k0 = at.k;
+      g.k1 = at.b == end.b && at.h == end.h && at.i == end.i ? end.k : tiles;
+      g.whole = g.k0 == 0 && g.k1 == tiles;
+      g.s = s;
+      g.e = a.pend ? a.pend[at.b * a.H + at.h] : -1;
+      g.n = s.n + (g.e >= 0);
+      at.k = g.k1;
+      if (g.k1 == tiles) {
+        at.k = 0;
+        if ((int64_t)++at.i * p.block_rows >= rows) {
+          at.i = 0;
+          if (++at.h == a.H) {
+            at.h = 0;
+            ++at.b;
+          }
+        }
+      }
+      return true;
+    }
+  }
+};
+
+// What a stream (w) does in a segment: its tiles, the segment's first.
+template <bool PAIR>
+__device__ __forceinline__ int stream_tiles(const TokensArgs& a, const Seg& g, int w) {
+  if (PAIR) return g.k1 - g.k0;
+  const int rows = g.s.nq * (a.G / a.H), lo = (2 * g.i + w) * kT;
+  if (lo >= rows) return 0;
+  return max(0, min(g.k1, tiles_of(a, g.s, min(rows, lo + kT))) - g.k0);
+}
+
+// Which tiles the helper warps mend before they are used.
+struct Mend {
+  int left;                // rows from here on are not there
+  int gap;                 // nor is this one, if 0 .. 127
+  bool scan;               // some rows of the block do not see all of the others
+  bool values, keys;       // what is to be mended
+};
+__device__ __forceinline__ Mend mend_of(const TokensArgs& a, const Seg& g, int block_rows, int kt) {
+  Mend m;
+  m.gap = -1;
+  m.scan = m.keys = false;
+  if (kt < g.s.ta) {
+    m.left = g.n - kt * kT;
+    if (g.e >= 0) {
+      m.gap = g.e - kt * kT;
+      m.keys = m.gap < kT - 1;                       // rows after it await their re-rotation
+    }
+    // rows behind the tensor's last are zeros already
+    m.values = (m.left < kT && (a.lens || a.pend)) || (m.gap >= 0 && m.gap < kT);
+  } else {
+    const int k = (kt - g.s.ta) * kT;
+    m.left = g.s.nq - k;
+    m.scan = a.parents || k + kT > (int)((unsigned)(g.i * block_rows) / (unsigned)(a.G / a.H)) + 1;
+    m.values = m.scan;
+  }
+  return m;
+}
+
+// Bits of any 16-bit float in a word whose exponent is all ones: NaN or infinity.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return std::is_same<T, __half>::value ? ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u
+                                        : ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t drop_not_finite(uint32_t w) {
+  const uint32_t f = not_finite<T>(w);
+  return (f & 0x8000u ? 0u : w & 0xFFFFu) | (f & 0x80000000u ? 0u : w & 0xFFFF0000u);
+}
+
+// Ancestors of the tokens lane and lane + 32 of sequence b, themselves included, as
+// bits (warp-collective): powers of two of the step to the parent.
+__device__ __forceinline__ void ancestors(const TokensArgs& a, int b, int nq, uint64_t (&m)[2]) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* parents = a.parents + b * a.parents_stride;
+  int p[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int t = lane + 32 * x;
+    p[x] = t < nq ? parents[t] : -1;
+    if (p[x] >= t) p[x] = -1;                        // not before it: none
+    m[x] = 1ull << t;
+  }
+#pragma unroll 1
+  for (int step = 1; step < 64; step *= 2) {
+    uint64_t um[2];
+    int up[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint64_t m0 = __shfl_sync(~0u, m[0], p[x] & 31), m1 = __shfl_sync(~0u, m[1], p[x] & 31);
+      const int p0 = __shfl_sync(~0u, p[0], p[x] & 31), p1 = __shfl_sync(~0u, p[1], p[x] & 31);
+      um[x] = p[x] < 0 ? m[x] : m[x] | (p[x] < 32 ? m0 : m1);
+      up[x] = p[x] < 0 ? -1 : p[x] < 32 ? p0 : p1;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      m[x] = um[x];
+      p[x] = up[x];
+    }
+  }
+}
+
+// The low `left` of 32 bits.
+__device__ __forceinline__ uint32_t low_bits(int left) { return left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u; }
+
+template <typename T, int D, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tokens_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                         const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
+                         const __grid_constant__ Params p) {
+  using Gm = Geo<D, PAIR>;
+  constexpr int NS = Gm::STAGES;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* smem = smem_raw + (base - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Gm::BARS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Gm::BARS + Gm::NBARS * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* marks = reinterpret_cast<volatile int*>(tmem_slot + 4);   // segments with values that are not finite
+  auto full = [&](int s) { return smem_addr(&bars[s]); };
+  auto empty = [&](int s) { return smem_addr(&bars[NS + s]); };
+  auto mended = [&](int s) { return smem_addr(&bars[2 * NS + s]); };
+  auto s_full = [&](int w) { return smem_addr(&bars[3 * NS + w]); };
+  auto o_done = [&](int w) { return smem_addr(&bars[3 * NS + 2 + w]); };
+  auto q_full = [&](int w) { return smem_addr(&bars[3 * NS + 4 + w]); };
+  auto p_full = [&](int w, int c) { return smem_addr(&bars[3 * NS + 6 + 2 * w + c]); };   // halves of 64 keys
+  const uint32_t drain = smem_addr(&bars[3 * NS + 10]);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const TokensArgs& a = p.a;
+  const int N = a.G / a.H;
+
+  launch_dependents();
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 3);          // the products, and either helper warp
+      mbar_init(mended(s), 2);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(s_full(w), 1);
+      mbar_init(o_done(w), 1);
+      mbar_init(q_full(w), PAIR ? 8 : 4);
+      mbar_init(p_full(w, 0), 4);
+      mbar_init(p_full(w, 1), 4);
+    }
+    mbar_init(drain, 1);               // abort path only
+    fence_mbar_init();
+    *abort_flag = 0;
+    for (int i = 0; i < kMarks; ++i) marks[i] = 0;
+  }
+  if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kTmem);
+  __shared__ int64_t sums_s[kThreads / 32];
+  __shared__ TokensAt ends_s[2];
+  find_range(a, p.plan, sums_s, ends_s);
+  if (tid == 0 && !p.plan.whole) {
+    p.first[blockIdx.x] = ends_s[0];
+    if (blockIdx.x == gridDim.x - 1) p.first[gridDim.x] = ends_s[1];
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // TMEM columns: O of stream w at 128 w, S (and P over it) at 256 + 128 w
+  auto tm_o = [&](int w) { return tmem + (uint32_t)(kT * w); };
+  auto tm_s = [&](int w) { return tmem + (uint32_t)(2 * kT + kT * w); };
+
+  Walk walk(ends_s);
+  Seg g;
+  // The launch's 384 x 168 registers, shared out anew: 4 warps of 120 and 8 of
+  // 192 a thread, so that a softmax thread holds a row's 128 logits.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      int s = 0, held = 0;               // next stage, stages in flight (at most NS)
+      uint32_t phase = 0;
+      bool ok = true, stall = p.stall && blockIdx.x == 0;   // test hook: CTA 0's first tile never comes
+      while (ok && walk.next(a, p.plan, g)) {
+        if (lane == 0) {
+          const int n = g.k1 - g.k0;
+          auto load = [&](bool value, int i) {
+            if (held == NS && !wait_or_abort(empty(s), phase ^ 1, abort_flag, p.err)) return false;
+            if (!stall) {
+              mbar_expect_tx(full(s), Gm::TILEB);
+              const int kt = g.k0 + i;
+              const bool own = kt < g.s.ta;
+              const CUtensorMap* map = value ? (own ? &vmap : &vnmap) : (own ? &kmap : &knmap);
+              const Coords& c = value ? (own ? p.at.v : p.at.vn) : (own ? p.at.k : p.at.kn);
+              const int row = own ? kt * kT : g.s.tok0 + (kt - g.s.ta) * kT;
+              for (int kh = 0; kh < Gm::KH; ++kh)
+                tma_load_rows(base + Gm::RING + s * Gm::TILEB + kh * Gm::HALFB, map, c, kh * 64, row, g.h, g.b, full(s));
+            }
+            stall = false;
+            held = min(held + 1, NS);
+            if (++s == NS) s = 0, phase ^= 1;
+            return true;
+          };
+          for (int i = 0; i < n && ok; ++i) {
+            if (i == 0) {
+              ok = load(false, 0);
+              if (PAIR && ok && n > 1) ok = load(false, 1);
+            }
+            ok = ok && load(true, i);
+            const int nk = PAIR ? i + 2 : i + 1;
+            if (ok && nk < n) ok = load(false, nk);
+          }
+        }
+        ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+      }
+      if (lane == 0 && *abort_flag)      // let copies in flight land before the CTA leaves
+        for (int i = 0; i < held; ++i) {
+          if (--s < 0) s = NS - 1, phase ^= 1;
+          (void)mbar_wait_bounded(full(s), phase, 10000000ull);
+        }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t kIdS = f16_idesc<T>(kT, false), kIdO = f16_idesc<T>(D, true);
+      // descriptors of the first query block and ring stage; an offset adds to the
+      // address field, in 16-byte units
+      const uint64_t qd = sw128_desc(base + Gm::Q), kd = sw128_desc(base + Gm::RING);
+      const uint64_t vd = sw128_mn_desc(base + Gm::RING, Gm::HALFB);
+      int next = 0;                      // ring stage and its phase
+      uint32_t phase = 0, mends = 0;     // mends: the mended stages' phases
+      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // weights tiles and query blocks consumed, per stream
+      bool ok = true;
+      while (ok && walk.next(a, p.plan, g)) {
+        const int n = g.k1 - g.k0;
+        auto tile = [&](bool value, int i) -> int {   // the next ring stage, once its tile is there; -1 on abort
+          const int s = next;
+          const Mend m = mend_of(a, g, p.plan.block_rows, g.k0 + i);
+          bool here;
+          if (value ? m.values : m.keys) {
+            here = wait_or_abort(mended(s), (mends >> s) & 1, abort_flag, p.err);
+            mends ^= 1u << s;
+          } else {
+            here = wait_or_abort(full(s), phase, abort_flag, p.err);
+          }
+          if (++next == NS) next = 0, phase ^= 1;
+          here = __all_sync(~0u, here);
+          tc_fence_after();
+          return here ? s : -1;
+        };
+        auto mma_s = [&](int w, int s) {
+          if (elect_one()) {
+            const uint64_t qa = qd + (uint64_t)((PAIR ? 0 : w) * (Gm::TILEB >> 4)), kb = kd + (uint64_t)(s * (Gm::TILEB >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)(((kk >> 2) * Gm::HALFB + (kk & 3) * 32) >> 4);
+              tc_mma_ss(tm_s(w), qa + off, kb + off, kIdS, kk > 0);
+            }
+            tc_commit(s_full(w));
+          }
+        };
+        auto commit = [&](uint32_t bar) {
+          if (elect_one()) tc_commit(bar);
+        };
+        // O_w += P_w V: P of keys 0..63 in S's columns 0..31, of keys 64..127 in
+        // 64..95, the second parts (PAIR) 32 columns on
+        auto mma_o = [&](int w, int s, bool first) {
+          const uint64_t vb = vd + (uint64_t)(s * (Gm::TILEB >> 4));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (!__all_sync(~0u, wait_or_abort(p_full(w, c), np[w] & 1, abort_flag, p.err))) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int part = 0; part < (PAIR ? 2 : 1); ++part)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_ts(tm_o(w), tm_s(w) + (uint32_t)(c * 64 + kk * 8 + 32 * part),
+                            vb + (uint64_t)((4 * c + kk) * (2048 >> 4)), kIdO, !(first && c + kk + part == 0));
+            }
+          }
+          ++np[w];
+          return true;
+        };
+        auto queries = [&](int w) {
+          const bool here = __all_sync(~0u, wait_or_abort(q_full(w), nq[w] & 1, abort_flag, p.err));
+          ++nq[w];
+          tc_fence_after();
+          return here;
+        };
+        int s;
+        if (PAIR) {
+          if (!(ok = queries(0))) break;
+          for (int i = 0; i < min(n, 2) && ok; ++i) {
+            ok = (s = tile(false, i)) >= 0;
+            if (ok) mma_s(i, s), commit(empty(s));
+          }
+          for (int i = 0; i < n && ok; ++i) {
+            const int w = i & 1;
+            if (!(ok = (s = tile(true, i)) >= 0)) break;
+            if (!(ok = mma_o(w, s, i < 2))) break;
+            commit(empty(s));
+            if (i + 2 >= n) commit(o_done(w));
+            if (i + 2 < n) {
+              if (!(ok = (s = tile(false, i + 2)) >= 0)) break;
+              mma_s(w, s);
+              commit(empty(s));
+            }
+          }
+        } else {
+          const int n0 = stream_tiles<PAIR>(a, g, 0), n1 = stream_tiles<PAIR>(a, g, 1);
+          if (!(ok = (s = tile(false, 0)) >= 0)) break;
+          if (n0 > 0) {
+            if (!(ok = queries(0))) break;
+            mma_s(0, s);
+          }
+          if (n1 > 0) {
+            if (!(ok = queries(1))) break;
+            mma_s(1, s);
+          }
+          commit(empty(s));
+          for (int i = 0; i < n && ok; ++i) {
+            const bool more = i + 1 < n;
+            int sk = 0;
+            if (!(ok = (s = tile(true, i)) >= 0)) break;
+            if (i < n0 && !(ok = mma_o(0, s, i == 0))) break;
+            if (more) {
+              if (!(ok = (sk = tile(false, i + 1)) >= 0)) break;
+              if (i + 1 < n0) mma_s(0, sk);
+            }
+            if (i == n0 - 1) commit(o_done(0));
+            if (i < n1 && !(ok = mma_o(1, s, i == 0))) break;
+            commit(empty(s));
+            if (more) {
+              if (i + 1 < n1) mma_s(1, sk);
+              commit(empty(sk));
+            }
+            if (i == n1 - 1) commit(o_done(1));
+          }
+        }
+      }
+    } else {
+      // ---------------------------------------------------------------- tile mending
+      const int ht = (warp - 2) * 32 + lane;         // of 64 threads
+      int next = 0, seg = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      // re-rotation: a thread has one 16-byte piece of a row's first half and its pair
+      constexpr int PC = D / 16, PER = 64 / PC;      // pieces, rows at a time
+      const int pc = ht % PC, pr = ht / PC;
+      auto piece = [&](int s, int r, int c) {
+        return reinterpret_cast<uint4*>(smem + Gm::RING + s * Gm::TILEB + (c >> 3) * Gm::HALFB + r * 128 + (((c ^ r) & 7) << 4));
+      };
+      while (ok && walk.next(a, p.plan, g)) {
+        ++seg;
+        const int n = g.k1 - g.k0;
+        auto visit = [&](bool value, int i) {
+          const int s = next;
+          const uint32_t ph = phase;
+          if (++next == NS) next = 0, phase ^= 1;
+          const Mend m = mend_of(a, g, p.plan.block_rows, g.k0 + i);
+          // (every tile is waited for, and given back: a phase's parity alone does not
+          // tell a tile from the one two rounds of the ring before it)
+          if (!__all_sync(~0u, wait_or_abort(full(s), ph, abort_flag, p.err))) return false;
+          if (!(value ? m.values : m.keys)) {
+            if (lane == 0) mbar_arrive(empty(s));
+            return true;
+          }
+          if (!value) {
+            if constexpr (std::is_same<T, __half>::value) {   // (a handle's rows)
+              for (int r = max(0, m.gap + 1) + pr; r < min(kT, m.left); r += PER)
+                rotate_back(*piece(s, r, pc), *piece(s, r, pc + PC), a.rope_c + 8 * pc, a.rope_s + 8 * pc);
+            }
+          } else {
+            const int left = max(0, min(kT, m.left));
+            for (int x = ht; x < (kT - left) * (D / 8); x += 64)
+              *piece(s, left + x / (D / 8), x % (D / 8)) = make_uint4(0, 0, 0, 0);
+            if (m.gap >= 0 && m.gap < kT && ht < D / 8) *piece(s, m.gap, ht) = make_uint4(0, 0, 0, 0);
+            if (m.scan) {
+              uint32_t found = 0;
+#pragma unroll 4
+              for (int x = ht; x < left * (D / 8); x += 64) {
+                const uint4 v = *piece(s, x / (D / 8), x % (D / 8));
+                found |= not_finite<T>(v.x) | not_finite<T>(v.y) | not_finite<T>(v.z) | not_finite<T>(v.w);
+              }
+              if (__any_sync(~0u, found != 0)) {
+                for (int x = ht; x < left * (D / 8); x += 64) {
+                  uint4* at = piece(s, x / (D / 8), x % (D / 8));
+                  const uint4 v = *at;
+                  *at = make_uint4(drop_not_finite<T>(v.x), drop_not_finite<T>(v.y), drop_not_finite<T>(v.z),
+                                   drop_not_finite<T>(v.w));
+                }
+                marks[seg % kMarks] = seg;
+              }
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(mended(s));
+            mbar_arrive(empty(s));
+          }
+          return true;
+        };
+        for (int i = 0; i < n && ok; ++i) {
+          if (i == 0) {
+            ok = visit(false, 0);
+            if (PAIR && ok && n > 1) ok = visit(false, 1);
+          }
+          ok = ok && visit(true, i);
+          const int nk = PAIR ? i + 2 : i + 1;
+          if (ok && nk < n) ok = visit(false, nk);
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax warpgroups
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int w = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;          // query row of the stream = TMEM lane
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t ns = 0, no = 0;                         // logits tiles and finished outputs seen
+    int seg = 0;
+    bool ok = true;
+    // The warp's 32 rows of the query block, as TMA would swizzle them; PAIR: each
+    // warpgroup has half of every row's pieces. Between global and shared memory
+    // neighbouring lanes move neighbouring pieces of a row.
+    constexpr int CPR = PAIR ? D / 16 : D / 8;       // 16-byte pieces of a row
+    unsigned char* const mine = smem + Gm::Q + (PAIR ? 0 : w) * Gm::TILEB;
+    // this thread's row of a segment: its token, its query head, whether it is there
+    auto place = [&](const Seg& g, int& t, int& head) {
+      const int r = g.i * p.plan.block_rows + (PAIR ? 0 : w * kT) + row, rows = g.s.nq * N, x = min(r, rows - 1);
+      t = (int)((unsigned)x / (unsigned)N);
+      head = g.h * N + x - t * N;
+      return r < rows;
+    };
+    uint4 qv[CPR];
+    auto load_queries = [&](const Seg& g) {
+      int t, head;
+      const bool valid = place(g, t, head);
+      const T* const q = static_cast<const T*>(a.q);
+      const int64_t offset = g.b * a.q_stride[0] + (int64_t)(g.s.tok0 + t) * a.q_stride[1] + head * a.q_stride[2];
+#pragma unroll
+      for (int i = 0; i < CPR; ++i) {
+        const int from = i * (32 / CPR) + lane / CPR, c = (PAIR ? w * CPR : 0) + lane % CPR;
+        const int64_t at = __shfl_sync(~0u, offset, from);
+        const bool on = __shfl_sync(~0u, (int)valid, from);
+        qv[i] = on ? *reinterpret_cast<const uint4*>(q + at + 8 * c) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto store_queries = [&] {
+#pragma unroll
+      for (int i = 0; i < CPR; ++i) {
+        const int r = (warp & 3) * 32 + i * (32 / CPR) + lane / CPR, c = (PAIR ? w * CPR : 0) + lane % CPR;
+        *reinterpret_cast<uint4*>(mine + r * 128 + (c >> 3) * Gm::HALFB + (((c ^ r) & 7) << 4)) = qv[i];
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(PAIR ? 0 : w));
+    };
+    bool some = walk.next(a, p.plan, g);
+    if (some && stream_tiles<PAIR>(a, g, w) > 0) {
+      load_queries(g);
+      store_queries();
+    }
+    while (some) {
+      ++seg;
+      const int n = stream_tiles<PAIR>(a, g, w);
+      int t, head;
+      const bool valid = place(g, t, head);
+      float m = kNegInf, l = 0.f;
+      bool begun = false;
+      const uint32_t ts = tm_s(w) + lanes, to = tm_o(w) + lanes;
+      for (int i = PAIR ? w : 0; i < n && ok; i += PAIR ? 2 : 1) {
+        ok = __all_sync(~0u, wait_or_abort(s_full(w), ns & 1, abort_flag, p.err));
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        // which of the tile's keys the row sees
+        const int kt = g.k0 + i;
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        bool partial;
+        if (kt < g.s.ta) {
+          const int left = g.n - kt * kT, gap = g.e - kt * kT;
+          const bool hole = g.e >= 0 && gap >= 0 && gap < kT;
+          partial = left < kT || hole;
+          if (partial) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x) & ~(hole && (gap >> 5) == x ? 1u << (gap & 31) : 0u);
+          }
+        } else if (a.parents) {
+          uint64_t anc[2];
+          ancestors(a, g.b, g.s.nq, anc);
+          const uint64_t m0 = __shfl_sync(~0u, anc[0], t & 31), m1 = __shfl_sync(~0u, anc[1], t & 31), mm = t < 32 ? m0 : m1;
+          partial = true;
+          see[0] = (uint32_t)mm;
+          see[1] = (uint32_t)(mm >> 32);
+          see[2] = see[3] = 0u;
+        } else {
+          const int left = t + 1 - (kt - g.s.ta) * kT;
+          partial = __any_sync(~0u, left < kT);
+          if (partial) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x);
+          }
+        }
+        const bool none = (see[0] | see[1] | see[2] | see[3]) == 0u;
+        float v[kT];
+        tmem_ld128(ts, v);
+        if (partial) {
+#pragma unroll
+          for (int e = 0; e < kT; ++e) v[e] = (see[e >> 5] >> (e & 31)) & 1u ? v[e] : kNegInf;
+        }
+        // (a NaN stays in the maximum, so that one compare finds logits that are not finite)
+        float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int e = 4; e < kT; e += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            m4[x] = e + 4 < kT ? max_nan(m4[x], max_nan(v[e + x], v[e + 4 + x])) : max_nan(m4[x], v[e + x]);
+        const float mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])) * a.scale2;
+        // Rare: logits of NaN or +-inf, and a maximum so large that it is rounded by a half
+        // or more, as its own logit need not be near it in the fused product and
+        // difference below.
+        const bool odd = !none && !(fabsf(mx) < kFar), up = mx > m + (kLazy + kLift<T>);
+        float nb = m == kNegInf ? 0.f : -m;          // masked: every weight 2^-inf = 0
+        if (__any_sync(~0u, up || odd)) {
+          const float nm = odd ? fmaxf(m, mx) : up ? mx - kLift<T> : m, f = nm == m ? 1.f : ex2(m - nm);
+          m = nm;
+          l *= f;
+          if (begun) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float x[16];
+              uint32_t o[16];
+              tmem_ld16(to + 16 * c, x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(x[e] * f);
+              tmem_st16(to + 16 * c, o);
+            }
+          }
+          nb = m == kNegInf ? 0.f : -m;
+          if (__builtin_expect(__any_sync(~0u, odd), 0)) {
+            // the difference, of a product rounded as the maximum was, goes through the
+            // fused product instead (in such rows alone: no row's bits depend on its neighbours)
+            const float inv = 1.f / a.scale2;
+#pragma unroll 1
+            for (int c = 0; c < kT / 16; ++c) {
+              float x[16];
+              uint32_t o[16];
+              const uint32_t bits = (c < 2 ? see[0] : c < 4 ? see[1] : c < 6 ? see[2] : see[3]) >> (16 * (c & 1));
+              tmem_ld16(ts + 16 * c, x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = __float_as_uint(!((bits >> e) & 1u) ? kNegInf
+                                       : odd ? __fadd_rn(__fmul_rn(x[e], a.scale2), nb) * inv : x[e]);
+              tmem_st16(ts + 16 * c, o);
+            }
+            tmem_st_wait();
+            tmem_ld128(ts, v);
+            if (odd) nb = 0.f;
+          }
+        }
+        begun = true;
+        const float2 sc2 = make_float2(a.scale2, a.scale2), nb2 = make_float2(nb, nb);
+        float2 l4[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) l4[x] = make_float2(0.f, 0.f);
+        // 64 keys at a time: the tensor cores start on the first half's weights
+        // while the second half's are computed
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const int k = 64 * c + 32 * h + e;
+              const float2 x = ffma2(make_float2(v[k], v[k + 1]), sc2, nb2);
+              const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+              l4[(e >> 1) & 3] = fadd2(l4[(e >> 1) & 3], pp);
+              hi[e / 2] = pack16<T>(pp.x, pp.y);
+              if (PAIR) {
+                const float2 back = unpack16<T>(hi[e / 2]);
+                lo[e / 2] = pack16<T>(pp.x - back.x, pp.y - back.y);
+              }
+            }
+            tmem_st16(ts + 64 * c + 16 * h, hi);
+            if (PAIR) tmem_st16(ts + 64 * c + 32 + 16 * h, lo);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(w, c));
+        }
+        l4[0] = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
+        l += l4[0].x + l4[0].y;
+      }
+      // The next block's queries, on their way while the last products run. Their place
+      // is free once this stream (PAIR: both) has seen its last logits.
+      Seg ng;
+      some = walk.next(a, p.plan, ng);
+      const bool feed = some && stream_tiles<PAIR>(a, ng, w) > 0;
+      if (feed) load_queries(ng);
+      if (!PAIR && feed) store_queries();
+      if (begun && ok) {
+        ok = __all_sync(~0u, wait_or_abort(o_done(w), no & 1, abort_flag, p.err));
+        ++no;
+        tc_fence_after();
+      }
+      float f0 = 1.f, f1 = 0.f;
+      if (!ok) l = __int_as_float(0x7FFFFFFF);       // NaN: this row's result is lost
+      if (PAIR) {
+        // the two streams' maxima and sums meet in shared memory, their O in the
+        // registers of whichever warpgroup writes the columns: a warp of either
+        // reaches the same TMEM lanes
+        float2* ml = reinterpret_cast<float2*>(smem + Gm::ML);
+        ml[w * kT + row] = make_float2(m, l);
+        tc_fence_before();
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        tc_fence_after();
+        if (feed) store_queries();
+        const float2 x = ml[row], y = ml[kT + row];
+        m = fmaxf(x.x, y.x);
+        f0 = x.x == m ? 1.f : ex2(x.x - m);
+        f1 = y.x == m ? 1.f : ex2(y.x - m);
+        l = x.y * f0 + y.y * f1;
+      }
+      const bool poisoned = marks[seg % kMarks] == seg;
+      auto columns = [&](int c, float (&v)[32]) {    // O's columns 32 c .. + 31 of this row
+        const uint32_t at = tmem + lanes + 32 * c;
+        if (n == 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        } else if (!PAIR) {
+          tmem_ld32(at + kT * w, v);
+        } else {
+          tmem_ld32(at, v);
+          if (n > 1) {
+            float y[32];
+            tmem_ld32(at + kT, y);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(y[e], f1, v[e] * f0);
+          }
+        }
+        if (__builtin_expect(poisoned, 0)) {
+          // values that are not finite, dropped from the tiles that rows see in part
+          uint64_t anc[2] = {0, 0};
+          uint64_t seen = 0;
+          if (a.parents) {
+            ancestors(a, g.b, g.s.nq, anc);
+            const uint64_t m0 = __shfl_sync(~0u, anc[0], t & 31), m1 = __shfl_sync(~0u, anc[1], t & 31);
+            seen = t < 32 ? m0 : m1;
+          }
+          for (int kt = max(g.k0, g.s.ta); kt < g.k1; ++kt) {
+            if (!mend_of(a, g, p.plan.block_rows, kt).scan) continue;
+            const int j0 = (kt - g.s.ta) * kT;
+            for (int j = j0; j < min(j0 + kT, t + 1); ++j) {
+              if (a.parents && !((seen >> j) & 1)) continue;
+              const T* src = static_cast<const T*>(a.v_new) + g.b * a.vn_stride[0] + (int64_t)(g.s.tok0 + j) * a.vn_stride[1] +
+                             g.h * a.vn_stride[2] + 32 * c;
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const uint32_t word = *reinterpret_cast<const uint32_t*>(src + e), f = not_finite<T>(word);
+                const float2 x = unpack16<T>(word);
+                if (f & 0x8000u) v[e] += x.x;
+                if (f & 0x80000000u) v[e + 1] += x.y;
+              }
+            }
+          }
+        }
+      };
+      constexpr int CC = PAIR ? D / 64 : D / 32;     // groups of 32 columns
+      if (g.whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        constexpr int CW = Gm::CW, PR = CW / 8;      // columns at a time; their 16-byte pieces
+        unsigned char* const stage = smem + Gm::STAGE + (warp - 4) * (32 * CW * 2);
+        auto staged = [&](int r, int c) {
+          return reinterpret_cast<uint4*>(stage + r * (CW * 2) + (((PR == 8 ? c ^ r : c ^ (r >> 1)) & (PR - 1)) << 4));
+        };
+        T* const out = static_cast<T*>(a.out);
+        const int64_t offset = g.b * a.out_stride[0] + (int64_t)(g.s.tok0 + t) * a.out_stride[1] + head * a.out_stride[2];
+#pragma unroll 1
+        for (int i = 0; i < CC; i += CW / 32) {
+          const int c0 = (PAIR ? w * CC : 0) + i;
+#pragma unroll
+          for (int x = 0; x < CW / 32; ++x) {
+            float v[32];
+            columns(c0 + x, v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *staged(lane, 4 * x + e / 8) =
+                  make_uint4(pack16<T>(v[e] * inv, v[e + 1] * inv), pack16<T>(v[e + 2] * inv, v[e + 3] * inv),
+                             pack16<T>(v[e + 4] * inv, v[e + 5] * inv), pack16<T>(v[e + 6] * inv, v[e + 7] * inv));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < PR; ++x) {
+            const int from = x * (32 / PR) + lane / PR, c = lane % PR;
+            const int64_t at = __shfl_sync(~0u, offset, from);
+            const bool on = __shfl_sync(~0u, (int)valid, from);
+            if (on) *reinterpret_cast<uint4*>(out + at + 32 * c0 + 8 * c) = *staged(from, c);
+          }
+          __syncwarp();
+        }
+        if (valid && a.lse && !(PAIR && w))
+          a.lse[((int64_t)(a.starts ? g.s.tok0 : (int64_t)g.b * a.S) + t) * a.G + head] =
+              l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+      } else {
+        const int64_t slot = 2 * blockIdx.x + (g.k0 == 0);
+        const int R = p.plan.block_rows, rr = (PAIR ? 0 : w * kT) + row;
+        float4* o = reinterpret_cast<float4*>(p.part_o) + slot * (R * (D / 4)) + rr;
+#pragma unroll 1
+        for (int i = 0; i < CC; ++i) {
+          const int c = (PAIR ? w * CC : 0) + i;
+          float v[32];
+          columns(c, v);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) o[(int64_t)(8 * c + e / 4) * R] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+        if (!(PAIR && w)) p.part_ml[slot * R + rr] = make_float2(m, l);
+      }
+      tc_fence_before();
+      // (PAIR: either warpgroup reads both accumulators, and the maxima)
+      if (PAIR) asm volatile("bar.sync 3, 256;" ::: "memory");
+      g = ng;
+    }
+  }
+
+  // -------------------------------------------------------------------- teardown
+  __syncthreads();
+  if (*abort_flag && tid == 32) {
+    // let any MMA still in flight finish before the accumulators are freed
+    tc_commit(drain);
+    (void)mbar_wait_bounded(drain, 0, 10000000ull);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+// Joins the parts of cut blocks: grid (boundary between CTAs, 32 rows of the block, 32
+// columns), where the first boundary inside a block takes it. A lane is a row, a warp
+// four columns; the parts are few.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) tokens_join_kernel(const __grid_constant__ Params p) {
+  const TokensArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = p.plan.block_rows;
+  const int rr = blockIdx.y * 32 + lane, d4 = blockIdx.z * 8 + warp, c0 = blockIdx.x;
+  wait_for_primary();                        // in every block: this kernel ends after the one before it
+  const TokensAt x = p.first[c0 + 1], y = p.first[c0];
+  auto same = [&](const TokensAt& o) { return o.b == x.b && o.h == x.h && o.i == x.i; };
+  if (x.b >= a.B || x.k == 0 || (same(y) && y.k > 0)) return;
+  // a range that begins where the next one does is empty and has left no part
+  float m = kNegInf, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  TokensAt at = y, to = x;
+  for (int c = c0;; ++c) {
+    if (c > c0) {
+      at = to;
+      if (c == p.plan.ctas || !same(at)) break;
+      to = p.first[c + 1];
+    }
+    if (same(to) && to.k <= at.k && c > c0) continue;
+    const int64_t slot = 2 * c + (c == c0);
+    const float2 ml = p.part_ml[slot * R + rr];
+    const float4 v = reinterpret_cast<const float4*>(p.part_o)[slot * (R * (D / 4)) + (int64_t)d4 * R + rr];
+    const float nm = fmaxf(m, ml.x), f = m == nm ? 1.f : ex2(m - nm), h = ml.x == nm ? 1.f : ex2(ml.x - nm);
+    m = nm;
+    l = l * f + ml.y * h;
+    o = make_float4(o.x * f + v.x * h, o.y * f + v.y * h, o.z * f + v.z * h, o.w * f + v.w * h);
+  }
+  const Seq s = load_seq(a, x.b);
+  const int N = a.G / a.H, r = x.i * R + rr;
+  if (r >= s.nq * N) return;
+  const int t = r / N, head = x.h * N + r - t * N;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* dst = static_cast<T*>(a.out) + x.b * a.out_stride[0] + (int64_t)(s.tok0 + t) * a.out_stride[1] + head * a.out_stride[2] + 4 * d4;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * inv, o.y * inv), pack16<T>(o.z * inv, o.w * inv));
+  if (d4 == 0 && a.lse)
+    a.lse[((int64_t)(a.starts ? s.tok0 : (int64_t)x.b * a.S) + t) * a.G + head] =
+        l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+template <typename Elem, int Dim, bool Pair>
+struct Kind {
+  using T = Elem;
+  static constexpr int D = Dim, SMEM = Geo<Dim, Pair>::SMEM;
+  static constexpr auto kernel = attend_tokens_kernel<Elem, Dim, Pair>;
+};
+template <typename F>
+auto pick(int D, int dtype, bool pair, F&& f) {
+  if (dtype == kBf16) {
+    if (D == 64) return pair ? f(Kind<__nv_bfloat16, 64, true>{}) : f(Kind<__nv_bfloat16, 64, false>{});
+    return pair ? f(Kind<__nv_bfloat16, 128, true>{}) : f(Kind<__nv_bfloat16, 128, false>{});
+  }
+  if (D == 64) return pair ? f(Kind<__half, 64, true>{}) : f(Kind<__half, 64, false>{});
+  return pair ? f(Kind<__half, 128, true>{}) : f(Kind<__half, 128, false>{});
+}
+
+// Rows as a 4-D tensor, the dimensions in the order of their strides (one that all
+// share, or of a single entry, last and of extent 1); boxes of 64 elements (128 bytes) x
+// 128 rows; rows past the last read as zeros.
+bool encode_rows(CUtensorMap* map, const TokensRows& r, int D, int dtype, Coords* c) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  struct Dim {
+    int64_t stride, extent;
+    int what;                // 0 rows, 1 heads, 2 sequences
+  } d[3] = {{r.rows == 1 ? D : r.stride[2], r.rows, 0}, {r.stride[1], r.H, 1}, {r.stride[0], r.B, 2}};
+  c->hm = r.H > 1 && r.stride[1] != 0;
+  c->bm = r.B > 1 && r.stride[0] != 0;
+  if (!c->hm) d[1].extent = 1;
+  if (!c->bm) d[2].extent = 1;
+  int64_t top = d[0].stride;
+  for (int i = 1; i < 3; ++i)
+    if (d[i].extent > 1) top = std::max(top, d[i].stride);
+  for (int i = 1; i < 3; ++i)
+    if (d[i].extent == 1) d[i].stride = top;
+  std::stable_sort(d, d + 3, [](const Dim& x, const Dim& y) {
+    return (x.extent == 1 && x.what) != (y.extent == 1 && y.what) ? !(x.extent == 1 && x.what) : x.stride < y.stride;
+  });
+  cuuint64_t dims[4] = {(cuuint64_t)D}, strides[3];
+  cuuint32_t box[4] = {64, 1, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = (cuuint64_t)d[i].extent;
+    strides[i] = (cuuint64_t)d[i].stride * 2;
+    (d[i].what == 0 ? c->row : d[i].what == 1 ? c->h : c->b) = i;
+    if (d[i].what == 0) box[i + 1] = kT;
+  }
+  return enc(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(r.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+TokensPlan tokens_plan(int B, int64_t rows, int64_t blocks, int H, int64_t tiles, int sms) {
+  TokensPlan pl{};
+  pl.pair = rows <= kT;
+  pl.block_rows = pl.pair ? kT : 2 * kT;
+  const int64_t units = blocks * H;
+  // Few short blocks: one a CTA, no join.
+  pl.whole = pl.even = units <= sms && tiles <= 6;
+  pl.ctas = (int)std::min<int64_t>(sms, pl.whole ? units : units * tiles);
+  return pl;
+}
+
+bool tokens_kernel_ready(int D, int dtype, bool pair, int device) {
+  if (!encode_fn()) return false;
+  return pick(D, dtype, pair, [&](auto kind) {
+    using K = decltype(kind);
+    // The kernel's redistribution of registers needs the 168 a thread that its
+    // launch bound gives it: checked, as it would wait forever with fewer.
+    static std::atomic<uint64_t> ready{0};   // devices on which that, and its shared memory, are settled
+    const uint64_t bit = 1ull << device;
+    if (ready.load(std::memory_order_relaxed) & bit) return true;
+    cudaFuncAttributes f;
+    if (cudaFuncGetAttributes(&f, K::kernel) != cudaSuccess || f.numRegs != 168 ||
+        cudaFuncSetAttribute(K::kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    ready.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+  });
+}
+
+cudaError_t launch_attend_tokens(const TokensLaunch& l, int D, int dtype, cudaStream_t s) {
+  Params p{};
+  p.a = l.a;
+  p.plan = l.plan;
+  p.err = l.err;
+  p.stall = l.stall;
+  if (!l.plan.whole) {
+    char* space = static_cast<char*>(l.workspace);
+    p.part_o = reinterpret_cast<float*>(space);
+    p.part_ml = reinterpret_cast<float2*>(space + l.plan.o_bytes(D));
+    p.first = reinterpret_cast<TokensAt*>(space + l.plan.o_bytes(D) + l.plan.ml_bytes());
+  }
+  CUtensorMap kmap{}, vmap{}, knmap{}, vnmap{};
+  if (!encode_rows(&knmap, l.k_new, D, dtype, &p.at.kn) || !encode_rows(&vnmap, l.v_new, D, dtype, &p.at.vn))
+    return cudaErrorInvalidValue;
+  if (l.a.n + (l.a.pend ? 1 : 0) > 0 &&
+      (!encode_rows(&kmap, l.k, D, dtype, &p.at.k) || !encode_rows(&vmap, l.v, D, dtype, &p.at.v)))
+    return cudaErrorInvalidValue;
+  return pick(D, dtype, l.plan.pair, [&](auto kind) {
+    using K = decltype(kind);
+    K::kernel<<<l.plan.ctas, kThreads, K::SMEM, s>>>(kmap, vmap, knmap, vnmap, p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || l.plan.whole || l.plan.ctas < 2) return e;
+    const dim3 grid(l.plan.ctas - 1, l.plan.block_rows / 32, K::D / 32);
+    return launch_after(tokens_join_kernel<typename K::T, K::D>, grid, 256, 0, 1, true, s, p);
+  });
+}
+
+}  // namespace kvx
