@@ -143,7 +143,8 @@ _ATTENTION = struct.Struct("=8i f i 12Q 18q Q")
 _TOKENS = struct.Struct("=8i f i 12Q 19q Q")
 _JOIN = struct.Struct("=8i 18Q 27q")
 _U64 = struct.Struct("=Q")
-_WORKSPACE_AT = 40 + 11 * 8              # offset in kvevict_attention and kvevict_tokens (workspace_bytes is the last)
+_WORKSPACE_AT, _WORKSPACE_BYTES_AT = 40 + 11 * 8, _ATTENTION.size - 8    # offsets in kvevict_attention
+_TOKENS_BYTES_AT = _TOKENS.size - 8      # in kvevict_tokens, whose workspace is at the same offset
 _NO3, _NO4 = (0, 0, 0), (0, 0, 0, 0)     # strides of tensors that are not there
 
 
@@ -307,16 +308,18 @@ def _attention(q, out, k, v, lens, k_new, v_new, prefix_k, prefix_v, prefix_lens
         spv[0], spv[1], 0), s
 
 
-def _with_workspace(args, cache, q, stream, size=None):
+def _with_workspace(args, cache, q, stream, tokens=False):
     """The same call with the workspace it needs, taken from torch's allocator for its stream, and that tensor."""
     torch, need = _torch(), ctypes.c_size_t(0)
-    _check((size or lib().kvevict_attend_workspace)(args, cache, ctypes.addressof(need)))
+    size, end = (lib().kvevict_attend_tokens_workspace, _TOKENS_BYTES_AT) if tokens else \
+        (lib().kvevict_attend_workspace, _WORKSPACE_BYTES_AT)
+    _check(size(args, cache, ctypes.addressof(need)))
     if stream == torch._C._cuda_getCurrentRawStream(q.get_device()):
         space = torch.empty(need.value, dtype=torch.uint8, device=q.device)
     else:
         with torch.cuda.stream(torch.cuda.ExternalStream(stream or 0)):
             space = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    return b"".join((args[:_WORKSPACE_AT], _U64.pack(space.data_ptr()), args[_WORKSPACE_AT + 8:-8],
+    return b"".join((args[:_WORKSPACE_AT], _U64.pack(space.data_ptr()), args[_WORKSPACE_AT + 8:end],
                      _U64.pack(need.value))), space
 
 
@@ -406,7 +409,7 @@ def _call_tokens(call, cache, q, args, stream):
     """Makes a call that takes a ``kvevict_tokens``, with a workspace where it needs one."""
     rc = call(args, stream)
     if rc == ERR_WORKSPACE:
-        args, space = _with_workspace(args, cache, q, stream, lib().kvevict_attend_tokens_workspace)
+        args, space = _with_workspace(args, cache, q, stream, True)
         rc = call(args, stream)
     if rc:
         _check(rc)
