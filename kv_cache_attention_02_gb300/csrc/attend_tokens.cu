@@ -17,8 +17,9 @@
 // leaves its unnormalised O, m and l in the workspace for the join kernel below.
 //
 // Roles in a 384-thread CTA, one an SM:
-//   warp 0      one thread issues TMA loads of key and value tiles (128 rows, 128-byte
-//               swizzle) into one ring, in the order they are used;
+//   warp 0      walks the CTA's range and tells the others (Seg); one thread issues TMA
+//               loads of key and value tiles (128 rows, 128-byte swizzle) into one ring,
+//               in the order they are used;
 //   warp 1      issues tcgen05.mma: S = Q K^T from shared memory, then O += P V with P
 //               from TMEM and V as it lies in memory;
 //   warps 2, 3  mend tiles on their way: values that no row of the block sees, or some
@@ -51,21 +52,6 @@ constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 constexpr float kFar = 0x1p23f;        // base-2 logits from here on are whole numbers
 // What the start of a block costs, in tiles of half a block.
 constexpr int kStartTiles = 2;
-constexpr int kMarks = 8;              // more segments than the ring can hold tiles of, at once
-
-template <int D, bool PAIR>
-struct Geo {
-  static constexpr int KH = D / 64;              // 128-byte halves of a row
-  static constexpr int HALFB = kT * 128;         // one half tile, 16 KB
-  static constexpr int TILEB = KH * HALFB;
-  static constexpr int STAGES = (PAIR ? 160 : 128) * 1024 / TILEB;
-  static constexpr int CW = PAIR ? 32 : 64;      // output columns staged at a time
-  static constexpr int Q = 0, RING = (PAIR ? 1 : 2) * TILEB, STAGE = RING + STAGES * TILEB;
-  static constexpr int ML = STAGE + 8 * 32 * CW * 2;   // PAIR: the streams' maxima and sums
-  static constexpr int BARS = ML + (PAIR ? 2 * kT * 8 : 0);
-  static constexpr int NBARS = 3 * STAGES + 11;
-  static constexpr int SMEM = BARS + NBARS * 8 + 16 + kMarks * 4 + 1024;   // slack to align to 1024 bytes
-};
 
 // TMA coordinates of a row tensor: which of the map's dimensions 1..3 is which.
 struct Coords {
@@ -219,16 +205,26 @@ __device__ __forceinline__ void find_range(const TokensArgs& a, const TokensPlan
   __syncthreads();
 }
 
-// A block's tiles k0 .. k1 - 1.
+// A block's tiles k0 .. k1 - 1, as the producer finds them and the other roles read them
+// in shared memory (tiles counted from k0). Kept there, none of it stands in the softmax
+// threads' registers.
 struct Seg {
-  int b, h, i, k0, k1;
-  int e;                   // the evicted row still in place, or -1
-  int n;                   // own rows as they lie, that one included
-  bool whole;
-  Seq s;
+  int n[2];                // tiles that the first and the second half's rows visit (PAIR: all)
+  int tiles;               // k1 - k0
+  int own, first;          // the first of them: of own rows, from row `first` on
+  int left;                // own rows from the first tile on
+  int gap;                 // the evicted row still in place, so too; or -1
+  int part, hole;          // the own tile that ends inside, and that with the evicted row; or -1
+  int turn;                // the first own tile with keys that await their re-rotation
+  int mask;                // the first tile of the tokens' that some rows see in part
+  int kb;                  // what a tile's index is short of its place among the tokens'
+  int b, h, tok0, nq, row0;
+  int whole, from_start;   // all of the block's tiles; its first
 };
+constexpr int kSegs = 8;                 // more than the ring can hold tiles of, at once
+constexpr int kNever = 0x7FFFFFFF;
 
-// The walk over a CTA's range, the same in every role (warp-collective).
+// The walk over a CTA's range (warp-collective).
 struct Walk {
   TokensAt at, end;
   int loaded;
@@ -242,7 +238,7 @@ struct Walk {
         s = load_seq(a, at.b);
         loaded = at.b;
       }
-      const int rows = s.nq * (a.G / a.H);
+      const int N = a.G / a.H, rows = s.nq * N;
       if (rows == 0) {                               // on to the next sequence that has tokens
         const int lane = threadIdx.x & 31;
         const bool some = at.b + 1 + lane >= a.B || load_seq(a, at.b + 1 + lane).nq > 0;
@@ -251,18 +247,32 @@ struct Walk {
         if (at.b >= a.B) return false;
         continue;
       }
-      const int tiles = block_tiles(a, p, s, at.i);
+      const int all = block_tiles(a, p, s, at.i), k0 = at.k;
+      const int k1 = at.b == end.b && at.h == end.h && at.i == end.i ? end.k : all;
+      const int e = a.pend ? a.pend[at.b * a.H + at.h] : -1, n = s.n + (e >= 0);
+      g.tiles = k1 - k0;
+      g.row0 = at.i * p.block_rows;
+      for (int w = 0; w < 2; ++w) {
+        const int lo = g.row0 + w * kT;
+        g.n[w] = p.pair ? g.tiles : lo >= rows ? 0 : max(0, min(k1, tiles_of(a, s, min(rows, lo + kT))) - k0);
+      }
+      g.own = max(0, min(s.ta - k0, g.tiles));
+      g.first = k0 * kT;
+      g.left = n - k0 * kT;
+      g.part = n < s.ta * kT && s.ta > k0 && s.ta <= k1 ? s.ta - 1 - k0 : -1;
+      g.gap = e < 0 ? -1 : e - k0 * kT;
+      g.hole = e >= 0 && g.gap >= 0 && g.gap < g.own * kT ? g.gap / kT : -1;
+      g.turn = e < 0 ? kNever : max(0, g.gap + 1) / kT;
+      g.kb = k0 - s.ta;
+      g.mask = a.parents ? g.own : max(g.own, (int)((unsigned)(g.row0 / N + 1) / kT) - g.kb);
       g.b = at.b;
       g.h = at.h;
-      g.i = at.i;
-      g.k0 = at.k;
-      g.k1 = at.b == end.b && at.h == end.h && at.i == end.i ? end.k : tiles;
-      g.whole = g.k0 == 0 && g.k1 == tiles;
-      g.s = s;
-      g.e = a.pend ? a.pend[at.b * a.H + at.h] : -1;
-      g.n = s.n + (g.e >= 0);
-      at.k = g.k1;
-      if (g.k1 == tiles) {
+      g.tok0 = s.tok0;
+      g.nq = s.nq;
+      g.whole = k0 == 0 && k1 == all;
+      g.from_start = k0 == 0;
+      at.k = k1;
+      if (k1 == all) {
         at.k = 0;
         if ((int64_t)++at.i * p.block_rows >= rows) {
           at.i = 0;
@@ -277,41 +287,27 @@ struct Walk {
   }
 };
 
-// What a stream (w) does in a segment: its tiles, the segment's first.
-template <bool PAIR>
-__device__ __forceinline__ int stream_tiles(const TokensArgs& a, const Seg& g, int w) {
-  if (PAIR) return g.k1 - g.k0;
-  const int rows = g.s.nq * (a.G / a.H), lo = (2 * g.i + w) * kT;
-  if (lo >= rows) return 0;
-  return max(0, min(g.k1, tiles_of(a, g.s, min(rows, lo + kT))) - g.k0);
-}
-
-// Which tiles the helper warps mend before they are used.
-struct Mend {
-  int left;                // rows from here on are not there
-  int gap;                 // nor is this one, if 0 .. 127
-  bool scan;               // some rows of the block do not see all of the others
-  bool values, keys;       // what is to be mended
+template <int D, bool PAIR>
+struct Geo {
+  static constexpr int KH = D / 64;              // 128-byte halves of a row
+  static constexpr int HALFB = kT * 128;         // one half tile, 16 KB
+  static constexpr int TILEB = KH * HALFB;
+  static constexpr int STAGES = (PAIR ? 160 : 128) * 1024 / TILEB;
+  static constexpr int CW = PAIR ? 32 : 64;      // output columns staged at a time
+  static constexpr int Q = 0, RING = (PAIR ? 1 : 2) * TILEB, STAGE = RING + STAGES * TILEB;
+  static constexpr int ML = STAGE + 8 * 32 * CW * 2;   // PAIR: the streams' maxima and sums
+  static constexpr int BARS = ML + (PAIR ? 2 * kT * 8 : 0);
+  static constexpr int NBARS = 3 * STAGES + 11 + 2 * kSegs;
+  static constexpr int SEGS = BARS + NBARS * 8 + 16 + kSegs * 4;
+  static constexpr int SMEM = SEGS + kSegs * (int)sizeof(Seg) + 1024;   // slack to align to 1024 bytes
 };
-__device__ __forceinline__ Mend mend_of(const TokensArgs& a, const Seg& g, int block_rows, int kt) {
-  Mend m;
-  m.gap = -1;
-  m.scan = m.keys = false;
-  if (kt < g.s.ta) {
-    m.left = g.n - kt * kT;
-    if (g.e >= 0) {
-      m.gap = g.e - kt * kT;
-      m.keys = m.gap < kT - 1;                       // rows after it await their re-rotation
-    }
-    // rows behind the tensor's last are zeros already
-    m.values = (m.left < kT && (a.lens || a.pend)) || (m.gap >= 0 && m.gap < kT);
-  } else {
-    const int k = (kt - g.s.ta) * kT;
-    m.left = g.s.nq - k;
-    m.scan = a.parents || k + kT > (int)((unsigned)(g.i * block_rows) / (unsigned)(a.G / a.H)) + 1;
-    m.values = m.scan;
-  }
-  return m;
+
+// Whether the helper warps mend a tile before it is used: values that are not there, or
+// that some rows do not see; keys that await their re-rotation.
+__device__ __forceinline__ bool mends(const TokensArgs& a, const Seg& g, bool value, int i) {
+  if (!value) return i >= g.turn && i < g.own;
+  // (rows behind the tensor's last are zeros already)
+  return i >= g.own ? i >= g.mask : i == g.hole || (i == g.part && (a.lens || a.pend));
 }
 
 // Bits of any 16-bit float in a word whose exponent is all ones: NaN or infinity.
@@ -384,6 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto q_full = [&](int w) { return smem_addr(&bars[3 * NS + 4 + w]); };
   auto p_full = [&](int w, int c) { return smem_addr(&bars[3 * NS + 6 + 2 * w + c]); };   // halves of 64 keys
   const uint32_t drain = smem_addr(&bars[3 * NS + 10]);
+  auto seg_full = [&](int i) { return smem_addr(&bars[3 * NS + 11 + i % kSegs]); };
+  auto seg_empty = [&](int i) { return smem_addr(&bars[3 * NS + 11 + kSegs + i % kSegs]); };
+  Seg* const segs = reinterpret_cast<Seg*>(smem + Gm::SEGS);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const TokensArgs& a = p.a;
@@ -403,10 +402,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full(w, 0), 4);
       mbar_init(p_full(w, 1), 4);
     }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(seg_full(i), 1);
+      mbar_init(seg_empty(i), 11);     // all warps but the producer's
+      marks[i] = -1;
+    }
     mbar_init(drain, 1);               // abort path only
     fence_mbar_init();
     *abort_flag = 0;
-    for (int i = 0; i < kMarks; ++i) marks[i] = 0;
   }
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kTmem);
   __shared__ int64_t sums_s[kThreads / 32];
@@ -424,8 +427,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tm_o = [&](int w) { return tmem + (uint32_t)(kT * w); };
   auto tm_s = [&](int w) { return tmem + (uint32_t)(2 * kT + kT * w); };
 
-  Walk walk(ends_s);
-  Seg g;
+  // The segments, in order: the producer finds one after the other; after the last comes
+  // one of no tiles. After a wait that ran out (ok is false) the roles still go through
+  // them, without work, so that the softmax warps come to every row.
+  int seg = 0;
+  bool ok = true;
+  auto take = [&]() -> const Seg* {      // the next one, or null
+    const uint32_t phase = (uint32_t)(seg / kSegs) & 1;
+    if (ok) ok = wait_or_abort(seg_full(seg), phase, abort_flag, p.err);
+    ok = __all_sync(~0u, ok);
+    if (!ok && !mbar_wait_bounded(seg_full(seg), phase)) return nullptr;
+    __syncwarp();
+    const Seg* g = &segs[seg % kSegs];
+    return g->tiles ? g : nullptr;
+  };
+  auto give = [&] {                      // it is not needed any more
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty(seg));
+    ++seg;
+  };
   // The launch's 384 x 168 registers, shared out anew: 4 warps of 120 and 8 of
   // 192 a thread, so that a softmax thread holds a row's 128 logits.
   if (warp < 4) {
@@ -434,19 +454,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- TMA producer
       int s = 0, held = 0;               // next stage, stages in flight (at most NS)
       uint32_t phase = 0;
-      bool ok = true, stall = p.stall && blockIdx.x == 0;   // test hook: CTA 0's first tile never comes
-      while (ok && walk.next(a, p.plan, g)) {
+      bool more = true, stall = p.stall && blockIdx.x == 0;   // test hook: CTA 0's first tile never comes
+      Walk walk(ends_s);
+      for (; more; ++seg) {
+        Seg g;
+        more = walk.next(a, p.plan, g);
+        if (!more) g.tiles = 0;
+        if (seg >= kSegs) {
+          const uint32_t free = (uint32_t)(seg / kSegs - 1) & 1;
+          if (ok) ok = wait_or_abort(seg_empty(seg), free, abort_flag, p.err);
+          ok = __all_sync(~0u, ok);
+          if (!ok && !__all_sync(~0u, mbar_wait_bounded(seg_empty(seg), free))) break;
+        }
         if (lane == 0) {
-          const int n = g.k1 - g.k0;
+          segs[seg % kSegs] = g;
+          mbar_arrive(seg_full(seg));
+        }
+        if (lane == 0 && ok) {
           auto load = [&](bool value, int i) {
             if (held == NS && !wait_or_abort(empty(s), phase ^ 1, abort_flag, p.err)) return false;
             if (!stall) {
               mbar_expect_tx(full(s), Gm::TILEB);
-              const int kt = g.k0 + i;
-              const bool own = kt < g.s.ta;
+              const bool own = i < g.own;
               const CUtensorMap* map = value ? (own ? &vmap : &vnmap) : (own ? &kmap : &knmap);
               const Coords& c = value ? (own ? p.at.v : p.at.vn) : (own ? p.at.k : p.at.kn);
-              const int row = own ? kt * kT : g.s.tok0 + (kt - g.s.ta) * kT;
+              const int row = own ? g.first + i * kT : g.tok0 + (g.kb + i) * kT;
               for (int kh = 0; kh < Gm::KH; ++kh)
                 tma_load_rows(base + Gm::RING + s * Gm::TILEB + kh * Gm::HALFB, map, c, kh * 64, row, g.h, g.b, full(s));
             }
@@ -455,14 +487,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++s == NS) s = 0, phase ^= 1;
             return true;
           };
-          for (int i = 0; i < n && ok; ++i) {
+          for (int i = 0; i < g.tiles && ok; ++i) {
             if (i == 0) {
               ok = load(false, 0);
-              if (PAIR && ok && n > 1) ok = load(false, 1);
+              if (PAIR && ok && g.tiles > 1) ok = load(false, 1);
             }
             ok = ok && load(true, i);
             const int nk = PAIR ? i + 2 : i + 1;
-            if (ok && nk < n) ok = load(false, nk);
+            if (ok && nk < g.tiles) ok = load(false, nk);
           }
         }
         ok = __shfl_sync(~0u, (int)ok, 0) != 0;
@@ -480,18 +512,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qd = sw128_desc(base + Gm::Q), kd = sw128_desc(base + Gm::RING);
       const uint64_t vd = sw128_mn_desc(base + Gm::RING, Gm::HALFB);
       int next = 0;                      // ring stage and its phase
-      uint32_t phase = 0, mends = 0;     // mends: the mended stages' phases
+      uint32_t phase = 0, mend_phase = 0;   // (of each stage, a bit)
       uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // weights tiles and query blocks consumed, per stream
-      bool ok = true;
-      while (ok && walk.next(a, p.plan, g)) {
-        const int n = g.k1 - g.k0;
+      for (const Seg* sg; (sg = take()); give()) {
+        if (!ok) continue;
+        const Seg& g = *sg;
+        const int n = g.tiles;
         auto tile = [&](bool value, int i) -> int {   // the next ring stage, once its tile is there; -1 on abort
           const int s = next;
-          const Mend m = mend_of(a, g, p.plan.block_rows, g.k0 + i);
           bool here;
-          if (value ? m.values : m.keys) {
-            here = wait_or_abort(mended(s), (mends >> s) & 1, abort_flag, p.err);
-            mends ^= 1u << s;
+          if (mends(a, g, value, i)) {
+            here = wait_or_abort(mended(s), (mend_phase >> s) & 1, abort_flag, p.err);
+            mend_phase ^= 1u << s;
           } else {
             here = wait_or_abort(full(s), phase, abort_flag, p.err);
           }
@@ -542,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int s;
         if (PAIR) {
-          if (!(ok = queries(0))) break;
+          if (!(ok = queries(0))) continue;
           for (int i = 0; i < min(n, 2) && ok; ++i) {
             ok = (s = tile(false, i)) >= 0;
             if (ok) mma_s(i, s), commit(empty(s));
@@ -560,14 +592,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          const int n0 = stream_tiles<PAIR>(a, g, 0), n1 = stream_tiles<PAIR>(a, g, 1);
-          if (!(ok = (s = tile(false, 0)) >= 0)) break;
+          const int n0 = g.n[0], n1 = g.n[1];
+          if (!(ok = (s = tile(false, 0)) >= 0)) continue;
           if (n0 > 0) {
-            if (!(ok = queries(0))) break;
+            if (!(ok = queries(0))) continue;
             mma_s(0, s);
           }
           if (n1 > 0) {
-            if (!(ok = queries(1))) break;
+            if (!(ok = queries(1))) continue;
             mma_s(1, s);
           }
           commit(empty(s));
@@ -594,41 +626,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ---------------------------------------------------------------- tile mending
       const int ht = (warp - 2) * 32 + lane;         // of 64 threads
-      int next = 0, seg = 0;
+      int next = 0;
       uint32_t phase = 0;
-      bool ok = true;
       // re-rotation: a thread has one 16-byte piece of a row's first half and its pair
       constexpr int PC = D / 16, PER = 64 / PC;      // pieces, rows at a time
       const int pc = ht % PC, pr = ht / PC;
       auto piece = [&](int s, int r, int c) {
         return reinterpret_cast<uint4*>(smem + Gm::RING + s * Gm::TILEB + (c >> 3) * Gm::HALFB + r * 128 + (((c ^ r) & 7) << 4));
       };
-      while (ok && walk.next(a, p.plan, g)) {
-        ++seg;
-        const int n = g.k1 - g.k0;
+      for (const Seg* sg; (sg = take()); give()) {
+        if (!ok) continue;
+        const Seg& g = *sg;
+        const int n = g.tiles;
         auto visit = [&](bool value, int i) {
           const int s = next;
           const uint32_t ph = phase;
           if (++next == NS) next = 0, phase ^= 1;
-          const Mend m = mend_of(a, g, p.plan.block_rows, g.k0 + i);
           // (every tile is waited for, and given back: a phase's parity alone does not
           // tell a tile from the one two rounds of the ring before it)
           if (!__all_sync(~0u, wait_or_abort(full(s), ph, abort_flag, p.err))) return false;
-          if (!(value ? m.values : m.keys)) {
+          if (!mends(a, g, value, i)) {
             if (lane == 0) mbar_arrive(empty(s));
             return true;
           }
+          const int left = max(0, min(kT, i < g.own ? g.left - i * kT : g.nq - (g.kb + i) * kT));
           if (!value) {
             if constexpr (std::is_same<T, __half>::value) {   // (a handle's rows)
-              for (int r = max(0, m.gap + 1) + pr; r < min(kT, m.left); r += PER)
+              for (int r = max(0, g.gap + 1 - i * kT) + pr; r < left; r += PER)
                 rotate_back(*piece(s, r, pc), *piece(s, r, pc + PC), a.rope_c + 8 * pc, a.rope_s + 8 * pc);
             }
           } else {
-            const int left = max(0, min(kT, m.left));
             for (int x = ht; x < (kT - left) * (D / 8); x += 64)
               *piece(s, left + x / (D / 8), x % (D / 8)) = make_uint4(0, 0, 0, 0);
-            if (m.gap >= 0 && m.gap < kT && ht < D / 8) *piece(s, m.gap, ht) = make_uint4(0, 0, 0, 0);
-            if (m.scan) {
+            if (i == g.hole && ht < D / 8) *piece(s, g.gap - i * kT, ht) = make_uint4(0, 0, 0, 0);
+            if (i >= g.own) {
               uint32_t found = 0;
 #pragma unroll 4
               for (int x = ht; x < left * (D / 8); x += 64) {
@@ -642,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   *at = make_uint4(drop_not_finite<T>(v.x), drop_not_finite<T>(v.y), drop_not_finite<T>(v.z),
                                    drop_not_finite<T>(v.w));
                 }
-                marks[seg % kMarks] = seg;
+                marks[seg % kSegs] = seg;
               }
             }
           }
@@ -672,8 +703,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;          // query row of the stream = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t ns = 0, no = 0;                         // logits tiles and finished outputs seen
-    int seg = 0;
-    bool ok = true;
     // The warp's 32 rows of the query block, as TMA would swizzle them; PAIR: each
     // warpgroup has half of every row's pieces. Between global and shared memory
     // neighbouring lanes move neighbouring pieces of a row.
@@ -681,17 +710,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* const mine = smem + Gm::Q + (PAIR ? 0 : w) * Gm::TILEB;
     // this thread's row of a segment: its token, its query head, whether it is there
     auto place = [&](const Seg& g, int& t, int& head) {
-      const int r = g.i * p.plan.block_rows + (PAIR ? 0 : w * kT) + row, rows = g.s.nq * N, x = min(r, rows - 1);
+      const int r = g.row0 + (PAIR ? 0 : w * kT) + row, rows = g.nq * N, x = min(r, rows - 1);
       t = (int)((unsigned)x / (unsigned)N);
       head = g.h * N + x - t * N;
       return r < rows;
+    };
+    // a tree: the tokens that token t sees, as bits (warp-collective)
+    auto seen_of = [&](const Seg& g, int t) {
+      uint64_t anc[2];
+      ancestors(a, g.b, g.nq, anc);
+      const uint64_t m0 = __shfl_sync(~0u, anc[0], t & 31), m1 = __shfl_sync(~0u, anc[1], t & 31);
+      return t < 32 ? m0 : m1;
     };
     uint4 qv[CPR];
     auto load_queries = [&](const Seg& g) {
       int t, head;
       const bool valid = place(g, t, head);
       const T* const q = static_cast<const T*>(a.q);
-      const int64_t offset = g.b * a.q_stride[0] + (int64_t)(g.s.tok0 + t) * a.q_stride[1] + head * a.q_stride[2];
+      const int64_t offset = g.b * a.q_stride[0] + (int64_t)(g.tok0 + t) * a.q_stride[1] + head * a.q_stride[2];
 #pragma unroll
       for (int i = 0; i < CPR; ++i) {
         const int from = i * (32 / CPR) + lane / CPR, c = (PAIR ? w * CPR : 0) + lane % CPR;
@@ -710,14 +746,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full(PAIR ? 0 : w));
     };
-    bool some = walk.next(a, p.plan, g);
-    if (some && stream_tiles<PAIR>(a, g, w) > 0) {
-      load_queries(g);
+    const Seg* sg = take();
+    if (sg && sg->n[w] > 0 && ok) {
+      load_queries(*sg);
       store_queries();
     }
-    while (some) {
-      ++seg;
-      const int n = stream_tiles<PAIR>(a, g, w);
+    while (sg) {
+      const Seg& g = *sg;
+      const int n = g.n[w];
       int t, head;
       const bool valid = place(g, t, head);
       float m = kNegInf, l = 0.f;
@@ -729,29 +765,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ns;
         tc_fence_after();
         // which of the tile's keys the row sees
-        const int kt = g.k0 + i;
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        bool partial;
-        if (kt < g.s.ta) {
-          const int left = g.n - kt * kT, gap = g.e - kt * kT;
-          const bool hole = g.e >= 0 && gap >= 0 && gap < kT;
-          partial = left < kT || hole;
-          if (partial) {
+        bool partial = i == g.part || i == g.hole;
+        if (partial) {
+          const int left = g.left - i * kT, gap = i == g.hole ? g.gap - i * kT : -1;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x) & ~(hole && (gap >> 5) == x ? 1u << (gap & 31) : 0u);
-          }
-        } else if (a.parents) {
-          uint64_t anc[2];
-          ancestors(a, g.b, g.s.nq, anc);
-          const uint64_t m0 = __shfl_sync(~0u, anc[0], t & 31), m1 = __shfl_sync(~0u, anc[1], t & 31), mm = t < 32 ? m0 : m1;
+          for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x) & ~((gap >> 5) == x ? 1u << (gap & 31) : 0u);
+        } else if (i >= g.mask) {
           partial = true;
-          see[0] = (uint32_t)mm;
-          see[1] = (uint32_t)(mm >> 32);
-          see[2] = see[3] = 0u;
-        } else {
-          const int left = t + 1 - (kt - g.s.ta) * kT;
-          partial = __any_sync(~0u, left < kT);
-          if (partial) {
+          if (a.parents) {
+            const uint64_t mm = seen_of(g, t);
+            see[0] = (uint32_t)mm;
+            see[1] = (uint32_t)(mm >> 32);
+            see[2] = see[3] = 0u;
+          } else {
+            const int left = t + 1 - (g.kb + i) * kT;
 #pragma unroll
             for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x);
           }
@@ -850,10 +878,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The next block's queries, on their way while the last products run. Their place
       // is free once this stream (PAIR: both) has seen its last logits.
-      Seg ng;
-      some = walk.next(a, p.plan, ng);
-      const bool feed = some && stream_tiles<PAIR>(a, ng, w) > 0;
-      if (feed) load_queries(ng);
+      ++seg;
+      const Seg* const ng = take();
+      --seg;
+      const bool feed = ng && ng->n[w] > 0 && ok;
+      if (feed) load_queries(*ng);
       if (!PAIR && feed) store_queries();
       if (begun && ok) {
         ok = __all_sync(~0u, wait_or_abort(o_done(w), no & 1, abort_flag, p.err));
@@ -878,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f1 = y.x == m ? 1.f : ex2(y.x - m);
         l = x.y * f0 + y.y * f1;
       }
-      const bool poisoned = marks[seg % kMarks] == seg;
+      const bool poisoned = marks[seg % kSegs] == seg;
       auto columns = [&](int c, float (&v)[32]) {    // O's columns 32 c .. + 31 of this row
         const uint32_t at = tmem + lanes + 32 * c;
         if (n == 0) {
@@ -897,19 +926,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (__builtin_expect(poisoned, 0)) {
           // values that are not finite, dropped from the tiles that rows see in part
-          uint64_t anc[2] = {0, 0};
-          uint64_t seen = 0;
-          if (a.parents) {
-            ancestors(a, g.b, g.s.nq, anc);
-            const uint64_t m0 = __shfl_sync(~0u, anc[0], t & 31), m1 = __shfl_sync(~0u, anc[1], t & 31);
-            seen = t < 32 ? m0 : m1;
-          }
-          for (int kt = max(g.k0, g.s.ta); kt < g.k1; ++kt) {
-            if (!mend_of(a, g, p.plan.block_rows, kt).scan) continue;
-            const int j0 = (kt - g.s.ta) * kT;
+          const uint64_t seen = a.parents ? seen_of(g, t) : 0;
+          for (int i = max(g.own, g.mask); i < g.tiles; ++i) {
+            const int j0 = (g.kb + i) * kT;
             for (int j = j0; j < min(j0 + kT, t + 1); ++j) {
               if (a.parents && !((seen >> j) & 1)) continue;
-              const T* src = static_cast<const T*>(a.v_new) + g.b * a.vn_stride[0] + (int64_t)(g.s.tok0 + j) * a.vn_stride[1] +
+              const T* src = static_cast<const T*>(a.v_new) + g.b * a.vn_stride[0] + (int64_t)(g.tok0 + j) * a.vn_stride[1] +
                              g.h * a.vn_stride[2] + 32 * c;
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -931,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return reinterpret_cast<uint4*>(stage + r * (CW * 2) + (((PR == 8 ? c ^ r : c ^ (r >> 1)) & (PR - 1)) << 4));
         };
         T* const out = static_cast<T*>(a.out);
-        const int64_t offset = g.b * a.out_stride[0] + (int64_t)(g.s.tok0 + t) * a.out_stride[1] + head * a.out_stride[2];
+        const int64_t offset = g.b * a.out_stride[0] + (int64_t)(g.tok0 + t) * a.out_stride[1] + head * a.out_stride[2];
 #pragma unroll 1
         for (int i = 0; i < CC; i += CW / 32) {
           const int c0 = (PAIR ? w * CC : 0) + i;
@@ -956,10 +978,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (valid && a.lse && !(PAIR && w))
-          a.lse[((int64_t)(a.starts ? g.s.tok0 : (int64_t)g.b * a.S) + t) * a.G + head] =
+          a.lse[((a.starts ? (int64_t)g.tok0 : (int64_t)g.b * a.S) + t) * a.G + head] =
               l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
       } else {
-        const int64_t slot = 2 * blockIdx.x + (g.k0 == 0);
+        const int64_t slot = 2 * blockIdx.x + g.from_start;
         const int R = p.plan.block_rows, rr = (PAIR ? 0 : w * kT) + row;
         float4* o = reinterpret_cast<float4*>(p.part_o) + slot * (R * (D / 4)) + rr;
 #pragma unroll 1
@@ -975,7 +997,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       // (PAIR: either warpgroup reads both accumulators, and the maxima)
       if (PAIR) asm volatile("bar.sync 3, 256;" ::: "memory");
-      g = ng;
+      give();
+      sg = ng;
     }
   }
 
@@ -1032,7 +1055,7 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(const __grid_constant_
   T* dst = static_cast<T*>(a.out) + x.b * a.out_stride[0] + (int64_t)(s.tok0 + t) * a.out_stride[1] + head * a.out_stride[2] + 4 * d4;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * inv, o.y * inv), pack16<T>(o.z * inv, o.w * inv));
   if (d4 == 0 && a.lse)
-    a.lse[((int64_t)(a.starts ? s.tok0 : (int64_t)x.b * a.S) + t) * a.G + head] =
+    a.lse[((a.starts ? (int64_t)s.tok0 : (int64_t)x.b * a.S) + t) * a.G + head] =
         l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
