@@ -22,12 +22,12 @@
 //               in the order they are used;
 //   warp 1      issues tcgen05.mma: S = Q K^T from shared memory, then O += P V with P
 //               from TMEM and V as it lies in memory;
-//   warps 2, 3  mend tiles on their way: values that no row of the block sees, or some
+//   warps 2, 3  load the query rows, the next block's as soon as the last logits of this
+//               one are done; mend tiles on their way: values that no row of the block sees, or some
 //               rows do not and that are not finite, become zeros (0 * NaN would spoil
 //               the sums); a cache's keys whose compaction is pending are re-rotated;
 //   warps 4..11 two softmax warpgroups, one per stream, a query row a thread. The next
-//               block's queries are loaded while the last products run, and its first
-//               logits computed while the outputs are written.
+//               block's first logits are computed while the outputs are written.
 // A value that is not finite, in a tile that some rows see in part, is added to the
 // output of the rows that see it at the end, from memory.
 // Every mbarrier wait is bounded; on expiry the CTA leaves NaN in its rows.
@@ -292,15 +292,27 @@ struct Geo {
   static constexpr int KH = D / 64;              // 128-byte halves of a row
   static constexpr int HALFB = kT * 128;         // one half tile, 16 KB
   static constexpr int TILEB = KH * HALFB;
-  static constexpr int STAGES = (PAIR ? 160 : 128) * 1024 / TILEB;
+  static constexpr int STAGES = 128 * 1024 / TILEB;
   static constexpr int CW = PAIR ? 32 : 64;      // output columns staged at a time
-  static constexpr int Q = 0, RING = (PAIR ? 1 : 2) * TILEB, STAGE = RING + STAGES * TILEB;
+  static constexpr int Q = 0, RING = 2 * TILEB, STAGE = RING + STAGES * TILEB;   // (PAIR: segments take turns with Q)
   static constexpr int ML = STAGE + 8 * 32 * CW * 2;   // PAIR: the streams' maxima and sums
   static constexpr int BARS = ML + (PAIR ? 2 * kT * 8 : 0);
-  static constexpr int NBARS = 3 * STAGES + 11 + 2 * kSegs;
+  static constexpr int NBARS = 3 * STAGES + 13 + 2 * kSegs;
   static constexpr int SEGS = BARS + NBARS * 8 + 16 + kSegs * 4;
   static constexpr int SMEM = SEGS + kSegs * (int)sizeof(Seg) + 1024;   // slack to align to 1024 bytes
 };
+
+// The order in which a segment's key and value tiles are used, n of each: K0 V0 K1 V1 ..;
+// PAIR, whose streams have a tile each under way, K0 K1 V0 K2 V1 ..
+template <bool PAIR>
+__device__ __forceinline__ int tile_at(int j, int n, bool& value) {
+  if (!PAIR) {
+    value = j & 1;
+    return j >> 1;
+  }
+  value = j == 2 * n - 1 || (j && !(j & 1));
+  return j == 2 * n - 1 ? n - 1 : value ? j / 2 - 1 : (j + 1) / 2;
+}
 
 // Whether the helper warps mend a tile before it is used: values that are not there, or
 // that some rows do not see; keys that await their re-rotation.
@@ -377,11 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto mended = [&](int s) { return smem_addr(&bars[2 * NS + s]); };
   auto s_full = [&](int w) { return smem_addr(&bars[3 * NS + w]); };
   auto o_done = [&](int w) { return smem_addr(&bars[3 * NS + 2 + w]); };
-  auto q_full = [&](int w) { return smem_addr(&bars[3 * NS + 4 + w]); };
+  // query blocks: of a stream; PAIR: of every other segment
+  auto q_full = [&](int x) { return smem_addr(&bars[3 * NS + 4 + x]); };
   auto p_full = [&](int w, int c) { return smem_addr(&bars[3 * NS + 6 + 2 * w + c]); };   // halves of 64 keys
-  const uint32_t drain = smem_addr(&bars[3 * NS + 10]);
-  auto seg_full = [&](int i) { return smem_addr(&bars[3 * NS + 11 + i % kSegs]); };
-  auto seg_empty = [&](int i) { return smem_addr(&bars[3 * NS + 11 + kSegs + i % kSegs]); };
+  auto q_free = [&](int x) { return smem_addr(&bars[3 * NS + 10 + x]); };
+  const uint32_t drain = smem_addr(&bars[3 * NS + 12]);
+  auto seg_full = [&](int i) { return smem_addr(&bars[3 * NS + 13 + i % kSegs]); };
+  auto seg_empty = [&](int i) { return smem_addr(&bars[3 * NS + 13 + kSegs + i % kSegs]); };
   Seg* const segs = reinterpret_cast<Seg*>(smem + Gm::SEGS);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -398,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full(w), 1);
       mbar_init(o_done(w), 1);
-      mbar_init(q_full(w), PAIR ? 8 : 4);
+      mbar_init(q_full(w), 2);
+      mbar_init(q_free(w), 1);
       mbar_init(p_full(w, 0), 4);
       mbar_init(p_full(w, 1), 4);
     }
@@ -487,14 +502,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++s == NS) s = 0, phase ^= 1;
             return true;
           };
-          for (int i = 0; i < g.tiles && ok; ++i) {
-            if (i == 0) {
-              ok = load(false, 0);
-              if (PAIR && ok && g.tiles > 1) ok = load(false, 1);
-            }
-            ok = ok && load(true, i);
-            const int nk = PAIR ? i + 2 : i + 1;
-            if (ok && nk < g.tiles) ok = load(false, nk);
+#pragma unroll 1
+          for (int j = 0; j < 2 * g.tiles && ok; ++j) {
+            bool value;
+            const int i = tile_at<PAIR>(j, g.tiles, value);
+            ok = load(value, i);
           }
         }
         ok = __shfl_sync(~0u, (int)ok, 0) != 0;
@@ -513,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vd = sw128_mn_desc(base + Gm::RING, Gm::HALFB);
       int next = 0;                      // ring stage and its phase
       uint32_t phase = 0, mend_phase = 0;   // (of each stage, a bit)
-      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // weights tiles and query blocks consumed, per stream
+      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // weights tiles and (not PAIR) query blocks consumed, per stream
       for (const Seg* sg; (sg = take()); give()) {
         if (!ok) continue;
-        const Seg& g = *sg;
+        const Seg g = *sg;
         const int n = g.tiles;
         auto tile = [&](bool value, int i) -> int {   // the next ring stage, once its tile is there; -1 on abort
           const int s = next;
@@ -534,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto mma_s = [&](int w, int s) {
           if (elect_one()) {
-            const uint64_t qa = qd + (uint64_t)((PAIR ? 0 : w) * (Gm::TILEB >> 4)), kb = kd + (uint64_t)(s * (Gm::TILEB >> 4));
+            const uint64_t qa = qd + (uint64_t)((PAIR ? seg & 1 : w) * (Gm::TILEB >> 4)), kb = kd + (uint64_t)(s * (Gm::TILEB >> 4));
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint64_t off = (uint64_t)(((kk >> 2) * Gm::HALFB + (kk & 3) * 32) >> 4);
@@ -566,19 +578,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++np[w];
           return true;
         };
-        auto queries = [&](int w) {
-          const bool here = __all_sync(~0u, wait_or_abort(q_full(w), nq[w] & 1, abort_flag, p.err));
-          ++nq[w];
+        auto queries = [&](int x, uint32_t count) {
+          const bool here = __all_sync(~0u, wait_or_abort(q_full(x), count & 1, abort_flag, p.err));
           tc_fence_after();
           return here;
         };
         int s;
         if (PAIR) {
-          if (!(ok = queries(0))) continue;
+          if (!(ok = queries(seg & 1, (uint32_t)seg >> 1))) continue;
           for (int i = 0; i < min(n, 2) && ok; ++i) {
             ok = (s = tile(false, i)) >= 0;
             if (ok) mma_s(i, s), commit(empty(s));
           }
+          if (n <= 2) commit(q_free(seg & 1));
           for (int i = 0; i < n && ok; ++i) {
             const int w = i & 1;
             if (!(ok = (s = tile(true, i)) >= 0)) break;
@@ -589,20 +601,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = (s = tile(false, i + 2)) >= 0)) break;
               mma_s(w, s);
               commit(empty(s));
+              if (i + 3 == n) commit(q_free(seg & 1));
             }
           }
         } else {
+          // (the softmax warps give the stages back)
           const int n0 = g.n[0], n1 = g.n[1];
           if (!(ok = (s = tile(false, 0)) >= 0)) continue;
           if (n0 > 0) {
-            if (!(ok = queries(0))) continue;
+            if (!(ok = queries(0, nq[0]++))) continue;
             mma_s(0, s);
+            if (n0 == 1) commit(q_free(0));
           }
           if (n1 > 0) {
-            if (!(ok = queries(1))) continue;
+            if (!(ok = queries(1, nq[1]++))) continue;
             mma_s(1, s);
+            if (n1 == 1) commit(q_free(1));
           }
-          commit(empty(s));
           for (int i = 0; i < n && ok; ++i) {
             const bool more = i + 1 < n;
             int sk = 0;
@@ -611,23 +626,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) {
               if (!(ok = (sk = tile(false, i + 1)) >= 0)) break;
               if (i + 1 < n0) mma_s(0, sk);
+              if (i + 2 == n0) commit(q_free(0));
             }
             if (i == n0 - 1) commit(o_done(0));
             if (i < n1 && !(ok = mma_o(1, s, i == 0))) break;
-            commit(empty(s));
-            if (more) {
-              if (i + 1 < n1) mma_s(1, sk);
-              commit(empty(sk));
-            }
+            if (more && i + 1 < n1) mma_s(1, sk);
+            if (i + 2 == n1) commit(q_free(1));
             if (i == n1 - 1) commit(o_done(1));
           }
         }
       }
     } else {
-      // ---------------------------------------------------------------- tile mending
+      // ---------------------------------------------------------------- queries, tile mending
       const int ht = (warp - 2) * 32 + lane;         // of 64 threads
       int next = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, nq[2] = {0, 0};
+      // queries: a thread has one 16-byte piece of every QS-th row
+      constexpr int QP = D / 8, QS = 64 / QP;
+      const int qc = ht % QP, qr = ht / QP, step_t = QS / N, step_j = QS - step_t * N;
       // re-rotation: a thread has one 16-byte piece of a row's first half and its pair
       constexpr int PC = D / 16, PER = 64 / PC;      // pieces, rows at a time
       const int pc = ht % PC, pr = ht / PC;
@@ -636,8 +652,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (const Seg* sg; (sg = take()); give()) {
         if (!ok) continue;
-        const Seg& g = *sg;
-        const int n = g.tiles;
+        const Seg g = *sg;
+        // A query block sets out when its place is free: when the last logits there are
+        // done, while their softmax and the last products run.
+#pragma unroll
+        for (int w = 0; w < (PAIR ? 1 : 2); ++w) {
+          if (g.n[w] == 0 || !ok) continue;
+          const int x = PAIR ? seg & 1 : w;
+          const uint32_t count = PAIR ? (uint32_t)seg >> 1 : nq[w]++;
+          if (count > 0) ok = __all_sync(~0u, wait_or_abort(q_free(x), (count - 1) & 1, abort_flag, p.err));
+          if (!ok) continue;
+          const int rows = g.nq * N, first = g.row0 + w * kT + qr;
+          int t = (int)((unsigned)first / (unsigned)N), j = first - t * N;
+          const T* const q = static_cast<const T*>(a.q) + g.b * a.q_stride[0] + (int64_t)g.h * N * a.q_stride[2] + 8 * qc;
+          const uint32_t to = base + Gm::Q + x * Gm::TILEB + (qc >> 3) * Gm::HALFB;
+#pragma unroll 4
+          for (int r = qr; r < kT; r += QS) {
+            const bool on = first - qr + r < rows;   // (the rest zeros)
+            const T* const from = q + (on ? (int64_t)(g.tok0 + t) * a.q_stride[1] + j * a.q_stride[2] : 0);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + r * 128 + (((qc ^ r) & 7) << 4)), "l"(from),
+                         "r"(on ? 16 : 0)
+                         : "memory");
+            t += step_t;
+            j += step_j;
+            if (j >= N) j -= N, ++t;
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full(x));
+        }
         auto visit = [&](bool value, int i) {
           const int s = next;
           const uint32_t ph = phase;
@@ -685,14 +729,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        for (int i = 0; i < n && ok; ++i) {
-          if (i == 0) {
-            ok = visit(false, 0);
-            if (PAIR && ok && n > 1) ok = visit(false, 1);
-          }
-          ok = ok && visit(true, i);
-          const int nk = PAIR ? i + 2 : i + 1;
-          if (ok && nk < n) ok = visit(false, nk);
+#pragma unroll 1
+        for (int j = 0; j < 2 * g.tiles && ok; ++j) {
+          bool value;
+          const int i = tile_at<PAIR>(j, g.tiles, value);
+          ok = visit(value, i);
         }
       }
     }
@@ -703,11 +744,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;          // query row of the stream = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t ns = 0, no = 0;                         // logits tiles and finished outputs seen
-    // The warp's 32 rows of the query block, as TMA would swizzle them; PAIR: each
-    // warpgroup has half of every row's pieces. Between global and shared memory
-    // neighbouring lanes move neighbouring pieces of a row.
-    constexpr int CPR = PAIR ? D / 16 : D / 8;       // 16-byte pieces of a row
-    unsigned char* const mine = smem + Gm::Q + (PAIR ? 0 : w) * Gm::TILEB;
+    int ring = 0;                                    // stage of the segment's first tile
+    // One stream (the second, where it has rows: it has every tile) gives the ring's stages
+    // back. When it sees its logits of key tile i (the segment's tile 2 i), those keys have
+    // been read, and the values of tile i - 1 (2 i - 1) by the products before. A commit by
+    // the MMA warp for each would be one more stop in its stream of products; PAIR waits
+    // for memory and wants its stages sooner.
+    auto release = [&](int nth) {
+      if (lane == 0 && (warp & 3) == 0) mbar_arrive(empty((ring + nth) % NS));
+    };
     // this thread's row of a segment: its token, its query head, whether it is there
     auto place = [&](const Seg& g, int& t, int& head) {
       const int r = g.row0 + (PAIR ? 0 : w * kT) + row, rows = g.nq * N, x = min(r, rows - 1);
@@ -722,38 +767,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t m0 = __shfl_sync(~0u, anc[0], t & 31), m1 = __shfl_sync(~0u, anc[1], t & 31);
       return t < 32 ? m0 : m1;
     };
-    uint4 qv[CPR];
-    auto load_queries = [&](const Seg& g) {
-      int t, head;
-      const bool valid = place(g, t, head);
-      const T* const q = static_cast<const T*>(a.q);
-      const int64_t offset = g.b * a.q_stride[0] + (int64_t)(g.tok0 + t) * a.q_stride[1] + head * a.q_stride[2];
-#pragma unroll
-      for (int i = 0; i < CPR; ++i) {
-        const int from = i * (32 / CPR) + lane / CPR, c = (PAIR ? w * CPR : 0) + lane % CPR;
-        const int64_t at = __shfl_sync(~0u, offset, from);
-        const bool on = __shfl_sync(~0u, (int)valid, from);
-        qv[i] = on ? *reinterpret_cast<const uint4*>(q + at + 8 * c) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto store_queries = [&] {
-#pragma unroll
-      for (int i = 0; i < CPR; ++i) {
-        const int r = (warp & 3) * 32 + i * (32 / CPR) + lane / CPR, c = (PAIR ? w * CPR : 0) + lane % CPR;
-        *reinterpret_cast<uint4*>(mine + r * 128 + (c >> 3) * Gm::HALFB + (((c ^ r) & 7) << 4)) = qv[i];
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(PAIR ? 0 : w));
-    };
-    const Seg* sg = take();
-    if (sg && sg->n[w] > 0 && ok) {
-      load_queries(*sg);
-      store_queries();
-    }
-    while (sg) {
+    for (const Seg* sg; (sg = take()); give()) {
       const Seg& g = *sg;
-      const int n = g.n[w];
+      const int n = g.n[w], part = g.part, hole = g.hole, mask = g.mask, tiles = g.tiles;
+      const bool releases = !PAIR && (w == 1 ? n > 0 : g.n[1] == 0);
       int t, head;
       const bool valid = place(g, t, head);
       float m = kNegInf, l = 0.f;
@@ -764,14 +781,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++ns;
         tc_fence_after();
+        if (releases) {
+          release(2 * i);
+          if (i > 0) release(2 * i - 1);
+        }
         // which of the tile's keys the row sees
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        bool partial = i == g.part || i == g.hole;
+        bool partial = i == part || i == hole;
         if (partial) {
-          const int left = g.left - i * kT, gap = i == g.hole ? g.gap - i * kT : -1;
+          const int left = g.left - i * kT, gap = i == hole ? g.gap - i * kT : -1;
 #pragma unroll
           for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x) & ~((gap >> 5) == x ? 1u << (gap & 31) : 0u);
-        } else if (i >= g.mask) {
+        } else if (i >= mask) {
           partial = true;
           if (a.parents) {
             const uint64_t mm = seen_of(g, t);
@@ -792,12 +813,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < kT; ++e) v[e] = (see[e >> 5] >> (e & 31)) & 1u ? v[e] : kNegInf;
         }
         // (a NaN stays in the maximum, so that one compare finds logits that are not finite)
-        float m4[4] = {v[0], v[1], v[2], v[3]};
+        float m4[4];
 #pragma unroll
-        for (int e = 4; e < kT; e += 8)
+        for (int x = 0; x < 4; ++x) m4[x] = max_nan(v[x], v[4 + x], v[8 + x]);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            m4[x] = e + 4 < kT ? max_nan(m4[x], max_nan(v[e + x], v[e + 4 + x])) : max_nan(m4[x], v[e + x]);
+        for (int e = 12; e < kT; e += 8)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) m4[x] = e + 4 < kT ? max_nan(m4[x], v[e + x], v[e + 4 + x]) : max_nan(m4[x], v[e + x]);
         const float mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])) * a.scale2;
         // Rare: logits of NaN or +-inf, and a maximum so large that it is rounded by a half
         // or more, as its own logit need not be near it in the fused product and
@@ -876,19 +898,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         l4[0] = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
         l += l4[0].x + l4[0].y;
       }
-      // The next block's queries, on their way while the last products run. Their place
-      // is free once this stream (PAIR: both) has seen its last logits.
-      ++seg;
-      const Seg* const ng = take();
-      --seg;
-      const bool feed = ng && ng->n[w] > 0 && ok;
-      if (feed) load_queries(*ng);
-      if (!PAIR && feed) store_queries();
       if (begun && ok) {
         ok = __all_sync(~0u, wait_or_abort(o_done(w), no & 1, abort_flag, p.err));
         ++no;
         tc_fence_after();
+        if (releases) release(2 * n - 1);
       }
+      ring = (ring + 2 * tiles) % NS;
       float f0 = 1.f, f1 = 0.f;
       if (!ok) l = __int_as_float(0x7FFFFFFF);       // NaN: this row's result is lost
       if (PAIR) {
@@ -900,7 +916,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         asm volatile("bar.sync 3, 256;" ::: "memory");
         tc_fence_after();
-        if (feed) store_queries();
         const float2 x = ml[row], y = ml[kT + row];
         m = fmaxf(x.x, y.x);
         f0 = x.x == m ? 1.f : ex2(x.x - m);
@@ -908,13 +923,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = x.y * f0 + y.y * f1;
       }
       const bool poisoned = marks[seg % kSegs] == seg;
-      auto columns = [&](int c, float (&v)[32]) {    // O's columns 32 c .. + 31 of this row
-        const uint32_t at = tmem + lanes + 32 * c;
+      constexpr int CW = Gm::CW;
+      auto columns = [&](int c, float (&v)[CW]) {    // O's columns c .. c + CW - 1 of this row
+        const uint32_t at = tmem + lanes + c;
         if (n == 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        } else if (!PAIR) {
-          tmem_ld32(at + kT * w, v);
+          for (int e = 0; e < CW; ++e) v[e] = 0.f;
+        } else if constexpr (!PAIR) {
+          tmem_ld64(at + kT * w, v);
         } else {
           tmem_ld32(at, v);
           if (n > 1) {
@@ -932,9 +948,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = j0; j < min(j0 + kT, t + 1); ++j) {
               if (a.parents && !((seen >> j) & 1)) continue;
               const T* src = static_cast<const T*>(a.v_new) + g.b * a.vn_stride[0] + (int64_t)(g.tok0 + j) * a.vn_stride[1] +
-                             g.h * a.vn_stride[2] + 32 * c;
+                             g.h * a.vn_stride[2] + c;
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
+              for (int e = 0; e < CW; e += 2) {
                 const uint32_t word = *reinterpret_cast<const uint32_t*>(src + e), f = not_finite<T>(word);
                 const float2 x = unpack16<T>(word);
                 if (f & 0x8000u) v[e] += x.x;
@@ -944,37 +960,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      constexpr int CC = PAIR ? D / 64 : D / 32;     // groups of 32 columns
+      constexpr int COLS = PAIR ? D / 2 : D;         // this warpgroup's columns, from `begin` on
+      const int begin = PAIR ? w * COLS : 0;
       if (g.whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        constexpr int CW = Gm::CW, PR = CW / 8;      // columns at a time; their 16-byte pieces
+        constexpr int PR = CW / 8;                   // 16-byte pieces of a row
         unsigned char* const stage = smem + Gm::STAGE + (warp - 4) * (32 * CW * 2);
         auto staged = [&](int r, int c) {
           return reinterpret_cast<uint4*>(stage + r * (CW * 2) + (((PR == 8 ? c ^ r : c ^ (r >> 1)) & (PR - 1)) << 4));
         };
         T* const out = static_cast<T*>(a.out);
         const int64_t offset = g.b * a.out_stride[0] + (int64_t)(g.tok0 + t) * a.out_stride[1] + head * a.out_stride[2];
+        // where the rows go that this lane has pieces of
+        const unsigned rows_on = __ballot_sync(~0u, valid);
+        int64_t row_at[PR];
+#pragma unroll
+        for (int x = 0; x < PR; ++x) row_at[x] = __shfl_sync(~0u, offset, x * (32 / PR) + lane / PR);
 #pragma unroll 1
-        for (int i = 0; i < CC; i += CW / 32) {
-          const int c0 = (PAIR ? w * CC : 0) + i;
+        for (int c0 = begin; c0 < begin + COLS; c0 += CW) {
+          float v[CW];
+          columns(c0, v);
 #pragma unroll
-          for (int x = 0; x < CW / 32; ++x) {
-            float v[32];
-            columns(c0 + x, v);
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *staged(lane, 4 * x + e / 8) =
-                  make_uint4(pack16<T>(v[e] * inv, v[e + 1] * inv), pack16<T>(v[e + 2] * inv, v[e + 3] * inv),
-                             pack16<T>(v[e + 4] * inv, v[e + 5] * inv), pack16<T>(v[e + 6] * inv, v[e + 7] * inv));
-          }
+          for (int e = 0; e < CW; e += 8)
+            *staged(lane, e / 8) =
+                make_uint4(pack16<T>(v[e] * inv, v[e + 1] * inv), pack16<T>(v[e + 2] * inv, v[e + 3] * inv),
+                           pack16<T>(v[e + 4] * inv, v[e + 5] * inv), pack16<T>(v[e + 6] * inv, v[e + 7] * inv));
           __syncwarp();
+          uint4 y[PR];
 #pragma unroll
-          for (int x = 0; x < PR; ++x) {
-            const int from = x * (32 / PR) + lane / PR, c = lane % PR;
-            const int64_t at = __shfl_sync(~0u, offset, from);
-            const bool on = __shfl_sync(~0u, (int)valid, from);
-            if (on) *reinterpret_cast<uint4*>(out + at + 32 * c0 + 8 * c) = *staged(from, c);
-          }
+          for (int x = 0; x < PR; ++x) y[x] = *staged(x * (32 / PR) + lane / PR, lane % PR);
+#pragma unroll
+          for (int x = 0; x < PR; ++x)
+            if ((rows_on >> (x * (32 / PR) + lane / PR)) & 1u)
+              *reinterpret_cast<uint4*>(out + row_at[x] + c0 + 8 * (lane % PR)) = y[x];
           __syncwarp();
         }
         if (valid && a.lse && !(PAIR && w))
@@ -985,20 +1003,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int R = p.plan.block_rows, rr = (PAIR ? 0 : w * kT) + row;
         float4* o = reinterpret_cast<float4*>(p.part_o) + slot * (R * (D / 4)) + rr;
 #pragma unroll 1
-        for (int i = 0; i < CC; ++i) {
-          const int c = (PAIR ? w * CC : 0) + i;
-          float v[32];
-          columns(c, v);
+        for (int c0 = begin; c0 < begin + COLS; c0 += CW) {
+          float v[CW];
+          columns(c0, v);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) o[(int64_t)(8 * c + e / 4) * R] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < CW; e += 4) o[(int64_t)((c0 + e) / 4) * R] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
         if (!(PAIR && w)) p.part_ml[slot * R + rr] = make_float2(m, l);
       }
       tc_fence_before();
       // (PAIR: either warpgroup reads both accumulators, and the maxima)
       if (PAIR) asm volatile("bar.sync 3, 256;" ::: "memory");
-      give();
-      sg = ng;
     }
   }
 

@@ -190,6 +190,12 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   return r;
 }
 
+__device__ __forceinline__ float max_nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 // One thread of the warp, always the same, chosen in a way that tells the
 // compiler that the warp stays uniform: descriptors then live in uniform
 // registers. With `lane == 0` instead, moving them there bound the rate at which

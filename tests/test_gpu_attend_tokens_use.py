@@ -232,6 +232,7 @@ def test_two_threads_at_once(kvx):
 
     def once(job, stream):
         outs = [torch.zeros_like(q) for _, q, _ in job]
+        stream.wait_stream(torch.cuda.current_stream())          # the zeros are there
         for (call, q, args), out in zip(job, outs):
             call(q, out, stream=stream, **args)
         return outs
