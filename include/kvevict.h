@@ -262,7 +262,7 @@ int kvevict_check(kvevict_t* h, void* stream);
  * handle then reports DEVICE_CHECK, the allocation-free call writes NaN
  * scores. A launch of kvevict_attend's prefix kernel that comes first takes the
  * hook instead (its first key tile), and writes NaN; so does one of
- * kvevict_attend_prompt or kvevict_attend_tree. Nothing faults or hangs. One-shot. Errors: none. */
+ * the tensor-core kernel of kvevict_attend_prompt and kvevict_attend_tree. Nothing faults or hangs. One-shot. Errors: none. */
 int kvevict_test_stall_next_step(kvevict_t* h);
 
 /* Position the next decode key will occupy (= tokens absorbed so far): the
@@ -507,8 +507,9 @@ int kvevict_attend_cache(const kvevict_t* h, int32_t l, const kvevict_attention*
  * kvevict_prefill takes their keys, and of trees of drafted tokens, before those
  * that are accepted go into the cache as steps (kvevict_decode_kv takes several).
  * The rules of the block above hold: no state, nothing allocated, the current
- * device, strides in elements. Keys and values are read through tensor maps: their
- * strides are >= 0 and below 2^39, and tokens (rows) lie at least D apart. */
+ * device, strides in elements. Queries, keys and values are read through tensor maps:
+ * their strides are >= 0 and below 2^39, and tokens (rows), and heads of q, lie at least
+ * D apart. */
 #define KVEVICT_MAX_TREE 64   /* tokens of a tree */
 #define KVEVICT_MAX_JOIN 8    /* parts that one join takes */
 
@@ -579,8 +580,12 @@ int kvevict_attend_tree(const kvevict_tokens* args, void* stream);
  * kvevict_attend_tree and kvevict_attend_cache. */
 int kvevict_attend_tree_cache(const kvevict_t* h, int32_t l, const kvevict_tokens* args, void* stream);
 
+/* Test hook: while `without` is not 0, calls of this process never take the kernel for
+ * few query rows, but the tensor cores' whatever their size. Errors: none. */
+int kvevict_test_without_few_kernel(int32_t without);
+
 /* Device bytes that a call of this description needs as workspace, on the current
- * device; of the pointers only starts counts (whether it is null). with_cache: 1 for
+ * device (at most); of the pointers only starts counts (whether it is null). with_cache: 1 for
  * kvevict_attend_tree_cache, else 0. *bytes: host. Errors: INVALID_ARG, CUDA. */
 int kvevict_attend_tokens_workspace(const kvevict_tokens* args, int32_t with_cache, size_t* bytes);
 

@@ -89,6 +89,7 @@ SIGNATURES = {
     "kvevict_attend_tree_cache": (ctypes.c_int, [P, i32, P, P]),
     "kvevict_attend_tokens_workspace": (ctypes.c_int, [P, i32, P]),
     "kvevict_attend_join": (ctypes.c_int, [P, P]),
+    "kvevict_test_without_few_kernel": (ctypes.c_int, [i32]),
 }
 
 

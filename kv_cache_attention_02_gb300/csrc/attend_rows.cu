@@ -50,7 +50,7 @@
 // (54-59), L2 prefetches throughout (150 against 139 on the unequal lengths). Bound by
 // the loads that a warp's registers hold in flight, 16 KB, 8 warps an SM, with the
 // latencies of start, join and unequal SMs on top (SMs are busy 84% of the time).
-#include "attend_internal.cuh"
+#include "mma_rows.cuh"
 
 #include <cooperative_groups.h>
 
@@ -75,11 +75,6 @@ constexpr int kClusterTiles = 8;
 // 10.0 with eight, 11.5 with one.
 constexpr int kFewParts = 32;
 
-// What the weights of the second product are multiplied by: the top of fp16's range
-// (65504) is used, with a factor of two to spare.
-template <typename T>
-constexpr float kLift = std::is_same<T, __half>::value ? 32768.f : 1.f;
-
 constexpr int stream_ctas_per_sm(int D) { return D == 64 ? 3 : 2; }
 int rows_qt(int N) { return N <= 8 ? 1 : 2; }
 // Rows a warp takes at a time: 32 where a stream's registers hold them.
@@ -95,65 +90,6 @@ int cluster_ctas(int64_t units, int64_t tiles, int sms) {
 int64_t rows_tiles(int rows, int n, int P, bool has_new, bool pend) {   // of a unit, at most
   return ((int64_t)P + rows - 1) / rows + ((int64_t)n + pend + rows - 1) / rows + has_new;
 }
-
-template <typename T>
-__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__half>(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                 uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                        uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-
-// 16 KG consecutive rows of one source; row r is there if bit r of `live` is set.
-template <typename T>
-struct Tile {
-  const T* k;
-  const T* v;
-  int64_t ks, vs;
-  uint32_t live;
-  int moved;    // rows from here on await the re-rotation by -1 (32: none)
-};
-
-template <typename T, int D, int KG>
-struct Rows {
-  static constexpr int KC = D / 32;   // 16-byte pieces of a key row in one lane
-  static constexpr int VH = D / 64;   // 64-wide column groups of a value row
-
-  __device__ __forceinline__ static void load_k(uint4 (&kr)[2 * KG][KC], const Tile<T>& t, int g, int c) {
-#pragma unroll
-    for (int nt = 0; nt < 2 * KG; ++nt) {
-      const int r = g + 8 * nt;
-      const T* p = t.k + (int64_t)r * t.ks + 8 * c;
-      const bool on = (t.live >> r) & 1u;
-#pragma unroll
-      for (int i = 0; i < KC; ++i) kr[nt][i] = on ? ld_stream16(p + 32 * i) : make_uint4(0, 0, 0, 0);
-    }
-  }
-  __device__ __forceinline__ static void load_v(uint4 (&vr)[VH][4 * KG], const Tile<T>& t, int g, int c) {
-#pragma unroll
-    for (int j = 0; j < 4 * KG; ++j) {
-      const int r = 2 * c + (j & 1) + 8 * (j >> 1);
-      const T* p = t.v + (int64_t)r * t.vs + 8 * g;
-      const bool on = (t.live >> r) & 1u;
-#pragma unroll
-      for (int h = 0; h < VH; ++h) vr[h][j] = on ? ld_stream16(p + 64 * h) : make_uint4(0, 0, 0, 0);
-    }
-  }
-};
 
 // Starts a tile towards L2 (rows that lie together only). Used for a range's
 // second tile, whose loads the registers cannot yet take; for every tile it
@@ -455,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
         for (int nt = 0; nt < 2 * KG; ++nt) {
           const float p0 = ex2(s[nt][2 * i] - base), p1 = ex2(s[nt][2 * i + 1] - base);
           l[i] += p0 + p1;
-          const float2 w = make_float2(p0 * kLift<T>, p1 * kLift<T>);
+          const float2 w = make_float2(p0 * kWeightLift<T>, p1 * kWeightLift<T>);
           hi[i][nt] = pack16<T>(w.x, w.y);
           const float2 back = unpack16<T>(hi[i][nt]);
           lo[i][nt] = pack16<T>(w.x - back.x, w.y - back.y);
@@ -480,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, STREAM ? stream_ctas_per_sm(D) : 1)
       if (more) R::load_v(vr, cur, g, c);
     }
 #pragma unroll
-    for (int x = 0; x < VH * 4 * QT * 4; ++x) (&acc[0][0][0][0])[x] *= 1.f / kLift<T>;
+    for (int x = 0; x < VH * 4 * QT * 4; ++x) (&acc[0][0][0][0])[x] *= 1.f / kWeightLift<T>;
 
     // ---------------------------------------------------------------- the prefix's parts
     // Each part (a range of shared rows that one CTA of attend_prefix.cu took) joins

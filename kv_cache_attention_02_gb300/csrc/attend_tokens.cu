@@ -3,7 +3,8 @@
 // that the sequence already has or none) and trees of drafted tokens over a cache.
 //
 // For one sequence and key head the query rows are those of one matrix Q [nq*N, D], N =
-// G / H, row t*N + j for token t and query head j:
+// G / H (of a part of the key head's, where they are more than 128), row t*N + j for token
+// t and query head j:
 //   S = Q K^T * scale,  P = e^(S - m),  O = P V,  l = sum P,
 // over the sequence's own rows, which every token sees, and its tokens' keys, of which
 // token t sees 0..t (a prompt) or itself and its ancestors (a tree). The arithmetic is
@@ -11,8 +12,9 @@
 // parts with up to 128 query rows), the sum l of the unrounded ones in fp32 relative to
 // m, which moves only when the maximum has grown by 2^8.
 //
-// Work: see TokensPlan. A block is PAIR: 128 query rows, its key tiles dealt alternately
-// to two streams; else 256 rows, a stream for either half, both on every tile. Key tiles
+// Work: see TokensPlan. A half block is the rows of 128 / N tokens, which one TMA box
+// brings. A block is PAIR: one half, its key tiles dealt alternately to two streams; else
+// two halves, a stream for either, both on every tile. Key tiles
 // past the last row's are not visited. A piece of a block that another CTA finishes
 // leaves its unnormalised O, m and l in the workspace for the join kernel below.
 //
@@ -22,8 +24,8 @@
 //               in the order they are used;
 //   warp 1      issues tcgen05.mma: S = Q K^T from shared memory, then O += P V with P
 //               from TMEM and V as it lies in memory;
-//   warps 2, 3  load the query rows, the next block's as soon as the last logits of this
-//               one are done; mend tiles on their way: values that no row of the block sees, or some
+//   warps 2, 3  issue the TMA loads of the query rows, the next block's as soon as the last
+//               logits of this one are done; mend tiles on their way: values that no row of the block sees, or some
 //               rows do not and that are not finite, become zeros (0 * NaN would spoil
 //               the sums); a cache's keys whose compaction is pending are re-rotated;
 //   warps 4..11 two softmax warpgroups, one per stream, a query row a thread. The next
@@ -53,13 +55,13 @@ constexpr float kFar = 0x1p23f;        // base-2 logits from here on are whole n
 // What the start of a block costs, in tiles of half a block.
 constexpr int kStartTiles = 2;
 
-// TMA coordinates of a row tensor: which of the map's dimensions 1..3 is which.
+// What a row tensor's TMA coordinates of heads and sequences are multiplied by: 0 where
+// all share the rows.
 struct Coords {
-  int row, h, b;           // their places, 0..2
-  int hm, bm;              // 0 where all heads (sequences) share the rows
+  int h, b;
 };
 struct MapArgs {
-  Coords k, v, kn, vn;
+  Coords q, k, v, kn, vn;
 };
 
 struct Params {
@@ -75,96 +77,70 @@ struct Params {
 
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, const Coords& c, int d, int row, int h,
                                               int b, uint32_t bar) {
-  h *= c.hm;
-  b *= c.bm;
-  const int x0 = c.row == 0 ? row : c.h == 0 ? h : b;
-  const int x1 = c.row == 1 ? row : c.h == 1 ? h : b;
-  const int x2 = c.row == 2 ? row : c.h == 2 ? h : b;
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(x0), "r"(x1), "r"(x2), "r"(bar)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(h * c.h), "r"(row), "r"(b * c.b), "r"(bar)
       : "memory");
 }
 
 // ---------------------------------------------------------------- the work
-struct Seq {
-  int tok0, nq, n, ta;     // first token (packed), tokens, own rows, tiles of own rows
-};
-__device__ __forceinline__ Seq load_seq(const TokensArgs& a, int b) {
-  Seq s;
-  s.tok0 = 0;
-  s.nq = a.S;
-  if (a.starts) {
-    s.tok0 = max(0, min(a.starts[b], a.S));
-    s.nq = max(0, min(a.starts[b + 1], a.S) - s.tok0);
-  } else if (a.new_lens) {
-    s.nq = max(0, min(a.new_lens[b], a.S));
-  }
-  s.n = a.lens ? max(0, min(a.lens[b], a.n)) : a.n;
-  s.ta = (s.n + (a.pend ? 1 : 0) + kT - 1) / kT;     // an evicted row may still be in place
-  return s;
-}
-
-// Costs of one key head's half blocks (PAIR: blocks) of a sequence: j costs base + j / N
-// for causal tokens (rows 128 j .. are tokens up to (128 j + 127) / N, which see 1 + j / N
-// tiles), base alone for a tree or where all are to count the same.
+// Costs of one head group's half blocks (PAIR: blocks) of a sequence, in 1/128 tiles:
+// half block j of causal tokens sees up to (j + 1) * half tokens' keys; a tree's see all.
 struct Cost {
-  int64_t base, N;         // N = 0: base alone
-  int halves;
+  int64_t base;
+  int step, halves;        // of half block j: base + j * step
   __device__ __forceinline__ Cost(const TokensArgs& a, const TokensPlan& p, const Seq& s) {
-    const int n = a.G / a.H;
-    const int64_t rows = (int64_t)s.nq * n;
-    halves = p.pair ? (int)((rows + kT - 1) / kT) : 2 * (int)((rows + 2 * kT - 1) / (2 * kT));
-    base = p.even ? 1 : 1 + s.ta + kStartTiles;
-    N = p.even || a.parents ? 0 : n;
+    const int per = p.pair ? a.half : 2 * a.half;
+    halves = (int)((unsigned)(s.nq + per - 1) / (unsigned)per) * (p.pair ? 1 : 2);
+    base = p.even ? 1 : (int64_t)(1 + s.ta + kStartTiles) * kT;
+    step = p.even || a.parents ? 0 : a.half;
   }
-  __device__ __forceinline__ int64_t before(int64_t j) const {   // of 0 .. j - 1
-    if (!N) return j * base;
-    const int64_t q = (unsigned)j / (unsigned)N, r = j - q * N;
-    return j * base + N * (q * (q - 1) / 2) + q * r;
+  __device__ __forceinline__ int64_t before(int j) const {   // of 0 .. j - 1
+    return j * base + (int64_t)step * ((int64_t)j * (j - 1) / 2);
   }
   __device__ __forceinline__ int64_t head() const { return before(halves); }
   // The last j with before(j) <= y, 0 <= y < head().
   __device__ __forceinline__ int find(int64_t y) const {
-    int64_t j;
-    if (!N) {
-      j = y / base;
-    } else {
-      const float b = (float)base - 0.5f, n = (float)N;
-      j = (int64_t)(n * (sqrtf(b * b + 2.f * (float)y / n) - b));
-    }
-    j = max((int64_t)0, min(j, (int64_t)halves - 1));
+    // (the root of step j^2 / 2 + b j = y, without a difference)
+    const float b = (float)base - 0.5f * (float)step, f = (float)y;
+    int j = (int)__fdividef(2.f * f, b + sqrtf(b * b + 2.f * (float)step * f));
+    j = max(0, min(j, halves - 1));
     while (j > 0 && before(j) > y) --j;
     while (j < halves - 1 && before(j + 1) <= y) ++j;
-    return (int)j;
+    return j;
   }
 };
 
-// Tiles that the first `rows` query rows of a sequence visit.
-__device__ __forceinline__ int tiles_of(const TokensArgs& a, const Seq& s, int rows) {
-  const int N = a.G / a.H;
-  const int keys = a.parents ? s.nq : min(s.nq, (rows + N - 1) / N);
-  return s.ta + (keys + kT - 1) / kT;
+// Tiles that the tokens before `tokens` of a sequence visit.
+__device__ __forceinline__ int tiles_of(const TokensArgs& a, const Seq& s, int tokens) {
+  return s.ta + ((a.parents ? s.nq : min(s.nq, tokens)) + kT - 1) / kT;
 }
+__device__ __forceinline__ int block_tokens(const TokensArgs& a, const TokensPlan& p) { return p.pair ? a.half : 2 * a.half; }
+// (blocks are of at most 256 tokens, and there are fewer than 2^30)
 __device__ __forceinline__ int block_tiles(const TokensArgs& a, const TokensPlan& p, const Seq& s, int i) {
-  return tiles_of(a, s, min(s.nq * (a.G / a.H), (i + 1) * p.block_rows));
+  return tiles_of(a, s, (i + 1) * block_tokens(a, p));
 }
 
-// Start of the range that begins at cost y of sequence b, which is in it.
-__device__ __forceinline__ TokensAt locate(const TokensArgs& a, const TokensPlan& p, int b, int64_t y) {
+// Start of the range that begins at cost y of sequence b, which is in it. Quotients are
+// taken in floats: whatever they round to, both CTAs that meet here find the same.
+__device__ __noinline__ TokensAt locate(const TokensArgs& a, const TokensPlan& p, int b, int64_t y) {
   const Seq s = load_seq(a, b);
   const Cost c(a, p, s);
+  const int64_t head = c.head();
   TokensAt at;
   at.b = b;
-  at.h = (int)(y / c.head());
-  y -= at.h * c.head();
+  at.h = max(0, min((int)__fdividef((float)y, (float)head), a.heads - 1));
+  while (at.h > 0 && at.h * head > y) --at.h;
+  while (at.h < a.heads - 1 && (at.h + 1) * head <= y) ++at.h;
+  y -= at.h * head;
   const int per = p.pair ? 1 : 2;
   at.i = c.find(y) / per;
   at.k = 0;
   if (!p.whole) {
-    const int64_t c0 = c.before((int64_t)at.i * per), c1 = c.before((int64_t)(at.i + 1) * per);
-    at.k = (int)((y - c0) * block_tiles(a, p, s, at.i) / (c1 - c0));
+    const int64_t c0 = c.before(at.i * per), c1 = c.before((at.i + 1) * per);
+    const int tiles = block_tiles(a, p, s, at.i);
+    at.k = max(0, min((int)((float)tiles * __fdividef((float)(y - c0), (float)(c1 - c0))), tiles - 1));
   }
   return at;
 }
@@ -172,11 +148,13 @@ __device__ __forceinline__ TokensAt locate(const TokensArgs& a, const TokensPlan
 // The range of this CTA, [ends_s[0], ends_s[1]); all threads, with barriers.
 __device__ __forceinline__ void find_range(const TokensArgs& a, const TokensPlan& p, int64_t* sums_s, TokensAt* ends_s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int share = (a.B + kThreads - 1) / kThreads;
+  const int share = (int)((unsigned)(a.B + kThreads - 1) / (unsigned)kThreads);
   const int b0 = min(a.B, tid * share), b1 = min(a.B, b0 + share);
   int64_t own = 0;
-  for (int b = b0; b < b1; ++b) own += a.H * Cost(a, p, load_seq(a, b)).head();
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) own += a.heads * Cost(a, p, load_seq(a, b)).head();
   int64_t to = own;                                  // of this and lower lanes
+#pragma unroll 1
   for (int d = 1; d < 32; d *= 2) {
     const int64_t x = __shfl_up_sync(~0u, to, d);
     if (lane >= d) to += x;
@@ -185,16 +163,23 @@ __device__ __forceinline__ void find_range(const TokensArgs& a, const TokensPlan
   if (tid < 2) ends_s[tid] = TokensAt{a.B, 0, 0, 0};
   __syncthreads();
   int64_t total = 0, from = to - own;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) from += sums_s[w];
     total += sums_s[w];
   }
+  if (own == 0) return;
+#pragma unroll 1
   for (int e = 0; e < 2; ++e) {
-    const int64_t x = (blockIdx.x + e) * total / p.ctas;
+    // c * total / ctas (or about that: any ascending function does)
+    const int c = blockIdx.x + e;
+    if (c == p.ctas) break;
+    const int64_t x = min((int64_t)(((double)total * c + 0.5) * p.per_cta), total - 1);
     if (x < from || x >= from + own) continue;
     int64_t y = x - from;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const int64_t seq = a.H * Cost(a, p, load_seq(a, b)).head();
+      const int64_t seq = a.heads * Cost(a, p, load_seq(a, b)).head();
       if (y < seq) {
         ends_s[e] = locate(a, p, b, y);
         break;
@@ -202,7 +187,6 @@ __device__ __forceinline__ void find_range(const TokensArgs& a, const TokensPlan
       y -= seq;
     }
   }
-  __syncthreads();
 }
 
 // A block's tiles k0 .. k1 - 1, as the producer finds them and the other roles read them
@@ -218,7 +202,8 @@ struct Seg {
   int turn;                // the first own tile with keys that await their re-rotation
   int mask;                // the first tile of the tokens' that some rows see in part
   int kb;                  // what a tile's index is short of its place among the tokens'
-  int b, h, tok0, nq, row0;
+  int b, h, kv, tok0, nq;  // sequence, head group, key head; its first token (packed) and number
+  int tok;                 // the block's first token
   int whole, from_start;   // all of the block's tiles; its first
 };
 constexpr int kSegs = 8;                 // more than the ring can hold tiles of, at once
@@ -238,8 +223,7 @@ struct Walk {
         s = load_seq(a, at.b);
         loaded = at.b;
       }
-      const int N = a.G / a.H, rows = s.nq * N;
-      if (rows == 0) {                               // on to the next sequence that has tokens
+      if (s.nq == 0) {                               // on to the next sequence that has tokens
         const int lane = threadIdx.x & 31;
         const bool some = at.b + 1 + lane >= a.B || load_seq(a, at.b + 1 + lane).nq > 0;
         const unsigned found = __ballot_sync(~0u, some);
@@ -249,12 +233,15 @@ struct Walk {
       }
       const int all = block_tiles(a, p, s, at.i), k0 = at.k;
       const int k1 = at.b == end.b && at.h == end.h && at.i == end.i ? end.k : all;
-      const int e = a.pend ? a.pend[at.b * a.H + at.h] : -1, n = s.n + (e >= 0);
+      g.b = at.b;
+      g.h = at.h;
+      g.kv = a.groups == 1 ? at.h : at.h / a.groups;
+      const int e = a.pend ? a.pend[g.b * (a.groups == 1 ? a.heads : a.heads / a.groups) + g.kv] : -1, n = s.n + (e >= 0);
       g.tiles = k1 - k0;
-      g.row0 = at.i * p.block_rows;
+      g.tok = at.i * block_tokens(a, p);
       for (int w = 0; w < 2; ++w) {
-        const int lo = g.row0 + w * kT;
-        g.n[w] = p.pair ? g.tiles : lo >= rows ? 0 : max(0, min(k1, tiles_of(a, s, min(rows, lo + kT))) - k0);
+        const int lo = g.tok + w * a.half;
+        g.n[w] = p.pair ? g.tiles : lo >= s.nq ? 0 : max(0, min(k1, tiles_of(a, s, lo + a.half)) - k0);
       }
       g.own = max(0, min(s.ta - k0, g.tiles));
       g.first = k0 * kT;
@@ -264,9 +251,7 @@ struct Walk {
       g.hole = e >= 0 && g.gap >= 0 && g.gap < g.own * kT ? g.gap / kT : -1;
       g.turn = e < 0 ? kNever : max(0, g.gap + 1) / kT;
       g.kb = k0 - s.ta;
-      g.mask = a.parents ? g.own : max(g.own, (int)((unsigned)(g.row0 / N + 1) / kT) - g.kb);
-      g.b = at.b;
-      g.h = at.h;
+      g.mask = a.parents ? g.own : max(g.own, (g.tok + 1) / kT - g.kb);
       g.tok0 = s.tok0;
       g.nq = s.nq;
       g.whole = k0 == 0 && k1 == all;
@@ -274,9 +259,10 @@ struct Walk {
       at.k = k1;
       if (k1 == all) {
         at.k = 0;
-        if ((int64_t)++at.i * p.block_rows >= rows) {
+        ++at.i;
+        if (g.tok + block_tokens(a, p) >= s.nq) {
           at.i = 0;
-          if (++at.h == a.H) {
+          if (++at.h == a.heads) {
             at.h = 0;
             ++at.b;
           }
@@ -299,7 +285,8 @@ struct Geo {
   static constexpr int BARS = ML + (PAIR ? 2 * kT * 8 : 0);
   static constexpr int NBARS = 3 * STAGES + 13 + 2 * kSegs;
   static constexpr int SEGS = BARS + NBARS * 8 + 16 + kSegs * 4;
-  static constexpr int SMEM = SEGS + kSegs * (int)sizeof(Seg) + 1024;   // slack to align to 1024 bytes
+  static constexpr int ROWS = SEGS + kSegs * (int)sizeof(Seg);
+  static constexpr int SMEM = ROWS + kT * 4 + 1024;   // slack to align to 1024 bytes
 };
 
 // The order in which a segment's key and value tiles are used, n of each: K0 V0 K1 V1 ..;
@@ -322,56 +309,12 @@ __device__ __forceinline__ bool mends(const TokensArgs& a, const Seg& g, bool va
   return i >= g.own ? i >= g.mask : i == g.hole || (i == g.part && (a.lens || a.pend));
 }
 
-// Bits of any 16-bit float in a word whose exponent is all ones: NaN or infinity.
-template <typename T>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  return std::is_same<T, __half>::value ? ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u
-                                        : ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-}
-template <typename T>
-__device__ __forceinline__ uint32_t drop_not_finite(uint32_t w) {
-  const uint32_t f = not_finite<T>(w);
-  return (f & 0x8000u ? 0u : w & 0xFFFFu) | (f & 0x80000000u ? 0u : w & 0xFFFF0000u);
-}
-
-// Ancestors of the tokens lane and lane + 32 of sequence b, themselves included, as
-// bits (warp-collective): powers of two of the step to the parent.
-__device__ __forceinline__ void ancestors(const TokensArgs& a, int b, int nq, uint64_t (&m)[2]) {
-  const int lane = threadIdx.x & 31;
-  const int32_t* parents = a.parents + b * a.parents_stride;
-  int p[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int t = lane + 32 * x;
-    p[x] = t < nq ? parents[t] : -1;
-    if (p[x] >= t) p[x] = -1;                        // not before it: none
-    m[x] = 1ull << t;
-  }
-#pragma unroll 1
-  for (int step = 1; step < 64; step *= 2) {
-    uint64_t um[2];
-    int up[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint64_t m0 = __shfl_sync(~0u, m[0], p[x] & 31), m1 = __shfl_sync(~0u, m[1], p[x] & 31);
-      const int p0 = __shfl_sync(~0u, p[0], p[x] & 31), p1 = __shfl_sync(~0u, p[1], p[x] & 31);
-      um[x] = p[x] < 0 ? m[x] : m[x] | (p[x] < 32 ? m0 : m1);
-      up[x] = p[x] < 0 ? -1 : p[x] < 32 ? p0 : p1;
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      m[x] = um[x];
-      p[x] = up[x];
-    }
-  }
-}
-
 // The low `left` of 32 bits.
 __device__ __forceinline__ uint32_t low_bits(int left) { return left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u; }
 
 template <typename T, int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_tokens_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+    attend_tokens_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
                          const __grid_constant__ Params p) {
   using Gm = Geo<D, PAIR>;
@@ -400,23 +343,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const TokensArgs& a = p.a;
-  const int N = a.G / a.H;
 
   launch_dependents();
   if (tid == 0) {
+#pragma unroll 1
     for (int s = 0; s < NS; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 3);          // the products, and either helper warp
       mbar_init(mended(s), 2);
     }
+#pragma unroll 1
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full(w), 1);
       mbar_init(o_done(w), 1);
-      mbar_init(q_full(w), 2);
+      mbar_init(q_full(w), 1);
       mbar_init(q_free(w), 1);
       mbar_init(p_full(w, 0), 4);
       mbar_init(p_full(w, 1), 4);
     }
+#pragma unroll 1
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(seg_full(i), 1);
       mbar_init(seg_empty(i), 11);     // all warps but the producer's
@@ -427,16 +372,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
   }
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kTmem);
-  __shared__ int64_t sums_s[kThreads / 32];
-  __shared__ TokensAt ends_s[2];
+  // The query rows that no box brings are zeros: what lies there could send their warp the
+  // way of logits that are not finite.
+  for (int x = tid; x < 2 * Gm::KH * (kT - a.N * a.half) * 8; x += kThreads) {
+    const int c = x & 7, h = (x >> 3) % (2 * Gm::KH), r = a.N * a.half + (x >> 3) / (2 * Gm::KH);
+    *reinterpret_cast<uint4*>(smem + Gm::Q + h * Gm::HALFB + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  // a half block's rows: token and query head
+  uint32_t* const row_of = reinterpret_cast<uint32_t*>(smem + Gm::ROWS);
+  if (warp >= 8) {
+    const unsigned r = tid - 256, t = r / (unsigned)a.N;
+    row_of[r] = t << 16 | (r - t * a.N);
+  }
+  // (where outputs are staged: the producer has its range before it tells of any block)
+  int64_t* const sums_s = reinterpret_cast<int64_t*>(smem + Gm::STAGE);
+  TokensAt* const ends_s = reinterpret_cast<TokensAt*>(sums_s + kThreads / 32);
   find_range(a, p.plan, sums_s, ends_s);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   if (tid == 0 && !p.plan.whole) {
     p.first[blockIdx.x] = ends_s[0];
     if (blockIdx.x == gridDim.x - 1) p.first[gridDim.x] = ends_s[1];
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // TMEM columns: O of stream w at 128 w, S (and P over it) at 256 + 128 w
   auto tm_o = [&](int w) { return tmem + (uint32_t)(kT * w); };
@@ -495,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const Coords& c = value ? (own ? p.at.v : p.at.vn) : (own ? p.at.k : p.at.kn);
               const int row = own ? g.first + i * kT : g.tok0 + (g.kb + i) * kT;
               for (int kh = 0; kh < Gm::KH; ++kh)
-                tma_load_rows(base + Gm::RING + s * Gm::TILEB + kh * Gm::HALFB, map, c, kh * 64, row, g.h, g.b, full(s));
+                tma_load_rows(base + Gm::RING + s * Gm::TILEB + kh * Gm::HALFB, map, c, kh * 64, row, g.kv, g.b, full(s));
             }
             stall = false;
             held = min(held + 1, NS);
@@ -525,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vd = sw128_mn_desc(base + Gm::RING, Gm::HALFB);
       int next = 0;                      // ring stage and its phase
       uint32_t phase = 0, mend_phase = 0;   // (of each stage, a bit)
-      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};   // weights tiles and (not PAIR) query blocks consumed, per stream
+      uint32_t np = 0, nq = 0;           // phases of the weights, and (not PAIR) queries, of either stream: a bit each
       for (const Seg* sg; (sg = take()); give()) {
         if (!ok) continue;
         const Seg g = *sg;
@@ -533,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto tile = [&](bool value, int i) -> int {   // the next ring stage, once its tile is there; -1 on abort
           const int s = next;
           bool here;
-          if (mends(a, g, value, i)) {
+          if (__builtin_expect(mends(a, g, value, i), 0)) {
             here = wait_or_abort(mended(s), (mend_phase >> s) & 1, abort_flag, p.err);
             mend_phase ^= 1u << s;
           } else {
@@ -564,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t vb = vd + (uint64_t)(s * (Gm::TILEB >> 4));
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (!__all_sync(~0u, wait_or_abort(p_full(w, c), np[w] & 1, abort_flag, p.err))) return false;
+            if (!__all_sync(~0u, wait_or_abort(p_full(w, c), np >> w & 1, abort_flag, p.err))) return false;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -575,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             vb + (uint64_t)((4 * c + kk) * (2048 >> 4)), kIdO, !(first && c + kk + part == 0));
             }
           }
-          ++np[w];
+          np ^= 1u << w;
           return true;
         };
         auto queries = [&](int x, uint32_t count) {
@@ -583,22 +542,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           return here;
         };
-        int s;
+        // (one place for either product, in the code: instructions that are not in the
+        // SM's cache cost more than the loops)
         if (PAIR) {
           if (!(ok = queries(seg & 1, (uint32_t)seg >> 1))) continue;
-          for (int i = 0; i < min(n, 2) && ok; ++i) {
-            ok = (s = tile(false, i)) >= 0;
-            if (ok) mma_s(i, s), commit(empty(s));
-          }
-          if (n <= 2) commit(q_free(seg & 1));
-          for (int i = 0; i < n && ok; ++i) {
+#pragma unroll 1
+          for (int i = -2; i < n; ++i) {
             const int w = i & 1;
-            if (!(ok = (s = tile(true, i)) >= 0)) break;
-            if (!(ok = mma_o(w, s, i < 2))) break;
-            commit(empty(s));
-            if (i + 2 >= n) commit(o_done(w));
+            if (i >= 0) {
+              const int s = tile(true, i);
+              if (!(ok = s >= 0) || !(ok = mma_o(w, s, i < 2))) break;
+              commit(empty(s));
+              if (i + 2 >= n) commit(o_done(w));
+            }
             if (i + 2 < n) {
-              if (!(ok = (s = tile(false, i + 2)) >= 0)) break;
+              const int s = tile(false, i + 2);
+              if (!(ok = s >= 0)) break;
               mma_s(w, s);
               commit(empty(s));
               if (i + 3 == n) commit(q_free(seg & 1));
@@ -606,33 +565,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           // (the softmax warps give the stages back)
-          const int n0 = g.n[0], n1 = g.n[1];
-          if (!(ok = (s = tile(false, 0)) >= 0)) continue;
-          if (n0 > 0) {
-            if (!(ok = queries(0, nq[0]++))) continue;
-            mma_s(0, s);
-            if (n0 == 1) commit(q_free(0));
-          }
-          if (n1 > 0) {
-            if (!(ok = queries(1, nq[1]++))) continue;
-            mma_s(1, s);
-            if (n1 == 1) commit(q_free(1));
-          }
-          for (int i = 0; i < n && ok; ++i) {
-            const bool more = i + 1 < n;
-            int sk = 0;
-            if (!(ok = (s = tile(true, i)) >= 0)) break;
-            if (i < n0 && !(ok = mma_o(0, s, i == 0))) break;
-            if (more) {
-              if (!(ok = (sk = tile(false, i + 1)) >= 0)) break;
-              if (i + 1 < n0) mma_s(0, sk);
-              if (i + 2 == n0) commit(q_free(0));
+#pragma unroll 1
+          for (int i = -1; i < n && ok; ++i) {
+            int s = 0, sk = 0;
+            if (i >= 0 && !(ok = (s = tile(true, i)) >= 0)) break;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int nw = w ? g.n[1] : g.n[0];
+              if (i >= 0 && i < nw && !(ok = mma_o(w, s, i == 0))) break;
+              if (w == 0 && i + 1 < n && !(ok = (sk = tile(false, i + 1)) >= 0)) break;
+              if (i + 1 < nw) {
+                if (i < 0) {
+                  if (!(ok = queries(w, nq >> w & 1))) break;
+                  nq ^= 1u << w;
+                }
+                mma_s(w, sk);
+                if (i + 2 == nw) commit(q_free(w));
+              } else if (i + 1 == nw && i >= 0) {
+                commit(o_done(w));
+              }
             }
-            if (i == n0 - 1) commit(o_done(0));
-            if (i < n1 && !(ok = mma_o(1, s, i == 0))) break;
-            if (more && i + 1 < n1) mma_s(1, sk);
-            if (i + 2 == n1) commit(q_free(1));
-            if (i == n1 - 1) commit(o_done(1));
           }
         }
       }
@@ -640,10 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- queries, tile mending
       const int ht = (warp - 2) * 32 + lane;         // of 64 threads
       int next = 0;
-      uint32_t phase = 0, nq[2] = {0, 0};
-      // queries: a thread has one 16-byte piece of every QS-th row
-      constexpr int QP = D / 8, QS = 64 / QP;
-      const int qc = ht % QP, qr = ht / QP, step_t = QS / N, step_j = QS - step_t * N;
+      uint32_t phase = 0;
+      int queries[2] = {0, 0};           // that either place has had
       // re-rotation: a thread has one 16-byte piece of a row's first half and its pair
       constexpr int PC = D / 16, PER = 64 / PC;      // pieces, rows at a time
       const int pc = ht % PC, pr = ht / PC;
@@ -653,34 +603,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (const Seg* sg; (sg = take()); give()) {
         if (!ok) continue;
         const Seg g = *sg;
-        // A query block sets out when its place is free: when the last logits there are
-        // done, while their softmax and the last products run.
-#pragma unroll
+        // Queries set out when their place is free: when the last logits there are done,
+        // while their softmax and the last products run.
+#pragma unroll 1
         for (int w = 0; w < (PAIR ? 1 : 2); ++w) {
-          if (g.n[w] == 0 || !ok) continue;
+          if ((w ? g.n[1] : g.n[0]) == 0) continue;
           const int x = PAIR ? seg & 1 : w;
-          const uint32_t count = PAIR ? (uint32_t)seg >> 1 : nq[w]++;
-          if (count > 0) ok = __all_sync(~0u, wait_or_abort(q_free(x), (count - 1) & 1, abort_flag, p.err));
-          if (!ok) continue;
-          const int rows = g.nq * N, first = g.row0 + w * kT + qr;
-          int t = (int)((unsigned)first / (unsigned)N), j = first - t * N;
-          const T* const q = static_cast<const T*>(a.q) + g.b * a.q_stride[0] + (int64_t)g.h * N * a.q_stride[2] + 8 * qc;
-          const uint32_t to = base + Gm::Q + x * Gm::TILEB + (qc >> 3) * Gm::HALFB;
-#pragma unroll 4
-          for (int r = qr; r < kT; r += QS) {
-            const bool on = first - qr + r < rows;   // (the rest zeros)
-            const T* const from = q + (on ? (int64_t)(g.tok0 + t) * a.q_stride[1] + j * a.q_stride[2] : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + r * 128 + (((qc ^ r) & 7) << 4)), "l"(from),
-                         "r"(on ? 16 : 0)
-                         : "memory");
-            t += step_t;
-            j += step_j;
-            if (j >= N) j -= N, ++t;
+          const int had = x ? queries[1]++ : queries[0]++;
+          if (had && !(ok = __all_sync(~0u, wait_or_abort(q_free(x), (had - 1) & 1, abort_flag, p.err)))) break;
+          if (ht == 0) {
+            mbar_expect_tx(q_full(x), Gm::KH * 128 * a.N * a.half);
+            for (int kh = 0; kh < Gm::KH; ++kh)
+              tma_load_rows(base + Gm::Q + x * Gm::TILEB + kh * Gm::HALFB, &qmap, p.at.q, kh * 64, g.tok0 + g.tok + w * a.half,
+                            g.h * a.N, g.b, q_full(x));
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full(x));
         }
         auto visit = [&](bool value, int i) {
           const int s = next;
@@ -736,6 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = visit(value, i);
         }
       }
+      if (ht == 0 && *abort_flag)        // let queries in flight land before the CTA leaves
+        for (int x = 0; x < 2; ++x)
+          if (queries[x]) (void)mbar_wait_bounded(q_full(x), (queries[x] - 1) & 1, 10000000ull);
     }
   } else {
     // ---------------------------------------------------------------- softmax warpgroups
@@ -753,13 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto release = [&](int nth) {
       if (lane == 0 && (warp & 3) == 0) mbar_arrive(empty((ring + nth) % NS));
     };
-    // this thread's row of a segment: its token, its query head, whether it is there
-    auto place = [&](const Seg& g, int& t, int& head) {
-      const int r = g.row0 + (PAIR ? 0 : w * kT) + row, rows = g.nq * N, x = min(r, rows - 1);
-      t = (int)((unsigned)x / (unsigned)N);
-      head = g.h * N + x - t * N;
-      return r < rows;
-    };
+    // this thread's row of a half block: a token's place in it and a query head
+    const int row_t = (int)((unsigned)row / (unsigned)a.N), row_h = row - row_t * a.N;
     // a tree: the tokens that token t sees, as bits (warp-collective)
     auto seen_of = [&](const Seg& g, int t) {
       uint64_t anc[2];
@@ -771,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Seg& g = *sg;
       const int n = g.n[w], part = g.part, hole = g.hole, mask = g.mask, tiles = g.tiles;
       const bool releases = !PAIR && (w == 1 ? n > 0 : g.n[1] == 0);
-      int t, head;
-      const bool valid = place(g, t, head);
+      const int tok = g.tok + (PAIR ? 0 : w * a.half), t = min(tok + row_t, g.nq - 1);
+      const bool valid = row_t < a.half && tok + row_t < g.nq;
       float m = kNegInf, l = 0.f;
       bool begun = false;
       const uint32_t ts = tm_s(w) + lanes, to = tm_o(w) + lanes;
@@ -905,6 +839,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (releases) release(2 * n - 1);
       }
       ring = (ring + 2 * tiles) % NS;
+      const bool poisoned = marks[seg % kSegs] == seg;
+      if (__builtin_expect(poisoned && begun, 0)) {
+        // values that are not finite, dropped from the tiles that rows see in part
+        const uint64_t seen = a.parents ? seen_of(g, t) : 0;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float x[16];
+          tmem_ld16(to + c, x);
+#pragma unroll 1
+          for (int j = (g.kb + max(g.own, g.mask)) * kT; j < min((g.kb + g.tiles) * kT, t + 1); ++j) {
+            // (PAIR: of this stream's tiles)
+            if ((a.parents && !((seen >> j) & 1)) || (PAIR && ((j / kT - g.kb) & 1) != w)) continue;
+            const T* src = static_cast<const T*>(a.v_new) + g.b * a.vn_stride[0] + (int64_t)(g.tok0 + j) * a.vn_stride[1] +
+                           g.kv * a.vn_stride[2] + c;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint32_t word = *reinterpret_cast<const uint32_t*>(src + e), f = not_finite<T>(word);
+              const float2 y = unpack16<T>(word);
+              if (f & 0x8000u) x[e] += y.x;
+              if (f & 0x80000000u) x[e + 1] += y.y;
+            }
+          }
+          uint32_t o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(x[e]);
+          tmem_st16(to + c, o);
+        }
+        tmem_st_wait();
+      }
       float f0 = 1.f, f1 = 0.f;
       if (!ok) l = __int_as_float(0x7FFFFFFF);       // NaN: this row's result is lost
       if (PAIR) {
@@ -922,7 +885,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         f1 = y.x == m ? 1.f : ex2(y.x - m);
         l = x.y * f0 + y.y * f1;
       }
-      const bool poisoned = marks[seg % kSegs] == seg;
       constexpr int CW = Gm::CW;
       auto columns = [&](int c, float (&v)[CW]) {    // O's columns c .. c + CW - 1 of this row
         const uint32_t at = tmem + lanes + c;
@@ -940,25 +902,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e) v[e] = fmaf(y[e], f1, v[e] * f0);
           }
         }
-        if (__builtin_expect(poisoned, 0)) {
-          // values that are not finite, dropped from the tiles that rows see in part
-          const uint64_t seen = a.parents ? seen_of(g, t) : 0;
-          for (int i = max(g.own, g.mask); i < g.tiles; ++i) {
-            const int j0 = (g.kb + i) * kT;
-            for (int j = j0; j < min(j0 + kT, t + 1); ++j) {
-              if (a.parents && !((seen >> j) & 1)) continue;
-              const T* src = static_cast<const T*>(a.v_new) + g.b * a.vn_stride[0] + (int64_t)(g.tok0 + j) * a.vn_stride[1] +
-                             g.h * a.vn_stride[2] + c;
-#pragma unroll
-              for (int e = 0; e < CW; e += 2) {
-                const uint32_t word = *reinterpret_cast<const uint32_t*>(src + e), f = not_finite<T>(word);
-                const float2 x = unpack16<T>(word);
-                if (f & 0x8000u) v[e] += x.x;
-                if (f & 0x80000000u) v[e + 1] += x.y;
-              }
-            }
-          }
-        }
       };
       constexpr int COLS = PAIR ? D / 2 : D;         // this warpgroup's columns, from `begin` on
       const int begin = PAIR ? w * COLS : 0;
@@ -969,13 +912,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto staged = [&](int r, int c) {
           return reinterpret_cast<uint4*>(stage + r * (CW * 2) + (((PR == 8 ? c ^ r : c ^ (r >> 1)) & (PR - 1)) << 4));
         };
-        T* const out = static_cast<T*>(a.out);
-        const int64_t offset = g.b * a.out_stride[0] + (int64_t)(g.tok0 + t) * a.out_stride[1] + head * a.out_stride[2];
-        // where the rows go that this lane has pieces of
+        T* const out = static_cast<T*>(a.out) + g.b * a.out_stride[0] + (int64_t)(g.tok0 + tok) * a.out_stride[1] +
+                       (int64_t)g.h * a.N * a.out_stride[2];
         const unsigned rows_on = __ballot_sync(~0u, valid);
-        int64_t row_at[PR];
-#pragma unroll
-        for (int x = 0; x < PR; ++x) row_at[x] = __shfl_sync(~0u, offset, x * (32 / PR) + lane / PR);
 #pragma unroll 1
         for (int c0 = begin; c0 < begin + COLS; c0 += CW) {
           float v[CW];
@@ -990,13 +929,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < PR; ++x) y[x] = *staged(x * (32 / PR) + lane / PR, lane % PR);
 #pragma unroll
-          for (int x = 0; x < PR; ++x)
-            if ((rows_on >> (x * (32 / PR) + lane / PR)) & 1u)
-              *reinterpret_cast<uint4*>(out + row_at[x] + c0 + 8 * (lane % PR)) = y[x];
+          for (int x = 0; x < PR; ++x) {
+            const int r = x * (32 / PR) + lane / PR;
+            const uint32_t th = row_of[(warp & 3) * 32 + r];
+            if ((rows_on >> r) & 1u)
+              *reinterpret_cast<uint4*>(out + (th >> 16) * a.out_stride[1] + (th & 0xFFFFu) * a.out_stride[2] + c0 + 8 * (lane % PR)) = y[x];
+          }
           __syncwarp();
         }
         if (valid && a.lse && !(PAIR && w))
-          a.lse[((a.starts ? (int64_t)g.tok0 : (int64_t)g.b * a.S) + t) * a.G + head] =
+          a.lse[((a.starts ? (int64_t)g.tok0 : (int64_t)g.b * a.S) + t) * a.G + g.h * a.N + row_h] =
               l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
       } else {
         const int64_t slot = 2 * blockIdx.x + g.from_start;
@@ -1063,9 +1005,9 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(const __grid_constant_
     o = make_float4(o.x * f + v.x * h, o.y * f + v.y * h, o.z * f + v.z * h, o.w * f + v.w * h);
   }
   const Seq s = load_seq(a, x.b);
-  const int N = a.G / a.H, r = x.i * R + rr;
-  if (r >= s.nq * N) return;
-  const int t = r / N, head = x.h * N + r - t * N;
+  const int r = rr & (kT - 1), rt = (int)((unsigned)r / (unsigned)a.N), head = x.h * a.N + r - rt * a.N;
+  const int t = x.i * block_tokens(a, p.plan) + (rr / kT) * a.half + rt;
+  if (rt >= a.half || t >= s.nq) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* dst = static_cast<T*>(a.out) + x.b * a.out_stride[0] + (int64_t)(s.tok0 + t) * a.out_stride[1] + head * a.out_stride[2] + 4 * d4;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * inv, o.y * inv), pack16<T>(o.z * inv, o.w * inv));
@@ -1076,6 +1018,7 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(const __grid_constant_
 
 template <typename Elem, int Dim, bool Pair>
 struct Kind {
+  static_assert(Geo<Dim, Pair>::SMEM <= 227 * 1024, "shared memory of a block");
   using T = Elem;
   static constexpr int D = Dim, SMEM = Geo<Dim, Pair>::SMEM;
   static constexpr auto kernel = attend_tokens_kernel<Elem, Dim, Pair>;
@@ -1090,37 +1033,18 @@ auto pick(int D, int dtype, bool pair, F&& f) {
   return pair ? f(Kind<__half, 128, true>{}) : f(Kind<__half, 128, false>{});
 }
 
-// Rows as a 4-D tensor, the dimensions in the order of their strides (one that all
-// share, or of a single entry, last and of extent 1); boxes of 64 elements (128 bytes) x
-// 128 rows; rows past the last read as zeros.
-bool encode_rows(CUtensorMap* map, const TokensRows& r, int D, int dtype, Coords* c) {
+// Rows as a 4-D tensor [sequence, row, head, D], whatever the strides (a dimension of one
+// entry, or that all share, with any); boxes of 64 elements (128 bytes) of so many heads
+// and rows; rows past the last read as zeros.
+bool encode_rows(CUtensorMap* map, const TokensRows& r, int heads, int rows, int D, int dtype, Coords* c) {
   auto enc = encode_fn();
   if (!enc) return false;
-  struct Dim {
-    int64_t stride, extent;
-    int what;                // 0 rows, 1 heads, 2 sequences
-  } d[3] = {{r.rows == 1 ? D : r.stride[2], r.rows, 0}, {r.stride[1], r.H, 1}, {r.stride[0], r.B, 2}};
-  c->hm = r.H > 1 && r.stride[1] != 0;
-  c->bm = r.B > 1 && r.stride[0] != 0;
-  if (!c->hm) d[1].extent = 1;
-  if (!c->bm) d[2].extent = 1;
-  int64_t top = d[0].stride;
-  for (int i = 1; i < 3; ++i)
-    if (d[i].extent > 1) top = std::max(top, d[i].stride);
-  for (int i = 1; i < 3; ++i)
-    if (d[i].extent == 1) d[i].stride = top;
-  std::stable_sort(d, d + 3, [](const Dim& x, const Dim& y) {
-    return (x.extent == 1 && x.what) != (y.extent == 1 && y.what) ? !(x.extent == 1 && x.what) : x.stride < y.stride;
-  });
-  cuuint64_t dims[4] = {(cuuint64_t)D}, strides[3];
-  cuuint32_t box[4] = {64, 1, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  for (int i = 0; i < 3; ++i) {
-    dims[i + 1] = (cuuint64_t)d[i].extent;
-    strides[i] = (cuuint64_t)d[i].stride * 2;
-    (d[i].what == 0 ? c->row : d[i].what == 1 ? c->h : c->b) = i;
-    if (d[i].what == 0) box[i + 1] = kT;
-  }
+  c->h = r.H > 1 && r.stride[1] != 0;
+  c->b = r.B > 1 && r.stride[0] != 0;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(c->h ? r.H : 1), (cuuint64_t)r.rows, (cuuint64_t)(c->b ? r.B : 1)};
+  const cuuint64_t strides[3] = {(cuuint64_t)(c->h ? r.stride[1] : D) * 2, (cuuint64_t)(r.rows > 1 ? r.stride[2] : D) * 2,
+                                 (cuuint64_t)(c->b ? r.stride[0] : D) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1}, estr[4] = {1, 1, 1, 1};
   return enc(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
              const_cast<void*>(r.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1128,14 +1052,15 @@ bool encode_rows(CUtensorMap* map, const TokensRows& r, int D, int dtype, Coords
 
 }  // namespace
 
-TokensPlan tokens_plan(int B, int64_t rows, int64_t blocks, int H, int64_t tiles, int sms) {
+TokensPlan tokens_plan(bool pair, int64_t blocks, int heads, int64_t tiles, int sms) {
   TokensPlan pl{};
-  pl.pair = rows <= kT;
+  pl.pair = pair;
   pl.block_rows = pl.pair ? kT : 2 * kT;
-  const int64_t units = blocks * H;
+  const int64_t units = blocks * heads;
   // Few short blocks: one a CTA, no join.
   pl.whole = pl.even = units <= sms && tiles <= 6;
   pl.ctas = (int)std::min<int64_t>(sms, pl.whole ? units : units * tiles);
+  pl.per_cta = 1.0 / pl.ctas;
   return pl;
 }
 
@@ -1171,15 +1096,16 @@ cudaError_t launch_attend_tokens(const TokensLaunch& l, int D, int dtype, cudaSt
     p.part_ml = reinterpret_cast<float2*>(space + l.plan.o_bytes(D));
     p.first = reinterpret_cast<TokensAt*>(space + l.plan.o_bytes(D) + l.plan.ml_bytes());
   }
-  CUtensorMap kmap{}, vmap{}, knmap{}, vnmap{};
-  if (!encode_rows(&knmap, l.k_new, D, dtype, &p.at.kn) || !encode_rows(&vnmap, l.v_new, D, dtype, &p.at.vn))
+  CUtensorMap qmap{}, kmap{}, vmap{}, knmap{}, vnmap{};
+  if (!encode_rows(&qmap, l.q, l.a.N, l.a.half, D, dtype, &p.at.q) || !encode_rows(&knmap, l.k_new, 1, kT, D, dtype, &p.at.kn) ||
+      !encode_rows(&vnmap, l.v_new, 1, kT, D, dtype, &p.at.vn))
     return cudaErrorInvalidValue;
   if (l.a.n + (l.a.pend ? 1 : 0) > 0 &&
-      (!encode_rows(&kmap, l.k, D, dtype, &p.at.k) || !encode_rows(&vmap, l.v, D, dtype, &p.at.v)))
+      (!encode_rows(&kmap, l.k, 1, kT, D, dtype, &p.at.k) || !encode_rows(&vmap, l.v, 1, kT, D, dtype, &p.at.v)))
     return cudaErrorInvalidValue;
   return pick(D, dtype, l.plan.pair, [&](auto kind) {
     using K = decltype(kind);
-    K::kernel<<<l.plan.ctas, kThreads, K::SMEM, s>>>(kmap, vmap, knmap, vnmap, p);
+    K::kernel<<<l.plan.ctas, kThreads, K::SMEM, s>>>(qmap, kmap, vmap, knmap, vnmap, p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || l.plan.whole || l.plan.ctas < 2) return e;
     const dim3 grid(l.plan.ctas - 1, l.plan.block_rows / 32, K::D / 32);

@@ -5,10 +5,13 @@
 #include "attend_tokens.cuh"
 #include "entry.cuh"
 
+#include <atomic>
 #include <cmath>
 
 namespace kvx {
 namespace {
+
+std::atomic<bool> g_without_few{false};   // test hook
 
 int tokens_check(const kvevict_tokens* d, bool tree) {
   if (!d) return invalid("args must not be null");
@@ -40,11 +43,19 @@ bool map_strides_fit(const int64_t (&s)[3], int B, int H, int64_t rows, int row,
          (rows <= 1 || (s[row] >= D && s[row] < top));
 }
 
+// Query heads of a key head in groups of at most 128.
+int head_groups(int N) {
+  int c = 1;
+  while (N % c || N / c > 128) ++c;
+  return c;
+}
+
 TokensPlan plan_of(const kvevict_tokens* d, int64_t n, const DeviceInfo& dev) {
-  const int64_t N = d->n_heads / d->n_kv_heads, rows = d->seq * N;
-  auto blocks = [&](int64_t per) { return d->starts ? rows / per + d->batch : d->batch * ((rows + per - 1) / per); };
-  return tokens_plan(d->batch, rows, blocks(rows <= 128 ? 128 : 256), d->n_kv_heads, (n + 127) / 128 + (d->seq + 127) / 128,
-                     dev.sms);
+  const int all = d->n_heads / d->n_kv_heads, groups = head_groups(all), half = 128 / (all / groups);
+  const bool pair = d->seq <= half;
+  const int64_t per = pair ? half : 2 * half;
+  const int64_t blocks = d->starts ? d->seq / per + d->batch : d->batch * ((d->seq + per - 1) / per);
+  return tokens_plan(pair, blocks, d->n_kv_heads * groups, (n + 127) / 128 + (d->seq + 127) / 128, dev.sms);
 }
 
 }  // namespace
@@ -74,13 +85,14 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
       (d->n > 0 && (!map_strides_fit(d->k_stride, d->batch, d->n_kv_heads, d->n, 2, D) ||
                     !map_strides_fit(d->v_stride, d->batch, d->n_kv_heads, d->n, 2, D))))
     return invalid("strides of keys and values must be >= 0, between tokens and rows at least head_dim, and below 2^39");
+  if (!map_strides_fit(d->q_stride, B, d->n_heads, d->seq, 1, D) || (d->n_heads > 1 && d->q_stride[2] < D))
+    return invalid("strides of q must be >= 0, between tokens and heads at least head_dim, and below 2^39");
   if (!aligned(d->lse, 4) || !aligned(d->starts, 4) || !aligned(d->new_lens, 4) || !aligned(d->parents, 4) || !aligned(d->lens, 4))
     return invalid("lse, starts, new_lens, parents and lens must be 4-byte aligned");
   DeviceInfo dev;
   if (int rc = device_info(&dev)) return rc;
   TokensLaunch l{};
   TokensArgs& a = l.a;
-  a.q = d->q;
   a.out = d->out;
   a.lse = d->lse;
   a.v_new = d->v_new;
@@ -91,33 +103,56 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
   a.B = d->batch;
   a.S = d->seq;
   a.G = d->n_heads;
-  a.H = d->n_kv_heads;
+  a.groups = head_groups(d->n_heads / d->n_kv_heads);
+  a.heads = d->n_kv_heads * a.groups;
+  a.N = a.G / a.heads;
+  a.half = 128 / a.N;
   for (int i = 0; i < 3; ++i) {
     const bool on = i > 0 || !d->starts;                              // packed: no stride between sequences
-    a.q_stride[i] = on ? d->q_stride[i] : 0;
     a.out_stride[i] = on ? d->out_stride[i] : 0;
     a.vn_stride[i] = on ? d->v_new_stride[i] : 0;
   }
-  l.k_new = TokensRows{d->k_new, {d->k_new_stride[0], d->k_new_stride[2], d->k_new_stride[1]}, B, a.H, a.S};
-  l.v_new = TokensRows{d->v_new, {d->v_new_stride[0], d->v_new_stride[2], d->v_new_stride[1]}, B, a.H, a.S};
+  l.q = TokensRows{d->q, {d->q_stride[0], d->q_stride[2], d->q_stride[1]}, B, a.G, a.S};
+  l.k_new = TokensRows{d->k_new, {d->k_new_stride[0], d->k_new_stride[2], d->k_new_stride[1]}, B, d->n_kv_heads, a.S};
+  l.v_new = TokensRows{d->v_new, {d->v_new_stride[0], d->v_new_stride[2], d->v_new_stride[1]}, B, d->n_kv_heads, a.S};
   if (rows) {
     a.n = rows->n;
     a.pend = rows->pend;
     a.rope_c = rows->rope_c;
     a.rope_s = rows->rope_s;
-    l.k = TokensRows{rows->k, {rows->stride[0], rows->stride[1], rows->stride[2]}, a.B, a.H, (int64_t)a.n + 1};
+    l.k = TokensRows{rows->k, {rows->stride[0], rows->stride[1], rows->stride[2]}, a.B, d->n_kv_heads, (int64_t)a.n + 1};
     l.v = l.k;
     l.v.base = rows->v;
     l.err = rows->err;
   } else {
     a.n = d->n;
     a.lens = d->n > 0 ? d->lens : nullptr;
-    l.k = TokensRows{d->k, {d->k_stride[0], d->k_stride[1], d->k_stride[2]}, a.B, a.H, a.n};
-    l.v = TokensRows{d->v, {d->v_stride[0], d->v_stride[1], d->v_stride[2]}, a.B, a.H, a.n};
+    l.k = TokensRows{d->k, {d->k_stride[0], d->k_stride[1], d->k_stride[2]}, a.B, d->n_kv_heads, a.n};
+    l.v = TokensRows{d->v, {d->v_stride[0], d->v_stride[1], d->v_stride[2]}, a.B, d->n_kv_heads, a.n};
   }
   const double scale = d->scale > 0.f ? (double)d->scale : 1.0 / std::sqrt((double)D);
   a.scale2 = (float)(scale * 1.4426950408889634);
-  l.plan = plan_of(d, (int64_t)a.n + (a.pend ? 1 : 0), dev);
+  const int64_t all = (int64_t)a.n + (a.pend ? 1 : 0);
+  const FewPlan few = few_plan(d->batch, (int64_t)d->seq * (d->n_heads / d->n_kv_heads), d->starts != nullptr, d->n_kv_heads, all,
+                               d->seq, dev.sms);
+  if (few.use && !g_without_few.load(std::memory_order_relaxed)) {
+    FewArgs f{};
+    f.q = d->q;
+    f.k = l.k.base;
+    f.v = l.v.base;
+    f.k_new = d->k_new;
+    for (int i = 0; i < 3; ++i) {
+      const bool on = i > 0 || !d->starts;
+      f.q_stride[i] = on ? d->q_stride[i] : 0;
+      f.kn_stride[i] = on ? d->k_new_stride[i] : 0;
+      f.k_stride[i] = l.k.stride[i];
+      f.v_stride[i] = l.v.stride[i];
+    }
+    f.H = d->n_kv_heads;
+    f.chunks = (int)few.chunks;
+    return cuda_result(launch_attend_tokens_few(a, f, few, D, d->dtype, s), "launch");
+  }
+  l.plan = plan_of(d, all, dev);
   if (!tokens_kernel_ready(D, d->dtype, l.plan.pair, dev.device)) {
     set_last_error("the attention kernel cannot be launched here: no tensor maps, or another register count than it needs");
     return KVEVICT_ERR_CUDA;
@@ -192,6 +227,11 @@ extern "C" int kvevict_attend_tokens_workspace(const kvevict_tokens* args, int32
     *bytes = kvx::plan_of(args, with_cache ? 1 << 29 : args->n, dev).bytes(args->head_dim);
     return KVEVICT_OK;
   });
+}
+
+extern "C" int kvevict_test_without_few_kernel(int32_t without) {
+  kvx::g_without_few.store(without != 0);
+  return KVEVICT_OK;
 }
 
 extern "C" int kvevict_attend_join(const kvevict_join* args, void* stream) {

@@ -9,13 +9,15 @@ pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
 
 
-@pytest.fixture(scope="module")
-def kvx():
+@pytest.fixture(scope="module", params=["chosen", "tensor"])
+def kvx(request):
+    """By the kernel that the library chooses (another one for few query rows), and all by the tensor cores'."""
     import kv_cache_attention_02_gb300 as k
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
-    k.lib()
-    return k
+    k.lib().kvevict_test_without_few_kernel(request.param == "tensor")
+    yield k
+    k.lib().kvevict_test_without_few_kernel(0)
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])

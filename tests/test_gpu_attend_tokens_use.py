@@ -18,13 +18,16 @@ F16, BF16 = torch.float16, torch.bfloat16
 NAN, INF = float("nan"), math.inf
 
 
-@pytest.fixture(scope="module")
-def kvx():
+@pytest.fixture(scope="module", params=["chosen", "tensor"])
+def kvx(request):
+    """By the kernel that the library chooses (another one for few query rows), and all by the tensor cores'."""
     import kv_cache_attention_02_gb300 as k
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
-    k.lib()
-    return k
+    k.lib().kvevict_test_without_few_kernel(request.param == "tensor")
+    k.all_tensor = request.param == "tensor"
+    yield k
+    k.lib().kvevict_test_without_few_kernel(0)
 
 
 # (blocks of 128 query rows, of 256, cut ones)
@@ -315,6 +318,8 @@ def test_empty_calls_and_sequences(kvx):
 def test_a_wait_that_runs_out(kvx, B, S, N, H, D, n):
     """NaN where the lost tile belongs, what is elsewhere right, and the next call as ever. (The library's test hook leaves one
     copy unissued: the bounded wait runs out, nothing hangs.)"""
+    if not kvx.all_tensor:
+        pytest.skip("the kernel for few query rows waits for nothing")
     q, args = make(B, S, N, H, D, n=n, seed=3)
     want, wlse = tref.check("call", kvx.attend_prompt, q, **args)
     out, lse = torch.zeros_like(q), torch.zeros_like(wlse)
@@ -419,6 +424,8 @@ def test_handle_refusals(kvx):
 
 
 def test_a_wait_that_runs_out_on_a_handle(kvx):
+    if not kvx.all_tensor:
+        pytest.skip("the kernel for few query rows waits for nothing")
     h = kvx.KVEvict(batch=1, n_layers=1, n_kv_heads=2, head_dim=64, avg_budget=16, max_prefill=8, with_values=True)
     q, args = make(1, 5, 2, 2, 64)
     want, out = torch.empty_like(q), torch.zeros_like(q)
