@@ -85,8 +85,8 @@ struct FewPlan {
   int cluster;
   bool use;
 };
-// Taken where a warp has at most this many tiles of 16 keys, over all waves of CTAs.
-constexpr int kFewTiles = 8;
+// Taken where all CTAs run at once and a warp has at most this many tiles of 16 keys.
+constexpr int kFewTiles = 24;
 FewPlan few_plan(int64_t B, int64_t rows, bool packed, int H, int64_t n, int64_t tokens, int sms);
 cudaError_t launch_attend_tokens_few(const TokensArgs& a, const FewArgs& f, const FewPlan& p, int D, int dtype, cudaStream_t s);
 
@@ -147,7 +147,7 @@ __device__ __forceinline__ void ancestors(const TokensArgs& a, int b, int nq, ui
     m[x] = 1ull << t;
   }
 #pragma unroll 1
-  for (int step = 1; step < 64; step *= 2) {
+  for (int step = 1; step < nq; step *= 2) {
     uint64_t um[2];
     int up[2];
 #pragma unroll
