@@ -73,6 +73,7 @@ struct Params {
   TokensAt* first;         // [ctas + 1]
   int* err;
   int stall;
+  int out_box;             // a warp's 32 query rows are whole tokens, which omap's boxes store
 };
 
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, const Coords& c, int d, int row, int h,
@@ -124,7 +125,7 @@ __device__ __forceinline__ int block_tiles(const TokensArgs& a, const TokensPlan
 
 // Start of the range that begins at cost y of sequence b, which is in it. Quotients are
 // taken in floats: whatever they round to, both CTAs that meet here find the same.
-__device__ __noinline__ TokensAt locate(const TokensArgs& a, const TokensPlan& p, int b, int64_t y) {
+__device__ __forceinline__ TokensAt locate(const TokensArgs& a, const TokensPlan& p, int b, int64_t y) {
   const Seq s = load_seq(a, b);
   const Cost c(a, p, s);
   const int64_t head = c.head();
@@ -145,48 +146,64 @@ __device__ __noinline__ TokensAt locate(const TokensArgs& a, const TokensPlan& p
   return at;
 }
 
-// The range of this CTA, [ends_s[0], ends_s[1]); all threads, with barriers.
+// The range of this CTA, [ends_s[0], ends_s[1]), once the CTA has synchronised; all
+// threads, with a barrier. Either end is found by a thread of its own.
 __device__ __forceinline__ void find_range(const TokensArgs& a, const TokensPlan& p, int64_t* sums_s, TokensAt* ends_s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool even = !a.starts && !a.new_lens && !a.lens;
   const int share = (int)((unsigned)(a.B + kThreads - 1) / (unsigned)kThreads);
-  const int b0 = min(a.B, tid * share), b1 = min(a.B, b0 + share);
-  int64_t own = 0;
+  int64_t* const from_s = sums_s + kThreads / 32;    // where each thread's share begins in its warp's
+  if (!even) {
+    const int b0 = min(a.B, tid * share), b1 = min(a.B, b0 + share);
+    int64_t own = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) own += a.heads * Cost(a, p, load_seq(a, b)).head();
-  int64_t to = own;                                  // of this and lower lanes
+    for (int b = b0; b < b1; ++b) own += a.heads * Cost(a, p, load_seq(a, b)).head();
+    int64_t to = own;                                // of this and lower lanes
 #pragma unroll 1
-  for (int d = 1; d < 32; d *= 2) {
-    const int64_t x = __shfl_up_sync(~0u, to, d);
-    if (lane >= d) to += x;
-  }
-  if (lane == 31) sums_s[warp] = to;
-  if (tid < 2) ends_s[tid] = TokensAt{a.B, 0, 0, 0};
-  __syncthreads();
-  int64_t total = 0, from = to - own;
-#pragma unroll 1
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) from += sums_s[w];
-    total += sums_s[w];
-  }
-  if (own == 0) return;
-#pragma unroll 1
-  for (int e = 0; e < 2; ++e) {
-    // c * total / ctas (or about that: any ascending function does)
-    const int c = blockIdx.x + e;
-    if (c == p.ctas) break;
-    const int64_t x = min((int64_t)(((double)total * c + 0.5) * p.per_cta), total - 1);
-    if (x < from || x >= from + own) continue;
-    int64_t y = x - from;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      const int64_t seq = a.heads * Cost(a, p, load_seq(a, b)).head();
-      if (y < seq) {
-        ends_s[e] = locate(a, p, b, y);
-        break;
-      }
-      y -= seq;
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t x = __shfl_up_sync(~0u, to, d);
+      if (lane >= d) to += x;
     }
+    from_s[tid] = to - own;
+    if (lane == 31) sums_s[warp] = to;
+    __syncthreads();
   }
+  if (tid & ~32) return;                             // (threads 0 and 32 go on)
+  int64_t seq = 0, total = 0;
+  if (even) {
+    seq = a.heads * Cost(a, p, load_seq(a, 0)).head();
+    total = a.B * seq;
+  } else {
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) total += sums_s[w];
+  }
+  const int c = blockIdx.x + (tid >> 5);
+  TokensAt at{a.B, 0, 0, 0};
+  if (c < p.ctas && total > 0) {
+    // c * total / ctas (or about that: any ascending function does)
+    int64_t x = min((int64_t)(((double)total * c + 0.5) * p.per_cta), total - 1);
+    int b;
+    if (even) {
+      b = max(0, min((int)__fdividef((float)x, (float)seq), a.B - 1));
+      while (b > 0 && b * seq > x) --b;
+      while (b < a.B - 1 && (b + 1) * seq <= x) ++b;
+      x -= b * seq;
+    } else {
+      int w = 0;
+      while (w < kThreads / 32 - 1 && x >= sums_s[w]) x -= sums_s[w++];
+      int i = 31;                                    // the last share that begins at or before x
+      while (i > 0 && from_s[w * 32 + i] > x) --i;
+      x -= from_s[w * 32 + i];
+#pragma unroll 1
+      for (b = (w * 32 + i) * share; b < a.B - 1; ++b) {
+        const int64_t of = a.heads * Cost(a, p, load_seq(a, b)).head();
+        if (x < of) break;
+        x -= of;
+      }
+    }
+    at = locate(a, p, b, x);
+  }
+  ends_s[tid >> 5] = at;
 }
 
 // A block's tiles k0 .. k1 - 1, as the producer finds them and the other roles read them
@@ -314,7 +331,7 @@ __device__ __forceinline__ uint32_t low_bits(int left) { return left >= 32 ? ~0u
 
 template <typename T, int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_tokens_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+    attend_tokens_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
                          const __grid_constant__ Params p) {
   using Gm = Geo<D, PAIR>;
@@ -387,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // (where outputs are staged: the producer has its range before it tells of any block)
   int64_t* const sums_s = reinterpret_cast<int64_t*>(smem + Gm::STAGE);
-  TokensAt* const ends_s = reinterpret_cast<TokensAt*>(sums_s + kThreads / 32);
+  TokensAt* const ends_s = reinterpret_cast<TokensAt*>(sums_s + kThreads / 32 + kThreads);
   find_range(a, p.plan, sums_s, ends_s);
   tc_fence_before();
   __syncthreads();
@@ -640,14 +657,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               *piece(s, left + x / (D / 8), x % (D / 8)) = make_uint4(0, 0, 0, 0);
             if (i == g.hole && ht < D / 8) *piece(s, g.gap - i * kT, ht) = make_uint4(0, 0, 0, 0);
             if (i >= g.own) {
+              // (keys up to the block's first token all of its rows see)
+              const int seen = a.parents ? 0 : max(0, g.tok + 1 - (g.kb + i) * kT) * (D / 8);
               uint32_t found = 0;
 #pragma unroll 4
-              for (int x = ht; x < left * (D / 8); x += 64) {
+              for (int x = seen + ht; x < left * (D / 8); x += 64) {
                 const uint4 v = *piece(s, x / (D / 8), x % (D / 8));
                 found |= not_finite<T>(v.x) | not_finite<T>(v.y) | not_finite<T>(v.z) | not_finite<T>(v.w);
               }
               if (__any_sync(~0u, found != 0)) {
-                for (int x = ht; x < left * (D / 8); x += 64) {
+                for (int x = seen + ht; x < left * (D / 8); x += 64) {
                   uint4* at = piece(s, x / (D / 8), x % (D / 8));
                   const uint4 v = *at;
                   *at = make_uint4(drop_not_finite<T>(v.x), drop_not_finite<T>(v.y), drop_not_finite<T>(v.z),
@@ -848,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float x[16];
           tmem_ld16(to + c, x);
 #pragma unroll 1
-          for (int j = (g.kb + max(g.own, g.mask)) * kT; j < min((g.kb + g.tiles) * kT, t + 1); ++j) {
+          for (int j = a.parents ? max(0, g.kb) * kT : max((g.kb + g.own) * kT, g.tok + 1); j < min((g.kb + g.tiles) * kT, t + 1); ++j) {
             // (PAIR: of this stream's tiles)
             if ((a.parents && !((seen >> j) & 1)) || (PAIR && ((j / kT - g.kb) & 1) != w)) continue;
             const T* src = static_cast<const T*>(a.v_new) + g.b * a.vn_stride[0] + (int64_t)(g.tok0 + j) * a.vn_stride[1] +
@@ -907,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int begin = PAIR ? w * COLS : 0;
       if (g.whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float2 inv2 = make_float2(inv, inv);
         constexpr int PR = CW / 8;                   // 16-byte pieces of a row
         unsigned char* const stage = smem + Gm::STAGE + (warp - 4) * (32 * CW * 2);
         auto staged = [&](int r, int c) {
@@ -915,27 +935,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         T* const out = static_cast<T*>(a.out) + g.b * a.out_stride[0] + (int64_t)(g.tok0 + tok) * a.out_stride[1] +
                        (int64_t)g.h * a.N * a.out_stride[2];
         const unsigned rows_on = __ballot_sync(~0u, valid);
+        // Whole tokens of the warp's rows, all there, go out by TMA; else row by row.
+        const bool box = !PAIR && p.out_box && rows_on == ~0u;
 #pragma unroll 1
         for (int c0 = begin; c0 < begin + COLS; c0 += CW) {
           float v[CW];
           columns(c0, v);
-#pragma unroll
-          for (int e = 0; e < CW; e += 8)
-            *staged(lane, e / 8) =
-                make_uint4(pack16<T>(v[e] * inv, v[e + 1] * inv), pack16<T>(v[e + 2] * inv, v[e + 3] * inv),
-                           pack16<T>(v[e + 4] * inv, v[e + 5] * inv), pack16<T>(v[e + 6] * inv, v[e + 7] * inv));
-          __syncwarp();
-          uint4 y[PR];
-#pragma unroll
-          for (int x = 0; x < PR; ++x) y[x] = *staged(x * (32 / PR) + lane / PR, lane % PR);
-#pragma unroll
-          for (int x = 0; x < PR; ++x) {
-            const int r = x * (32 / PR) + lane / PR;
-            const uint32_t th = row_of[(warp & 3) * 32 + r];
-            if ((rows_on >> r) & 1u)
-              *reinterpret_cast<uint4*>(out + (th >> 16) * a.out_stride[1] + (th & 0xFFFFu) * a.out_stride[2] + c0 + 8 * (lane % PR)) = y[x];
+          if (!PAIR) {                               // the last box has been read
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
           }
-          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < CW; e += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 y = fmul2(make_float2(v[e + 2 * x], v[e + 2 * x + 1]), inv2);
+              o[x] = pack16<T>(y.x, y.y);
+            }
+            *staged(lane, e / 8) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          if (box) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                               reinterpret_cast<uint64_t>(&omap)),
+                           "r"(c0), "r"(g.h * a.N), "r"(g.tok0 + tok + row_t), "r"(a.starts ? 0 : g.b), "r"(smem_addr(stage))
+                           : "memory");
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          } else {
+            __syncwarp();
+            uint4 y[PR];
+#pragma unroll
+            for (int x = 0; x < PR; ++x) y[x] = *staged(x * (32 / PR) + lane / PR, lane % PR);
+#pragma unroll
+            for (int x = 0; x < PR; ++x) {
+              const int r = x * (32 / PR) + lane / PR;
+              const uint32_t th = row_of[(warp & 3) * 32 + r];
+              if ((rows_on >> r) & 1u)
+                *reinterpret_cast<uint4*>(out + (th >> 16) * a.out_stride[1] + (th & 0xFFFFu) * a.out_stride[2] + c0 + 8 * (lane % PR)) = y[x];
+            }
+            __syncwarp();
+          }
         }
         if (valid && a.lse && !(PAIR && w))
           a.lse[((a.starts ? (int64_t)g.tok0 : (int64_t)g.b * a.S) + t) * a.G + g.h * a.N + row_h] =
@@ -959,6 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if (!PAIR) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // outputs on their way
   // -------------------------------------------------------------------- teardown
   __syncthreads();
   if (*abort_flag && tid == 32) {
@@ -1096,16 +1140,19 @@ cudaError_t launch_attend_tokens(const TokensLaunch& l, int D, int dtype, cudaSt
     p.part_ml = reinterpret_cast<float2*>(space + l.plan.o_bytes(D));
     p.first = reinterpret_cast<TokensAt*>(space + l.plan.o_bytes(D) + l.plan.ml_bytes());
   }
-  CUtensorMap qmap{}, kmap{}, vmap{}, knmap{}, vnmap{};
+  CUtensorMap qmap{}, omap{}, kmap{}, vmap{}, knmap{}, vnmap{};
   if (!encode_rows(&qmap, l.q, l.a.N, l.a.half, D, dtype, &p.at.q) || !encode_rows(&knmap, l.k_new, 1, kT, D, dtype, &p.at.kn) ||
       !encode_rows(&vnmap, l.v_new, 1, kT, D, dtype, &p.at.vn))
     return cudaErrorInvalidValue;
+  // (outputs have any strides: those that no map describes are stored row by row)
+  Coords none;
+  p.out_box = !l.plan.pair && 32 % l.a.N == 0 && l.out_fits && encode_rows(&omap, l.out, l.a.N, 32 / l.a.N, D, dtype, &none);
   if (l.a.n + (l.a.pend ? 1 : 0) > 0 &&
       (!encode_rows(&kmap, l.k, 1, kT, D, dtype, &p.at.k) || !encode_rows(&vmap, l.v, 1, kT, D, dtype, &p.at.v)))
     return cudaErrorInvalidValue;
   return pick(D, dtype, l.plan.pair, [&](auto kind) {
     using K = decltype(kind);
-    K::kernel<<<l.plan.ctas, kThreads, K::SMEM, s>>>(qmap, kmap, vmap, knmap, vnmap, p);
+    K::kernel<<<l.plan.ctas, kThreads, K::SMEM, s>>>(qmap, omap, kmap, vmap, knmap, vnmap, p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || l.plan.whole || l.plan.ctas < 2) return e;
     const dim3 grid(l.plan.ctas - 1, l.plan.block_rows / 32, K::D / 32);

@@ -61,7 +61,8 @@ struct TokensRows {
 struct TokensLaunch {
   TokensArgs a;
   TokensPlan plan;
-  TokensRows q, k, v, k_new, v_new;   // (q's rows are tokens)
+  TokensRows q, out, k, v, k_new, v_new;   // (q's and out's rows are tokens)
+  bool out_fits;           // a tensor map can describe out
   void* workspace;
   int* err;                // error word for bounded waits, or null
   int stall;               // test hook: CTA 0's first tile is never issued

@@ -113,6 +113,9 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
     a.vn_stride[i] = on ? d->v_new_stride[i] : 0;
   }
   l.q = TokensRows{d->q, {d->q_stride[0], d->q_stride[2], d->q_stride[1]}, B, a.G, a.S};
+  l.out = TokensRows{d->out, {d->out_stride[0], d->out_stride[2], d->out_stride[1]}, B, a.G, a.S};
+  l.out_fits = map_strides_fit(d->out_stride, B, d->n_heads, d->seq, 1, D) && (d->n_heads == 1 || d->out_stride[2] >= D) &&
+               (B == 1 || d->out_stride[0] >= D);
   l.k_new = TokensRows{d->k_new, {d->k_new_stride[0], d->k_new_stride[2], d->k_new_stride[1]}, B, d->n_kv_heads, a.S};
   l.v_new = TokensRows{d->v_new, {d->v_new_stride[0], d->v_new_stride[2], d->v_new_stride[1]}, B, d->n_kv_heads, a.S};
   if (rows) {
