@@ -14,7 +14,9 @@
 //
 // Work: see TokensPlan. A half block is the rows of 128 / N tokens, which one TMA box
 // brings. A block is PAIR: one half, its key tiles dealt alternately to two streams; else
-// two halves, a stream for either, both on every tile. Key tiles
+// two halves, a stream for either, both on every tile. SPLIT, a PAIR of at most 64 query
+// rows: they lie in Q twice, and of a tile's keys the first copy's weights are kept for the
+// first 64 and the second's for the rest, so that all softmax threads have work. Key tiles
 // past the last row's are not visited. A piece of a block that another CTA finishes
 // leaves its unnormalised O, m and l in the workspace for the join kernel below.
 //
@@ -169,6 +171,12 @@ __device__ __forceinline__ void find_range(const TokensArgs& a, const TokensPlan
     __syncthreads();
   }
   if (tid & ~32) return;                             // (threads 0 and 32 go on)
+  if (even && p.even) {                              // a block a CTA
+    const unsigned per = block_tokens(a, p), n = (a.S + per - 1) / per, u = blockIdx.x + (tid >> 5), hb = u / n;
+    const int b = (int)(hb / (unsigned)a.heads);
+    ends_s[tid >> 5] = TokensAt{b, (int)hb - b * a.heads, (int)(u - hb * n), 0};
+    return;
+  }
   int64_t seq = 0, total = 0;
   if (even) {
     seq = a.heads * Cost(a, p, load_seq(a, 0)).head();
@@ -329,13 +337,15 @@ __device__ __forceinline__ bool mends(const TokensArgs& a, const Seg& g, bool va
 // The low `left` of 32 bits.
 __device__ __forceinline__ uint32_t low_bits(int left) { return left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u; }
 
-template <typename T, int D, bool PAIR>
+template <typename T, int D, bool PAIR, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tokens_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                          const __grid_constant__ CUtensorMap knmap, const __grid_constant__ CUtensorMap vnmap,
                          const __grid_constant__ Params p) {
   using Gm = Geo<D, PAIR>;
   constexpr int NS = Gm::STAGES;
+  constexpr int kRows = SPLIT ? kT / 2 : kT;         // query rows of a half block
+  constexpr int KC = kRows;                          // keys of a tile that a softmax thread has
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -391,16 +401,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), kTmem);
   // The query rows that no box brings are zeros: what lies there could send their warp the
   // way of logits that are not finite.
-  for (int x = tid; x < 2 * Gm::KH * (kT - a.N * a.half) * 8; x += kThreads) {
+  for (int x = tid; x < 2 * Gm::KH * (kRows - a.N * a.half) * 8; x += kThreads) {
     const int c = x & 7, h = (x >> 3) % (2 * Gm::KH), r = a.N * a.half + (x >> 3) / (2 * Gm::KH);
-    *reinterpret_cast<uint4*>(smem + Gm::Q + h * Gm::HALFB + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    for (int s = 0; s < kT; s += kRows)
+      *reinterpret_cast<uint4*>(smem + Gm::Q + h * Gm::HALFB + (s + r) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   // a half block's rows: token and query head
   uint32_t* const row_of = reinterpret_cast<uint32_t*>(smem + Gm::ROWS);
   if (warp >= 8) {
-    const unsigned r = tid - 256, t = r / (unsigned)a.N;
-    row_of[r] = t << 16 | (r - t * a.N);
+    const unsigned r = (tid - 256) % kRows, t = r / (unsigned)a.N;
+    row_of[tid - 256] = t << 16 | (r - t * a.N);
   }
   // (where outputs are staged: the producer has its range before it tells of any block)
   int64_t* const sums_s = reinterpret_cast<int64_t*>(smem + Gm::STAGE);
@@ -629,10 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int had = x ? queries[1]++ : queries[0]++;
           if (had && !(ok = __all_sync(~0u, wait_or_abort(q_free(x), (had - 1) & 1, abort_flag, p.err)))) break;
           if (ht == 0) {
-            mbar_expect_tx(q_full(x), Gm::KH * 128 * a.N * a.half);
+            mbar_expect_tx(q_full(x), (kT / kRows) * Gm::KH * 128 * a.N * a.half);
             for (int kh = 0; kh < Gm::KH; ++kh)
-              tma_load_rows(base + Gm::Q + x * Gm::TILEB + kh * Gm::HALFB, &qmap, p.at.q, kh * 64, g.tok0 + g.tok + w * a.half,
-                            g.h * a.N, g.b, q_full(x));
+              for (int s = 0; s < kT; s += kRows)
+                tma_load_rows(base + Gm::Q + x * Gm::TILEB + kh * Gm::HALFB + s * 128, &qmap, p.at.q, kh * 64,
+                              g.tok0 + g.tok + w * a.half, g.h * a.N, g.b, q_full(x));
           }
         }
         auto visit = [&](bool value, int i) {
@@ -712,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && (warp & 3) == 0) mbar_arrive(empty((ring + nth) % NS));
     };
     // this thread's row of a half block: a token's place in it and a query head
-    const int row_t = (int)((unsigned)row / (unsigned)a.N), row_h = row - row_t * a.N;
+    const int share = row / kRows;                   // (SPLIT: 0 or 1, the keys that this thread has of the row's)
+    const int row_t = (int)((unsigned)(row % kRows) / (unsigned)a.N), row_h = row % kRows - row_t * a.N;
     // a tree: the tokens that token t sees, as bits (warp-collective)
     auto seen_of = [&](const Seg& g, int t) {
       uint64_t anc[2];
@@ -728,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = row_t < a.half && tok + row_t < g.nq;
       float m = kNegInf, l = 0.f;
       bool begun = false;
-      const uint32_t ts = tm_s(w) + lanes, to = tm_o(w) + lanes;
+      const uint32_t ts = tm_s(w) + lanes, to = tm_o(w) + lanes, tsv = ts + (SPLIT ? 64 * share : 0);
       for (int i = PAIR ? w : 0; i < n && ok; i += PAIR ? 2 : 1) {
         ok = __all_sync(~0u, wait_or_abort(s_full(w), ns & 1, abort_flag, p.err));
         if (!ok) break;
@@ -758,21 +771,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x);
           }
         }
-        const bool none = (see[0] | see[1] | see[2] | see[3]) == 0u;
-        float v[kT];
-        tmem_ld128(ts, v);
+        if (SPLIT && share) {
+          see[0] = see[2];
+          see[1] = see[3];
+        }
+        const bool none = (see[0] | see[1] | (SPLIT ? 0u : see[2] | see[3])) == 0u;
+        float v[KC];
+        auto load_logits = [&] {
+          if constexpr (SPLIT) {
+            tmem_ld64(tsv, v);
+          } else {
+            tmem_ld128(tsv, v);
+          }
+        };
+        load_logits();
         if (partial) {
 #pragma unroll
-          for (int e = 0; e < kT; ++e) v[e] = (see[e >> 5] >> (e & 31)) & 1u ? v[e] : kNegInf;
+          for (int e = 0; e < KC; ++e) v[e] = (see[e >> 5] >> (e & 31)) & 1u ? v[e] : kNegInf;
         }
         // (a NaN stays in the maximum, so that one compare finds logits that are not finite)
         float m4[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) m4[x] = max_nan(v[x], v[4 + x], v[8 + x]);
 #pragma unroll
-        for (int e = 12; e < kT; e += 8)
+        for (int e = 12; e < KC; e += 8)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) m4[x] = e + 4 < kT ? max_nan(m4[x], v[e + x], v[e + 4 + x]) : max_nan(m4[x], v[e + x]);
+          for (int x = 0; x < 4; ++x) m4[x] = e + 4 < KC ? max_nan(m4[x], v[e + x], v[e + 4 + x]) : max_nan(m4[x], v[e + x]);
         const float mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3])) * a.scale2;
         // Rare: logits of NaN or +-inf, and a maximum so large that it is rounded by a half
         // or more, as its own logit need not be near it in the fused product and
@@ -800,21 +824,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             // fused product instead (in such rows alone: no row's bits depend on its neighbours)
             const float inv = 1.f / a.scale2;
 #pragma unroll 1
-            for (int c = 0; c < kT / 16; ++c) {
+            for (int c = 0; c < KC / 16; ++c) {
               float x[16];
               uint32_t o[16];
               const uint32_t bits = (c < 2 ? see[0] : c < 4 ? see[1] : c < 6 ? see[2] : see[3]) >> (16 * (c & 1));
-              tmem_ld16(ts + 16 * c, x);
+              tmem_ld16(tsv + 16 * c, x);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 o[e] = __float_as_uint(!((bits >> e) & 1u) ? kNegInf
                                        : odd ? __fadd_rn(__fmul_rn(x[e], a.scale2), nb) * inv : x[e]);
-              tmem_st16(ts + 16 * c, o);
+              tmem_st16(tsv + 16 * c, o);
             }
             tmem_st_wait();
-            tmem_ld128(ts, v);
+            load_logits();
             if (odd) nb = 0.f;
           }
+        }
+        if (SPLIT) {
+          // the other thread's keys: weights of 0 (O is as it is to be: their product reads and
+          // writes it)
+          uint32_t zero[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) zero[e] = 0u;
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) tmem_st16(ts + 64 * (1 - share) + c, zero);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(w, 1 - share));
         }
         begun = true;
         const float2 sc2 = make_float2(a.scale2, a.scale2), nb2 = make_float2(nb, nb);
@@ -824,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 64 keys at a time: the tensor cores start on the first half's weights
         // while the second half's are computed
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < KC / 64; ++c) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t hi[16], lo[16];
@@ -840,13 +877,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lo[e / 2] = pack16<T>(pp.x - back.x, pp.y - back.y);
               }
             }
-            tmem_st16(ts + 64 * c + 16 * h, hi);
-            if (PAIR) tmem_st16(ts + 64 * c + 32 + 16 * h, lo);
+            tmem_st16(tsv + 64 * c + 16 * h, hi);
+            if (PAIR) tmem_st16(tsv + 64 * c + 32 + 16 * h, lo);
           }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(w, c));
+          if (lane == 0) mbar_arrive(p_full(w, SPLIT ? share : c));
         }
         l4[0] = fadd2(fadd2(l4[0], l4[1]), fadd2(l4[2], l4[3]));
         l += l4[0].x + l4[0].y;
@@ -900,9 +937,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float2 x = ml[row], y = ml[kT + row];
         m = fmaxf(x.x, y.x);
+        if (SPLIT) m = fmaxf(m, fmaxf(ml[row ^ 64].x, ml[kT + (row ^ 64)].x));
         f0 = x.x == m ? 1.f : ex2(x.x - m);
         f1 = y.x == m ? 1.f : ex2(y.x - m);
         l = x.y * f0 + y.y * f1;
+        if (SPLIT) {
+          const float2 z = ml[row ^ 64], u = ml[kT + (row ^ 64)];
+          l += z.y * (z.x == m ? 1.f : ex2(z.x - m)) + u.y * (u.x == m ? 1.f : ex2(u.x - m));
+        }
       }
       constexpr int CW = Gm::CW;
       auto columns = [&](int c, float (&v)[CW]) {    // O's columns c .. c + CW - 1 of this row
@@ -919,8 +961,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(at + kT, y);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = fmaf(y[e], f1, v[e] * f0);
+          } else if (SPLIT) {                        // (the other share's maximum may be larger)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= f0;
           }
         }
+      };
+      // SPLIT: the second thread of a row hands its part of O to the first, 32 columns at a
+      // time: [piece of 4 columns][row]
+      float4* const halves = reinterpret_cast<float4*>(smem + Gm::STAGE + w * (64 * 32 * 4));
+      auto join_shares = [&](float (&v)[CW]) {
+        if (share) {
+#pragma unroll
+          for (int e = 0; e < CW; e += 4) halves[(e / 4) * 64 + row % kRows] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(4 + w) : "memory");
+        if (!share) {
+#pragma unroll
+          for (int e = 0; e < CW; e += 4) {
+            const float4 y = halves[(e / 4) * 64 + row];
+            v[e] += y.x;
+            v[e + 1] += y.y;
+            v[e + 2] += y.z;
+            v[e + 3] += y.w;
+          }
+        }
+        asm volatile("bar.sync %0, 128;" ::"r"(4 + w) : "memory");
       };
       constexpr int COLS = PAIR ? D / 2 : D;         // this warpgroup's columns, from `begin` on
       const int begin = PAIR ? w * COLS : 0;
@@ -941,6 +1007,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c0 = begin; c0 < begin + COLS; c0 += CW) {
           float v[CW];
           columns(c0, v);
+          if constexpr (SPLIT) {
+            // few rows, straight from the registers
+            join_shares(v);
+            T* const dst = out + row_t * a.out_stride[1] + row_h * a.out_stride[2] + c0;
+            if (valid && !share) {
+#pragma unroll
+              for (int e = 0; e < CW; e += 8)
+                *reinterpret_cast<uint4*>(dst + e) =
+                    make_uint4(pack16<T>(v[e] * inv, v[e + 1] * inv), pack16<T>(v[e + 2] * inv, v[e + 3] * inv),
+                               pack16<T>(v[e + 4] * inv, v[e + 5] * inv), pack16<T>(v[e + 6] * inv, v[e + 7] * inv));
+            }
+            continue;
+          }
           if (!PAIR) {                               // the last box has been read
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
@@ -980,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
         }
-        if (valid && a.lse && !(PAIR && w))
+        if (valid && a.lse && !(PAIR && w) && !share)
           a.lse[((a.starts ? (int64_t)g.tok0 : (int64_t)g.b * a.S) + t) * a.G + g.h * a.N + row_h] =
               l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
       } else {
@@ -991,10 +1070,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c0 = begin; c0 < begin + COLS; c0 += CW) {
           float v[CW];
           columns(c0, v);
+          if constexpr (SPLIT) join_shares(v);
 #pragma unroll
-          for (int e = 0; e < CW; e += 4) o[(int64_t)((c0 + e) / 4) * R] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < CW; e += 4)
+            if (valid && !share) o[(int64_t)((c0 + e) / 4) * R] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
-        if (!(PAIR && w)) p.part_ml[slot * R + rr] = make_float2(m, l);
+        if (!(PAIR && w) && !share) p.part_ml[slot * R + rr] = make_float2(m, l);
       }
       tc_fence_before();
       // (PAIR: either warpgroup reads both accumulators, and the maxima)
@@ -1029,6 +1110,10 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(const __grid_constant_
   const TokensAt x = p.first[c0 + 1], y = p.first[c0];
   auto same = [&](const TokensAt& o) { return o.b == x.b && o.h == x.h && o.i == x.i; };
   if (x.b >= a.B || x.k == 0 || (same(y) && y.k > 0)) return;
+  const Seq s = load_seq(a, x.b);
+  const int r = rr & (kT - 1), rt = (int)((unsigned)r / (unsigned)a.N), head = x.h * a.N + r - rt * a.N;
+  const int t = x.i * block_tokens(a, p.plan) + (rr / kT) * a.half + rt;
+  if (rt >= a.half || t >= s.nq) return;
   // a range that begins where the next one does is empty and has left no part
   float m = kNegInf, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1048,10 +1133,6 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(const __grid_constant_
     l = l * f + ml.y * h;
     o = make_float4(o.x * f + v.x * h, o.y * f + v.y * h, o.z * f + v.z * h, o.w * f + v.w * h);
   }
-  const Seq s = load_seq(a, x.b);
-  const int r = rr & (kT - 1), rt = (int)((unsigned)r / (unsigned)a.N), head = x.h * a.N + r - rt * a.N;
-  const int t = x.i * block_tokens(a, p.plan) + (rr / kT) * a.half + rt;
-  if (rt >= a.half || t >= s.nq) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* dst = static_cast<T*>(a.out) + x.b * a.out_stride[0] + (int64_t)(s.tok0 + t) * a.out_stride[1] + head * a.out_stride[2] + 4 * d4;
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<T>(o.x * inv, o.y * inv), pack16<T>(o.z * inv, o.w * inv));
@@ -1060,21 +1141,21 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(const __grid_constant_
         l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-template <typename Elem, int Dim, bool Pair>
+template <typename Elem, int Dim, bool Pair, bool Split>
 struct Kind {
-  static_assert(Geo<Dim, Pair>::SMEM <= 227 * 1024, "shared memory of a block");
   using T = Elem;
   static constexpr int D = Dim, SMEM = Geo<Dim, Pair>::SMEM;
-  static constexpr auto kernel = attend_tokens_kernel<Elem, Dim, Pair>;
+  static_assert(SMEM <= 227 * 1024, "shared memory of a block");
+  static constexpr auto kernel = attend_tokens_kernel<Elem, Dim, Pair, Split>;
 };
+template <typename Elem, typename F>
+auto pick_shape(int D, const TokensPlan& p, F&& f) {
+  if (D == 64) return p.split ? f(Kind<Elem, 64, true, true>{}) : p.pair ? f(Kind<Elem, 64, true, false>{}) : f(Kind<Elem, 64, false, false>{});
+  return p.split ? f(Kind<Elem, 128, true, true>{}) : p.pair ? f(Kind<Elem, 128, true, false>{}) : f(Kind<Elem, 128, false, false>{});
+}
 template <typename F>
-auto pick(int D, int dtype, bool pair, F&& f) {
-  if (dtype == kBf16) {
-    if (D == 64) return pair ? f(Kind<__nv_bfloat16, 64, true>{}) : f(Kind<__nv_bfloat16, 64, false>{});
-    return pair ? f(Kind<__nv_bfloat16, 128, true>{}) : f(Kind<__nv_bfloat16, 128, false>{});
-  }
-  if (D == 64) return pair ? f(Kind<__half, 64, true>{}) : f(Kind<__half, 64, false>{});
-  return pair ? f(Kind<__half, 128, true>{}) : f(Kind<__half, 128, false>{});
+auto pick(int D, int dtype, const TokensPlan& p, F&& f) {
+  return dtype == kBf16 ? pick_shape<__nv_bfloat16>(D, p, f) : pick_shape<__half>(D, p, f);
 }
 
 // Rows as a 4-D tensor [sequence, row, head, D], whatever the strides (a dimension of one
@@ -1096,21 +1177,26 @@ bool encode_rows(CUtensorMap* map, const TokensRows& r, int heads, int rows, int
 
 }  // namespace
 
-TokensPlan tokens_plan(bool pair, int64_t blocks, int heads, int64_t tiles, int sms) {
+TokensPlan tokens_plan(bool pair, bool split, int64_t blocks, int heads, int64_t tiles, int64_t mean, int sms) {
   TokensPlan pl{};
   pl.pair = pair;
+  pl.split = split;
   pl.block_rows = pl.pair ? kT : 2 * kT;
   const int64_t units = blocks * heads;
-  // Few short blocks: one a CTA, no join.
-  pl.whole = pl.even = units <= sms && tiles <= 6;
+  // Cut blocks cost their parts' way through memory and the join, about nine tiles' time;
+  // whole ones leave CTAs with less than others: 32 query heads on 8 of 1024 tokens 20.9 us
+  // whole, 33.8 cut, of 2048 60.3 and 55.7; 2 x 40 drafted tokens on 1500 rows 28.3 and 21.5.
+  const double even = (double)(units * mean) / sms;
+  pl.whole = tiles <= 6 || (units <= sms ? (double)tiles : even + 0.6 * (double)tiles) < even + 9;
+  pl.even = pl.whole && units <= sms;
   pl.ctas = (int)std::min<int64_t>(sms, pl.whole ? units : units * tiles);
   pl.per_cta = 1.0 / pl.ctas;
   return pl;
 }
 
-bool tokens_kernel_ready(int D, int dtype, bool pair, int device) {
+bool tokens_kernel_ready(int D, int dtype, const TokensPlan& plan, int device) {
   if (!encode_fn()) return false;
-  return pick(D, dtype, pair, [&](auto kind) {
+  return pick(D, dtype, plan, [&](auto kind) {
     using K = decltype(kind);
     // The kernel's redistribution of registers needs the 168 a thread that its
     // launch bound gives it: checked, as it would wait forever with fewer.
@@ -1150,7 +1236,7 @@ cudaError_t launch_attend_tokens(const TokensLaunch& l, int D, int dtype, cudaSt
   if (l.a.n + (l.a.pend ? 1 : 0) > 0 &&
       (!encode_rows(&kmap, l.k, 1, kT, D, dtype, &p.at.k) || !encode_rows(&vmap, l.v, 1, kT, D, dtype, &p.at.v)))
     return cudaErrorInvalidValue;
-  return pick(D, dtype, l.plan.pair, [&](auto kind) {
+  return pick(D, dtype, l.plan, [&](auto kind) {
     using K = decltype(kind);
     K::kernel<<<l.plan.ctas, kThreads, K::SMEM, s>>>(qmap, omap, kmap, vmap, knmap, vnmap, p);
     const cudaError_t e = cudaGetLastError();

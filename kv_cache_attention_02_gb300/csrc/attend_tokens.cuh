@@ -23,7 +23,7 @@ struct TokensArgs {
   int B, S, G, n;          // S: tokens of a sequence, or in all with starts
   // Query heads are dealt to `heads` groups of N <= 128, a key head's to `groups` of them
   // (one, but for more than 128 query heads a key head); half a block of query rows is
-  // `half` = 128 / N tokens of one.
+  // `half` = 128 / N (split: 64 / N) tokens of one.
   int N, heads, groups, half;
   float scale2;            // scale * log2(e): logits in base-2 units
 };
@@ -38,7 +38,7 @@ struct TokensAt {
 // form, about half a block's tiles and a constant for its start, so that every CTA finds
 // its range itself.
 struct TokensPlan {
-  int ctas, pair, block_rows;
+  int ctas, pair, split, block_rows;
   int whole;               // ranges begin and end with blocks: no parts to join
   int even;                // (with whole) every block costs the same
   double per_cta;          // 1 / ctas
@@ -46,9 +46,9 @@ struct TokensPlan {
   size_t ml_bytes() const { return (size_t)2 * ctas * block_rows * 8; }
   size_t bytes(int D) const { return whole ? 0 : o_bytes(D) + ml_bytes() + (size_t)(ctas + 1) * sizeof(TokensAt); }
 };
-// pair: no sequence has more than half a block. blocks: of all sequences in one head group,
-// at most; tiles: of a block, at most.
-TokensPlan tokens_plan(bool pair, int64_t blocks, int heads, int64_t tiles, int sms);
+// pair: no sequence has more than half a block; split: of at most 64 query rows. blocks: of all sequences in one head group,
+// at most; tiles, mean: of a block, at most and on average.
+TokensPlan tokens_plan(bool pair, bool split, int64_t blocks, int heads, int64_t tiles, int64_t mean, int sms);
 
 // Rows [batch, head, row] as TMA sees them.
 struct TokensRows {
@@ -67,7 +67,7 @@ struct TokensLaunch {
   int* err;                // error word for bounded waits, or null
   int stall;               // test hook: CTA 0's first tile is never issued
 };
-bool tokens_kernel_ready(int D, int dtype, bool pair, int device);
+bool tokens_kernel_ready(int D, int dtype, const TokensPlan& plan, int device);
 cudaError_t launch_attend_tokens(const TokensLaunch& l, int D, int dtype, cudaStream_t s);
 int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaStream_t s);
 

@@ -51,11 +51,14 @@ int head_groups(int N) {
 }
 
 TokensPlan plan_of(const kvevict_tokens* d, int64_t n, const DeviceInfo& dev) {
-  const int all = d->n_heads / d->n_kv_heads, groups = head_groups(all), half = 128 / (all / groups);
-  const bool pair = d->seq <= half;
+  const int all = d->n_heads / d->n_kv_heads, groups = head_groups(all), N = all / groups;
+  const bool split = (int64_t)d->seq * N <= 64, pair = split || d->seq <= 128 / N;
+  const int half = (split ? 64 : 128) / N;
   const int64_t per = pair ? half : 2 * half;
   const int64_t blocks = d->starts ? d->seq / per + d->batch : d->batch * ((d->seq + per - 1) / per);
-  return tokens_plan(pair, blocks, d->n_kv_heads * groups, (n + 127) / 128 + (d->seq + 127) / 128, dev.sms);
+  const int64_t own = (n + 127) / 128, top = (d->seq + 127) / 128;
+  const int64_t tokens = d->starts ? d->seq / std::max(1, d->batch) : d->seq;   // of a sequence, about
+  return tokens_plan(pair, split, blocks, d->n_kv_heads * groups, own + top, own + ((tokens + 127) / 128 + 1) / 2, dev.sms);
 }
 
 }  // namespace
@@ -106,7 +109,6 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
   a.groups = head_groups(d->n_heads / d->n_kv_heads);
   a.heads = d->n_kv_heads * a.groups;
   a.N = a.G / a.heads;
-  a.half = 128 / a.N;
   for (int i = 0; i < 3; ++i) {
     const bool on = i > 0 || !d->starts;                              // packed: no stride between sequences
     a.out_stride[i] = on ? d->out_stride[i] : 0;
@@ -156,7 +158,8 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
     return cuda_result(launch_attend_tokens_few(a, f, few, D, d->dtype, s), "launch");
   }
   l.plan = plan_of(d, all, dev);
-  if (!tokens_kernel_ready(D, d->dtype, l.plan.pair, dev.device)) {
+  a.half = (l.plan.split ? 64 : 128) / a.N;
+  if (!tokens_kernel_ready(D, d->dtype, l.plan, dev.device)) {
     set_last_error("the attention kernel cannot be launched here: no tensor maps, or another register count than it needs");
     return KVEVICT_ERR_CUDA;
   }

@@ -181,12 +181,12 @@ def test_offsets_past_32_bits(kvx):
 
 
 def _calls(kvx, seed=0):
-    """One block a CTA, cut blocks, and a tree over ranges."""
+    """One block a CTA, ranges of whole blocks, cut blocks, and a tree over ranges."""
     found = []
     for B, S, N, H, D, n in ((1, 60, 3, 2, 128, 0), (3, 900, 4, 2, 128, 100), (1, 400, 4, 2, 64, 3000)):
         q, args = make(B, S, N, H, D, n=n, seed=seed)
         found.append((kvx.attend_prompt, q, args))
-    q, args = make(9, 16, 4, 8, 128, n=2000, seed=seed)
+    q, args = make(9, 16, 4, 8, 128, n=3000, seed=seed)
     found.append((kvx.attend_tree, q, dict(args, parents=trees(9, 16, seed))))
     return found
 
@@ -279,7 +279,7 @@ def test_other_stream_than_the_current_one(kvx, which):
 
 def test_workspace_of_the_c_call(kvx):
     """Too little workspace launches nothing; the size asked for is enough, and nothing past it is written."""
-    _, q, args = _calls(kvx)[1]
+    _, q, args = _calls(kvx)[2]
     want, wlse = tref.check("call", kvx.attend_prompt, q, **args)
     out, lse = torch.full_like(q, 5.0), torch.empty_like(wlse)
     packed, stream = kvx._tokens(q, out, args["k_new"], args["v_new"], None, None, None, args["k"], args["v"], None, lse, None, None,
