@@ -1189,6 +1189,7 @@ TokensPlan tokens_plan(bool pair, bool split, int64_t blocks, int heads, int64_t
   const double even = (double)(units * mean) / sms;
   pl.whole = tiles <= 6 || (units <= sms ? (double)tiles : even + 0.6 * (double)tiles) < even + 9;
   pl.even = pl.whole && units <= sms;
+  pl.us = 7 + 1.3 * (pl.even ? (double)tiles : pl.whole ? even + 0.6 * (double)tiles : even + 8);
   pl.ctas = (int)std::min<int64_t>(sms, pl.whole ? units : units * tiles);
   pl.per_cta = 1.0 / pl.ctas;
   return pl;

@@ -42,6 +42,7 @@ struct TokensPlan {
   int whole;               // ranges begin and end with blocks: no parts to join
   int even;                // (with whole) every block costs the same
   double per_cta;          // 1 / ctas
+  double us;               // the call's time, about
   size_t o_bytes(int D) const { return (size_t)2 * ctas * block_rows * D * 4; }
   size_t ml_bytes() const { return (size_t)2 * ctas * block_rows * 8; }
   size_t bytes(int D) const { return whole ? 0 : o_bytes(D) + ml_bytes() + (size_t)(ctas + 1) * sizeof(TokensAt); }
@@ -84,10 +85,8 @@ struct FewArgs {
 struct FewPlan {
   int64_t units, chunks;
   int cluster;
-  bool use;
+  double us;               // the call's time, about; infinite where the kernel cannot take it
 };
-// Taken where all CTAs run at once and a warp has at most this many tiles of 16 keys.
-constexpr int kFewTiles = 24;
 FewPlan few_plan(int64_t B, int64_t rows, bool packed, int H, int64_t n, int64_t tokens, int sms);
 cudaError_t launch_attend_tokens_few(const TokensArgs& a, const FewArgs& f, const FewPlan& p, int D, int dtype, cudaStream_t s);
 

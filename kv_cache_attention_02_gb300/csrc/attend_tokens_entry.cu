@@ -140,7 +140,8 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
   const int64_t all = (int64_t)a.n + (a.pend ? 1 : 0);
   const FewPlan few = few_plan(d->batch, (int64_t)d->seq * (d->n_heads / d->n_kv_heads), d->starts != nullptr, d->n_kv_heads, all,
                                d->seq, dev.sms);
-  if (few.use && !g_without_few.load(std::memory_order_relaxed)) {
+  l.plan = plan_of(d, all, dev);
+  if (few.us < l.plan.us && !g_without_few.load(std::memory_order_relaxed)) {
     FewArgs f{};
     f.q = d->q;
     f.k = l.k.base;
@@ -157,7 +158,6 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
     f.chunks = (int)few.chunks;
     return cuda_result(launch_attend_tokens_few(a, f, few, D, d->dtype, s), "launch");
   }
-  l.plan = plan_of(d, all, dev);
   a.half = (l.plan.split ? 64 : 128) / a.N;
   if (!tokens_kernel_ready(D, d->dtype, l.plan, dev.device)) {
     set_last_error("the attention kernel cannot be launched here: no tensor maps, or another register count than it needs");

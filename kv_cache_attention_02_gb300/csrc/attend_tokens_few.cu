@@ -387,16 +387,20 @@ FewPlan few_plan(int64_t B, int64_t rows, bool packed, int H, int64_t n, int64_t
   p.chunks = (rows + kRows - 1) / kRows;
   p.units = (packed ? rows / kRows + B : B * p.chunks) * H;
   const int64_t tiles = (n + 15) / 16 + (tokens + 15) / 16;
+  p.us = 1e30;
   if (packed && B > kThreads) return p;
   // CTAs of a unit's cluster: its tiles are split while all CTAs are resident together
   // and a warp has more than one tile.
   p.cluster = 1;
   while (p.cluster < kCluster && p.units * p.cluster <= sms && (int64_t)p.cluster * kWarps < tiles) p.cluster *= 2;
-  // One wave of CTAs, a warp's tiles few: 8 tokens x 24 query heads on 8 of 8192 rows (17
-  // tiles a warp) 26.5 us against the tensor-core kernel's 29.8, on 512 rows 9.4 against
-  // 16.4; 128 tokens of a prompt 8.8 against 12.0, but 160, in two waves, 14.7 against 12.3.
-  const int64_t warp_tiles = (tiles + p.cluster * kWarps - 1) / (p.cluster * kWarps);
-  p.use = p.units * p.cluster <= 2 * sms && warp_tiles <= kFewTiles;
+  // Taken where all CTAs run at once and this time, from the cases below, is shorter than
+  // the tensor-core kernel's (this | that, us): 8 drafted tokens of 24 query heads on 8 on
+  // 512 rows 8.7 | 12.2, on 8192 26.1 | 24.5; 8 x 8 tokens, 32 heads, on 2048 rows 29.9 |
+  // 25.8, one sequence of 16 on 2048 12.5 | 19.7; 128 tokens of a prompt 9.0 | 8.5, 64 6.4 | 8.3.
+  const double warp_tiles = (double)((tiles + p.cluster * kWarps - 1) / (p.cluster * kWarps));
+  const int64_t ctas = p.units * p.cluster;
+  if (ctas <= 2 * sms)
+    p.us = 4.5 + 0.9 * warp_tiles + (p.cluster > 1 ? 1.5 : 0) + (ctas > sms ? 1 + 0.5 * warp_tiles : 0);
   return p;
 }
 
