@@ -75,7 +75,7 @@ struct Params {
   TokensAt* first;         // [ctas + 1]
   int* err;
   int stall;
-  int out_box;             // a warp's 32 query rows are whole tokens, which omap's boxes store
+  int out_box;             // omap describes the outputs, a half block's 32 columns a box
 };
 
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, const Coords& c, int d, int row, int h,
@@ -304,9 +304,10 @@ struct Geo {
   static constexpr int HALFB = kT * 128;         // one half tile, 16 KB
   static constexpr int TILEB = KH * HALFB;
   static constexpr int STAGES = 128 * 1024 / TILEB;
-  static constexpr int CW = PAIR ? 32 : 64;      // output columns staged at a time
+  static constexpr int CW = 32;                  // output columns staged at a time
   static constexpr int Q = 0, RING = 2 * TILEB, STAGE = RING + STAGES * TILEB;   // (PAIR: segments take turns with Q)
-  static constexpr int ML = STAGE + 8 * 32 * CW * 2;   // PAIR: the streams' maxima and sums
+  static constexpr int BUFB = kT * CW * 2;       // a stream's staged outputs; two of them, but in PAIR
+  static constexpr int ML = STAGE + 2 * (PAIR ? 1 : 2) * BUFB;   // PAIR: the streams' maxima and sums
   static constexpr int BARS = ML + (PAIR ? 2 * kT * 8 : 0);
   static constexpr int NBARS = 3 * STAGES + 13 + 2 * kSegs;
   static constexpr int SEGS = BARS + NBARS * 8 + 16 + kSegs * 4;
@@ -953,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < CW; ++e) v[e] = 0.f;
         } else if constexpr (!PAIR) {
-          tmem_ld64(at + kT * w, v);
+          tmem_ld32(at + kT * w, v);
         } else {
           tmem_ld32(at, v);
           if (n > 1) {
@@ -994,15 +995,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float2 inv2 = make_float2(inv, inv);
         constexpr int PR = CW / 8;                   // 16-byte pieces of a row
-        unsigned char* const stage = smem + Gm::STAGE + (warp - 4) * (32 * CW * 2);
+        unsigned char* stage = smem + Gm::STAGE + w * (PAIR ? 1 : 2) * Gm::BUFB;   // [row][64 bytes], as TMA swizzles them
         auto staged = [&](int r, int c) {
-          return reinterpret_cast<uint4*>(stage + r * (CW * 2) + (((PR == 8 ? c ^ r : c ^ (r >> 1)) & (PR - 1)) << 4));
+          return reinterpret_cast<uint4*>(stage + r * (CW * 2) + (((c ^ (r >> 1)) & (PR - 1)) << 4));
         };
         T* const out = static_cast<T*>(a.out) + g.b * a.out_stride[0] + (int64_t)(g.tok0 + tok) * a.out_stride[1] +
                        (int64_t)g.h * a.N * a.out_stride[2];
         const unsigned rows_on = __ballot_sync(~0u, valid);
-        // Whole tokens of the warp's rows, all there, go out by TMA; else row by row.
-        const bool box = !PAIR && p.out_box && rows_on == ~0u;
+        // Half blocks whose tokens are all there go out by TMA, 32 columns at a time from two
+        // buffers in turn; others row by row.
+        const bool box = !PAIR && p.out_box && tok + a.half <= g.nq, first = (warp & 3) == 0 && lane == 0;
+        if (!PAIR && !box) {                         // the last box has been read
+          if (first) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+        }
 #pragma unroll 1
         for (int c0 = begin; c0 < begin + COLS; c0 += CW) {
           float v[CW];
@@ -1020,10 +1026,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             continue;
           }
-          if (!PAIR) {                               // the last box has been read
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-          }
 #pragma unroll
           for (int e = 0; e < CW; e += 8) {
             uint32_t o[4];
@@ -1032,23 +1034,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 y = fmul2(make_float2(v[e + 2 * x], v[e + 2 * x + 1]), inv2);
               o[x] = pack16<T>(y.x, y.y);
             }
-            *staged(lane, e / 8) = make_uint4(o[0], o[1], o[2], o[3]);
+            *staged(row, e / 8) = make_uint4(o[0], o[1], o[2], o[3]);
           }
           if (box) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
+            if (first) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the other buffer is free
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+            if (first) {
               asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
                                reinterpret_cast<uint64_t>(&omap)),
-                           "r"(c0), "r"(g.h * a.N), "r"(g.tok0 + tok + row_t), "r"(a.starts ? 0 : g.b), "r"(smem_addr(stage))
+                           "r"(c0), "r"(g.h * a.N), "r"(g.tok0 + tok), "r"(a.starts ? 0 : g.b), "r"(smem_addr(stage))
                            : "memory");
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
+            stage = smem + Gm::STAGE + 2 * w * Gm::BUFB + (stage == smem + Gm::STAGE + 2 * w * Gm::BUFB ? Gm::BUFB : 0);
           } else {
             __syncwarp();
             uint4 y[PR];
 #pragma unroll
-            for (int x = 0; x < PR; ++x) y[x] = *staged(x * (32 / PR) + lane / PR, lane % PR);
+            for (int x = 0; x < PR; ++x) y[x] = *staged((warp & 3) * 32 + x * (32 / PR) + lane / PR, lane % PR);
 #pragma unroll
             for (int x = 0; x < PR; ++x) {
               const int r = x * (32 / PR) + lane / PR;
@@ -1159,9 +1163,9 @@ auto pick(int D, int dtype, const TokensPlan& p, F&& f) {
 }
 
 // Rows as a 4-D tensor [sequence, row, head, D], whatever the strides (a dimension of one
-// entry, or that all share, with any); boxes of 64 elements (128 bytes) of so many heads
-// and rows; rows past the last read as zeros.
-bool encode_rows(CUtensorMap* map, const TokensRows& r, int heads, int rows, int D, int dtype, Coords* c) {
+// entry, or that all share, with any); boxes of 64 elements (128 bytes), or 32, of so many
+// heads and rows; rows past the last read as zeros.
+bool encode_rows(CUtensorMap* map, const TokensRows& r, int heads, int rows, int D, int dtype, Coords* c, int cols = 64) {
   auto enc = encode_fn();
   if (!enc) return false;
   c->h = r.H > 1 && r.stride[1] != 0;
@@ -1169,9 +1173,10 @@ bool encode_rows(CUtensorMap* map, const TokensRows& r, int heads, int rows, int
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(c->h ? r.H : 1), (cuuint64_t)r.rows, (cuuint64_t)(c->b ? r.B : 1)};
   const cuuint64_t strides[3] = {(cuuint64_t)(c->h ? r.stride[1] : D) * 2, (cuuint64_t)(r.rows > 1 ? r.stride[2] : D) * 2,
                                  (cuuint64_t)(c->b ? r.stride[0] : D) * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1}, estr[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)cols, (cuuint32_t)heads, (cuuint32_t)rows, 1}, estr[4] = {1, 1, 1, 1};
   return enc(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-             const_cast<void*>(r.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             const_cast<void*>(r.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1233,7 +1238,7 @@ cudaError_t launch_attend_tokens(const TokensLaunch& l, int D, int dtype, cudaSt
     return cudaErrorInvalidValue;
   // (outputs have any strides: those that no map describes are stored row by row)
   Coords none;
-  p.out_box = !l.plan.pair && 32 % l.a.N == 0 && l.out_fits && encode_rows(&omap, l.out, l.a.N, 32 / l.a.N, D, dtype, &none);
+  p.out_box = !l.plan.pair && l.out_fits && encode_rows(&omap, l.out, l.a.N, l.a.half, D, dtype, &none, 32);
   if (l.a.n + (l.a.pend ? 1 : 0) > 0 &&
       (!encode_rows(&kmap, l.k, 1, kT, D, dtype, &p.at.k) || !encode_rows(&vmap, l.v, 1, kT, D, dtype, &p.at.v)))
     return cudaErrorInvalidValue;
