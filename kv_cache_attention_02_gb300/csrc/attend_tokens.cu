@@ -752,31 +752,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(2 * i);
           if (i > 0) release(2 * i - 1);
         }
-        // which of the tile's keys the row sees
+        // Which of the tile's keys the row sees: the first `left`, but for a cache's evicted
+        // row, or an ancestor's bits.
+        const bool ends = i == part || (i >= mask && !a.parents), bitwise = i == hole || (i >= mask && a.parents);
+        int left = kT;
+        if (ends) left = i == part ? g.left - i * kT : t + 1 - (g.kb + i) * kT;
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        bool partial = i == part || i == hole;
-        if (partial) {
-          const int left = g.left - i * kT, gap = i == hole ? g.gap - i * kT : -1;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x) & ~((gap >> 5) == x ? 1u << (gap & 31) : 0u);
-        } else if (i >= mask) {
-          partial = true;
-          if (a.parents) {
-            const uint64_t mm = seen_of(g, t);
-            see[0] = (uint32_t)mm;
-            see[1] = (uint32_t)(mm >> 32);
-            see[2] = see[3] = 0u;
-          } else {
-            const int left = t + 1 - (g.kb + i) * kT;
+        if constexpr (PAIR) {                        // masked in registers, below
+          if (ends) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) see[x] = low_bits(left - 32 * x);
           }
+          if (bitwise) {
+            const uint64_t mm = i == hole ? 0 : seen_of(g, t);
+            const int gap = g.gap - i * kT;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              see[x] &= i == hole ? ~((gap >> 5) == x ? 1u << (gap & 31) : 0u) : x < 2 ? (uint32_t)(mm >> (32 * x)) : 0u;
+          }
+          if (SPLIT && share) {
+            see[0] = see[2];
+            see[1] = see[3];
+          }
+        } else {
+          // Masked where the logits are, 16 TMEM columns at a time: selects over all of v, in
+          // a row, are 6 KB of instructions that the SM's cache for them does not keep, nor
+          // what is behind them (8 x 4096 tokens 855 us so, 815 thus; PAIR, which waits for
+          // memory, is faster with the selects: 64 trees of 32 tokens on 1000 rows 73 | 83).
+          if (ends) {
+            const int lo = max(0, (int)__reduce_min_sync(~0u, left)), hi = __reduce_max_sync(~0u, left);   // of the warp's rows
+#pragma unroll 1
+            for (int c = lo / 16; c < KC / 16; ++c) {
+              float x[16];
+              uint32_t o[16];
+              if (16 * c < hi) tmem_ld16(ts + 16 * c, x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(16 * c + e < left ? x[e] : kNegInf);
+              tmem_st16(ts + 16 * c, o);
+            }
+            tmem_st_wait();
+          }
+          if (bitwise) {
+            const uint64_t mm = i == hole ? 0 : seen_of(g, t);
+            const int gap = g.gap - i * kT;
+#pragma unroll 1
+            for (int c = 0; c < KC / 16; ++c) {
+              const int c0 = 16 * c;
+              const uint32_t bits = i == hole ? ~(gap >= c0 && gap < c0 + 16 ? 1u << (gap - c0) : 0u) : c0 < 64 ? (uint32_t)(mm >> c0) : 0u;
+              if (__all_sync(~0u, (bits & 0xFFFFu) == 0xFFFFu)) continue;
+              float x[16];
+              uint32_t o[16];
+              tmem_ld16(ts + c0, x);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint((bits >> e) & 1u ? x[e] : kNegInf);
+              tmem_st16(ts + c0, o);
+            }
+            tmem_st_wait();
+          }
         }
-        if (SPLIT && share) {
-          see[0] = see[2];
-          see[1] = see[3];
-        }
-        const bool none = (see[0] | see[1] | (SPLIT ? 0u : see[2] | see[3])) == 0u;
         float v[KC];
         auto load_logits = [&] {
           if constexpr (SPLIT) {
@@ -786,9 +819,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         load_logits();
-        if (partial) {
+        if constexpr (PAIR) {
+          if (ends || bitwise) {
 #pragma unroll
-          for (int e = 0; e < KC; ++e) v[e] = (see[e >> 5] >> (e & 31)) & 1u ? v[e] : kNegInf;
+            for (int e = 0; e < KC; ++e) v[e] = (see[e >> 5] >> (e & 31)) & 1u ? v[e] : kNegInf;
+          }
         }
         // (a NaN stays in the maximum, so that one compare finds logits that are not finite)
         float m4[4];
@@ -802,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Rare: logits of NaN or +-inf, and a maximum so large that it is rounded by a half
         // or more, as its own logit need not be near it in the fused product and
         // difference below.
+        const bool none = PAIR ? (see[0] | see[1] | (SPLIT ? 0u : see[2] | see[3])) == 0u : left <= 0;
         const bool odd = !none && !(fabsf(mx) < kFar), up = mx > m + (kLazy + kLift<T>);
         float nb = m == kNegInf ? 0.f : -m;          // masked: every weight 2^-inf = 0
         if (__any_sync(~0u, up || odd)) {
@@ -828,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < KC / 16; ++c) {
               float x[16];
               uint32_t o[16];
-              const uint32_t bits = (c < 2 ? see[0] : c < 4 ? see[1] : c < 6 ? see[2] : see[3]) >> (16 * (c & 1));
+              const uint32_t bits = (c < 2 ? see[0] : c < 4 ? see[1] : c < 6 ? see[2] : see[3]) >> (16 * (c & 1));   // (TILES: all)
               tmem_ld16(tsv + 16 * c, x);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
@@ -1026,6 +1062,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             continue;
           }
+          if (!PAIR && box && c0 != CW) {            // the buffer's last box has been read
+            if (first) {
+              if (c0 == 0)
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              else
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+          }
 #pragma unroll
           for (int e = 0; e < CW; e += 8) {
             uint32_t o[4];
@@ -1038,7 +1083,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (box) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            if (first) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the other buffer is free
             asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
             if (first) {
               asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
