@@ -39,7 +39,9 @@ BOTH = [
     (dict(out_stride=(0, 256, 64)), "overlap"), (dict(k_new_stride=(1024, 0, 64)), "strides of keys"),
     (dict(k_new_stride=(-1024, 128, 64)), "strides of keys"), (dict(v_new_stride=(1024, 32, 64)), "strides of keys"),
     (dict(k_stride=(1 << 39, 512, 64)), "strides of keys"), (dict(v_stride=(1024, -512, 64)), "strides of keys"),
-    (dict(v_stride=(1024, 512, 0)), "strides of keys"), (dict(lse=A + 2), "4-byte"), (dict(lens=A + 1), "4-byte"),
+    (dict(v_stride=(1024, 512, 0)), "strides of keys"), (dict(q_stride=(2048, 256, 0)), "strides of q"),
+    (dict(q_stride=(2048, 0, 64)), "strides of q"), (dict(q_stride=(-2048, 256, 64)), "strides of q"),
+    (dict(q_stride=(2048, 256, 32)), "strides of q"), (dict(lse=A + 2), "4-byte"), (dict(lens=A + 1), "4-byte"),
     (dict(new_lens=A + 2), "4-byte"),
 ]
 

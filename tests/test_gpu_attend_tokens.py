@@ -141,3 +141,32 @@ def test_layouts(kvx, D):
 def test_scales(kvx, scale, S):
     q, args = make(2, S, 4, 2, 128, n=100, seed=9)
     tref.check("scale", kvx.attend_prompt, q, scale=scale, **args)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("n", [0, 40])
+def test_thousands_of_sequences(kvx, packed, n):
+    """Most of them empty, several for each thread that adds up the work."""
+    B, N, H, D = 2500, 2, 2, 64
+    gen = torch.Generator().manual_seed(1)
+    count = torch.randint(0, 4, (B,), generator=gen) * (torch.rand(B, generator=gen) < 0.1)
+    count[100:900] = 0
+    count[-3:] = torch.tensor([0, 90, 0])
+    at = torch.cat([torch.zeros(1, dtype=torch.long), count.cumsum(0)]).int()
+    lens = torch.randint(0, n + 1, (B,), generator=gen, dtype=torch.int32).cuda() if n else None
+    if packed:
+        q, args = make(B, int(at[-1]) + 2, N, H, D, n=n, packed=True, seed=6)
+        tref.check("packed", kvx.attend_prompt, q, starts=at.cuda(), lens=lens, **args)
+    else:
+        q, args = make(B, 90, N, H, D, n=n, seed=6)
+        tref.check("batch", kvx.attend_prompt, q, new_lens=count.int().cuda(), lens=lens, **args)
+
+
+@pytest.mark.parametrize("S,n", [(20, 0), (20, 4000), (300, 60), (2500, 0)])
+def test_without_log_sums(kvx, S, n):
+    q, args = make(1, S, 3, 2, 128, n=n, seed=S)
+    want, _ = tref.check("prompt", kvx.attend_prompt, q, **args)
+    out = torch.empty_like(q)
+    kvx.attend_prompt(q, out, **args)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
