@@ -1,6 +1,6 @@
 // attend_tokens_few.cu -- attention of several query tokens a sequence (kvevict_attend_prompt,
 // kvevict_attend_tree) where there is little of it: short prompts, small trees. The
-// tensor-core kernel of attend_tokens.cu takes 8 us for its start, one tile and its end.
+// tensor-core kernel of attend_tokens.cu takes 7 to 8 us for its start, one tile and its end.
 //
 // A unit is 16 query rows (tokens x the query heads of a key head) of a sequence's key
 // head: one cluster of CTAs, the unit's tiles of 16 keys dealt to the cluster's warps, the
@@ -12,6 +12,11 @@
 // Of the tokens' keys, token t sees 0..t, or itself and its ancestors. Values that are not
 // finite, in tiles that the unit's rows see in part, are left out of the products (their
 // weight of 0 would spoil the sums) and added at the end to the rows that see them.
+//
+// Bound by latency. Measured on GB300 (us, a call among others on the device): a prompt of 37
+// tokens, 4 heads of 64, 3.6; 8 drafted tokens on 32 rows 3.7; 16 tokens x 24 query heads on 8
+// of 512 rows 8.9, on 2048 (32 heads) 12.5. The cluster's sums one after the other instead
+// of all at once: 0.4 to 0.8 more.
 #include "attend_tokens.cuh"
 #include "mma_rows.cuh"
 
