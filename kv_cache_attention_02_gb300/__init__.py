@@ -147,6 +147,7 @@ _U64 = struct.Struct("=Q")
 _WORKSPACE_AT, _WORKSPACE_BYTES_AT = 40 + 11 * 8, _ATTENTION.size - 8    # offsets in kvevict_attention
 _TOKENS_BYTES_AT = _TOKENS.size - 8      # in kvevict_tokens, whose workspace is at the same offset
 _NO3, _NO4 = (0, 0, 0), (0, 0, 0, 0)     # strides of tensors that are not there
+_NO_PARTS = [(0,) * (MAX_JOIN - i) for i in range(MAX_JOIN + 1)]   # of a join's parts behind the last of i
 
 
 def _torch():
@@ -346,10 +347,11 @@ def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_
 def _tokens(q, out, k_new, v_new, starts, new_lens, parents, k, v, lens, lse, scale, stream, tree):
     """The ``kvevict_tokens`` of a call and its stream."""
     torch = _torch()
-    packed = q.dim() == 3 and not tree
-    if q.dim() != 4 and not packed:
+    shape, own = q.shape, k_new.shape
+    packed = len(shape) == 3 and not tree
+    if len(shape) != 4 and not packed:
         raise ValueError("q must have shape [batch, tokens, heads, head_dim]" + ("" if tree else " or [tokens, heads, head_dim]"))
-    kind, heads = q.dtype, q.shape[-2]
+    kind = q.dtype
     if kind not in _OUT:
         raise ValueError("q must be fp16 or bf16")
     if (k is None) != (v is None):
@@ -358,9 +360,9 @@ def _tokens(q, out, k_new, v_new, starts, new_lens, parents, k, v, lens, lse, sc
         raise ValueError("lens goes with k")
     if scale is not None and not 2.0**-126 <= scale <= 2.0**127:
         raise ValueError("scale must be from 2^-126 to 2^127")
-    if k_new.dim() != q.dim():
+    if len(own) != len(shape):
         raise ValueError("k_new must have as many dimensions as q")
-    B, S, H, D = 1, q.shape[-3], k_new.shape[-2], q.shape[-1]
+    H, D, B = own[-2], shape[-1], 1
     if packed:
         if new_lens is not None:
             raise ValueError("new_lens goes with a batch [batch, tokens, heads, head_dim], starts with packed tokens")
@@ -368,42 +370,50 @@ def _tokens(q, out, k_new, v_new, starts, new_lens, parents, k, v, lens, lse, sc
             if starts.dim() != 1 or starts.shape[0] < 1:
                 raise ValueError("starts must have shape [batch + 1]")
             B = starts.shape[0] - 1
-        room = (S,)
+        S, heads, _ = shape
+        own = (S, H, D)
     else:
         if starts is not None:
             raise ValueError("starts goes with packed tokens [tokens, heads, head_dim]")
-        B = q.shape[0]
-        room = (B, S)
+        B, S, heads, _ = shape
+        own = (B, S, H, D)
     n = 0
     if k is not None:
         if k.dim() != 4:
             raise ValueError("k must have shape [batch, kv_heads, rows, head_dim]")
         n = k.shape[2]
     device, s = _place(torch, q, stream)
-    own = (S, H, D) if packed else (B, S, H, D)
-    pointers, strides = [], []
-    for name, t, shape in (("q", q, q.shape), ("out", out, q.shape), ("k_new", k_new, own), ("v_new", v_new, own)):
-        at, st = _strided(name, t, shape, kind, device)
-        pointers.append(at)
-        strides += (0, *st[:2]) if packed else st[:3]
-    pk = pv = pp = tree_stride = 0
+    pq, sq = _strided("q", q, shape, kind, device)
+    po, so = _strided("out", out, shape, kind, device)
+    pkn, skn = _strided("k_new", k_new, own, kind, device)
+    pvn, svn = _strided("v_new", v_new, own, kind, device)
+    if packed:
+        sq, so, skn, svn = (0, *sq), (0, *so), (0, *skn), (0, *svn)
+    pk = pv = pp = tree_stride = pl = pst = pnl = plens = 0
     sk = sv = _NO4
     if n:
         pk, sk = _strided("k", k, (B, H, n, D), kind, device)
         pv, sv = _strided("v", v, (B, H, n, D), kind, device)
+    ints = torch.int32
     if parents is not None:
         if parents.dim() == 1:
             parents = parents.expand(B, -1)
         if parents.shape[-1:] == (1,):                          # (a single token's stride may be anything)
             parents = parents.as_strided((parents.shape[0], 1), (parents.stride(0), 1))
-        pp, st = _strided("parents", parents, (B, S), torch.int32, device)
+        pp, st = _strided("parents", parents, (B, S), ints, device)
         tree_stride = st[0]
-    ints = torch.int32
+    if lse is not None:
+        pl = _dense("lse", lse, shape[:-1], torch.float32, device)
+    if starts is not None:
+        pst = _dense("starts", starts, (B + 1,), ints, device)
+    if new_lens is not None:
+        pnl = _dense("new_lens", new_lens, (B,), ints, device)
+    if lens is not None:
+        plens = _dense("lens", lens, (B,), ints, device)
     return _TOKENS.pack(
-        _OUT[kind], B, S, heads, H, D, n, 0, scale or 0.0, 0, pointers[0], pointers[1],
-        _dense("lse", lse, (*room, heads), torch.float32, device), pointers[2], pointers[3],
-        _dense("starts", starts, (B + 1,), ints, device), _dense("new_lens", new_lens, (B,), ints, device), pp, pk, pv,
-        _dense("lens", lens, (B,), ints, device), 0, *strides, *sk[:3], *sv[:3], tree_stride, 0), s
+        _OUT[kind], B, S, heads, H, D, n, 0, scale or 0.0, 0, pq, po, pl, pkn, pvn, pst, pnl, pp, pk, pv, plens, 0,
+        sq[0], sq[1], sq[2], so[0], so[1], so[2], skn[0], skn[1], skn[2], svn[0], svn[1], svn[2], sk[0], sk[1], sk[2],
+        sv[0], sv[1], sv[2], tree_stride, 0), s
 
 
 def _call_tokens(call, cache, q, args, stream):
@@ -461,17 +471,21 @@ def attend_join(out, parts, *, lse=None, stream=None):
         raise ValueError(f"1 to {MAX_JOIN} parts can be joined, got {len(parts)}")
     device, s = _place(torch, out, stream)
     flat = len(shape) == 3
-    pointers, lses, strides = [0] * MAX_JOIN, [0] * MAX_JOIN, [0] * (3 * MAX_JOIN)
+    rows, count = shape[:-1], len(parts)
+    pointers, lses, strides = (), (), ()
     for i, (part, part_lse) in enumerate(parts):
-        pointers[i], st = _strided(f"part {i}", part, shape, kind, device)
-        strides[3 * i:3 * i + 3] = (0, *st[:2]) if flat else st[:3]
         if part_lse is None:
             raise ValueError(f"part {i} needs its lse")
-        lses[i] = _dense(f"lse of part {i}", part_lse, shape[:-1], torch.float32, device)
+        at, st = _strided(f"part {i}", part, shape, kind, device)
+        pointers += at,
+        lses += _dense(f"lse of part {i}", part_lse, rows, torch.float32, device),
+        strides += (0, st[0], st[1]) if flat else st[:3]
+    none = _NO_PARTS[count]
     to, st = _strided("out", out, shape, kind, device)
     B, S, G, D = (1, *shape) if flat else shape
-    args = _JOIN.pack(_OUT[kind], B, S, G, D, len(parts), 0, 0, *pointers, *lses, to,
-                      _dense("lse", lse, shape[:-1], torch.float32, device), *strides, *((0, *st[:2]) if flat else st[:3]))
+    args = _JOIN.pack(_OUT[kind], B, S, G, D, count, 0, 0, *pointers, *none, *lses, *none, to,
+                      _dense("lse", lse, rows, torch.float32, device), *strides, *none, *none, *none,
+                      *((0, st[0], st[1]) if flat else st[:3]))
     rc = lib().kvevict_attend_join(args, s)
     if rc:
         _check(rc)
