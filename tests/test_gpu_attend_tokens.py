@@ -36,6 +36,15 @@ def test_prompt_head_groups(kvx, N, D, n):
     tref.check("prompt", kvx.attend_prompt, q, **args)
 
 
+@pytest.mark.parametrize("N", [64, 65, 100, 127, 128, 131, 256])
+@pytest.mark.parametrize("D,n", [(64, 0), (128, 200)])
+def test_many_query_heads_a_key_head(kvx, N, D, n):
+    """One or two tokens a half block; more than 128 heads go in several groups (131, a prime: one each)."""
+    q, args = make(2, 7, N, 2, D, n=n, dtype=BF16, seed=N)
+    tref.check("prompt", kvx.attend_prompt, q, **args)
+    tref.check("tree", kvx.attend_tree, q, parents=trees(2, 7, N), **args)
+
+
 @pytest.mark.parametrize("B,S,N,H,D,n,dtype", [
     (1, 3000, 4, 1, 128, 0, F16), (1, 2500, 1, 3, 64, 0, BF16), (3, 2049, 5, 2, 128, 0, BF16), (1, 700, 3, 2, 128, 9000, F16),
     (2, 64, 8, 8, 128, 5000, BF16), (40, 300, 4, 8, 64, 0, F16), (5, 1, 4, 2, 128, 3001, F16), (1, 130, 16, 1, 64, 20000, BF16)])
