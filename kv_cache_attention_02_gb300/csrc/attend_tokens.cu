@@ -67,7 +67,9 @@ constexpr float kLazy = 8.f;
 template <typename T>
 constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 constexpr float kFar = 0x1p23f;        // base-2 logits from here on are whole numbers
-// What the start of a block costs, in tiles of half a block.
+// What the start of a block costs, in tiles of half a block: with 1, 2, 3 and 4 a prompt of
+// 8192 tokens takes 392, 390, 395 and 399 us, unequal trees on up to 65521 rows 325, 297, 292 and
+// 291, packed prompts 806, 777, 789 and 808.
 constexpr int kStartTiles = 2;
 
 // What a row tensor's TMA coordinates of heads and sequences are multiplied by: 0 where
