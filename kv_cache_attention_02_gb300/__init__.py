@@ -177,6 +177,8 @@ def _wrong(name, t, shape, dtype, device):
 
 def _strided(name, t, shape, dtype, device):
     """Pointer and strides of one call's tensor, after the checks."""
+    if t is None:
+        raise ValueError(f"{name} must be given")
     stride = t.stride()
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device or stride[-1] != 1:
         raise _wrong(name, t, shape, dtype, device)
@@ -347,6 +349,8 @@ def attend(q, out, *, k=None, v=None, lens=None, k_new=None, v_new=None, prefix_
 def _tokens(q, out, k_new, v_new, starts, new_lens, parents, k, v, lens, lse, scale, stream, tree):
     """The ``kvevict_tokens`` of a call and its stream."""
     torch = _torch()
+    if q is None or out is None or k_new is None or v_new is None:
+        raise ValueError("q, out, k_new and v_new must be given")
     shape, own = q.shape, k_new.shape
     packed = len(shape) == 3 and not tree
     if len(shape) != 4 and not packed:
@@ -461,6 +465,8 @@ def attend_join(out, parts, *, lse=None, stream=None):
     takes no weight. Layouts as in ``attend``. Errors: ValueError, KVEvictError.
     """
     torch = _torch()
+    if out is None or parts is None:
+        raise ValueError("out and parts must be given")
     if out.dim() not in (3, 4):
         raise ValueError("out must have shape [batch, tokens, heads, head_dim] or [tokens, heads, head_dim]")
     kind, shape = out.dtype, out.shape
@@ -474,8 +480,8 @@ def attend_join(out, parts, *, lse=None, stream=None):
     rows, count = shape[:-1], len(parts)
     pointers, lses, strides = (), (), ()
     for i, (part, part_lse) in enumerate(parts):
-        if part_lse is None:
-            raise ValueError(f"part {i} needs its lse")
+        if part is None or part_lse is None:
+            raise ValueError(f"part {i} must be given, with its lse")
         at, st = _strided(f"part {i}", part, shape, kind, device)
         pointers += at,
         lses += _dense(f"lse of part {i}", part_lse, rows, torch.float32, device),
