@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t phase = (uint32_t)(seg / kSegs) & 1;
     if (ok) ok = wait_or_abort(seg_full(seg), phase, abort_flag, p.err);
     ok = __all_sync(~0u, ok);
-    if (!ok && !mbar_wait_bounded(seg_full(seg), phase)) return nullptr;
+    // (all lanes alike: the warp stays whole for the collective instructions behind this)
+    if (!ok && !__all_sync(~0u, mbar_wait_bounded(seg_full(seg), phase))) return nullptr;
     __syncwarp();
     const Seg* g = &segs[seg % kSegs];
     return g->tiles ? g : nullptr;
@@ -947,7 +948,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (releases) release(2 * n - 1);
       }
       ring = (ring + 2 * tiles) % NS;
-      const bool poisoned = marks[seg % kSegs] == seg;
+      // (all lanes alike, as the accumulators' loads want it. The mark may be on its way for a tile
+      // that only the second half of the block visits: either answer gives these rows the same sums.)
+      const bool poisoned = __any_sync(~0u, marks[seg % kSegs] == seg);
       if (__builtin_expect(poisoned && begun, 0)) {
         // values that are not finite, dropped from the tiles that rows see in part
         const uint64_t seen = a.parents ? seen_of(g, t) : 0;
