@@ -584,6 +584,12 @@ int kvevict_attend_tree_cache(const kvevict_t* h, int32_t l, const kvevict_token
  * few query rows, but the tensor cores' whatever their size. Errors: none. */
 int kvevict_test_without_few_kernel(int32_t without);
 
+/* Test hook: while `without` is not 0, calls of this process are planned as if the tensor-core
+ * kernel of kvevict_attend_prompt and kvevict_attend_tree could not be launched (a driver without
+ * tensor maps, a compiler that gave the kernel other registers): the kernel for few query rows then
+ * answers all of them, with the same results, large calls slowly. Errors: none. */
+int kvevict_test_without_tokens_kernel(int32_t without);
+
 /* Device bytes that a call of this description needs as workspace, on the current
  * device (at most); of the pointers only starts counts (whether it is null). with_cache: 1 for
  * kvevict_attend_tree_cache, else 0. *bytes: host. Errors: INVALID_ARG, CUDA. */

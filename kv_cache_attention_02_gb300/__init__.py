@@ -90,6 +90,7 @@ SIGNATURES = {
     "kvevict_attend_tokens_workspace": (ctypes.c_int, [P, i32, P]),
     "kvevict_attend_join": (ctypes.c_int, [P, P]),
     "kvevict_test_without_few_kernel": (ctypes.c_int, [i32]),
+    "kvevict_test_without_tokens_kernel": (ctypes.c_int, [i32]),
 }
 
 

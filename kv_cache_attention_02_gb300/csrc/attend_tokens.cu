@@ -1224,6 +1224,8 @@ auto pick(int D, int dtype, const TokensPlan& p, F&& f) {
   return dtype == kBf16 ? pick_shape<__nv_bfloat16>(D, p, f) : pick_shape<__half>(D, p, f);
 }
 
+std::atomic<bool> g_off{false};   // test hook
+
 // Rows as a 4-D tensor [sequence, row, head, D], whatever the strides (a dimension of one
 // entry, or that all share, with any); boxes of 64 elements (128 bytes), or 32, of so many
 // heads and rows; rows past the last read as zeros.
@@ -1263,7 +1265,7 @@ TokensPlan tokens_plan(bool pair, bool split, int64_t blocks, int heads, int64_t
 }
 
 bool tokens_kernel_ready(int D, int dtype, const TokensPlan& plan, int device) {
-  if (!encode_fn()) return false;
+  if (g_off.load(std::memory_order_relaxed) || !encode_fn()) return false;
   return pick(D, dtype, plan, [&](auto kind) {
     using K = decltype(kind);
     // The kernel's redistribution of registers needs the 168 a thread that its
@@ -1281,6 +1283,8 @@ bool tokens_kernel_ready(int D, int dtype, const TokensPlan& plan, int device) {
     return true;
   });
 }
+
+void tokens_kernel_off(bool off) { g_off.store(off); }
 
 cudaError_t launch_attend_tokens(const TokensLaunch& l, int D, int dtype, cudaStream_t s) {
   Params p{};

@@ -68,11 +68,14 @@ struct TokensLaunch {
   int* err;                // error word for bounded waits, or null
   int stall;               // test hook: CTA 0's first tile is never issued
 };
+// Whether the kernel can be launched as it was compiled, on a device below 64 (looked up once).
 bool tokens_kernel_ready(int D, int dtype, const TokensPlan& plan, int device);
+void tokens_kernel_off(bool off);   // test hook: never ready
 cudaError_t launch_attend_tokens(const TokensLaunch& l, int D, int dtype, cudaStream_t s);
 int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaStream_t s);
 
-// The kernel for few query rows (attend_tokens_few.cu).
+// The kernel for few query rows (attend_tokens_few.cu). It answers any call, one of many
+// rows slowly.
 struct FewArgs {
   const void* q;
   const void* k;
@@ -85,7 +88,7 @@ struct FewArgs {
 struct FewPlan {
   int64_t units, chunks;
   int cluster;
-  double us;               // the call's time, about; infinite where the kernel cannot take it
+  double us;               // the call's time, about; infinite where its CTAs do not all run at once
 };
 FewPlan few_plan(int64_t B, int64_t rows, bool packed, int H, int64_t n, int64_t tokens, int sms);
 cudaError_t launch_attend_tokens_few(const TokensArgs& a, const FewArgs& f, const FewPlan& p, int D, int dtype, cudaStream_t s);

@@ -141,7 +141,9 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
   const FewPlan few = few_plan(d->batch, (int64_t)d->seq * (d->n_heads / d->n_kv_heads), d->starts != nullptr, d->n_kv_heads, all,
                                d->seq, dev.sms);
   l.plan = plan_of(d, all, dev);
-  if (few.us < l.plan.us && !g_without_few.load(std::memory_order_relaxed)) {
+  // (where the tensor-core kernel cannot be launched, the other one answers every call)
+  if ((few.us < l.plan.us && !g_without_few.load(std::memory_order_relaxed)) ||
+      !tokens_kernel_ready(D, d->dtype, l.plan, dev.device)) {
     FewArgs f{};
     f.q = d->q;
     f.k = l.k.base;
@@ -159,10 +161,6 @@ int tokens_run(const kvevict_tokens* d, bool tree, const CacheRows* rows, cudaSt
     return cuda_result(launch_attend_tokens_few(a, f, few, D, d->dtype, s), "launch");
   }
   a.half = (l.plan.split ? 64 : 128) / a.N;
-  if (!tokens_kernel_ready(D, d->dtype, l.plan, dev.device)) {
-    set_last_error("the attention kernel cannot be launched here: no tensor maps, or another register count than it needs");
-    return KVEVICT_ERR_CUDA;
-  }
   const size_t need = l.plan.bytes(D);
   if (need && (d->workspace_bytes < need || !d->workspace || !aligned(d->workspace))) {
     set_last_error("workspace must be 16-byte aligned and hold kvevict_attend_tokens_workspace bytes");
@@ -237,6 +235,11 @@ extern "C" int kvevict_attend_tokens_workspace(const kvevict_tokens* args, int32
 
 extern "C" int kvevict_test_without_few_kernel(int32_t without) {
   kvx::g_without_few.store(without != 0);
+  return KVEVICT_OK;
+}
+
+extern "C" int kvevict_test_without_tokens_kernel(int32_t without) {
+  kvx::tokens_kernel_off(without != 0);
   return KVEVICT_OK;
 }
 

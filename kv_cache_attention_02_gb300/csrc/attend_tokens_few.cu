@@ -1,6 +1,7 @@
 // attend_tokens_few.cu -- attention of several query tokens a sequence (kvevict_attend_prompt,
 // kvevict_attend_tree) where there is little of it: short prompts, small trees. The
 // tensor-core kernel of attend_tokens.cu takes 7 to 8 us for its start, one tile and its end.
+// Where that kernel cannot be launched, this one answers its calls, too.
 //
 // A unit is 16 query rows (tokens x the query heads of a key head) of a sequence's key
 // head: one cluster of CTAs, the unit's tiles of 16 keys dealt to the cluster's warps, the
@@ -52,23 +53,35 @@ __global__ void __launch_bounds__(kThreads, 2) tokens_few_kernel(const __grid_co
     b = (int)((unsigned)chunk / (unsigned)f.chunks);
     chunk -= b * f.chunks;
   } else {
-    // packed (at most a sequence a thread): the sequence whose chunks this one is among
-    const Seq s = tid < a.B ? load_seq(a, tid) : Seq{0, 0, 0, 0};
-    const int own = (int)((unsigned)(s.nq * N + kRows - 1) / (unsigned)kRows);
-    int to = own;
-    for (int d = 1; d < 32; d *= 2) {
-      const int x = __shfl_up_sync(~0u, to, d);
-      if (lane >= d) to += x;
-    }
-    if (lane == 31) sums_s[warp] = to;
+    // packed: the sequence whose chunks this one is among, a sequence a thread at a time. (Sums
+    // end at a number above every chunk's: sequences that overlap could add up to anything.)
+    constexpr int kEnd = 1 << 29;
+    int before = 0;
     if (tid == 0) found_s[0] = -1;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) to += sums_s[w];
-    if (chunk >= to - own && chunk < to) {
-      found_s[0] = tid;
-      found_s[1] = chunk - (to - own);
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const Seq s = b0 + tid < a.B ? load_seq(a, b0 + tid) : Seq{0, 0, 0, 0};
+      const int own = (int)((unsigned)(s.nq * N + kRows - 1) / (unsigned)kRows);
+      int to = own;
+      for (int d = 1; d < 32; d *= 2) {
+        const int x = __shfl_up_sync(~0u, to, d);
+        if (lane >= d) to = min(to + x, kEnd);
+      }
+      if (lane == 31) sums_s[warp] = to;
+      __syncthreads();
+      for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) {
+          to = min(to + before, kEnd);
+          if (chunk >= to - own && chunk < to) {
+            found_s[0] = b0 + tid;
+            found_s[1] = chunk - (to - own);
+          }
+        }
+        before = min(before + sums_s[w], kEnd);
+      }
+      __syncthreads();
+      if (found_s[0] >= 0) break;
     }
-    __syncthreads();
     b = found_s[0];
     chunk = found_s[1];
     if (b < 0) return;                                 // (the whole cluster)
@@ -382,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) tokens_few_kernel(const __grid_co
 
 template <typename T, int D>
 cudaError_t launch_one(const TokensArgs& a, const FewArgs& f, const FewPlan& p, cudaStream_t s) {
+  if (p.units * p.cluster > 0x7FFFFFFF) return cudaErrorInvalidValue;
   return launch_after(tokens_few_kernel<T, D>, dim3((unsigned)(p.units * p.cluster)), kThreads, 0, p.cluster, false, s, a, f);
 }
 
@@ -393,7 +407,6 @@ FewPlan few_plan(int64_t B, int64_t rows, bool packed, int H, int64_t n, int64_t
   p.units = (packed ? rows / kRows + B : B * p.chunks) * H;
   const int64_t tiles = (n + 15) / 16 + (tokens + 15) / 16;
   p.us = 1e30;
-  if (packed && B > kThreads) return p;
   // CTAs of a unit's cluster: its tiles are split while all CTAs are resident together
   // and a warp has more than one tile.
   p.cluster = 1;
@@ -404,7 +417,7 @@ FewPlan few_plan(int64_t B, int64_t rows, bool packed, int H, int64_t n, int64_t
   // 25.8, one sequence of 16 on 2048 12.5 | 19.7; 128 tokens of a prompt 9.0 | 8.5, 64 6.4 | 8.3.
   const double warp_tiles = (double)((tiles + p.cluster * kWarps - 1) / (p.cluster * kWarps));
   const int64_t ctas = p.units * p.cluster;
-  if (ctas <= 2 * sms)
+  if (ctas <= 2 * sms && !(packed && B > kThreads))   // (a sequence a thread, in one go)
     p.us = 4.5 + 0.9 * warp_tiles + (p.cluster > 1 ? 1.5 : 0) + (ctas > sms ? 1 + 0.5 * warp_tiles : 0);
   return p;
 }
