@@ -1255,11 +1255,11 @@ TokensPlan tokens_plan(bool pair, bool split, int64_t blocks, int heads, int64_t
   // Cut blocks cost their parts' way through memory and the join, about nine tiles' time;
   // whole ones leave CTAs with less than others: 32 query heads on 8 of 1024 tokens 20.9 us
   // whole, 33.8 cut, of 2048 60.3 and 55.7; 2 x 40 drafted tokens on 1500 rows 28.3 and 21.5.
-  const double even = (double)(units * mean) / sms;
+  const double even = (double)units * (double)mean / sms;
   pl.whole = tiles <= 6 || (units <= sms ? (double)tiles : even + 0.6 * (double)tiles) < even + 9;
   pl.even = pl.whole && units <= sms;
   pl.us = 7 + 1.3 * (pl.even ? (double)tiles : pl.whole ? even + 0.6 * (double)tiles : even + 8);
-  pl.ctas = (int)std::min<int64_t>(sms, pl.whole ? units : units * tiles);
+  pl.ctas = (int)std::min<int64_t>(sms, pl.whole || units >= sms ? units : units * tiles);
   pl.per_cta = 1.0 / pl.ctas;
   return pl;
 }

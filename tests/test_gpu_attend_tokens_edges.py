@@ -186,3 +186,16 @@ def test_values_that_only_a_blocks_second_half_visits(kvx, D, dtype):
             assert torch.equal(out[:, :at], want[:, :at]) and torch.equal(lse, wlse)
             assert out[:, at:, :, 3].isnan().all()
             assert torch.equal(out[..., :3], want[..., :3]) and torch.equal(out[..., 4:], want[..., 4:])
+
+
+def test_workspace_of_the_largest_descriptions(kvx):
+    """As much work as the arguments allow, far more than any memory: the size that every cut call asks for."""
+    def need(B, S, G, H, n):
+        packed = kvx._TOKENS.pack(0, B, S, G, H, 128, n, 0, 0.0, 0, *(0,) * 12, *(0,) * 19, 0)
+        size = ctypes.c_size_t(0)
+        assert kvx.lib().kvevict_attend_tokens_workspace(packed, 0, ctypes.addressof(size)) == kvx.OK
+        return size.value
+    cut = need(1, 400, 4, 2, 3000)
+    assert cut > 0
+    assert need(1, 1 << 29, 1 << 26, 1 << 26, (1 << 29) - 1) == need(1 << 10, 1 << 29, 1 << 16, 1 << 16, (1 << 29) - 1) == \
+        need(64, 4096, 32, 8, 1 << 20)
