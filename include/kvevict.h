@@ -460,7 +460,8 @@ typedef struct kvevict_attention {
  * The shared rows are read once for all sequences, not once for each; without
  * own rows the call is the prefix's part of a longer attention (a prompt
  * chunk's tokens given as sequences), and lse joins it with the rest. Logits,
- * softmax and sums are fp32; out is rounded once. out and lse overlap no input.
+ * softmax and sums are fp32; out is rounded once, and where many query rows share a prefix
+ * every weight of its rows, too, before its product with v_j. out and lse overlap no input.
  * A key whose logit is NaN or +inf makes its sequences' out and lse NaN; one of
  * -inf takes no weight. A value that is NaN or infinite shows in its column of
  * out as NaN or infinite (which of the two depends on the sizes: a weight is
@@ -554,7 +555,8 @@ typedef struct kvevict_tokens {
  *   out = sum_j e^(s_j) v_j / sum_j e^(s_j),   lse = log sum_j e^(s_j).
  * Query head i reads key head i / (G / H). Tokens behind a sequence's last are neither
  * read nor written: their out and lse stay as they are. Logits, softmax and sums are
- * fp32; out is rounded once. out and lse overlap no input.
+ * fp32; out is rounded once, and in calls of many query rows every weight e^(s_j), too, before
+ * its product with v_j (to dtype: half a step of each, at random). out and lse overlap no input.
  * A key whose logit is NaN or +inf makes out and lse of the query heads that see it
  * NaN; one of -inf takes no weight. A value that is NaN or infinite shows in its
  * column of out, as NaN or infinite, wherever it is seen and nowhere else. Rows and
@@ -591,7 +593,8 @@ int kvevict_test_without_few_kernel(int32_t without);
 int kvevict_test_without_tokens_kernel(int32_t without);
 
 /* Device bytes that a call of this description needs as workspace, on the current
- * device (at most); of the pointers only starts counts (whether it is null). with_cache: 1 for
+ * device (at most); of the pointers only starts and parents count (whether they are null:
+ * packed tokens; a tree's limits). with_cache: 1 for
  * kvevict_attend_tree_cache, else 0. *bytes: host. Errors: INVALID_ARG, CUDA. */
 int kvevict_attend_tokens_workspace(const kvevict_tokens* args, int32_t with_cache, size_t* bytes);
 

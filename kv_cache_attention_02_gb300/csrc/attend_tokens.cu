@@ -10,7 +10,10 @@
 // token t sees 0..t (a prompt) or itself and its ancestors (a tree). The arithmetic is
 // that of attend_prefix.cu: 16-bit weights for the second product (the sum of two 16-bit
 // parts with up to 128 query rows), the sum l of the unrounded ones in fp32 relative to
-// m, which moves only when the maximum has grown by 2^8.
+// m, which moves only when the maximum has grown by 2^8. Two parts at more rows, too, would
+// give outputs whose error is their own rounding's; with one it is 1.2 to 1.5 times that (two
+// half steps, independent), and the products are two instead of three: 8 x 4096 tokens 823
+// us, 1265 with two parts, one prompt of 8192 390 and 585, of 512 13.6 and 16.6.
 //
 // Work: see TokensPlan. A half block is the rows of 128 / N tokens, which one TMA box
 // brings. A block is PAIR: one half, its key tiles dealt alternately to two streams; else
@@ -41,8 +44,11 @@
 // 385-400 us, 1.37-1.43 PFLOP/s (0.70-0.73 of the measured matrix rate; the tensor pipe 65%
 // busy); 8 x 4096 tokens 815-830 us; 8 x 1024 101 us; 160 tokens 8.7 us, of which start and
 // end are most; 32 sequences of 16 drafted tokens on 2048 rows 59 us, 4.7 TB/s of rows. A
-// tile of 256 query rows takes 1.35 us, in which the products have 0.6 of the time and the
-// rest is the chain from logits to weights and back; a change of blocks 2 us. Tried and
+// tile of 256 query rows, its rows in L2 and all to be seen, takes 1.55 (bf16) to 1.59 us
+// (fp16) at 2.07 GHz, in which the products have 1.05 and the rest is the chain from logits to
+// weights and back; D = 64 1.31; PAIR 1.24 and 1.0, SPLIT 1.12 and 0.91 (from the times of 152
+// blocks on 1024 and on 8192 rows). A change of blocks costs 3.5 us beside their tiles, D = 64
+// 3.1 (152 k blocks of three tiles, k 4 and 16). Tried and
 // slower: the query rows by cp.async of the softmax or the helper warps (5 us a block; TMA
 // below 1), every role walking its range itself (224 bytes of spills a thread, 1336 against
 // 1032 us for 8 x 4096 tokens at the time), one loop over the two streams' products (450
@@ -1166,7 +1172,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of cut blocks: grid (boundary between CTAs, 32 rows of the block, 32
 // columns), where the first boundary inside a block takes it. A lane is a row, a warp
-// four columns; the parts are few.
+// four columns, and a block's parts follow one another: few of them where there are many
+// blocks; one block over all SMs has up to one an SM, 0.37 us each (16 tokens of 4 query heads on
+// one key head of 16384 rows: 62 us in all, 8 key heads 30).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) tokens_join_kernel(const __grid_constant__ Params p) {
   const TokensArgs& a = p.a;
@@ -1258,6 +1266,8 @@ TokensPlan tokens_plan(bool pair, bool split, int64_t blocks, int heads, int64_t
   const double even = (double)units * (double)mean / sms;
   pl.whole = tiles <= 6 || (units <= sms ? (double)tiles : even + 0.6 * (double)tiles) < even + 9;
   pl.even = pl.whole && units <= sms;
+  // (a tile's time is that of 256 query rows at D = 64, between the others' 0.9 to 1.6 us; a cut
+  // call's parts are charged as if there were few, too little for one block over all SMs)
   pl.us = 7 + 1.3 * (pl.even ? (double)tiles : pl.whole ? even + 0.6 * (double)tiles : even + 8);
   pl.ctas = (int)std::min<int64_t>(sms, pl.whole || units >= sms ? units : units * tiles);
   pl.per_cta = 1.0 / pl.ctas;
